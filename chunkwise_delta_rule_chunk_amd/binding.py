@@ -17,6 +17,8 @@ REWY_GATE_NONE, REWY_GATE_SCALAR, REWY_GATE_VECTOR = 0, 1, 2
 REWY_BF16, REWY_F32 = 0, 1
 REWY_RECOMPUTE, REWY_SAVE = 0, 1
 REWY_SCHEDULE_JOINT, REWY_SCHEDULE_SEPARATE = 0, 1
+REWY_QUANT_NONE, REWY_QUANT_E4M3, REWY_QUANT_INT8 = 0, 1, 2
+REWY_ACT_NONE, REWY_ACT_SILU = 0, 1
 
 NOALLOC_SCRATCH_BYTES = 128 << 20  # REWY_NOALLOC_SCRATCH_BYTES
 
@@ -24,6 +26,8 @@ EXPORTS = ("rewy_workspace_bytes", "rewy_saved_bytes", "rewy_fwd", "rewy_bwd", "
            "rewy_fwd_gdn2",
            "rewy_bwd_gdn2", "rewy_fwd_kda_gate", "rewy_bwd_kda_gate", "rewy_recurrent_fwd",
            "rewy_recurrent_fwd_gdn2",
+           "rewy_norm_fwd", "rewy_norm_workspace_bytes", "rewy_norm_bwd",
+           "rewy_conv_fwd", "rewy_conv_step", "rewy_conv_workspace_bytes", "rewy_conv_bwd",
            "rewy_bwd_schedule", "rewy_trace_begin", "rewy_trace_end", "rewy_trace_select",
            "rewy_status_string",
            "rewy_last_error")
@@ -36,6 +40,24 @@ class RewyDesc(ctypes.Structure):
         ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
         ("dtype", ctypes.c_int32), ("beta_dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
         ("policy", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class RewyNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32), ("quant", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("res_stride", ctypes.c_int64),
+        ("sum_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+    ]
+
+
+class RewyConvDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("W", ctypes.c_int32),
+        ("N", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
     ]
 
 
@@ -88,6 +110,17 @@ def load():
         lib.rewy_recurrent_fwd.restype = ctypes.c_int
         lib.rewy_recurrent_fwd_gdn2.argtypes = [D] + [P] * 10
         lib.rewy_recurrent_fwd_gdn2.restype = ctypes.c_int
+        ND, CD = ctypes.POINTER(RewyNormDesc), ctypes.POINTER(RewyConvDesc)
+        for name, args, res in (
+                ("rewy_norm_fwd", [ND] + [P] * 9, ctypes.c_int),
+                ("rewy_norm_workspace_bytes", [ND], S),
+                ("rewy_norm_bwd", [ND] + [P] * 8 + [S, P], ctypes.c_int),
+                ("rewy_conv_fwd", [CD] + [P] * 7, ctypes.c_int),
+                ("rewy_conv_step", [CD] + [P] * 7, ctypes.c_int),
+                ("rewy_conv_workspace_bytes", [CD], S),
+                ("rewy_conv_bwd", [CD] + [P] * 11 + [S, P], ctypes.c_int)):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = res
         lib.rewy_bwd_schedule.argtypes = [ctypes.c_int]
         lib.rewy_bwd_schedule.restype = ctypes.c_int
         lib.rewy_trace_begin.argtypes = []
@@ -157,6 +190,37 @@ def rewy_recurrent_fwd(desc, q, k, v, g, beta, h0, o, ht, stream) -> int:
 
 def rewy_recurrent_fwd_gdn2(desc, q, k, v, g, b, w, h0, o, ht, stream) -> int:
     return load().rewy_recurrent_fwd_gdn2(ctypes.byref(desc), q, k, v, g, b, w, h0, o, ht, stream)
+
+
+def rewy_norm_fwd(desc, x, res, w, sum, y, q, scale, rstd, stream) -> int:
+    return load().rewy_norm_fwd(ctypes.byref(desc), x, res, w, sum, y, q, scale, rstd, stream)
+
+
+def rewy_norm_workspace_bytes(desc) -> int:
+    return load().rewy_norm_workspace_bytes(ctypes.byref(desc))
+
+
+def rewy_norm_bwd(desc, s, w, rstd, dy, ds, dx, dw, workspace, ws_bytes, stream) -> int:
+    return load().rewy_norm_bwd(ctypes.byref(desc), s, w, rstd, dy, ds, dx, dw, workspace, ws_bytes,
+                                stream)
+
+
+def rewy_conv_fwd(desc, x, w, bias, h0, y, ht, stream) -> int:
+    return load().rewy_conv_fwd(ctypes.byref(desc), x, w, bias, h0, y, ht, stream)
+
+
+def rewy_conv_step(desc, x, w, bias, h0, y, ht, stream) -> int:
+    return load().rewy_conv_step(ctypes.byref(desc), x, w, bias, h0, y, ht, stream)
+
+
+def rewy_conv_workspace_bytes(desc) -> int:
+    return load().rewy_conv_workspace_bytes(ctypes.byref(desc))
+
+
+def rewy_conv_bwd(desc, x, w, bias, h0, dy, dht, dx, dw, dbias, dh0, workspace, ws_bytes,
+                  stream) -> int:
+    return load().rewy_conv_bwd(ctypes.byref(desc), x, w, bias, h0, dy, dht, dx, dw, dbias, dh0,
+                                workspace, ws_bytes, stream)
 
 
 def rewy_bwd_schedule(schedule: int) -> int:

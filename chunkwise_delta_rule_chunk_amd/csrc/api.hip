@@ -2,21 +2,14 @@
 // workspace planning and the launch sequence of each pass.  Nothing here
 // allocates device memory or waits for the device.
 #include <cxxabi.h>
-#include <stdarg.h>
-#include <stdio.h>
 #include <stdlib.h>
-#include <string.h>
 
 #include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <string>
-#include <vector>
 
-#include "kernels.hpp"
-#include "rewy.h"
-
-#define REWY_API extern "C" __attribute__((visibility("default")))
+#include "host.hpp"
 
 namespace rewy {
 
@@ -24,8 +17,6 @@ const void*& last_kernel() {
   static thread_local const void* k = nullptr;
   return k;
 }
-
-namespace {
 
 thread_local char g_err[512] = "";
 
@@ -37,8 +28,9 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-constexpr size_t ALIGN = 256;
-size_t up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
+thread_local Tracer g_tr;
+
+namespace {
 
 struct Plan {
   int B, T, H, K, V, N, nc_max;
@@ -196,19 +188,12 @@ __global__ void k_copy_or_zero(float* dst, const float* src, int64_t n) {
     dst[i] = src ? src[i] : 0.f;
 }
 
-int hip_check(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(REWY_EHIP, "%s: %s", what, hipGetErrorString(e));
-  return REWY_OK;
-}
-
 int copy_state(float* dst, const float* src, int64_t n, hipStream_t s) {
   if (!dst || n == 0) return REWY_OK;
   const int blocks = (int)std::min<int64_t>((n + 255) / 256, 4096);
   REWY_LAUNCH(k_copy_or_zero, dim3(blocks), dim3(256), s, dst, src, n);
   return hip_check(hipGetLastError(), "state copy");
 }
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 void fill_common(Args& a, const Plan& p, const rewy_desc* d, char* ws, char* sv,
                  const Layout& L) {
@@ -241,43 +226,6 @@ int check_tensor_ptrs(const void* const* ps, const char* const* names, int n) {
     if (!aligned(ps[i], 16)) return fail(REWY_EINVAL, "%s is not 16-byte aligned", names[i]);
   }
   return REWY_OK;
-}
-
-// ---- tracing: event pairs around every launch, per thread ------------------
-struct TraceRec {
-  const void* fn;  // host stub of the launched kernel
-  hipStream_t s;
-  hipEvent_t e0, e1;
-};
-struct Tracer {
-  bool on = false;
-  char only[64] = {0};  // empty: every launch
-  std::vector<TraceRec> recs;
-  std::vector<hipEvent_t> pool;
-  size_t used = 0;
-  hipEvent_t ev() {
-    if (used == pool.size()) {
-      hipEvent_t e;
-      if (hipEventCreate(&e) != hipSuccess) return nullptr;
-      pool.push_back(e);
-    }
-    return pool[used++];
-  }
-};
-thread_local Tracer g_tr;
-
-// `stage` is the kernel's template name, which rewy_trace_select matches
-template <typename F>
-hipError_t traced(const char* stage, hipStream_t s, F&& launch) {
-  if (!g_tr.on || (g_tr.only[0] && strcmp(g_tr.only, stage) != 0)) return launch();
-  TraceRec r{nullptr, s, g_tr.ev(), g_tr.ev()};
-  if (r.e0) hipEventRecord(r.e0, s);
-  last_kernel() = nullptr;
-  const hipError_t e = launch();
-  if (r.e1) hipEventRecord(r.e1, s);
-  r.fn = last_kernel();
-  if (r.e0 && r.e1 && r.fn) g_tr.recs.push_back(r);
-  return e;
 }
 
 // The kernel's name as the profiler reports it: the symbol of the launched

@@ -1,0 +1,250 @@
+// Host side of the operators around the token mixer (include/rewy.h): argument
+// checks, workspace sizes and launches.  Nothing here allocates device memory
+// or waits for the device.
+#include <exception>
+
+#include "host.hpp"
+#include "layer.hpp"
+
+namespace rewy {
+namespace {
+
+// No exception leaves the C ABI.
+template <typename F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(REWY_EHIP, "host error: %s", e.what());
+  }
+}
+
+size_t esize(int dtype) { return dtype == REWY_F32 ? 4 : 2; }
+
+int check_dtype(const char* what, int v) {
+  if (v != REWY_BF16 && v != REWY_F32) return fail(REWY_EINVAL, "bad %s %d", what, v);
+  return REWY_OK;
+}
+
+// A given pointer has its elements' alignment.
+int check_ptr(const char* name, const void* p, size_t align, bool need) {
+  if (!p) return need ? fail(REWY_EINVAL, "%s is NULL", name) : (int)REWY_OK;
+  if (!aligned(p, align)) return fail(REWY_EINVAL, "%s is not %zu-byte aligned", name, align);
+  return REWY_OK;
+}
+#define REWY_TRY(expr)                \
+  do {                                \
+    const int rc_ = (expr);           \
+    if (rc_ != REWY_OK) return rc_;   \
+  } while (0)
+
+int check_stride(const char* name, int64_t given, int64_t len, int64_t& out) {
+  if (given != 0 && given < len)
+    return fail(REWY_EINVAL, "%s %lld is shorter than the row's %lld elements", name, (long long)given, (long long)len);
+  if (given > (int64_t)1 << 31) return fail(REWY_EINVAL, "%s %lld is too large", name, (long long)given);
+  out = given ? given : len;
+  return REWY_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need && (!ws || !aligned(ws, ALIGN) || have < need))
+    return fail(REWY_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, have);
+  return REWY_OK;
+}
+
+// ---- RMS norm -----------------------------------------------------------------
+int norm_args(const rewy_norm_desc* d, NormArgs& a) {
+  if (!d) return fail(REWY_EINVAL, "desc is NULL");
+  if (d->M < 0 || d->M > INT32_MAX || d->D <= 0) return fail(REWY_EINVAL, "bad shape M=%lld D=%d", (long long)d->M, d->D);
+  if (d->D > 16384) return fail(REWY_EUNSUPPORTED, "D=%d exceeds 16384", d->D);
+  REWY_TRY(check_dtype("dtype", d->dtype));
+  REWY_TRY(check_dtype("w_dtype", d->w_dtype));
+  if (d->quant < REWY_QUANT_NONE || d->quant > REWY_QUANT_INT8) return fail(REWY_EINVAL, "bad quant %d", d->quant);
+  if (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128 && d->group != 256)
+    return fail(REWY_EINVAL, "bad group %d (0, 32, 64, 128 or 256)", d->group);
+  if (!(d->eps >= 0.f) || d->eps > 3e38f) return fail(REWY_EINVAL, "bad eps %g", (double)d->eps);
+  memset(&a, 0, sizeof(a));
+  a.M = d->M; a.D = d->D; a.quant = d->quant; a.group = d->group; a.eps = d->eps;
+  a.ng = d->group ? (d->D + d->group - 1) / d->group : 1;
+  REWY_TRY(check_stride("x_stride", d->x_stride, d->D, a.xs));
+  REWY_TRY(check_stride("res_stride", d->res_stride, d->D, a.rs));
+  REWY_TRY(check_stride("sum_stride", d->sum_stride, d->D, a.ss));
+  REWY_TRY(check_stride("y_stride", d->y_stride, d->D, a.ys));
+  a.nblk = norm_bwd_blocks(d->M, d->D, d->dtype == REWY_F32);
+  return REWY_OK;
+}
+size_t norm_ws(const NormArgs& a) { return up(std::max<size_t>((size_t)a.nblk * a.D * 4, 1)); }
+
+// ---- sequences ------------------------------------------------------------------
+int seq_args(int B, int T, int N, const int32_t* cu, const int32_t* host, SeqArgs& q) {
+  if (B <= 0 || T < 0) return fail(REWY_EINVAL, "bad shape B=%d T=%d", B, T);
+  const int64_t total = (int64_t)B * T;
+  if (total > INT32_MAX - 65536) return fail(REWY_EINVAL, "B*T=%lld is too large", (long long)total);
+  q.cu = cu; q.T = T; q.total = (int)total;
+  if (cu) {
+    if (B != 1) return fail(REWY_EINVAL, "cu_seqlens requires B == 1 (got B=%d)", B);
+    if (N <= 0) return fail(REWY_EINVAL, "cu_seqlens requires N >= 1 (got N=%d)", N);
+    if (!aligned(cu, 4)) return fail(REWY_EINVAL, "cu_seqlens is not 4-byte aligned");
+    if (N > (1 << 24)) return fail(REWY_EINVAL, "N=%d is too large", N);
+    if (host) {
+      if (host[0] != 0 || host[N] > T) return fail(REWY_EINVAL, "cu_seqlens must start at 0 and end at T=%d at most", T);
+      for (int i = 0; i < N; ++i)
+        if (host[i + 1] < host[i]) return fail(REWY_EINVAL, "cu_seqlens not ascending at %d", i);
+    }
+    q.N = N;
+  } else {
+    if (N != 0 && N != B) return fail(REWY_EINVAL, "N=%d must equal B=%d without cu_seqlens", N, B);
+    q.N = B;
+  }
+  return REWY_OK;
+}
+
+// ---- short convolution ------------------------------------------------------------
+int conv_args(const rewy_conv_desc* d, ConvArgs& a) {
+  if (!d) return fail(REWY_EINVAL, "desc is NULL");
+  memset(&a, 0, sizeof(a));
+  REWY_TRY(seq_args(d->B, d->T, d->N, d->cu_seqlens, d->cu_seqlens_host, a.seq));
+  if (d->D <= 0 || d->D > 1 << 24) return fail(REWY_EINVAL, "bad shape D=%d", d->D);
+  if (d->W < 2 || d->W > 4) return fail(d->W < 1 ? REWY_EINVAL : REWY_EUNSUPPORTED, "W=%d not supported (2 to 4 taps)", d->W);
+  REWY_TRY(check_dtype("dtype", d->dtype));
+  REWY_TRY(check_dtype("w_dtype", d->w_dtype));
+  if (d->act != REWY_ACT_NONE && d->act != REWY_ACT_SILU) return fail(REWY_EINVAL, "bad act %d", d->act);
+  a.D = d->D; a.W = d->W; a.act = d->act;
+  REWY_TRY(check_stride("x_stride", d->x_stride, d->D, a.xs));
+  REWY_TRY(check_stride("y_stride", d->y_stride, d->D, a.ys));
+  REWY_TRY(check_stride("dx_stride", d->dx_stride, d->D, a.dxs));
+  conv_bwd_shape(a.seq.total, a.D, d->dtype == REWY_F32, a.run, a.tiles);
+  return REWY_OK;
+}
+size_t conv_ws(const ConvArgs& a) { return up(std::max<size_t>((size_t)a.tiles * (a.W + 1) * a.D * 4, 1)); }
+
+int conv_forward(const rewy_conv_desc* d, bool step, const void* x, const void* w, const void* bias, const void* h0,
+                 void* y, void* ht, void* stream) {
+  ConvArgs a;
+  REWY_TRY(conv_args(d, a));
+  if (step && (d->T != 1 || d->cu_seqlens)) return fail(REWY_EINVAL, "a step has T == 1 and no cu_seqlens (got T=%d)", d->T);
+  const bool some = a.seq.total > 0;
+  const size_t e = esize(d->dtype), we = esize(d->w_dtype);
+  REWY_TRY(check_ptr("x", x, e, some));
+  REWY_TRY(check_ptr("w", w, we, some));
+  REWY_TRY(check_ptr("bias", bias, we, false));
+  REWY_TRY(check_ptr("h0", h0, e, false));
+  REWY_TRY(check_ptr("y", y, e, some));
+  REWY_TRY(check_ptr("ht", ht, e, false));
+  if (!some && !ht) return REWY_OK;
+  a.x = x; a.w = w; a.bias = bias; a.h0 = h0; a.y = y; a.ht = ht;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const bool f32 = d->dtype == REWY_F32, wf32 = d->w_dtype == REWY_F32;
+  if (step) return hip_check(traced("k_conv_step", s, [&] { return launch_conv_step(a, f32, wf32, s); }), "convolution step");
+  return hip_check(traced("k_conv_fwd", s, [&] { return launch_conv_fwd(a, f32, wf32, s); }), "convolution");
+}
+
+}  // namespace
+}  // namespace rewy
+
+using namespace rewy;
+
+REWY_API int rewy_norm_fwd(const rewy_norm_desc* d, const void* x, const void* res, const void* w, void* sum, void* y,
+                           void* q, float* scale, float* rstd, void* stream) {
+  return guarded([&]() -> int {
+    NormArgs a;
+    REWY_TRY(norm_args(d, a));
+    const size_t e = esize(d->dtype);
+    const bool some = a.M > 0;
+    REWY_TRY(check_ptr("x", x, e, some));
+    REWY_TRY(check_ptr("res", res, e, false));
+    REWY_TRY(check_ptr("w", w, esize(d->w_dtype), false));
+    REWY_TRY(check_ptr("sum", sum, e, false));
+    REWY_TRY(check_ptr("y", y, e, false));
+    REWY_TRY(check_ptr("rstd", rstd, 4, false));
+    REWY_TRY(check_ptr("scale", scale, 4, some && d->quant != REWY_QUANT_NONE));
+    REWY_TRY(check_ptr("q", q, 1, some && d->quant != REWY_QUANT_NONE));
+    if (d->quant == REWY_QUANT_NONE && (q || scale)) return fail(REWY_EINVAL, "q and scale are given only when quant != NONE");
+    if (!some) return REWY_OK;
+    a.x = x; a.res = res; a.w = w; a.sum = sum; a.y = y; a.q = q; a.scale = scale; a.rstd = rstd;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    return hip_check(traced("k_norm_fwd", s,
+                            [&] { return launch_norm_fwd(a, d->dtype == REWY_F32, d->w_dtype == REWY_F32, s); }),
+                     "RMS norm");
+  });
+}
+
+REWY_API size_t rewy_norm_workspace_bytes(const rewy_norm_desc* d) {
+  NormArgs a;
+  return norm_args(d, a) == REWY_OK ? norm_ws(a) : 0;
+}
+
+REWY_API int rewy_norm_bwd(const rewy_norm_desc* d, const void* sv, const void* w, const float* rstd, const void* dy,
+                           const void* ds, void* dx, void* dw, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> int {
+    NormArgs a;
+    REWY_TRY(norm_args(d, a));
+    const size_t e = esize(d->dtype), we = esize(d->w_dtype);
+    const bool some = a.M > 0;
+    REWY_TRY(check_ptr("s", sv, e, some));
+    REWY_TRY(check_ptr("w", w, we, false));
+    REWY_TRY(check_ptr("rstd", rstd, 4, some));
+    REWY_TRY(check_ptr("dy", dy, e, some));
+    REWY_TRY(check_ptr("ds", ds, e, false));
+    REWY_TRY(check_ptr("dx", dx, e, some));
+    REWY_TRY(check_ptr("dw", dw, we, false));
+    if (dw && !w) return fail(REWY_EINVAL, "dw is given without w");
+    if (dw) REWY_TRY(check_workspace(workspace, ws_bytes, norm_ws(a)));
+    a.x = sv; a.w = w; a.rstd = const_cast<float*>(rstd); a.dy = dy; a.res = ds; a.sum = dx; a.dw = dw;
+    a.part = dw ? static_cast<float*>(workspace) : nullptr;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const bool wf32 = d->w_dtype == REWY_F32;
+    if (some)
+      REWY_TRY(hip_check(traced("k_norm_bwd", s, [&] { return launch_norm_bwd(a, d->dtype == REWY_F32, wf32, s); }),
+                         "RMS norm backward"));
+    if (!dw) return REWY_OK;
+    return hip_check(traced("k_colsum", s,
+                            [&] { return launch_colsum(a.part, some ? a.nblk : 0, a.D, a.D, dw, wf32, s); }),
+                     "weight gradient");
+  });
+}
+
+REWY_API int rewy_conv_fwd(const rewy_conv_desc* d, const void* x, const void* w, const void* bias, const void* h0,
+                           void* y, void* ht, void* stream) {
+  return guarded([&] { return conv_forward(d, false, x, w, bias, h0, y, ht, stream); });
+}
+
+REWY_API int rewy_conv_step(const rewy_conv_desc* d, const void* x, const void* w, const void* bias, const void* h0,
+                            void* y, void* ht, void* stream) {
+  return guarded([&] { return conv_forward(d, true, x, w, bias, h0, y, ht, stream); });
+}
+
+REWY_API size_t rewy_conv_workspace_bytes(const rewy_conv_desc* d) {
+  ConvArgs a;
+  return conv_args(d, a) == REWY_OK ? conv_ws(a) : 0;
+}
+
+REWY_API int rewy_conv_bwd(const rewy_conv_desc* d, const void* x, const void* w, const void* bias, const void* h0,
+                           const void* dy, const void* dht, void* dx, void* dw, void* dbias, void* dh0,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> int {
+    ConvArgs a;
+    REWY_TRY(conv_args(d, a));
+    const bool some = a.seq.total > 0;
+    const size_t e = esize(d->dtype), we = esize(d->w_dtype);
+    REWY_TRY(check_ptr("x", x, e, some));
+    REWY_TRY(check_ptr("w", w, we, true));
+    REWY_TRY(check_ptr("bias", bias, we, false));
+    REWY_TRY(check_ptr("h0", h0, e, false));
+    REWY_TRY(check_ptr("dy", dy, e, some));
+    REWY_TRY(check_ptr("dht", dht, e, false));
+    REWY_TRY(check_ptr("dx", dx, e, some));
+    REWY_TRY(check_ptr("dw", dw, we, true));
+    REWY_TRY(check_ptr("dbias", dbias, we, false));
+    REWY_TRY(check_ptr("dh0", dh0, e, h0 != nullptr));
+    if ((bias != nullptr) != (dbias != nullptr)) return fail(REWY_EINVAL, "dbias must be given exactly when bias is");
+    REWY_TRY(check_workspace(workspace, ws_bytes, conv_ws(a)));
+    a.x = x; a.w = w; a.bias = bias; a.h0 = h0; a.dy = dy; a.dht = dht;
+    a.dx = dx; a.dw = dw; a.dbias = dbias; a.dh0 = dh0;
+    a.part = static_cast<float*>(workspace);
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    return hip_check(traced("k_conv_bwd", s,
+                            [&] { return launch_conv_bwd(a, d->dtype == REWY_F32, d->w_dtype == REWY_F32, s); }),
+                     "convolution backward");
+  });
+}

@@ -1,0 +1,329 @@
+"""Torch-facing wrappers of the operators around the token mixer: RMS norm with
+the residual's addition and an 8-bit output, short causal convolution.  Like
+the wrappers of the delta rule they allocate outputs and workspaces with
+PyTorch and call the C ABI; no arithmetic happens here.
+
+Streams: work goes to ``stream`` (default: the device's current stream).  On
+another stream than the current one, outputs and workspaces are allocated on it
+and the inputs are marked as used by it; the caller orders the two streams as
+for any torch operation."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import binding as B
+
+_DT = {torch.bfloat16: B.REWY_BF16, torch.float32: B.REWY_F32}
+_QUANT = {None: B.REWY_QUANT_NONE, "e4m3": B.REWY_QUANT_E4M3, "int8": B.REWY_QUANT_INT8}
+_QDT = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+_ACT = {None: B.REWY_ACT_NONE, "silu": B.REWY_ACT_SILU}
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(rc, where):
+    if rc != B.REWY_OK:
+        raise B.RewyError(rc, where)
+
+
+def _dtype(t, what):
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what} must be bf16 or fp32 (got {t.dtype})")
+    return dt
+
+
+def _like(t, ref, shape, what, dtype=None):
+    """A given tensor is on ref's device, with this shape and type, and contiguous."""
+    if t is None:
+        return
+    if t.device != ref.device:
+        raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype} (got {t.dtype})")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _row_stride(t, what, inner):
+    """Elements between the rows of t, whose last ``inner`` dimensions are one
+    row: a row's elements are contiguous and the rows are evenly spaced."""
+    if t.is_contiguous():
+        n = 1
+        for k in t.shape[len(t.shape) - inner:]:
+            n *= k
+        return n
+    shape, stride = t.shape, t.stride()
+    need = 1
+    for i in range(len(shape) - 1, len(shape) - 1 - inner, -1):
+        if shape[i] != 1 and stride[i] != need:
+            raise ValueError(f"{what}: the elements of a row must be contiguous")
+        need *= shape[i]
+    rows = [(shape[i], stride[i]) for i in range(len(shape) - 1 - inner, -1, -1) if shape[i] != 1]
+    if not rows:
+        return need
+    out = rows[0][1]
+    for (n, st), (_, nxt) in zip(rows, rows[1:]):
+        if nxt != n * st:
+            raise ValueError(f"{what}: rows must be evenly spaced")
+    if out < need:
+        raise ValueError(f"{what}: rows must not overlap")
+    return out
+
+
+class _On:
+    """Device and stream of one call: allocations inside belong to the stream."""
+
+    def __init__(self, ref, stream, inputs):
+        if ref.device.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU (got {ref.device})")
+        for t in inputs:
+            if t is not None and t.device != ref.device:
+                raise ValueError(f"all tensors must be on {ref.device} (got one on {t.device})")
+        self.stack = None
+        idx = ref.device.index
+        cur = torch.cuda.current_stream(idx)
+        if stream is None:
+            stream = cur
+        elif stream.device != ref.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {ref.device}")
+        self.handle = stream.cuda_stream
+        if torch.cuda.current_device() != idx or stream != cur:
+            self.stack = contextlib.ExitStack()
+            self.stack.enter_context(torch.cuda.device(ref.device))
+            self.stack.enter_context(torch.cuda.stream(stream))
+            if stream != cur:
+                for t in inputs:
+                    if t is not None:
+                        t.record_stream(stream)
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
+        return False
+
+
+def _workspace(nbytes, ref, ws):
+    if nbytes == 0:
+        raise B.RewyError(B.REWY_EINVAL, "workspace size")
+    return torch.empty(nbytes, dtype=torch.uint8, device=ref.device) if ws is None else ws
+
+
+# ---- RMS norm -----------------------------------------------------------------
+def rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0, output=True,
+             stream=None):
+    """y = s (mean(s^2) + eps)^-1/2 weight over the last dimension, s = x + residual.
+
+    Returns (y, s, q, scale, ctx): s is the stored sum (x itself without a
+    residual); y is None with ``output=False``; with ``quant`` "e4m3" or "int8",
+    q holds y / scale in 8 bits with one fp32 scale per row (``group=0``: scale
+    [rows, 1]) or per ``group`` columns (scale [rows, ceil(D / group)]).  x and
+    residual may have a row stride.  ctx feeds ``rms_norm_backward``."""
+    dt = _dtype(x, "x")
+    if quant not in _QUANT:
+        raise ValueError(f"quant must be None, 'e4m3' or 'int8' (got {quant!r})")
+    D = x.shape[-1]
+    M = x.numel() // D if D else 0
+    wdt = dt
+    if weight is not None:
+        wdt = _dtype(weight, "weight")
+        _like(weight, x, (D,), "weight")
+    xs = _row_stride(x, "x", 1)
+    rs = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and type")
+        rs = _row_stride(residual, "residual", 1)
+    with _On(x, stream, (x, weight, residual)) as handle:
+        s = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if output else None
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+        q = scale = None
+        if quant is not None:
+            q = torch.empty(x.shape, dtype=_QDT[quant], device=x.device)
+            scale = torch.empty(M, -(-D // group) if group else 1, dtype=torch.float32, device=x.device)
+        desc = B.RewyNormDesc(M, D, dt, wdt, _QUANT[quant], group, eps, xs, rs, 0, 0)
+        _check(B.rewy_norm_fwd(desc, _p(x), _p(residual), _p(weight), _p(s), _p(y), _p(q), _p(scale),
+                               _p(rstd), handle), "rewy_norm_fwd")
+    if s is None:
+        s = x
+    return y, s, q, scale, dict(s=s, weight=weight, rstd=rstd, eps=eps)
+
+
+def rms_norm_backward(ctx, dy, ds=None, *, stream=None, ws=None):
+    """Gradients of the norm's y (and, through ``ds``, of the stored sum).
+    Returns dict(dx, dweight); dx is the gradient of x and of the residual."""
+    s, weight = ctx["s"], ctx["weight"]
+    D = s.shape[-1]
+    M = s.numel() // D if D else 0
+    for t, name in ((dy, "dy"), (ds, "ds")):
+        if t is not None and (t.shape != s.shape or t.dtype != s.dtype):
+            raise ValueError(f"{name} must have x's shape and type")
+    wdt = _DT[s.dtype] if weight is None else _DT[weight.dtype]
+    desc = B.RewyNormDesc(M, D, _DT[s.dtype], wdt, B.REWY_QUANT_NONE, 0, ctx["eps"],
+                          _row_stride(s, "s", 1), 0 if ds is None else _row_stride(ds, "ds", 1), 0,
+                          _row_stride(dy, "dy", 1))
+    with _On(s, stream, (s, weight, ctx["rstd"], dy, ds)) as handle:
+        dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
+        dw = None if weight is None else torch.empty_like(weight)
+        if dw is not None:
+            ws = _workspace(B.rewy_norm_workspace_bytes(desc), s, ws)
+        _check(B.rewy_norm_bwd(desc, _p(s), _p(weight), _p(ctx["rstd"]), _p(dy), _p(ds), _p(dx),
+                               _p(dw), _p(ws), 0 if ws is None else ws.numel(), handle),
+               "rewy_norm_bwd")
+    return dict(dx=dx, dweight=dw)
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """Autograd wrapper: y, s = RMSNormFunction.apply(x, weight, residual, eps)."""
+
+    @staticmethod
+    def forward(fctx, x, weight, residual, eps):
+        y, s, _, _, ctx = rms_norm(x, weight, residual, eps=eps)
+        fctx.save_for_backward(s, weight, ctx["rstd"])
+        fctx.eps, fctx.residual = eps, residual is not None
+        return y, (s if residual is not None else x.view_as(x))
+
+    @staticmethod
+    def backward(fctx, dy, ds):
+        s, weight, rstd = fctx.saved_tensors
+        g = rms_norm_backward(dict(s=s, weight=weight, rstd=rstd, eps=fctx.eps), dy.contiguous(),
+                              ds.contiguous())
+        return g["dx"], g["dweight"], g["dx"] if fctx.residual else None, None
+
+
+def rms_norm_autograd(x, weight=None, residual=None, *, eps=1e-6):
+    """Differentiable RMS norm on the HIP path: (y, s) with s = x + residual."""
+    return RMSNormFunction.apply(x, weight, residual, eps)
+
+
+# ---- sequences ------------------------------------------------------------------
+def _sequences(x, cu_seqlens, T):
+    """(N for the descriptor, device cu_seqlens or None, host copy or None).  A
+    GPU tensor (int32) is used as it is and not looked at by the host; a list
+    or host tensor is checked and copied."""
+    if cu_seqlens is None:
+        return 0, None, None
+    if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+            raise TypeError("a GPU cu_seqlens must be a vector of int32")
+        _like(cu_seqlens, x, cu_seqlens.shape, "cu_seqlens")
+        return cu_seqlens.numel() - 1, cu_seqlens, None
+    vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
+    if len(vals) < 2:
+        raise ValueError("cu_seqlens needs at least two offsets")
+    if vals[-1] != T:
+        raise ValueError(f"cu_seqlens must end at T={T}")
+    host = (ctypes.c_int32 * len(vals))(*vals)
+    return len(vals) - 1, torch.tensor(vals, dtype=torch.int32, device=x.device), host
+
+
+# ---- short convolution ------------------------------------------------------------
+def _conv_problem(x, weight, bias, h0, activation, cu_seqlens):
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, D]")
+    if activation not in _ACT:
+        raise ValueError(f"activation must be None or 'silu' (got {activation!r})")
+    Bsz, T, D = x.shape
+    if weight.dim() != 2:
+        raise ValueError("weight must be [D, W]")
+    W = weight.shape[1]
+    dt, wdt = _dtype(x, "x"), _dtype(weight, "weight")
+    _like(weight, x, (D, W), "weight")
+    _like(bias, x, (D,), "bias", weight.dtype)
+    n, cu, host = _sequences(x, cu_seqlens, T)
+    nseq = n if cu is not None else Bsz
+    _like(h0, x, (nseq, W - 1, D), "h0", x.dtype)
+    desc = B.RewyConvDesc(Bsz, T, D, W, n, _p(cu), None if host is None else ctypes.addressof(host),
+                          dt, wdt, _ACT[activation], _row_stride(x, "x", 1), 0, 0)
+    return desc, (nseq, W - 1, D), cu, host
+
+
+def short_conv(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=None,
+               output_final_state=False, stream=None):
+    """Causal convolution of x [B, T, D] with weight [D, W] (W = 2 .. 4) along the
+    tokens, bias [D] and SiLU (``activation=None``: none).  h0 [N, W-1, D] holds
+    the rows before each sequence (oldest first).  Returns (y, ht or None,
+    ctx); ht is the next call's h0, ctx feeds ``short_conv_backward``.  x may be
+    a slice of longer rows."""
+    desc, hshape, cu, host = _conv_problem(x, weight, bias, h0, activation, cu_seqlens)
+    with _On(x, stream, (x, weight, bias, h0, cu)) as handle:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        ht = torch.empty(hshape, dtype=x.dtype, device=x.device) if output_final_state else None
+        _check(B.rewy_conv_fwd(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(ht), handle),
+               "rewy_conv_fwd")
+    return y, ht, dict(desc=desc, x=x, weight=weight, bias=bias, h0=h0, cu=cu, host=host)
+
+
+def short_conv_step(x, h0, weight, bias=None, *, activation="silu", ht=None, stream=None):
+    """One new token x [N, D] for each sequence with state h0 [N, W-1, D].
+    Returns (y, ht); ``ht`` may be h0 itself (updated in place)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    desc, hshape, _, _ = _conv_problem(x[:, None], weight, bias, h0, activation, None)
+    _like(ht, x, hshape, "ht", x.dtype)
+    if h0 is None:
+        raise ValueError("h0 must be given")
+    desc.x_stride = _row_stride(x, "x", 1)
+    with _On(x, stream, (x, weight, bias, h0, ht)) as handle:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if ht is None:
+            ht = torch.empty(hshape, dtype=x.dtype, device=x.device)
+        _check(B.rewy_conv_step(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(ht), handle),
+               "rewy_conv_step")
+    return y, ht
+
+
+def short_conv_backward(ctx, dy, dht=None, *, stream=None, ws=None):
+    """Gradients of the convolution: dict(dx, dweight, dbias, dh0).  dy [B, T, D]
+    may have a token stride; dht [N, W-1, D] is the final state's adjoint."""
+    x, weight, bias, h0 = (ctx[k] for k in ("x", "weight", "bias", "h0"))
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and type")
+    d = ctx["desc"]
+    hshape = (d.N if ctx["cu"] is not None else d.B, d.W - 1, d.D)
+    _like(dht, x, hshape, "dht", x.dtype)
+    desc = B.RewyConvDesc(d.B, d.T, d.D, d.W, d.N, d.cu_seqlens, d.cu_seqlens_host, d.dtype, d.w_dtype,
+                          d.act, d.x_stride, _row_stride(dy, "dy", 1), 0)
+    with _On(x, stream, (x, weight, bias, h0, ctx["cu"], dy, dht)) as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty_like(weight)
+        db = None if bias is None else torch.empty_like(bias)
+        dh0 = None if h0 is None else torch.empty_like(h0)
+        ws = _workspace(B.rewy_conv_workspace_bytes(desc), x, ws)
+        _check(B.rewy_conv_bwd(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(dy), _p(dht), _p(dx),
+                               _p(dw), _p(db), _p(dh0), _p(ws), ws.numel(), handle), "rewy_conv_bwd")
+    return dict(dx=dx, dweight=dw, dbias=db, dh0=dh0)
+
+
+class ShortConvFunction(torch.autograd.Function):
+    """Autograd wrapper: y, ht = ShortConvFunction.apply(x, weight, bias, h0, activation, cu_seqlens)."""
+
+    @staticmethod
+    def forward(fctx, x, weight, bias, h0, activation, cu_seqlens):
+        y, ht, ctx = short_conv(x, weight, bias, activation=activation, h0=h0,
+                                cu_seqlens=cu_seqlens, output_final_state=True)
+        fctx.save_for_backward(x, weight, bias, h0)
+        fctx.rewy = {k: ctx[k] for k in ("desc", "cu", "host")}
+        return y, ht
+
+    @staticmethod
+    def backward(fctx, dy, dht):
+        ctx = dict(fctx.rewy, **dict(zip(("x", "weight", "bias", "h0"), fctx.saved_tensors)))
+        g = short_conv_backward(ctx, dy.contiguous(), dht.contiguous())
+        return g["dx"], g["dweight"], g["dbias"], g["dh0"], None, None
+
+
+def short_conv_autograd(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=None):
+    """Differentiable short convolution on the HIP path: (y, ht)."""
+    return ShortConvFunction.apply(x, weight, bias, h0, activation, cu_seqlens)

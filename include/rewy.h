@@ -224,6 +224,100 @@ int rewy_recurrent_fwd_gdn2(const rewy_desc *d, const void *q, const void *k, co
 typedef enum { REWY_SCHEDULE_JOINT = 0, REWY_SCHEDULE_SEPARATE = 1 } rewy_schedule;
 int rewy_bwd_schedule(int schedule);
 
+/* ---- The operators around the token mixer --------------------------------------
+ * What a layer built on a recurrence with a matrix state runs before, in place
+ * of and behind the chunkwise delta rule.  Ownership, streams, errors and
+ * alignment rules are those of the operator above, with these differences:
+ * tensors need only the alignment of their elements, the token (row) strides
+ * are given in elements (0 = the row's own length; the batch stride is T times
+ * the token stride; a row's elements are contiguous), and parameters
+ * (weights, biases, A_log, D) are small contiguous tensors.  Sums, statistics
+ * and states are fp32; every output is rounded once, to nearest even.  With
+ * cu_seqlens, rows behind the last sequence (cu_seqlens[N] < T) belong to none:
+ * they are not read, and what an output holds there stays.  No atomics: results
+ * are bitwise reproducible for a given shape and device. */
+
+/* RMS norm with the residual's addition and an 8-bit output:
+ *     s = x + res,  rstd = (mean(s^2) + eps)^-1/2,  y = s * rstd * w,
+ *     scale_g = max |y| over group g / qmax,  q = round(y / scale_g),
+ * row by row, all from the unrounded fp32 sum.  qmax is 448 (E4M3, the OCP
+ * format without infinities) or 127 (INT8, symmetric).  A group whose largest
+ * magnitude is below 2^-100 has the scale 1; one that holds an infinity or NaN
+ * has a scale that is no finite number. */
+typedef enum { REWY_QUANT_NONE = 0, REWY_QUANT_E4M3 = 1, REWY_QUANT_INT8 = 2 } rewy_quant;
+
+typedef struct {
+    int64_t M;                      /* rows, 0 .. 2^31 - 1 */
+    int32_t D;                      /* row length, 1 .. 16384 */
+    int32_t dtype;                  /* rewy_dtype of x, res, sum, y (and of s, ds, dy, dx) */
+    int32_t w_dtype;                /* rewy_dtype of w and dw */
+    int32_t quant;                  /* rewy_quant of q (forward) */
+    int32_t group;                  /* columns per scale: 0 = the whole row, else 32, 64, 128 or 256 */
+    float eps;                      /* >= 0 */
+    int64_t x_stride, res_stride, sum_stride, y_stride; /* between rows, in elements; 0 = D */
+} rewy_norm_desc;
+
+/* Forward.  res may be NULL (s = x); w may be NULL (1).  Each of sum (s in
+ * dtype), y and rstd (fp32 [M]) may be NULL and is then not written; q ([M, D],
+ * contiguous) and scale (fp32 [M, ceil(D / group)], or [M] for group 0) are
+ * given exactly when quant != NONE.  sum may be x or res itself (same stride);
+ * other overlaps of an output are not allowed. */
+int rewy_norm_fwd(const rewy_norm_desc *d, const void *x, const void *res, const void *w,
+                  void *sum, void *y, void *q, float *scale, float *rstd, void *stream);
+
+/* Bytes of workspace of the backward (0 for an invalid descriptor). */
+size_t rewy_norm_workspace_bytes(const rewy_norm_desc *d);
+
+/* Backward for y (gradients pass an 8-bit output straight through): s is the
+ * stored sum (x itself without a residual; x_stride), rstd what the forward
+ * wrote, dy [M, D] (y_stride), ds the adjoint of the sum's other use
+ * (res_stride) or NULL.  dx (sum_stride) is the gradient of x and of res
+ * alike and may be ds itself; dw ([D], w_dtype) may be NULL, and must be NULL when
+ * w is.  The workspace is 256-byte aligned. */
+int rewy_norm_bwd(const rewy_norm_desc *d, const void *s, const void *w, const float *rstd,
+                  const void *dy, const void *ds, void *dx, void *dw,
+                  void *workspace, size_t ws_bytes, void *stream);
+
+/* Short causal convolution along the tokens, channel by channel:
+ *     pre_t = bias + sum_{j < W} w[c, j] x_{t - (W-1) + j},   y_t = act(pre_t),
+ * the rows before a sequence's first token being its initial state h0
+ * [N, W-1, D] (oldest first; zeros without one).  The final state ht is the last
+ * W-1 rows of [h0 ; x] and is h0 for the sequence's continuation. */
+typedef enum { REWY_ACT_NONE = 0, REWY_ACT_SILU = 1 } rewy_act;
+
+typedef struct {
+    int32_t B, T, D;                /* batch rows, tokens of a row, channels */
+    int32_t W;                      /* taps, 2 .. 4 */
+    int32_t N;                      /* sequences: B (or 0) without cu_seqlens */
+    const int32_t *cu_seqlens;      /* device [N+1] or NULL; needs B == 1 */
+    const int32_t *cu_seqlens_host; /* optional host copy, validated if given */
+    int32_t dtype;                  /* rewy_dtype of x, y, h0, ht and their gradients */
+    int32_t w_dtype;                /* rewy_dtype of w, bias and their gradients */
+    int32_t act;                    /* rewy_act */
+    int64_t x_stride, y_stride, dx_stride; /* between tokens, in elements; 0 = D (y_stride: y and dy) */
+} rewy_conv_desc;
+
+/* Forward.  w is [D, W]; bias [D], h0 and ht may be NULL.  ht may not overlap
+ * an input. */
+int rewy_conv_fwd(const rewy_conv_desc *d, const void *x, const void *w, const void *bias,
+                  const void *h0, void *y, void *ht, void *stream);
+
+/* One token for each of N = B sequences (T == 1, no cu_seqlens): the forward
+ * with the state read and written in one pass; ht may be h0 itself. */
+int rewy_conv_step(const rewy_conv_desc *d, const void *x, const void *w, const void *bias,
+                   const void *h0, void *y, void *ht, void *stream);
+
+/* Bytes of workspace of the backward (0 for an invalid descriptor). */
+size_t rewy_conv_workspace_bytes(const rewy_conv_desc *d);
+
+/* Backward.  dht (the final state's adjoint) may be NULL; dw [D, W] is
+ * overwritten; dbias ([D]) is given exactly when bias is; dh0 must be given
+ * when h0 is.  The workspace is 256-byte aligned. */
+int rewy_conv_bwd(const rewy_conv_desc *d, const void *x, const void *w, const void *bias,
+                  const void *h0, const void *dy, const void *dht,
+                  void *dx, void *dw, void *dbias, void *dh0,
+                  void *workspace, size_t ws_bytes, void *stream);
+
 /* Per-kernel timing (a tracing aid: device events, as in the ReWY paper's timing
  * protocol).  After rewy_trace_begin(), calls made by this thread
  * record a HIP event pair on the call's stream around every kernel they

@@ -28,6 +28,7 @@ EXPORTS = ("rewy_workspace_bytes", "rewy_saved_bytes", "rewy_fwd", "rewy_bwd", "
            "rewy_recurrent_fwd_gdn2",
            "rewy_norm_fwd", "rewy_norm_workspace_bytes", "rewy_norm_bwd",
            "rewy_conv_fwd", "rewy_conv_step", "rewy_conv_workspace_bytes", "rewy_conv_bwd",
+           "rewy_ssm_workspace_bytes", "rewy_ssm_fwd", "rewy_ssm_bwd", "rewy_ssm_recurrent_fwd",
            "rewy_bwd_schedule", "rewy_trace_begin", "rewy_trace_end", "rewy_trace_select",
            "rewy_status_string",
            "rewy_last_error")
@@ -58,6 +59,18 @@ class RewyConvDesc(ctypes.Structure):
         ("N", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
         ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
         ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+    ]
+
+
+class RewySsmDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32), ("dt_dtype", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64), ("db_stride", ctypes.c_int64),
+        ("dc_stride", ctypes.c_int64),
     ]
 
 
@@ -111,6 +124,7 @@ def load():
         lib.rewy_recurrent_fwd_gdn2.argtypes = [D] + [P] * 10
         lib.rewy_recurrent_fwd_gdn2.restype = ctypes.c_int
         ND, CD = ctypes.POINTER(RewyNormDesc), ctypes.POINTER(RewyConvDesc)
+        SD = ctypes.POINTER(RewySsmDesc)
         for name, args, res in (
                 ("rewy_norm_fwd", [ND] + [P] * 9, ctypes.c_int),
                 ("rewy_norm_workspace_bytes", [ND], S),
@@ -118,7 +132,11 @@ def load():
                 ("rewy_conv_fwd", [CD] + [P] * 7, ctypes.c_int),
                 ("rewy_conv_step", [CD] + [P] * 7, ctypes.c_int),
                 ("rewy_conv_workspace_bytes", [CD], S),
-                ("rewy_conv_bwd", [CD] + [P] * 11 + [S, P], ctypes.c_int)):
+                ("rewy_conv_bwd", [CD] + [P] * 11 + [S, P], ctypes.c_int),
+                ("rewy_ssm_workspace_bytes", [SD, ctypes.c_int], S),
+                ("rewy_ssm_fwd", [SD] + [P] * 11 + [S, P], ctypes.c_int),
+                ("rewy_ssm_bwd", [SD] + [P] * 19 + [S, P], ctypes.c_int),
+                ("rewy_ssm_recurrent_fwd", [SD] + [P] * 11, ctypes.c_int)):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = res
         lib.rewy_bwd_schedule.argtypes = [ctypes.c_int]
@@ -221,6 +239,26 @@ def rewy_conv_bwd(desc, x, w, bias, h0, dy, dht, dx, dw, dbias, dh0, workspace, 
                   stream) -> int:
     return load().rewy_conv_bwd(ctypes.byref(desc), x, w, bias, h0, dy, dht, dx, dw, dbias, dh0,
                                 workspace, ws_bytes, stream)
+
+
+def rewy_ssm_workspace_bytes(desc, phase) -> int:
+    return load().rewy_ssm_workspace_bytes(ctypes.byref(desc), phase)
+
+
+def rewy_ssm_fwd(desc, x, dt, a_log, dt_bias, b, c, D, h0, y, ht, workspace, ws_bytes, stream) -> int:
+    return load().rewy_ssm_fwd(ctypes.byref(desc), x, dt, a_log, dt_bias, b, c, D, h0, y, ht,
+                               workspace, ws_bytes, stream)
+
+
+def rewy_ssm_bwd(desc, x, dt, a_log, dt_bias, b, c, D, h0, dy, dht, dx, ddt, da_log, ddt_bias, db, dc,
+                 dD, dh0, workspace, ws_bytes, stream) -> int:
+    return load().rewy_ssm_bwd(ctypes.byref(desc), x, dt, a_log, dt_bias, b, c, D, h0, dy, dht, dx,
+                               ddt, da_log, ddt_bias, db, dc, dD, dh0, workspace, ws_bytes, stream)
+
+
+def rewy_ssm_recurrent_fwd(desc, x, dt, a_log, dt_bias, b, c, D, h0, y, ht, stream) -> int:
+    return load().rewy_ssm_recurrent_fwd(ctypes.byref(desc), x, dt, a_log, dt_bias, b, c, D, h0, y,
+                                         ht, stream)
 
 
 def rewy_bwd_schedule(schedule: int) -> int:

@@ -21,7 +21,7 @@ OBJDIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(HERE, "librewy.so")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "k_fwd_prep.hip", "k_scan.hip", "k_bwd_chunk.hip", "k_recurrent.hip",
-           "api_layer.hip", "k_norm.hip", "k_conv.hip"]
+           "api_layer.hip", "k_norm.hip", "k_conv.hip", "k_ssm_fwd.hip", "k_ssm_bwd.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 CFLAGS = [

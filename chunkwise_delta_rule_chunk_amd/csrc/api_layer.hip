@@ -4,7 +4,7 @@
 #include <exception>
 
 #include "host.hpp"
-#include "layer.hpp"
+#include "ssm.hpp"
 
 namespace rewy {
 namespace {
@@ -19,6 +19,7 @@ int guarded(F&& f) {
   }
 }
 
+int64_t up64(int64_t v) { return (v + CH - 1) / CH * CH; }
 size_t esize(int dtype) { return dtype == REWY_F32 ? 4 : 2; }
 
 int check_dtype(const char* what, int v) {
@@ -139,6 +140,120 @@ int conv_forward(const rewy_conv_desc* d, bool step, const void* x, const void* 
   return hip_check(traced("k_conv_fwd", s, [&] { return launch_conv_fwd(a, f32, wf32, s); }), "convolution");
 }
 
+// ---- selective state space scan ---------------------------------------------------
+// Tokens of a segment: as long as the segments of all heads still fill the chip
+// (a longer segment means fewer states to join), and whole chunks.
+int ssm_segment(int64_t total, int H, int target, int most) {
+  const int64_t want = (total * H + target - 1) / target;
+  return (int)std::min<int64_t>(most, std::max<int64_t>(256, (want + CH - 1) / CH * CH));
+}
+
+int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
+  if (!d) return fail(REWY_EINVAL, "desc is NULL");
+  memset(&a, 0, sizeof(a));
+  REWY_TRY(seq_args(d->B, d->T, d->N, d->cu_seqlens, d->cu_seqlens_host, a.seq));
+  if (d->H <= 0 || d->G <= 0 || d->H > 65536 || d->H % d->G)
+    return fail(REWY_EINVAL, "bad heads H=%d G=%d (H must be a multiple of G)", d->H, d->G);
+  REWY_TRY(check_dtype("dtype", d->dtype));
+  REWY_TRY(check_dtype("dt_dtype", d->dt_dtype));
+  auto ok = [&](int v) { return v == 32 || v == 64 || (v == 128 && d->dtype == REWY_BF16); };
+  if (d->K <= 0 || d->V <= 0) return fail(REWY_EINVAL, "bad shape K=%d V=%d", d->K, d->V);
+  if (!ok(d->K) || !ok(d->V))
+    return fail(REWY_EUNSUPPORTED, "K=%d V=%d not supported (32, 64 or 128; fp32 32 or 64)", d->K, d->V);
+  a.H = d->H; a.G = d->G; a.K = d->K; a.V = d->V; a.per = d->H / d->G;
+  a.dt_f32 = d->dt_dtype == REWY_F32;
+  const int64_t xr = (int64_t)d->H * d->V, br = (int64_t)d->G * d->K;
+  struct { const char* name; int64_t given, row; int64_t* out; } st[] = {
+      {"x_stride", d->x_stride, xr, &a.xs},   {"b_stride", d->b_stride, br, &a.bs},   {"c_stride", d->c_stride, br, &a.cs},
+      {"y_stride", d->y_stride, xr, &a.ys},   {"dx_stride", d->dx_stride, xr, &a.dxs}, {"db_stride", d->db_stride, br, &a.dbs},
+      {"dc_stride", d->dc_stride, br, &a.dcs}};
+  for (const auto& e : st) {
+    REWY_TRY(check_stride(e.name, e.given, e.row, *e.out));
+    if (*e.out * esize(d->dtype) % 16) return fail(REWY_EINVAL, "%s is not a multiple of 16 bytes", e.name);
+    if (*e.out > 1 << 22) return fail(REWY_EUNSUPPORTED, "%s %lld exceeds 2^22 elements", e.name, (long long)*e.out);
+  }
+  const int64_t total = a.seq.total;
+  const int longest = a.seq.cu ? a.seq.total : a.seq.T;
+  a.seg = ssm_segment(total, a.H, 1024, bwd ? 1024 : 8192);
+  if (!bwd && !a.seq.cu && (int64_t)a.seq.N * a.H >= 512) a.seg = std::max(CH, (int)up64(longest));
+  a.two = longest > a.seg;
+  const int64_t nslot = total / a.seg + a.seq.N, nchunk = total / CH + a.seq.N;
+  if (nslot * a.H > INT32_MAX / 2 || nchunk * a.H > INT32_MAX / 2 || (int64_t)a.seq.N * a.H > INT32_MAX / 2)
+    return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
+                (long long)total, a.H);
+  a.nslot = (int)nslot;
+  a.nchunk = (int)nchunk;
+  // head ranges that share a group's dB and dC: enough workgroups for two a CU
+  a.split = 1;
+  while (a.split < a.per && nchunk * a.G * a.split < 512) a.split = std::min(a.per, a.split * 2);
+  return REWY_OK;
+}
+
+size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
+  size_t off = 0;
+  auto take = [&](auto*& p, size_t n) {
+    using E = std::remove_reference_t<decltype(*p)>;
+    p = reinterpret_cast<E*>(ws + off);
+    off += up(n);
+  };
+  const size_t kv = (size_t)a.H * a.K * a.V, e = f32 ? 4 : 2, tok = (size_t)a.H * a.seq.total * 4;
+  if (a.two) {
+    take(a.sf, a.nslot * kv * 4);
+    if (bwd) take(a.sr, a.nslot * kv * 4);
+    take(a.gsum, (size_t)2 * a.nslot * a.H * 4);
+  }
+  if (bwd) {
+    char *hs, *hd;
+    take(hs, a.nchunk * kv * e);
+    take(hd, a.nchunk * kv * e);
+    a.hs = hs;
+    a.hd = hd;
+    take(a.rx, tok);
+    take(a.cx, tok);
+    take(a.ri, tok);
+    take(a.ci, tok);
+    take(a.ends, (size_t)a.nslot * a.H * 4);
+    take(a.dpart, (size_t)a.nchunk * a.H * 4);
+    take(a.apart, (size_t)a.nslot * 2 * a.H * 4);
+    if (a.split > 1) take(a.bcpart, (size_t)2 * a.split * a.seq.total * a.G * a.K * 4);
+  }
+  return std::max<size_t>(off, ALIGN);
+}
+
+struct SsmIn {
+  const void *x, *dt;
+  const float *a_log, *dt_bias;
+  const void *b, *c;
+  const float *D, *h0;
+};
+int ssm_inputs(const rewy_ssm_desc* d, const SsmIn& in, SsmArgs& a) {
+  const bool some = a.seq.total > 0;
+  REWY_TRY(check_ptr("x", in.x, 16, some));
+  REWY_TRY(check_ptr("dt", in.dt, esize(d->dt_dtype), some));
+  REWY_TRY(check_ptr("A_log", in.a_log, 4, some));
+  REWY_TRY(check_ptr("dt_bias", in.dt_bias, 4, false));
+  REWY_TRY(check_ptr("b", in.b, 16, some));
+  REWY_TRY(check_ptr("c", in.c, 16, some));
+  REWY_TRY(check_ptr("D", in.D, 4, false));
+  REWY_TRY(check_ptr("h0", in.h0, 16, false));
+  a.x = in.x; a.dt = in.dt; a.a_log = in.a_log; a.dt_bias = in.dt_bias;
+  a.b = in.b; a.c = in.c; a.d = in.D; a.h0 = in.h0;
+  return REWY_OK;
+}
+
+// fp32 [N, H, K, V]: dst = src, or zeros (a call without tokens)
+__global__ __launch_bounds__(256) void k_state_through(f32x4* dst, const f32x4* src, int64_t n) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    dst[i] = src ? src[i] : zero4();
+}
+int state_through(const SsmArgs& a, float* dst, const float* src, hipStream_t s) {
+  if (!dst || dst == src) return REWY_OK;
+  const int64_t n = (int64_t)a.seq.N * a.H * a.K * a.V / 4;
+  REWY_LAUNCH(k_state_through, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256), s,
+              reinterpret_cast<f32x4*>(dst), reinterpret_cast<const f32x4*>(src), n);
+  return hip_check(hipGetLastError(), "state copy");
+}
+
 }  // namespace
 }  // namespace rewy
 
@@ -246,5 +361,97 @@ REWY_API int rewy_conv_bwd(const rewy_conv_desc* d, const void* x, const void* w
     return hip_check(traced("k_conv_bwd", s,
                             [&] { return launch_conv_bwd(a, d->dtype == REWY_F32, d->w_dtype == REWY_F32, s); }),
                      "convolution backward");
+  });
+}
+
+REWY_API size_t rewy_ssm_workspace_bytes(const rewy_ssm_desc* d, int phase) {
+  SsmArgs a;
+  if (phase != 0 && phase != 1) {
+    fail(REWY_EINVAL, "bad phase %d", phase);
+    return 0;
+  }
+  if (ssm_args(d, phase == 1, a) != REWY_OK) return 0;
+  return ssm_layout(a, d->dtype == REWY_F32, phase == 1, nullptr);
+}
+
+REWY_API int rewy_ssm_fwd(const rewy_ssm_desc* d, const void* x, const void* dt, const float* a_log,
+                          const float* dt_bias, const void* b, const void* c, const float* D, const float* h0, void* y,
+                          float* ht, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> int {
+    SsmArgs a;
+    REWY_TRY(ssm_args(d, false, a));
+    REWY_TRY(ssm_inputs(d, SsmIn{x, dt, a_log, dt_bias, b, c, D, h0}, a));
+    REWY_TRY(check_ptr("y", y, 16, a.seq.total > 0));
+    REWY_TRY(check_ptr("ht", ht, 16, false));
+    const bool f32 = d->dtype == REWY_F32;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (a.seq.total == 0) return state_through(a, ht, h0, s);
+    if (ht && ht == h0) return fail(REWY_EINVAL, "ht may not be h0");
+    REWY_TRY(check_workspace(workspace, ws_bytes, ssm_layout(a, f32, false, static_cast<char*>(workspace))));
+    a.y = y; a.ht = ht;
+    if (a.two) {
+      REWY_TRY(hip_check(traced("k_ssm_state", s, [&] { return launch_ssm_state(a, f32, false, s); }), "segment states"));
+      REWY_TRY(hip_check(traced("k_ssm_pass", s, [&] { return launch_ssm_pass(a, false, s); }), "segment pass"));
+    }
+    return hip_check(traced("k_ssm_fwd", s, [&] { return launch_ssm_fwd(a, f32, s); }), "scan");
+  });
+}
+
+REWY_API int rewy_ssm_recurrent_fwd(const rewy_ssm_desc* d, const void* x, const void* dt, const float* a_log,
+                                    const float* dt_bias, const void* b, const void* c, const float* D,
+                                    const float* h0, void* y, float* ht, void* stream) {
+  return guarded([&]() -> int {
+    SsmArgs a;
+    REWY_TRY(ssm_args(d, false, a));
+    REWY_TRY(ssm_inputs(d, SsmIn{x, dt, a_log, dt_bias, b, c, D, h0}, a));
+    REWY_TRY(check_ptr("y", y, 16, a.seq.total > 0));
+    REWY_TRY(check_ptr("ht", ht, 16, false));
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (a.seq.total == 0) return state_through(a, ht, h0, s);
+    a.y = y; a.ht = ht;
+    return hip_check(traced("k_ssm_recurrent", s, [&] { return launch_ssm_recurrent(a, d->dtype == REWY_F32, s); }),
+                     "recurrent scan");
+  });
+}
+
+REWY_API int rewy_ssm_bwd(const rewy_ssm_desc* d, const void* x, const void* dt, const float* a_log,
+                          const float* dt_bias, const void* b, const void* c, const float* D, const float* h0,
+                          const void* dy, const float* dht, void* dx, void* ddt, float* da_log, float* ddt_bias,
+                          void* db, void* dc, float* dD, float* dh0, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> int {
+    SsmArgs a;
+    REWY_TRY(ssm_args(d, true, a));
+    const bool some = a.seq.total > 0;
+    REWY_TRY(ssm_inputs(d, SsmIn{x, dt, a_log, dt_bias, b, c, D, h0}, a));
+    REWY_TRY(check_ptr("dy", dy, 16, some));
+    REWY_TRY(check_ptr("dht", dht, 16, false));
+    REWY_TRY(check_ptr("dx", dx, 16, some));
+    REWY_TRY(check_ptr("ddt", ddt, esize(d->dt_dtype), some));
+    REWY_TRY(check_ptr("dA_log", da_log, 4, true));
+    REWY_TRY(check_ptr("ddt_bias", ddt_bias, 4, dt_bias != nullptr));
+    REWY_TRY(check_ptr("db", db, 16, some));
+    REWY_TRY(check_ptr("dc", dc, 16, some));
+    REWY_TRY(check_ptr("dD", dD, 4, D != nullptr));
+    REWY_TRY(check_ptr("dh0", dh0, 16, h0 != nullptr));
+    if ((ddt_bias && !dt_bias) || (dD && !D)) return fail(REWY_EINVAL, "ddt_bias and dD are given exactly when dt_bias and D are");
+    const bool f32 = d->dtype == REWY_F32;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    REWY_TRY(check_workspace(workspace, ws_bytes, ssm_layout(a, f32, true, static_cast<char*>(workspace))));
+    a.dy = dy; a.dht = dht; a.dx = dx; a.ddt = ddt; a.da_log = da_log; a.ddt_bias = ddt_bias;
+    a.db = db; a.dc = dc; a.dd = dD; a.dh0 = dh0;
+    if (some) {
+      if (a.two) {
+        REWY_TRY(hip_check(traced("k_ssm_state", s, [&] { return launch_ssm_state(a, f32, true, s); }), "segment states"));
+        REWY_TRY(hip_check(traced("k_ssm_pass", s, [&] { return launch_ssm_pass(a, true, s); }), "segment pass"));
+      }
+      REWY_TRY(hip_check(traced("k_ssm_walk", s, [&] { return launch_ssm_walk(a, f32, s); }), "scan walks"));
+      REWY_TRY(hip_check(traced("k_ssm_chunk", s, [&] { return launch_ssm_chunk(a, f32, s); }), "scan chunk backward"));
+      if (a.split > 1)
+        REWY_TRY(hip_check(traced("k_ssm_bcsum", s, [&] { return launch_ssm_bcsum(a, f32, s); }), "group sums"));
+    } else {
+      REWY_TRY(state_through(a, dh0, dht, s));
+    }
+    REWY_TRY(hip_check(traced("k_ssm_gate", s, [&] { return launch_ssm_gate(a, s); }), "scan gate backward"));
+    return hip_check(traced("k_ssm_params", s, [&] { return launch_ssm_params(a, s); }), "parameter gradients");
   });
 }

@@ -1,0 +1,516 @@
+// Selective state space scan, backward.  With dS the adjoint of the state that
+// leaves a chunk, v = dt x and M0_ij = exp(G_i - G_j) (C_i . B_j), i >= j:
+//   dS_in = exp(G_L) dS + sum_i exp(G_i) C_i dy_i^T
+//   dv_j  = sum_i M0_ij dy_i + exp(G_L - G_j) dS^T B_j,     dx = dt dv + D dy
+//   W_ij  = exp(G_i - G_j) (dy_i . x_j) dt_j
+//   dC_i  = sum_heads [ sum_j W_ij B_j + exp(G_i) S_in dy_i ]
+//   dB_j  = sum_heads [ sum_i W_ij C_i + exp(G_L - G_j) dt_j dS x_j ]
+// and the decay's gradient from r_i = dy_i . (y_i - D x_i) and c_j = x_j . dv_j,
+//   dg_t = sum_{i >= t} (r_i - dt_i c_i) + <S, dS> at the segment's end,
+//   d raw_t = (c_t - exp(A_log) dg_t) sigmoid(raw_t + dt_bias),   dA_log = sum dg_t g_t.
+// r and c split into parts inside the chunk (formed where W is) and parts through
+// the states (formed by the walks, whose states are fp32); the states that the
+// 16-bit outputs need are handed over in the operand type, and everything that
+// sums into a parameter's gradient stays fp32.
+#include "ssm.hpp"
+
+namespace rewy {
+
+namespace {
+
+// Walks of one segment and head, both directions (blockIdx.y).  Forward: the
+// state that enters each chunk goes to hs, and rx_t = exp(G_t) dy_t . (S_in^T
+// C_t); reverse: the adjoint that leaves each chunk goes to hd, and cx_t =
+// exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds columns 16 w .. + 15.
+template <typename T, int K, int V>
+__global__ __launch_bounds__(4 * V) void k_ssm_walk(SsmArgs a) {
+  constexpr int NTH = 4 * V, NW = V / 16, LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>;
+  constexpr int NT = K / 16, KQ = K / KG<T>, NS = SPLIT<T>;
+  __shared__ __align__(16) T sk[CH * LK];  // update: B (forward), C (reverse)
+  __shared__ __align__(16) T sq[CH * LK];  // probe: C, B
+  __shared__ __align__(16) T su[CH * LV];  // update: x, dy
+  __shared__ __align__(16) T sp[CH * LV];  // probe: dy, x
+  __shared__ __align__(16) float sal[CH], sbe[CH], sdot[NW][CH];
+  __shared__ float sdec, sred[NW];
+  const int dir = blockIdx.y;
+  const int wk = xcd_range(blockIdx.x, a.nslot * a.H), slot = wk / a.H, h = wk - slot * a.H, grp = h / a.per;
+  const Piece pc = find_piece(a.seq, slot, a.seg);
+  if (!pc.on) return;
+  const int t0 = pc.bos + pc.k * a.seg, t1 = min(t0 + a.seg, pc.eos);
+  const int nch = (t1 - t0 + CH - 1) / CH, w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15;
+  const int cbase = slot_base(a.seq, pc.n, CH) + pc.k * (a.seg / CH);
+  const float A2 = gate_rate(a, h), bias = gate_bias(a, h);
+  const int64_t seqst = ((int64_t)pc.n * a.H + h) * K * V + 16 * w + r;
+  const int64_t segst = ((int64_t)slot * a.H + h) * K * V + 16 * w + r;
+  const float* given = dir ? a.dht : a.h0;
+  // (an empty sequence has no segment of its own: its state is given through)
+  const float* init = a.two && nch > 0 ? (dir ? a.sr : a.sf) + segst : given ? given + seqst : nullptr;
+  f32x4 S[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[nt][i] = init ? init[(int64_t)(16 * nt + 4 * g4 + i) * V] : 0.f;
+  TileRegs<T, CH, K, NTH> rk, rq;
+  TileRegs<T, CH, V, NTH> ru, rp;
+  auto fetch = [&](int c) {
+    const int tok = t0 + (dir ? nch - 1 - c : c) * CH, len = min(CH, t1 - tok);
+    load_tile<T, K, NTH>(rk, dir ? a.c : a.b, tok, dir ? a.cs : a.bs, grp * K, len);
+    load_tile<T, K, NTH>(rq, dir ? a.b : a.c, tok, dir ? a.bs : a.cs, grp * K, len);
+    load_tile<T, V, NTH>(ru, dir ? a.dy : a.x, tok, dir ? a.ys : a.xs, h * V, len);
+    load_tile<T, V, NTH>(rp, dir ? a.x : a.dy, tok, dir ? a.xs : a.ys, h * V, len);
+  };
+  if (nch > 0) fetch(0);
+  T* hand = reinterpret_cast<T*>(dir ? a.hd : a.hs);
+  float* dots = (dir ? a.cx : a.rx) + (int64_t)h * a.seq.total;
+  for (int c = 0; c < nch; ++c) {
+    const int ci = dir ? nch - 1 - c : c, tok = t0 + ci * CH, len = min(CH, t1 - tok);
+    rk.store(sk, LK, threadIdx.x);
+    rq.store(sq, LK, threadIdx.x);
+    ru.store(su, LV, threadIdx.x);
+    rp.store(sp, LV, threadIdx.x);
+    if (w == 0) {
+      const ChunkGate g = chunk_gate(a, tok, len, h, A2, bias);
+      const float eG = fexp2(g.G), eE = fexp2(g.E);
+      sal[l] = dir ? eG : eE * g.dt;
+      sbe[l] = dir ? eE : eG;
+      if (l == 0) sdec = fexp2(g.GL);
+    }
+    __syncthreads();
+    if (c + 1 < nch) fetch(c + 1);
+    T* hp = hand + (((int64_t)(cbase + ci) * a.H + h) * (V / 16) + w) * (K * 16) + l * 4;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) st4<T>(hp + nt * 256, S[nt]);
+    f32x4 Y[4];
+#pragma unroll
+    for (int I = 0; I < 4; ++I) Y[I] = zero4();
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      uint4 sf[NS];
+      frag_acc<T, NS>(sf, S, q);
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        const uint4 qf = frag_row_acc<T>(sq, LK, 16 * I, q);
+#pragma unroll
+        for (int s = NS - 1; s >= 0; --s) mma16B<T>(Y[I], sf[s], qf);
+      }
+    }
+    // Y[I] holds columns t = 16 I + r, rows 16 w + 4 g4 + i
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+      const f32x4 u = ld4<T>(sp + (16 * I + r) * LV + 16 * w + 4 * g4);
+      const float d = rows_sum((Y[I][0] * u[0] + Y[I][1] * u[1]) + (Y[I][2] * u[2] + Y[I][3] * u[3]));
+      if (g4 == I) sdot[w][16 * I + r] = d;
+    }
+    uint4 ut[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) ut[q] = frag_col<T>(su, LV, q * KG<T>, 16 * w);
+    state_update<T, K>(S, sk, LK, ut, sal, sdec);
+    float be = 0.f;
+    if (w == 0) be = sbe[l];
+    __syncthreads();  // dots complete, tiles free
+    if (w == 0 && l < len) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) d += sdot[i][l];
+      dots[tok + l] = be * d;
+    }
+  }
+  if (dir == 0) {
+    // <S, dS> at the segment's end
+    const float* adj = a.two && nch > 0 ? a.sr + segst : a.dht ? a.dht + seqst : nullptr;
+    float d = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (adj) d += S[nt][i] * adj[(int64_t)(16 * nt + 4 * g4 + i) * V];
+    d = rows_sum(row16_sum(d));
+    if (l == 0) sred[w] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      d = 0.f;
+      for (int i = 0; i < NW; ++i) d += sred[i];
+      a.ends[(int64_t)slot * a.H + h] = d;
+    }
+  } else if (a.dh0 && pc.k == 0) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a.dh0[seqst + (int64_t)(16 * nt + 4 * g4 + i) * V] = S[nt][i];
+  }
+}
+
+constexpr int CB_WAVES = 8;
+
+// One chunk, one group, a range of its heads: dx, the parts of r and c inside
+// the chunk, and dB, dC summed over the heads in registers.  Wave w owns rows
+// 16 (w & 3) .. + 15 of the chunk and half w >> 2 of the state rows (dB, dC) or
+// of the columns (dx).
+template <typename T, int K, int V>
+__global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
+  constexpr int NTH = 64 * CB_WAVES, LK = pitch<T>(K), LV = pitch<T>(V), LM = pitch<T>(CH), NQ = CH / KG<T>;
+  constexpr int KQ = K / KG<T>, VQ = V / KG<T>, NTW = K / 32, PTW = V / 32;  // tiles of a half
+  __shared__ __align__(16) T sb[CH * LK];
+  __shared__ __align__(16) T sc[CH * LK];
+  __shared__ __align__(16) T sx[CH * LV];
+  __shared__ __align__(16) T sy[CH * LV];  // dy
+  __shared__ __align__(16) T ss[V * LK];   // S_in^T
+  __shared__ __align__(16) T sd[V * LK];   // dS^T
+  __shared__ __align__(16) T sm[CH * LM];  // M0^T, at the end W^T
+  __shared__ __align__(16) float sG[CH], sdt[CH], seG[CH], seE[CH];
+  __shared__ float srp[4][CH], scp[4][CH], sdd[CB_WAVES];
+  const int nwork = a.nchunk * a.G * a.split;
+  int wk = xcd_range(blockIdx.x, nwork);
+  const int part = wk % a.split;
+  wk /= a.split;
+  const int grp = wk % a.G, cslot = wk / a.G;
+  const Piece pc = find_piece(a.seq, cslot, CH);
+  const int tok = pc.bos + pc.k * CH, len = min(CH, pc.eos - tok);
+  if (!pc.on || len <= 0) return;
+  const int h0 = grp * a.per + part * a.per / a.split, h1 = grp * a.per + (part + 1) * a.per / a.split;
+  const int w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15, tb = w & 3, half = w >> 2;
+
+  TileRegs<T, CH, V, NTH> rx, ry;
+  TileRegs<T, V, K, NTH> rs, rd;  // pieces of the handed-over states, 16 bytes = two lanes' fragments
+  auto fetch = [&](int h) {
+    load_tile<T, V, NTH>(rx, a.x, tok, a.xs, h * V, len);
+    load_tile<T, V, NTH>(ry, a.dy, tok, a.ys, h * V, len);
+    const int64_t o = ((int64_t)cslot * a.H + h) * K * V;
+    rs.load(gbuf(reinterpret_cast<const T*>(a.hs) + o, K * V * sizeof(T)), K, threadIdx.x);
+    rd.load(gbuf(reinterpret_cast<const T*>(a.hd) + o, K * V * sizeof(T)), K, threadIdx.x);
+  };
+  // element 4 f of a handed-over state (fragment f: tile f / 64, lane f % 64) goes to
+  // its place in [V][K] order
+  auto put_state = [&](T* s, const TileRegs<T, V, K, NTH>& t) {
+#pragma unroll
+    for (int j = 0; j < TileRegs<T, V, K, NTH>::N; ++j) {
+      const int idx = threadIdx.x + j * NTH;
+      if (idx < TileRegs<T, V, K, NTH>::TOTAL) {
+        constexpr int FP = VEC<T> / 4;  // fragments of a piece
+#pragma unroll
+        for (int k = 0; k < FP; ++k) {
+          const int f = idx * FP + k, lane = f & 63, tile = f >> 6, nt = tile % (K / 16), pt = tile / (K / 16);
+          T* p = s + (16 * pt + (lane & 15)) * LK + 16 * nt + 4 * (lane >> 4);
+          if constexpr (FP == 2) *reinterpret_cast<uint2*>(p) = k ? uint2{t.r[j].z, t.r[j].w} : uint2{t.r[j].x, t.r[j].y};
+          else *reinterpret_cast<uint4*>(p) = t.r[j];
+        }
+      }
+    }
+  };
+
+  {
+    TileRegs<T, CH, K, NTH> rb, rc;
+    load_tile<T, K, NTH>(rb, a.b, tok, a.bs, grp * K, len);
+    load_tile<T, K, NTH>(rc, a.c, tok, a.cs, grp * K, len);
+    rb.store(sb, LK, threadIdx.x);
+    rc.store(sc, LK, threadIdx.x);
+  }
+  for (int i = threadIdx.x; i < CH * LM; i += NTH) sm[i] = (T)0.f;
+  __syncthreads();
+  // blocks (I, J) of the lower triangle: 10 over 8 waves.  C B^T and the sum of W over
+  // the heads stay in registers (rows i = 16 I + 4 g4 + e, column j = 16 J + r).
+  constexpr int NB = (10 + CB_WAVES - 1) / CB_WAVES;
+  f32x4 cb[NB], wsum[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    cb[b] = wsum[b] = zero4();
+    const int blk = b * CB_WAVES + w;
+    if (blk < 10) {
+      const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+#pragma unroll
+      for (int q = 0; q < KQ; ++q)
+        mma16B<T>(cb[b], frag_row<T>(sc, LK, 16 * I, q * KG<T>), frag_row<T>(sb, LK, 16 * J, q * KG<T>));
+    }
+  }
+  f32x4 dC[NTW], dB[NTW];
+#pragma unroll
+  for (int i = 0; i < NTW; ++i) dC[i] = dB[i] = zero4();
+
+  if (h0 < h1) fetch(h0);
+  for (int h = h0; h < h1; ++h) {
+    __syncthreads();  // tiles free
+    rx.store(sx, LV, threadIdx.x);
+    ry.store(sy, LV, threadIdx.x);
+    put_state(ss, rs);
+    put_state(sd, rd);
+    if (w == 0) {
+      const ChunkGate g = chunk_gate(a, tok, len, h, gate_rate(a, h), gate_bias(a, h));
+      sG[l] = g.G;
+      sdt[l] = g.dt;
+      seG[l] = fexp2(g.G);
+      seE[l] = fexp2(g.E);
+    }
+    __syncthreads();
+    if (h + 1 < h1) fetch(h + 1);
+    float dd = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int blk = b * CB_WAVES + w;
+      if (blk < 10) {
+        const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+        f32x4 p = zero4();
+#pragma unroll
+        for (int q = 0; q < VQ; ++q)
+          mma16B<T>(p, frag_row<T>(sy, LV, 16 * I, q * KG<T>), frag_row<T>(sx, LV, 16 * J, q * KG<T>));
+        const int i0 = 16 * I + 4 * g4, j = 16 * J + r;
+        const f32x4 Gi = *reinterpret_cast<const f32x4*>(sG + i0);
+        const float Gj = sG[j], dj = sdt[j];
+        f32x4 m;
+        float col = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float dec = j <= i0 + e ? fexp2(Gi[e] - Gj) : 0.f;
+          if (j == i0 + e) dd += p[e];
+          m[e] = cb[b][e] * dec;
+          const float cm = m[e] * p[e];
+          col += cm;
+          wsum[b][e] += p[e] * dec * dj;
+          const float row = row16_sum(cm * dj);
+          if (r == 0) srp[J][i0 + e] = row;
+        }
+        st4<T>(sm + j * LM + i0, m);
+        col = rows_sum(col);
+        if (g4 == 0) scp[I][j] = col;
+      }
+    }
+    dd = rows_sum(row16_sum(dd));
+    if (l == 0) sdd[w] = dd;
+    __syncthreads();
+    if (w == 0 && l < len) {
+      float rr = 0.f, cc = 0.f;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (b <= (l >> 4)) rr += srp[b][l];
+        if (b >= (l >> 4)) cc += scp[b][l];
+      }
+      a.ri[(int64_t)h * a.seq.total + tok + l] = rr;
+      a.ci[(int64_t)h * a.seq.total + tok + l] = cc;
+    }
+    if (w == 1 && l == 0) {
+      float s = 0.f;
+      for (int i = 0; i < CB_WAVES; ++i) s += sdd[i];
+      a.dpart[(int64_t)cslot * a.H + h] = s;
+    }
+    // dX^T, rows p of this wave's half, columns j = 16 tb + r
+    {
+      const int j = 16 * tb + r;
+      const float eE = seE[j], dt = sdt[j], D = a.d ? a.d[h] : 0.f;
+#pragma unroll
+      for (int pi = 0; pi < PTW; ++pi) {
+        const int pt = half * PTW + pi;
+        f32x4 u = zero4(), v = zero4();
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if ((q + 1) * KG<T> > 16 * tb)
+            mma16B<T>(u, frag_col<T>(sy, LV, q * KG<T>, 16 * pt), frag_row<T>(sm, LM, 16 * tb, q * KG<T>));
+#pragma unroll
+        for (int q = 0; q < KQ; ++q)
+          mma16B<T>(v, frag_row<T>(sd, LK, 16 * pt, q * KG<T>), frag_row<T>(sb, LK, 16 * tb, q * KG<T>));
+        const int p = 16 * pt + 4 * g4;
+        const f32x4 dyv = ld4<T>(sy + j * LV + p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = dt * (u[e] + eE * v[e]) + D * dyv[e];
+        if (j < len) st4<T>(reinterpret_cast<T*>(a.dx) + (int64_t)(tok + j) * a.dxs + h * V + p, u);
+      }
+    }
+    // dC, dB through the states: rows 16 tb + 4 g4 + e
+    {
+      uint4 yf[VQ], xf[VQ];
+#pragma unroll
+      for (int q = 0; q < VQ; ++q) {
+        yf[q] = frag_row<T>(sy, LV, 16 * tb, q * KG<T>);
+        xf[q] = frag_row<T>(sx, LV, 16 * tb, q * KG<T>);
+      }
+      const f32x4 eG = *reinterpret_cast<const f32x4*>(seG + 16 * tb + 4 * g4);
+      const f32x4 eE = *reinterpret_cast<const f32x4*>(seE + 16 * tb + 4 * g4);
+      const f32x4 dt = *reinterpret_cast<const f32x4*>(sdt + 16 * tb + 4 * g4);
+#pragma unroll
+      for (int ni = 0; ni < NTW; ++ni) {
+        const int nt = half * NTW + ni;
+        f32x4 u = zero4(), v = zero4();
+#pragma unroll
+        for (int q = 0; q < VQ; ++q) {
+          mma16B<T>(u, yf[q], frag_col<T>(ss, LK, q * KG<T>, 16 * nt));
+          mma16B<T>(v, xf[q], frag_col<T>(sd, LK, q * KG<T>, 16 * nt));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dC[ni][e] += eG[e] * u[e];
+          dB[ni][e] += eE[e] * dt[e] * v[e];
+        }
+      }
+    }
+  }
+  // the heads' W: as W^T [j][i] for dB, then as W [i][j] for dC
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int blk = b * CB_WAVES + w;
+    if (blk < 10) {
+      const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+      st4<T>(sm + (16 * J + r) * LM + 16 * I + 4 * g4, wsum[b]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+    if ((q + 1) * KG<T> > 16 * tb) {
+      const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row j, contraction i
+#pragma unroll
+      for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dB[ni], wf, frag_col<T>(sc, LK, q * KG<T>, 16 * (half * NTW + ni)));
+    }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+    if (q * KG<T> <= 16 * tb) {
+      const uint4 wf = frag_col<T>(sm, LM, q * KG<T>, 16 * tb);  // column i of W^T, contraction j
+#pragma unroll
+      for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dC[ni], wf, frag_col<T>(sb, LK, q * KG<T>, 16 * (half * NTW + ni)));
+    }
+#pragma unroll
+  for (int ni = 0; ni < NTW; ++ni) {
+    const int n = 16 * (half * NTW + ni) + r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * tb + 4 * g4 + e;
+      if (i < len) {
+        if (a.split > 1) {
+          const int64_t rows = (int64_t)a.seq.total * a.G;
+          const int64_t o = ((int64_t)part * rows + (int64_t)(tok + i) * a.G + grp) * K + n;
+          a.bcpart[o] = dB[ni][e];
+          a.bcpart[(int64_t)a.split * rows * K + o] = dC[ni][e];
+        } else {
+          reinterpret_cast<T*>(a.db)[(int64_t)(tok + i) * a.dbs + grp * K + n] = (T)dB[ni][e];
+          reinterpret_cast<T*>(a.dc)[(int64_t)(tok + i) * a.dcs + grp * K + n] = (T)dC[ni][e];
+        }
+      }
+    }
+  }
+}
+
+// Gate gradients of one segment and head, one wave: the suffix sums of r - dt c
+// from the segment's end, 64 tokens a step.
+__global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
+  const int wk = blockIdx.x * 4 + wave_id(), l = lane_id();
+  if (wk >= a.nslot * a.H) return;
+  const int slot = wk / a.H, h = wk - slot * a.H;
+  const Piece pc = find_piece(a.seq, slot, a.seg);
+  float dA = 0.f, db = 0.f;
+  if (pc.on) {
+    const int t0 = pc.bos + pc.k * a.seg, t1 = min(t0 + a.seg, pc.eos);
+    const int nch = (t1 - t0 + CH - 1) / CH;
+    const float A = -expf(a.a_log[h]), bias = gate_bias(a, h);
+    const int64_t row = (int64_t)h * a.seq.total;
+    float tail = t1 > t0 ? a.ends[(int64_t)slot * a.H + h] : 0.f;
+    for (int c = nch - 1; c >= 0; --c) {
+      const int t = t0 + c * CH + l;
+      const bool on = t < t1;
+      float dt = 0.f, cc = 0.f, diff = 0.f, z = 0.f;
+      if (on) {
+        z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
+        dt = softplus_full(z);
+        cc = a.cx[row + t] + a.ci[row + t];
+        diff = a.rx[row + t] + a.ri[row + t] - dt * cc;
+      }
+      float s = diff;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const float u = __shfl_down(s, d, 64);
+        if (l + d < 64) s += u;
+      }
+      const float dg = s + tail;
+      tail += __shfl(s, 0, 64);
+      if (on) {
+        const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
+        const float dz = (cc + A * dg) * sg;
+        st_beta(a.ddt, a.dt_f32, (int64_t)t * a.H + h, dz);
+        dA += dg * (A * dt);
+        db += dz;
+      }
+    }
+  }
+  dA = rows_sum(row16_sum(dA));
+  db = rows_sum(row16_sum(db));
+  if (l == 0) {
+    a.apart[((int64_t)slot * 2 + 0) * a.H + h] = dA;
+    a.apart[((int64_t)slot * 2 + 1) * a.H + h] = db;
+  }
+}
+
+// dA_log, ddt_bias [H] over the segments and dD [H] over the chunks; a chunk
+// slot that no sequence uses holds nothing and is skipped.
+__global__ __launch_bounds__(256) void k_ssm_params(SsmArgs a) {
+  __shared__ float buf[4];
+  const int h = blockIdx.x, what = blockIdx.y;
+  float s = 0.f;
+  if (what < 2) {
+    for (int i = threadIdx.x; i < a.nslot; i += 256) s += a.apart[((int64_t)i * 2 + what) * a.H + h];
+  } else {
+    for (int i = threadIdx.x; i < a.nchunk; i += 256) {
+      const Piece pc = find_piece(a.seq, i, CH);
+      if (pc.on && pc.bos + pc.k * CH < pc.eos) s += a.dpart[(int64_t)i * a.H + h];
+    }
+  }
+  s = rows_sum(row16_sum(s));
+  if (lane_id() == 0) buf[wave_id()] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float* o = what == 0 ? a.da_log : what == 1 ? a.ddt_bias : a.dd;
+    if (o) o[h] = (buf[0] + buf[1]) + (buf[2] + buf[3]);
+  }
+}
+
+// dB and dC from the partial sums of the head ranges, four elements a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ssm_bcsum(SsmArgs a) {
+  const int64_t rows = (int64_t)a.seq.total * a.G, n = rows * a.K / 4;
+  const int end = seq_start(a.seq, a.seq.N);
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (i >= n) return;
+  const int64_t row = i * 4 / a.K, tok = row / a.G;
+  const int k = (int)(i * 4 - row * a.K), grp = (int)(row - tok * a.G);
+  if (tok >= end) return;
+  const float* p = a.bcpart + (blockIdx.y ? (int64_t)a.split * rows * a.K : 0) + i * 4;
+  f32x4 s = zero4();
+  for (int j = 0; j < a.split; ++j) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p + (int64_t)j * rows * a.K);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += v[e];
+  }
+  st4<T>(reinterpret_cast<T*>(blockIdx.y ? a.dc : a.db) + tok * (blockIdx.y ? a.dcs : a.dbs) + grp * a.K + k, s);
+}
+
+}  // namespace
+
+hipError_t launch_ssm_walk(const SsmArgs& a, bool f32, hipStream_t s) {
+  return ssm_kv(a.K, a.V, f32, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = decltype(k)::value, V = decltype(v)::value;
+    REWY_LAUNCH((k_ssm_walk<T, K, V>), dim3(a.nslot * a.H, 2), dim3(4 * V), s, a);
+    return hipGetLastError();
+  });
+}
+hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s) {
+  return ssm_kv(a.K, a.V, f32, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = decltype(k)::value, V = decltype(v)::value;
+    REWY_LAUNCH((k_ssm_chunk<T, K, V>), dim3(a.nchunk * a.G * a.split), dim3(64 * CB_WAVES), s, a);
+    return hipGetLastError();
+  });
+}
+hipError_t launch_ssm_gate(const SsmArgs& a, hipStream_t s) {
+  REWY_LAUNCH(k_ssm_gate, dim3((a.nslot * a.H + 3) / 4), dim3(256), s, a);
+  return hipGetLastError();
+}
+hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s) {
+  REWY_LAUNCH(k_ssm_params, dim3(a.H, 3), dim3(256), s, a);
+  return hipGetLastError();
+}
+hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s) {
+  const int64_t n = (int64_t)a.seq.total * a.G * a.K / 4;
+  const dim3 grid((unsigned)((n + 255) / 256), 2);
+  if (f32) REWY_LAUNCH((k_ssm_bcsum<float>), grid, dim3(256), s, a);
+  else REWY_LAUNCH((k_ssm_bcsum<bf16>), grid, dim3(256), s, a);
+  return hipGetLastError();
+}
+
+}  // namespace rewy

@@ -1,0 +1,329 @@
+// Selective state space scan: argument record, launchers and the device
+// pieces its kernels share.
+//
+// Per sequence and head, with the fp32 state S [K, V] and one scalar decay per
+// token,
+//   dt_t = softplus(raw_t + dt_bias),  g_t = -exp(A_log) dt_t,
+//   S_t = exp(g_t) S_{t-1} + dt_t B_t x_t^T,   y_t = S_t^T C_t + D x_t.
+// In a chunk of 64 tokens, G the inclusive prefix sum of g,
+//   y_i = sum_{j<=i} exp(G_i - G_j) (C_i . B_j) dt_j x_j + exp(G_i) S_in^T C_i + D x_i
+//   S_out = exp(G_L) S_in + sum_j exp(G_L - G_j) dt_j B_j x_j^T.
+// Every exponent is at most 0.  A sequence is cut into segments of whole chunks;
+// one workgroup walks a segment of one head with the state in its registers,
+// and the states that enter the segments come from a first pass over them.
+#pragma once
+#include "layer.hpp"
+
+namespace rewy {
+
+struct SsmArgs {
+  SeqArgs seq;
+  int H, G, K, V, per;     // per = H / G heads share a group's B and C
+  int dt_f32;
+  int seg;                 // tokens of a segment (whole chunks)
+  int nslot, nchunk;       // segment slots, chunk slots
+  int split;               // backward: head ranges that share a group's dB and dC
+  int two;                 // more than one segment per sequence is possible
+  int64_t xs, bs, cs, ys, dxs, dbs, dcs;  // token strides
+  const void* x;
+  const void* dt;          // raw [tokens, H]
+  const float* a_log;
+  const float* dt_bias;
+  const void* b;
+  const void* c;
+  const float* d;
+  const float* h0;
+  void* y;
+  float* ht;
+  // backward
+  const void* dy;
+  const float* dht;
+  void* dx;
+  void* ddt;
+  float* da_log;
+  void* db;
+  void* dc;
+  float* dd;
+  float* ddt_bias;
+  float* dh0;
+  // workspace
+  float* sf;               // [nslot, H, K, V] local end states, then the states that enter the segments
+  float* sr;               // [nslot, H, K, V] local adjoints, then the adjoints of the states that leave them
+  float* gsum;             // [nslot, H] sum of g (log2 units) over a segment
+  void* hs;                // [nchunk, H, V/16, K/16, 64 lanes, 4] state entering each chunk (operand type)
+  void* hd;                // same: adjoint of the state leaving each chunk
+  float* rx;               // [H, tokens] row part of the decay gradient through the entering state
+  float* cx;               // [H, tokens] column part (per unit of dt) through the leaving state
+  float* ri;               // [H, tokens] row part inside the chunk
+  float* ci;               // [H, tokens] column part inside the chunk
+  float* ends;             // [nslot, H] <state, adjoint> at each segment's end
+  float* dpart;            // [nchunk, H] partial sums of dD
+  float* apart;            // [nslot, 2, H] partial sums of dA_log and ddt_bias
+  float* bcpart;           // [2, split, tokens, G, K] partial sums of dB and dC (split > 1)
+};
+
+hipError_t launch_ssm_state(const SsmArgs& a, bool f32, bool both, hipStream_t s);
+hipError_t launch_ssm_pass(const SsmArgs& a, bool both, hipStream_t s);
+hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s);
+hipError_t launch_ssm_walk(const SsmArgs& a, bool f32, hipStream_t s);
+hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s);
+hipError_t launch_ssm_gate(const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s);
+hipError_t launch_ssm_recurrent(const SsmArgs& a, bool f32, hipStream_t s);
+
+// ---- slots --------------------------------------------------------------------
+// Pieces of L tokens of every sequence, numbered without a table: the pieces of
+// sequence n take the slots start(n) / L + n, + 1, ...  Slots of different
+// sequences never meet (a sequence of len tokens moves start / L by at least
+// ceil(len / L) - 1), every sequence has at least one, and there are at most
+// total / L + N.
+struct Piece {
+  int n;         // sequence
+  int bos, eos;  // its tokens
+  int k;         // piece of the sequence
+  bool on;       // the slot is used
+};
+__device__ __forceinline__ int slot_base(const SeqArgs& q, int n, int L) { return seq_start(q, n) / L + n; }
+__device__ __forceinline__ Piece find_piece(const SeqArgs& q, int slot, int L) {
+  int lo = 0, hi = q.N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (slot_base(q, mid, L) <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  Piece p;
+  p.n = lo;
+  seq_range(q, lo, p.bos, p.eos);
+  p.k = slot - slot_base(q, lo, L);
+  // (an empty sequence keeps its first slot, for its final state)
+  p.on = p.k >= 0 && (p.k == 0 || (int64_t)p.bos + (int64_t)p.k * L < p.eos);
+  return p;
+}
+
+// Workgroup b of n in an order that gives each XCD (workgroups go to the 8 XCDs
+// in turn) one contiguous range, so that neighbours, which share B and C, share
+// an L2.
+__device__ __forceinline__ int xcd_range(int b, int n) {
+  const int x = b & 7, per = n >> 3, rem = n & 7;
+  return x * per + min(x, rem) + (b >> 3);
+}
+
+// ---- gates ----------------------------------------------------------------------
+// softplus at full fp32 precision (small steps dt matter relative to themselves)
+__device__ __forceinline__ float softplus_full(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
+
+// The gates of a chunk, by one wave, lane t its token: dt, and in log2 units the
+// inclusive prefix G, the exclusive suffix E = G_L - G (summed on its own, so
+// that small ones are exact) and the total.  Rows past the end have dt = g = 0.
+struct ChunkGate {
+  float dt, G, E, GL;
+};
+__device__ __forceinline__ ChunkGate chunk_gate(const SsmArgs& a, int tok, int len, int h, float A2, float bias) {
+  const int t = lane_id();
+  ChunkGate r;
+  r.dt = 0.f;
+  if (t < len) r.dt = softplus_full(ld_beta(a.dt, a.dt_f32, (int64_t)(tok + t) * a.H + h) + bias);
+  const float g = A2 * r.dt;
+  float p = g, s = g;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const float u = __shfl_up(p, d, 64), v = __shfl_down(s, d, 64);
+    if (t >= d) p += u;
+    if (t + d < 64) s += v;
+  }
+  r.G = p;
+  r.E = __shfl_down(s, 1, 64);
+  if (t == 63) r.E = 0.f;
+  r.GL = __shfl(p, 63, 64);
+  return r;
+}
+// -exp(A_log) log2(e)
+__device__ __forceinline__ float gate_rate(const SsmArgs& a, int h) { return -expf(a.a_log[h]) * LOG2E; }
+__device__ __forceinline__ float gate_bias(const SsmArgs& a, int h) { return a.dt_bias ? a.dt_bias[h] : 0.f; }
+
+// ---- operand fragments ------------------------------------------------------------
+// One 16-byte fragment per lane serves a contraction of KG<T> indices (bf16 32,
+// fp32 16); lane l gives row (A) or column (B) l & 15.
+template <typename T>
+constexpr int KG = 64 / (int)sizeof(T);
+template <typename T>
+constexpr int VEC = 16 / (int)sizeof(T);
+
+// row r0 + (l & 15) of an LDS tile, contraction k0 + VEC (l >> 4) + e
+template <typename T>
+__device__ __forceinline__ uint4 frag_row(const T* p, int ld, int r0, int k0) {
+  const int l = lane_id();
+  return *reinterpret_cast<const uint4*>(p + (r0 + (l & 15)) * ld + k0 + VEC<T> * (l >> 4));
+}
+// the same with the slot order of frag_acc
+template <typename T>
+__device__ __forceinline__ uint4 frag_row_acc(const T* p, int ld, int r0, int q) {
+  const int l = lane_id();
+  return perm_row<T>(p + (r0 + (l & 15)) * ld + 4 * (l >> 4), q);
+}
+// column c0 + (l & 15) of an LDS tile, contraction over its rows t0 + VEC (l >> 4)
+// + e.  bf16: two transposing reads, each giving lane l of a 16-lane group column
+// l of four rows that the group reads as 32 contiguous bytes each.
+template <typename T>
+__device__ __forceinline__ uint4 frag_col(const T* p, int ld, int t0, int c0) {
+  const int l = lane_id(), g = l >> 4, r = l & 15;
+  if constexpr (std::is_same_v<T, bf16>) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    const T* q = p + (t0 + 8 * g + (r >> 2)) * ld + c0 + 4 * (r & 3);
+    const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q));
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 4 * ld));
+    const uint2 x = __builtin_bit_cast(uint2, u), y = __builtin_bit_cast(uint2, v);
+    return uint4{x.x, x.y, y.x, y.y};
+  } else {
+    const T* q = p + (t0 + 4 * g) * ld + c0 + r;
+    return uint4{__float_as_uint(q[0]), __float_as_uint(q[ld]), __float_as_uint(q[2 * ld]), __float_as_uint(q[3 * ld])};
+  }
+}
+// Element e of a fragment as fp32 / fragment of VEC fp32 values.
+template <typename T>
+__device__ __forceinline__ void frag_get(float (&f)[VEC<T>], uint4 v) {
+  if constexpr (std::is_same_v<T, bf16>) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+}
+// An fp32 value that meets a 16-bit operand in a product whose sum is kept in fp32
+// (states, decay gradients) is given as the sum of SPLIT bf16 values, hi + mid +
+// lo: 24 bits, as many as fp32 has.  fp32 operands are one piece.
+template <typename T>
+constexpr int SPLIT = std::is_same_v<T, bf16> ? 3 : 1;
+template <typename T, int NS>
+__device__ __forceinline__ void frag_split(uint4 (&out)[NS], const float (&f)[VEC<T>]) {
+  if constexpr (std::is_same_v<T, bf16>) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = f[e];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)x[2 * i], (bf16)x[2 * i + 1]});
+        asm("" : "+v"(w[i]));
+        if (s + 1 < NS) {
+          x[2 * i] -= __uint_as_float(w[i] << 16);
+          x[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+      out[s] = uint4{w[0], w[1], w[2], w[3]};
+    }
+  } else {
+    static_assert(NS == 1, "");
+    out[0] = uint4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
+}
+// Fragment q of a contraction over the rows of a matrix held as C fragments, acc[i]
+// = rows 16 i + 4 (l >> 4) .. + 3 (partner: frag_row_acc).
+template <typename T, int NS, int NT>
+__device__ __forceinline__ void frag_acc(uint4 (&out)[NS], const f32x4 (&acc)[NT], int q) {
+  float f[VEC<T>];
+  if constexpr (std::is_same_v<T, bf16>) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = acc[2 * q][e];
+      f[4 + e] = acc[2 * q + 1][e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = acc[q][e];
+  }
+  frag_split<T, NS>(out, f);
+}
+// four values as one store of the type
+template <typename T>
+__device__ __forceinline__ void st4(T* p, const f32x4& v) {
+  if constexpr (std::is_same_v<T, bf16>) {
+    bf16x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (bf16)v[e];
+    *reinterpret_cast<bf16x4*>(p) = o;
+  } else {
+    *reinterpret_cast<f32x4*>(p) = v;
+  }
+}
+template <typename T>
+__device__ __forceinline__ f32x4 ld4(const T* p) {
+  if constexpr (std::is_same_v<T, bf16>) {
+    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
+    return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+  } else {
+    return *reinterpret_cast<const f32x4*>(p);
+  }
+}
+
+// a chunk's rows of a token-major tensor, columns col .. + C - 1 (rows past len: zeros)
+template <typename T, int C, int NTH>
+__device__ __forceinline__ void load_tile(TileRegs<T, CH, C, NTH>& r, const void* base, int64_t tok, int64_t stride,
+                                          int col, int len) {
+  const T* p = reinterpret_cast<const T*>(base) + tok * stride + col;
+  r.load(gbuf(p, tile_bytes<T>(len, stride, C)), stride, threadIdx.x);
+}
+
+// State update S = exp(G_L) S + sum_t K_t (al_t u_t)^T for the wave's 16 columns:
+// A operand K^T (columns of sk), B operand al u (columns of su, scaled and split).
+template <typename T, int K>
+__device__ __forceinline__ void state_update(f32x4 (&S)[K / 16], const T* sk, int ldk, const uint4 (&ut)[CH / KG<T>],
+                                             const float* sal, float dec) {
+  constexpr int NQ = CH / KG<T>, VE = VEC<T>, NS = SPLIT<T>;
+  const int g = lane_id() >> 4;
+  uint4 uf[NQ][NS];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    float f[VE];
+    frag_get<T>(f, ut[q]);
+#pragma unroll
+    for (int e = 0; e < VE; e += 4) {
+      const f32x4 al = *reinterpret_cast<const f32x4*>(sal + q * KG<T> + VE * g + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[e + i] *= al[i];
+    }
+    frag_split<T, NS>(uf[q], f);
+  }
+#pragma unroll
+  for (int nt = 0; nt < K / 16; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[nt][i] *= dec;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const uint4 kf = frag_col<T>(sk, ldk, q * KG<T>, 16 * nt);
+#pragma unroll
+      for (int s = NS - 1; s >= 0; --s) mma16B<T>(S[nt], kf, uf[q][s]);
+    }
+  }
+}
+
+// the (type, K, V) variants of a kernel
+template <typename F>
+hipError_t ssm_kv(int K, int V, bool f32, F&& f) {
+  auto v_of = [&](auto t, auto k) -> hipError_t {
+    if (V == 32) return f(t, k, std::integral_constant<int, 32>{});
+    if (V == 64) return f(t, k, std::integral_constant<int, 64>{});
+    if constexpr (std::is_same_v<decltype(t), bf16>)
+      if (V == 128) return f(t, k, std::integral_constant<int, 128>{});
+    return hipErrorInvalidValue;
+  };
+  auto k_of = [&](auto t) -> hipError_t {
+    if (K == 32) return v_of(t, std::integral_constant<int, 32>{});
+    if (K == 64) return v_of(t, std::integral_constant<int, 64>{});
+    if constexpr (std::is_same_v<decltype(t), bf16>)
+      if (K == 128) return v_of(t, std::integral_constant<int, 128>{});
+    return hipErrorInvalidValue;
+  };
+  return f32 ? k_of(float{}) : k_of(bf16{});
+}
+
+}  // namespace rewy

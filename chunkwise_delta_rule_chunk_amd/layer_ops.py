@@ -1,5 +1,6 @@
 """Torch-facing wrappers of the operators around the token mixer: RMS norm with
-the residual's addition and an 8-bit output, short causal convolution.  Like
+the residual's addition and an 8-bit output, short causal convolution,
+selective state space scan.  Like
 the wrappers of the delta rule they allocate outputs and workspaces with
 PyTorch and call the C ABI; no arithmetic happens here.
 
@@ -327,3 +328,121 @@ class ShortConvFunction(torch.autograd.Function):
 def short_conv_autograd(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=None):
     """Differentiable short convolution on the HIP path: (y, ht)."""
     return ShortConvFunction.apply(x, weight, bias, h0, activation, cu_seqlens)
+
+
+# ---- selective state space scan ---------------------------------------------------
+def _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens):
+    if x.dim() != 4 or b.dim() != 4:
+        raise ValueError("x must be [B, T, H, V], b and c [B, T, G, K]")
+    Bsz, T, H, V = x.shape
+    G, K = b.shape[2:]
+    e = _dtype(x, "x")
+    for t, name in ((b, "b"), (c, "c")):
+        if t.dtype != x.dtype:
+            raise TypeError(f"{name} must have x's type")
+        if tuple(t.shape) != (Bsz, T, G, K):
+            raise ValueError(f"{name} must have shape {(Bsz, T, G, K)} (got {tuple(t.shape)})")
+    dte = _dtype(dt, "dt")
+    _like(dt, x, (Bsz, T, H), "dt")
+    for t, name in ((a_log, "a_log"), (d, "d"), (dt_bias, "dt_bias")):
+        _like(t, x, (H,), name, torch.float32)
+    n, cu, host = _sequences(x, cu_seqlens, T)
+    nseq = n if cu is not None else Bsz
+    shape = (nseq, H, K, V)
+    _like(h0, x, shape, "h0", torch.float32)
+    desc = B.RewySsmDesc(Bsz, T, H, G, K, V, n, _p(cu), None if host is None else ctypes.addressof(host),
+                         e, dte, _row_stride(x, "x", 2), _row_stride(b, "b", 2), _row_stride(c, "c", 2),
+                         0, 0, 0, 0)
+    return desc, shape, cu, host
+
+
+def selective_scan(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seqlens=None,
+                   output_final_state=True, stream=None, ws=None):
+    """y_t = S_t^T C_t + d x_t with S_t = exp(-exp(a_log) dt_t) S_{t-1} + dt_t B_t x_t^T
+    and dt_t = softplus(dt + dt_bias), in chunks (prompts, training).
+
+    x [B, T, H, V], b and c [B, T, G, K] (slices of longer rows allowed), dt [B, T, H]
+    (before the softplus), a_log, d, dt_bias [H] fp32, h0 [N, H, K, V] fp32.
+    Returns (y, ht or None, ctx); ctx feeds ``selective_scan_backward``."""
+    desc, shape, cu, host = _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)
+    with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, cu)) as handle:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        ht = torch.empty(shape, dtype=torch.float32, device=x.device) if output_final_state else None
+        ws = _workspace(B.rewy_ssm_workspace_bytes(desc, 0), x, ws)
+        _check(B.rewy_ssm_fwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
+                              _p(y), _p(ht), _p(ws), ws.numel(), handle), "rewy_ssm_fwd")
+    return y, ht, dict(desc=desc, x=x, dt=dt, a_log=a_log, b=b, c=c, d=d, dt_bias=dt_bias, h0=h0, cu=cu,
+                       host=host)
+
+
+def selective_scan_recurrent(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seqlens=None, ht=None,
+                             stream=None):
+    """The same scan token by token (decoding).  Returns (y, ht); ``ht`` may be
+    h0 itself (updated in place)."""
+    desc, shape, cu, host = _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)
+    _like(ht, x, shape, "ht", torch.float32)
+    with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, cu, ht)) as handle:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if ht is None:
+            ht = torch.empty(shape, dtype=torch.float32, device=x.device)
+        _check(B.rewy_ssm_recurrent_fwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d),
+                                        _p(h0), _p(y), _p(ht), handle), "rewy_ssm_recurrent_fwd")
+    return y, ht
+
+
+def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, stream=None, ws=None):
+    """Gradients of the scan: dict(dx, ddt, da_log, db, dc, dd, ddt_bias, dh0).
+    dy may be a slice of longer rows.  ``out=(dx, db, dc)`` gives the places of
+    those three (slices of one row, for the convolution's backward)."""
+    x, dt, a_log, b, c, d, dt_bias, h0 = (ctx[k] for k in ("x", "dt", "a_log", "b", "c", "d", "dt_bias",
+                                                           "h0"))
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and type")
+    f = ctx["desc"]
+    shape = (f.N if ctx["cu"] is not None else f.B, f.H, f.K, f.V)
+    _like(dht, x, shape, "dht", torch.float32)
+    if want_dh0 is None:
+        want_dh0 = h0 is not None
+    if out is not None:
+        for t, ref, name in zip(out, (x, b, c), ("dx", "db", "dc")):
+            if t.shape != ref.shape or t.dtype != ref.dtype:
+                raise ValueError(f"{name} must have the shape and type of its input")
+    with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, ctx["cu"], dy, dht, *(out or ()))) as handle:
+        if out is None:
+            out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (x, b, c))
+        dx, db, dc = out
+        desc = B.RewySsmDesc(f.B, f.T, f.H, f.G, f.K, f.V, f.N, f.cu_seqlens, f.cu_seqlens_host, f.dtype,
+                             f.dt_dtype, f.x_stride, f.b_stride, f.c_stride, _row_stride(dy, "dy", 2),
+                             _row_stride(dx, "dx", 2), _row_stride(db, "db", 2), _row_stride(dc, "dc", 2))
+        ddt, da_log = torch.empty_like(dt), torch.empty_like(a_log)
+        dd = None if d is None else torch.empty_like(d)
+        ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
+        dh0 = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dh0 else None
+        ws = _workspace(B.rewy_ssm_workspace_bytes(desc, 1), x, ws)
+        _check(B.rewy_ssm_bwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
+                              _p(dy), _p(dht), _p(dx), _p(ddt), _p(da_log), _p(ddt_bias), _p(db), _p(dc),
+                              _p(dd), _p(dh0), _p(ws), ws.numel(), handle), "rewy_ssm_bwd")
+    return dict(dx=dx, ddt=ddt, da_log=da_log, db=db, dc=dc, dd=dd, ddt_bias=ddt_bias, dh0=dh0)
+
+
+class SelectiveScanFunction(torch.autograd.Function):
+    """Autograd wrapper: y, ht = SelectiveScanFunction.apply(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)."""
+
+    @staticmethod
+    def forward(fctx, x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens):
+        y, ht, ctx = selective_scan(x, dt, a_log, b, c, d=d, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens)
+        fctx.save_for_backward(x, dt, a_log, b, c, d, dt_bias, h0)
+        fctx.rewy = {k: ctx[k] for k in ("desc", "cu", "host")}
+        return y, ht
+
+    @staticmethod
+    def backward(fctx, dy, dht):
+        names = ("x", "dt", "a_log", "b", "c", "d", "dt_bias", "h0")
+        g = selective_scan_backward(dict(fctx.rewy, **dict(zip(names, fctx.saved_tensors))), dy.contiguous(),
+                                    dht.contiguous())
+        return (g["dx"], g["ddt"], g["da_log"], g["db"], g["dc"], g["dd"], g["ddt_bias"], g["dh0"], None)
+
+
+def selective_scan_autograd(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seqlens=None):
+    """Differentiable selective state space scan on the HIP path: (y, ht)."""
+    return SelectiveScanFunction.apply(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)

@@ -11,8 +11,10 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .layer_ops import (rms_norm, rms_norm_backward, rms_norm_autograd, short_conv,  # noqa: F401
-                        short_conv_autograd, short_conv_backward, short_conv_step)
+from .layer_ops import (rms_norm, rms_norm_autograd, rms_norm_backward,  # noqa: F401
+                        selective_scan, selective_scan_autograd, selective_scan_backward,
+                        selective_scan_recurrent, short_conv, short_conv_autograd,
+                        short_conv_backward, short_conv_step)
 
 _DT = {torch.bfloat16: B.REWY_BF16, torch.float32: B.REWY_F32}
 _POLICY = {"recompute": B.REWY_RECOMPUTE, "save": B.REWY_SAVE}

@@ -318,6 +318,64 @@ int rewy_conv_bwd(const rewy_conv_desc *d, const void *x, const void *w, const v
                   void *dx, void *dw, void *dbias, void *dh0,
                   void *workspace, size_t ws_bytes, void *stream);
 
+/* Selective state space scan: per sequence n and head h the fp32 state S
+ * [K, V], token by token, with group g(h) = h / (H / G) sharing B and C,
+ *     dt_t = softplus(raw_t + dt_bias[h]),  a_t = exp(-exp(A_log[h]) dt_t),
+ *     S = a_t S + dt_t B_t x_t^T,   y_t = S^T C_t + D[h] x_t:
+ * the scalar-gate recurrence of the delta rule without its correction.
+ *
+ * Layouts (token-major):
+ *   x, y, dy, dx       [B, T, H, V]   dtype
+ *   b, c, db, dc       [B, T, G, K]   dtype
+ *   dt (raw), ddt      [B, T, H]      dt_dtype, contiguous
+ *   A_log, dt_bias, D and their gradients [H] fp32; dt_bias and D may be NULL
+ *   h0, ht, dht, dh0   [N, H, K, V]   fp32, contiguous
+ * x, b, c and y (dy) may be slices of longer rows (the convolution's output, for
+ * one): token strides in elements, 0 = contiguous.  Pointers of dtype tensors
+ * and states are 16-byte aligned and strides a multiple of 16 bytes, at most 2^22
+ * elements.  K and V are 32, 64 or 128 (fp32: 32 or 64); H is a multiple of G.
+ * With bf16 operands the coefficients inside a chunk and the states that only
+ * 16-bit outputs read are rounded to bf16 as operands; everything that sums into
+ * a state or a parameter's gradient keeps 24 bits. */
+typedef struct {
+    int32_t B, T, H, G, K, V;
+    int32_t N;                      /* sequences: B (or 0) without cu_seqlens */
+    const int32_t *cu_seqlens;      /* device [N+1] or NULL; needs B == 1 */
+    const int32_t *cu_seqlens_host; /* optional host copy, validated if given */
+    int32_t dtype;                  /* rewy_dtype of x, b, c, y, dy, dx, db, dc */
+    int32_t dt_dtype;               /* rewy_dtype of dt and ddt */
+    int64_t x_stride, b_stride, c_stride, y_stride;
+    int64_t dx_stride, db_stride, dc_stride;
+} rewy_ssm_desc;
+
+/* Bytes of workspace: phase 0 = rewy_ssm_fwd, 1 = rewy_ssm_bwd (256-byte
+ * aligned).  Returns 0 for an invalid descriptor or phase. */
+size_t rewy_ssm_workspace_bytes(const rewy_ssm_desc *d, int phase);
+
+/* Forward in chunks of 64 tokens, for prompts and training.  h0 and ht may be
+ * NULL; ht may not overlap h0. */
+int rewy_ssm_fwd(const rewy_ssm_desc *d, const void *x, const void *dt, const float *a_log,
+                 const float *dt_bias, const void *b, const void *c, const float *D,
+                 const float *h0, void *y, float *ht,
+                 void *workspace, size_t ws_bytes, void *stream);
+
+/* Backward (the forward's states are formed again; nothing is kept between the
+ * calls).  dht may be NULL; dh0 must be given when h0 is; ddt_bias and dD are given
+ * exactly when dt_bias and D are.  Outputs are overwritten. */
+int rewy_ssm_bwd(const rewy_ssm_desc *d, const void *x, const void *dt, const float *a_log,
+                 const float *dt_bias, const void *b, const void *c, const float *D,
+                 const float *h0, const void *dy, const float *dht,
+                 void *dx, void *ddt, float *da_log, float *ddt_bias, void *db, void *dc,
+                 float *dD, float *dh0,
+                 void *workspace, size_t ws_bytes, void *stream);
+
+/* Token-serial forward for decoding: the same recurrence, no workspace, the state
+ * on chip from h0 to ht; ht may be h0 itself.  Meant for one or a few new
+ * tokens per sequence. */
+int rewy_ssm_recurrent_fwd(const rewy_ssm_desc *d, const void *x, const void *dt,
+                           const float *a_log, const float *dt_bias, const void *b, const void *c,
+                           const float *D, const float *h0, void *y, float *ht, void *stream);
+
 /* Per-kernel timing (a tracing aid: device events, as in the ReWY paper's timing
  * protocol).  After rewy_trace_begin(), calls made by this thread
  * record a HIP event pair on the call's stream around every kernel they

@@ -110,6 +110,67 @@ def test_conv_pointers():
     assert bwd(n=need - 1) == B.REWY_EWORKSPACE and bwd(ws=None) == B.REWY_EWORKSPACE
 
 
+def _ssm(**kw):
+    d = dict(B=2, T=100, H=4, G=2, K=64, V=32, N=0, cu=None, host=None, dtype=B.REWY_BF16, dt_dtype=B.REWY_F32,
+             x_stride=0, b_stride=0, c_stride=0, y_stride=0, dx_stride=0, db_stride=0, dc_stride=0)
+    d.update(kw)
+    return B.RewySsmDesc(*d.values())
+
+
+@pytest.mark.parametrize("bad,status,msg", [
+    (dict(B=-1), B.REWY_EINVAL, "bad shape"), (dict(H=0), B.REWY_EINVAL, "bad heads"), (dict(G=0), B.REWY_EINVAL, "bad heads"),
+    (dict(G=3), B.REWY_EINVAL, "multiple of G"), (dict(K=48), B.REWY_EUNSUPPORTED, "not supported"),
+    (dict(V=256), B.REWY_EUNSUPPORTED, "not supported"), (dict(K=0), B.REWY_EINVAL, "bad shape"),
+    (dict(dtype=B.REWY_F32, K=128), B.REWY_EUNSUPPORTED, "not supported"), (dict(dtype=9), B.REWY_EINVAL, "bad dtype"),
+    (dict(dt_dtype=9), B.REWY_EINVAL, "bad dt_dtype"), (dict(x_stride=120), B.REWY_EINVAL, "shorter"),
+    (dict(b_stride=129), B.REWY_EINVAL, "16 bytes"), (dict(c_stride=1 << 23), B.REWY_EUNSUPPORTED, "2^22"),
+    (dict(N=1), B.REWY_EINVAL, "must equal"), (dict(cu=8), B.REWY_EINVAL, "B == 1"),
+])
+def test_ssm_descriptor(bad, status, msg):
+    rc = B.rewy_ssm_fwd(_ssm(**bad), *([P(OK)] * 10), P(OK), 1 << 40, None)
+    assert rc == status and msg in B.rewy_last_error()
+    assert B.rewy_ssm_workspace_bytes(_ssm(**bad), 0) == 0
+    assert B.rewy_ssm_workspace_bytes(_ssm(**bad), 1) == 0
+
+
+def test_ssm_pointers():
+    names = ("x", "dt", "a_log", "dt_bias", "b", "c", "D", "h0", "y", "ht")
+
+    def fwd(call=B.rewy_ssm_fwd, ws=OK, n=1 << 40, **kw):
+        a = {k: OK for k in names}
+        a["ht"] = 4 * OK
+        a.update(kw)
+        a = [None if v is None else P(v) for v in a.values()]
+        tail = [None] if call is B.rewy_ssm_recurrent_fwd else [None if ws is None else P(ws), n, None]
+        return call(_ssm(T=3000), *a, *tail)
+
+    for call in (B.rewy_ssm_fwd, B.rewy_ssm_recurrent_fwd):
+        for kw, msg in ((dict(x=None), "x is NULL"), (dict(dt=None), "dt is NULL"), (dict(a_log=None), "A_log is NULL"),
+                        (dict(b=None), "b is NULL"), (dict(c=None), "c is NULL"), (dict(y=None), "y is NULL"),
+                        (dict(x=OK + 8), "x is not 16-byte"), (dict(h0=OK + 4), "h0 is not 16-byte"),
+                        (dict(dt=OK + 2), "dt is not 4-byte")):
+            assert fwd(call, **kw) == B.REWY_EINVAL and msg in B.rewy_last_error(), msg
+    assert fwd(ht=OK) == B.REWY_EINVAL and "ht may not be h0" in B.rewy_last_error()
+    need = B.rewy_ssm_workspace_bytes(_ssm(T=3000), 0)
+    assert need > 0 and fwd(n=need - 1) == B.REWY_EWORKSPACE and fwd(ws=None) == B.REWY_EWORKSPACE
+    assert fwd(ws=OK + 128) == B.REWY_EWORKSPACE
+    assert B.rewy_ssm_workspace_bytes(_ssm(), 2) == 0 and "bad phase" in B.rewy_last_error()
+    need = B.rewy_ssm_workspace_bytes(_ssm(), 1)
+
+    def bwd(n=need, **kw):
+        a = {k: OK for k in ("x", "dt", "a_log", "dt_bias", "b", "c", "D", "h0", "dy", "dht", "dx", "ddt", "da_log",
+                             "ddt_bias", "db", "dc", "dD", "dh0", "ws")}
+        a.update(kw)
+        return B.rewy_ssm_bwd(_ssm(), *(None if v is None else P(v) for v in a.values()), n, None)
+
+    for kw, msg in ((dict(dy=None), "dy is NULL"), (dict(dx=None), "dx is NULL"), (dict(ddt=None), "ddt is NULL"),
+                    (dict(da_log=None), "dA_log is NULL"), (dict(db=None), "db is NULL"), (dict(dc=None), "dc is NULL"),
+                    (dict(dh0=None), "dh0 is NULL"), (dict(dD=None), "dD is NULL"), (dict(D=None), "exactly when"),
+                    (dict(dt_bias=None), "exactly when"), (dict(ddt_bias=None), "ddt_bias is NULL")):
+        assert bwd(**kw) == B.REWY_EINVAL and msg in B.rewy_last_error(), msg
+    assert bwd(n=need - 1) == B.REWY_EWORKSPACE
+
+
 def test_wrappers_refuse():
     x, w = torch.zeros(2, 8), torch.zeros(8)
     with pytest.raises(ValueError, match="GPU"):
@@ -124,6 +185,17 @@ def test_wrappers_refuse():
         L.rms_norm(x, w, torch.zeros(2, 7))
     with pytest.raises(ValueError, match="contiguous"):
         L.rms_norm(torch.zeros(8, 2).t(), w)
+    x, b, dt, al = torch.zeros(1, 4, 2, 32), torch.zeros(1, 4, 1, 32), torch.zeros(1, 4, 2), torch.zeros(2)
+    with pytest.raises(ValueError, match="GPU"):
+        L.selective_scan(x, dt, al, b, b)
+    with pytest.raises(ValueError, match="c must have shape"):
+        L.selective_scan(x, dt, al, b, torch.zeros(1, 4, 2, 32))
+    with pytest.raises(TypeError, match="b must have x's type"):
+        L.selective_scan(x, dt, al, b.bfloat16(), b)
+    with pytest.raises(ValueError, match="h0 must have shape"):
+        L.selective_scan(x, dt, al, b, b, h0=torch.zeros(2, 2, 32, 32))
+    with pytest.raises(TypeError, match="a_log must be"):
+        L.selective_scan(x, dt, al.double(), b, b)
     x = torch.zeros(1, 4, 8)
     with pytest.raises(ValueError, match="end at T"):
         L.short_conv(x, torch.zeros(8, 4), cu_seqlens=[0, 3])

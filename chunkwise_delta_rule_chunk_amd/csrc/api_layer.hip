@@ -174,7 +174,9 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   }
   const int64_t total = a.seq.total;
   const int longest = a.seq.cu ? a.seq.total : a.seq.T;
-  a.seg = ssm_segment(total, a.H, 1024, bwd ? 1024 : 8192);
+  // (the backward's decay gradient is summed from the ends of the segments, and its
+  // error grows with their length)
+  a.seg = bwd ? 256 : ssm_segment(total, a.H, 512, 8192);
   if (!bwd && !a.seq.cu && (int64_t)a.seq.N * a.H >= 512) a.seg = std::max(CH, (int)up64(longest));
   a.two = longest > a.seg;
   const int64_t nslot = total / a.seg + a.seq.N, nchunk = total / CH + a.seq.N;
@@ -197,6 +199,9 @@ size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
     off += up(n);
   };
   const size_t kv = (size_t)a.H * a.K * a.V, e = f32 ? 4 : 2, tok = (size_t)a.H * a.seq.total * 4;
+  char* gates;
+  take(gates, (size_t)a.nchunk * a.H * CH * sizeof(Gate));
+  a.gates = gates;
   if (a.two) {
     take(a.sf, a.nslot * kv * 4);
     if (bwd) take(a.sr, a.nslot * kv * 4);
@@ -212,6 +217,7 @@ size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
     take(a.cx, tok);
     take(a.ri, tok);
     take(a.ci, tok);
+    take(a.cd, tok);
     take(a.ends, (size_t)a.nslot * a.H * 4);
     take(a.dpart, (size_t)a.nchunk * a.H * 4);
     take(a.apart, (size_t)a.nslot * 2 * a.H * 4);
@@ -389,6 +395,7 @@ REWY_API int rewy_ssm_fwd(const rewy_ssm_desc* d, const void* x, const void* dt,
     if (ht && ht == h0) return fail(REWY_EINVAL, "ht may not be h0");
     REWY_TRY(check_workspace(workspace, ws_bytes, ssm_layout(a, f32, false, static_cast<char*>(workspace))));
     a.y = y; a.ht = ht;
+    REWY_TRY(hip_check(traced("k_ssm_gates", s, [&] { return launch_ssm_gates(a, s); }), "scan gates"));
     if (a.two) {
       REWY_TRY(hip_check(traced("k_ssm_state", s, [&] { return launch_ssm_state(a, f32, false, s); }), "segment states"));
       REWY_TRY(hip_check(traced("k_ssm_pass", s, [&] { return launch_ssm_pass(a, false, s); }), "segment pass"));
@@ -440,6 +447,7 @@ REWY_API int rewy_ssm_bwd(const rewy_ssm_desc* d, const void* x, const void* dt,
     a.dy = dy; a.dht = dht; a.dx = dx; a.ddt = ddt; a.da_log = da_log; a.ddt_bias = ddt_bias;
     a.db = db; a.dc = dc; a.dd = dD; a.dh0 = dh0;
     if (some) {
+      REWY_TRY(hip_check(traced("k_ssm_gates", s, [&] { return launch_ssm_gates(a, s); }), "scan gates"));
       if (a.two) {
         REWY_TRY(hip_check(traced("k_ssm_state", s, [&] { return launch_ssm_state(a, f32, true, s); }), "segment states"));
         REWY_TRY(hip_check(traced("k_ssm_pass", s, [&] { return launch_ssm_pass(a, true, s); }), "segment pass"));

@@ -14,34 +14,40 @@
 // sums into a parameter's gradient stays fp32.
 #include "ssm.hpp"
 
+#ifndef SSM_WAVES
+#define SSM_WAVES 4
+#endif
 namespace rewy {
 
 namespace {
 
-// Walks of one segment and head, both directions (blockIdx.y).  Forward: the
+// Walks of one segment and HB heads, both directions (blockIdx.y).  Forward: the
 // state that enters each chunk goes to hs, and rx_t = exp(G_t) dy_t . (S_in^T
 // C_t); reverse: the adjoint that leaves each chunk goes to hd, and cx_t =
-// exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds columns 16 w .. + 15.
-template <typename T, int K, int V>
-__global__ __launch_bounds__(4 * V) void k_ssm_walk(SsmArgs a) {
-  constexpr int NTH = 4 * V, NW = V / 16, LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>;
-  constexpr int NT = K / 16, KQ = K / KG<T>, NS = SPLIT<T>;
+// exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds 16 columns of one head.
+template <typename T, int K, int V, int HB>
+__global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
+  constexpr int CW = HB * V, NTH = 4 * CW, NW = CW / 16, LK = pitch<T>(K), LV = pitch<T>(CW);
+  constexpr int NT = K / 16, KQ = K / KG<T>, NS = SPLIT<T>, WH = V / 16;
   __shared__ __align__(16) T sk[CH * LK];  // update: B (forward), C (reverse)
   __shared__ __align__(16) T sq[CH * LK];  // probe: C, B
   __shared__ __align__(16) T su[CH * LV];  // update: x, dy
   __shared__ __align__(16) T sp[CH * LV];  // probe: dy, x
-  __shared__ __align__(16) float sal[CH], sbe[CH], sdot[NW][CH];
-  __shared__ float sdec, sred[NW];
+  __shared__ __align__(16) float sal[HB][CH], sdot[NW][CH];
+  __shared__ float sdec[HB], sred[NW];
   const int dir = blockIdx.y;
-  const int wk = xcd_range(blockIdx.x, a.nslot * a.H), slot = wk / a.H, h = wk - slot * a.H, grp = h / a.per;
+  const int nhb = head_blocks(a, HB), wk = xcd_range(blockIdx.x, a.nslot * nhb), slot = wk / nhb, hb = wk - slot * nhb;
   const Piece pc = find_piece(a.seq, slot, a.seg);
   if (!pc.on) return;
   const int t0 = pc.bos + pc.k * a.seg, t1 = min(t0 + a.seg, pc.eos);
+  const int gb = (a.per + HB - 1) / HB, grp = hb / gb, h0 = grp * a.per + (hb - grp * gb) * HB;
+  const int nh = min(HB, (grp + 1) * a.per - h0);  // heads of this block
   const int nch = (t1 - t0 + CH - 1) / CH, w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15;
+  const int hw = w / WH, h = min(h0 + hw, h0 + nh - 1), pc0 = 16 * w - hw * V;
+  const bool live = hw < nh;
   const int cbase = slot_base(a.seq, pc.n, CH) + pc.k * (a.seg / CH);
-  const float A2 = gate_rate(a, h), bias = gate_bias(a, h);
-  const int64_t seqst = ((int64_t)pc.n * a.H + h) * K * V + 16 * w + r;
-  const int64_t segst = ((int64_t)slot * a.H + h) * K * V + 16 * w + r;
+  const int64_t seqst = ((int64_t)pc.n * a.H + h) * K * V + pc0 + r;
+  const int64_t segst = ((int64_t)slot * a.H + h) * K * V + pc0 + r;
   const float* given = dir ? a.dht : a.h0;
   // (an empty sequence has no segment of its own: its state is given through)
   const float* init = a.two && nch > 0 ? (dir ? a.sr : a.sf) + segst : given ? given + seqst : nullptr;
@@ -51,35 +57,38 @@ __global__ __launch_bounds__(4 * V) void k_ssm_walk(SsmArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) S[nt][i] = init ? init[(int64_t)(16 * nt + 4 * g4 + i) * V] : 0.f;
   TileRegs<T, CH, K, NTH> rk, rq;
-  TileRegs<T, CH, V, NTH> ru, rp;
+  TileRegs<T, CH, CW, NTH> ru, rp;
+  Gate gt = {};
   auto fetch = [&](int c) {
-    const int tok = t0 + (dir ? nch - 1 - c : c) * CH, len = min(CH, t1 - tok);
-    load_tile<T, K, NTH>(rk, dir ? a.c : a.b, tok, dir ? a.cs : a.bs, grp * K, len);
-    load_tile<T, K, NTH>(rq, dir ? a.b : a.c, tok, dir ? a.bs : a.cs, grp * K, len);
-    load_tile<T, V, NTH>(ru, dir ? a.dy : a.x, tok, dir ? a.ys : a.xs, h * V, len);
-    load_tile<T, V, NTH>(rp, dir ? a.x : a.dy, tok, dir ? a.xs : a.ys, h * V, len);
+    const int ci = dir ? nch - 1 - c : c, tok = t0 + ci * CH, len = min(CH, t1 - tok);
+    if (w < nh) gt = chunk_gates(a, cbase + ci, h0 + w)[l];
+    load_tile<T, K, NTH>(rk, dir ? a.c : a.b, tok, dir ? a.cs : a.bs, grp * K, len, K);
+    load_tile<T, K, NTH>(rq, dir ? a.b : a.c, tok, dir ? a.bs : a.cs, grp * K, len, K);
+    load_tile<T, CW, NTH>(ru, dir ? a.dy : a.x, tok, dir ? a.ys : a.xs, h0 * V, len, nh * V);
+    load_tile<T, CW, NTH>(rp, dir ? a.x : a.dy, tok, dir ? a.xs : a.ys, h0 * V, len, nh * V);
   };
   if (nch > 0) fetch(0);
   T* hand = reinterpret_cast<T*>(dir ? a.hd : a.hs);
-  float* dots = (dir ? a.cx : a.rx) + (int64_t)h * a.seq.total;
   for (int c = 0; c < nch; ++c) {
     const int ci = dir ? nch - 1 - c : c, tok = t0 + ci * CH, len = min(CH, t1 - tok);
     rk.store(sk, LK, threadIdx.x);
     rq.store(sq, LK, threadIdx.x);
     ru.store(su, LV, threadIdx.x);
     rp.store(sp, LV, threadIdx.x);
-    if (w == 0) {
-      const ChunkGate g = chunk_gate(a, tok, len, h, A2, bias);
-      const float eG = fexp2(g.G), eE = fexp2(g.E);
-      sal[l] = dir ? eG : eE * g.dt;
-      sbe[l] = dir ? eE : eG;
-      if (l == 0) sdec = fexp2(g.GL);
+    float be = 0.f;
+    if (w < HB) {
+      const float eG = fexp2(gt.G), eE = fexp2(gt.E);
+      sal[w][slot_of<T>(l)] = dir ? eG : eE * gt.dt;
+      be = dir ? eE : eG;
+      if (l == 63) sdec[w] = eG;
     }
-    __syncthreads();
+    lds_barrier();
     if (c + 1 < nch) fetch(c + 1);
-    T* hp = hand + (((int64_t)(cbase + ci) * a.H + h) * (V / 16) + w) * (K * 16) + l * 4;
+    if (live) {
+      T* hp = hand + (((int64_t)(cbase + ci) * a.H + h) * WH + pc0 / 16) * (K * 16) + l * 4;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) st4<T>(hp + nt * 256, S[nt]);
+      for (int nt = 0; nt < NT; ++nt) st4<T>(hp + nt * 256, S[nt]);
+    }
     f32x4 Y[4];
 #pragma unroll
     for (int I = 0; I < 4; ++I) Y[I] = zero4();
@@ -94,25 +103,20 @@ __global__ __launch_bounds__(4 * V) void k_ssm_walk(SsmArgs a) {
         for (int s = NS - 1; s >= 0; --s) mma16B<T>(Y[I], sf[s], qf);
       }
     }
-    // Y[I] holds columns t = 16 I + r, rows 16 w + 4 g4 + i
+    // Y[I] holds columns t = 16 I + r, rows (columns of the state) 4 g4 + i
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
       const f32x4 u = ld4<T>(sp + (16 * I + r) * LV + 16 * w + 4 * g4);
       const float d = rows_sum((Y[I][0] * u[0] + Y[I][1] * u[1]) + (Y[I][2] * u[2] + Y[I][3] * u[3]));
       if (g4 == I) sdot[w][16 * I + r] = d;
     }
-    uint4 ut[NQ];
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) ut[q] = frag_col<T>(su, LV, q * KG<T>, 16 * w);
-    state_update<T, K>(S, sk, LK, ut, sal, sdec);
-    float be = 0.f;
-    if (w == 0) be = sbe[l];
-    __syncthreads();  // dots complete, tiles free
-    if (w == 0 && l < len) {
+    state_update<T, K>(S, sk, LK, su, LV, 16 * w, sal[hw], sdec[hw]);
+    lds_barrier();  // dots complete, tiles free
+    if (w < nh && l < len) {
       float d = 0.f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) d += sdot[i][l];
-      dots[tok + l] = be * d;
+      for (int i = 0; i < WH; ++i) d += sdot[w * WH + i][l];
+      ((dir ? a.cx : a.rx) + (int64_t)(h0 + w) * a.seq.total)[tok + l] = be * d;
     }
   }
   if (dir == 0) {
@@ -126,13 +130,13 @@ __global__ __launch_bounds__(4 * V) void k_ssm_walk(SsmArgs a) {
         if (adj) d += S[nt][i] * adj[(int64_t)(16 * nt + 4 * g4 + i) * V];
     d = rows_sum(row16_sum(d));
     if (l == 0) sred[w] = d;
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    lds_barrier();
+    if (w < nh && l == 0) {
       d = 0.f;
-      for (int i = 0; i < NW; ++i) d += sred[i];
-      a.ends[(int64_t)slot * a.H + h] = d;
+      for (int i = 0; i < WH; ++i) d += sred[w * WH + i];
+      a.ends[(int64_t)slot * a.H + h0 + w] = d;
     }
-  } else if (a.dh0 && pc.k == 0) {
+  } else if (a.dh0 && live && pc.k == 0) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -154,11 +158,11 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   __shared__ __align__(16) T sc[CH * LK];
   __shared__ __align__(16) T sx[CH * LV];
   __shared__ __align__(16) T sy[CH * LV];  // dy
-  __shared__ __align__(16) T ss[V * LK];   // S_in^T
-  __shared__ __align__(16) T sd[V * LK];   // dS^T
-  __shared__ __align__(16) T sm[CH * LM];  // M0^T, at the end W^T
-  __shared__ __align__(16) float sG[CH], sdt[CH], seG[CH], seE[CH];
-  __shared__ float srp[4][CH], scp[4][CH], sdd[CB_WAVES];
+  __shared__ __align__(16) T ss[V * LK];   // S_in^T, rows placed for frag_col
+  __shared__ __align__(16) T sd[V * LK];   // dS^T, the same
+  __shared__ __align__(16) T sm[CH * LM];  // M0^T (columns in slot order), at the end W^T, then W
+  __shared__ __align__(16) float sG[CH], sGl[CH], sdt[CH], seG[CH], seE[CH], tG[CH], tGl[CH];  // t: in slot order
+  __shared__ float srp[4][CH], scp[4][CH], scd[CH], sdd[CB_WAVES];
   const int nwork = a.nchunk * a.G * a.split;
   int wk = xcd_range(blockIdx.x, nwork);
   const int part = wk % a.split;
@@ -172,9 +176,11 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 
   TileRegs<T, CH, V, NTH> rx, ry;
   TileRegs<T, V, K, NTH> rs, rd;  // pieces of the handed-over states, 16 bytes = two lanes' fragments
+  Gate gt = {};
   auto fetch = [&](int h) {
-    load_tile<T, V, NTH>(rx, a.x, tok, a.xs, h * V, len);
-    load_tile<T, V, NTH>(ry, a.dy, tok, a.ys, h * V, len);
+    if (w == 0) gt = chunk_gates(a, cslot, h)[l];
+    load_tile<T, V, NTH>(rx, a.x, tok, a.xs, h * V, len, V);
+    load_tile<T, V, NTH>(ry, a.dy, tok, a.ys, h * V, len, V);
     const int64_t o = ((int64_t)cslot * a.H + h) * K * V;
     rs.load(gbuf(reinterpret_cast<const T*>(a.hs) + o, K * V * sizeof(T)), K, threadIdx.x);
     rd.load(gbuf(reinterpret_cast<const T*>(a.hd) + o, K * V * sizeof(T)), K, threadIdx.x);
@@ -190,7 +196,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 #pragma unroll
         for (int k = 0; k < FP; ++k) {
           const int f = idx * FP + k, lane = f & 63, tile = f >> 6, nt = tile % (K / 16), pt = tile / (K / 16);
-          T* p = s + (16 * pt + (lane & 15)) * LK + 16 * nt + 4 * (lane >> 4);
+          T* p = s + slot_place<T>(16 * pt + (lane & 15)) * LK + 16 * nt + 4 * (lane >> 4);
           if constexpr (FP == 2) *reinterpret_cast<uint2*>(p) = k ? uint2{t.r[j].z, t.r[j].w} : uint2{t.r[j].x, t.r[j].y};
           else *reinterpret_cast<uint4*>(p) = t.r[j];
         }
@@ -200,15 +206,15 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 
   {
     TileRegs<T, CH, K, NTH> rb, rc;
-    load_tile<T, K, NTH>(rb, a.b, tok, a.bs, grp * K, len);
-    load_tile<T, K, NTH>(rc, a.c, tok, a.cs, grp * K, len);
+    load_tile<T, K, NTH>(rb, a.b, tok, a.bs, grp * K, len, K);
+    load_tile<T, K, NTH>(rc, a.c, tok, a.cs, grp * K, len, K);
     rb.store(sb, LK, threadIdx.x);
     rc.store(sc, LK, threadIdx.x);
   }
   for (int i = threadIdx.x; i < CH * LM; i += NTH) sm[i] = (T)0.f;
-  __syncthreads();
+  lds_barrier();
   // blocks (I, J) of the lower triangle: 10 over 8 waves.  C B^T and the sum of W over
-  // the heads stay in registers (rows i = 16 I + 4 g4 + e, column j = 16 J + r).
+  // the heads stay in registers (rows i = 16 I + slot_row(4 g4 + e), column j = 16 J + r).
   constexpr int NB = (10 + CB_WAVES - 1) / CB_WAVES;
   f32x4 cb[NB], wsum[NB];
 #pragma unroll
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
 #pragma unroll
       for (int q = 0; q < KQ; ++q)
-        mma16B<T>(cb[b], frag_row<T>(sc, LK, 16 * I, q * KG<T>), frag_row<T>(sb, LK, 16 * J, q * KG<T>));
+        mma16B<T>(cb[b], frag_row_slot<T>(sc, LK, 16 * I, q * KG<T>), frag_row<T>(sb, LK, 16 * J, q * KG<T>));
     }
   }
   f32x4 dC[NTW], dB[NTW];
@@ -228,19 +234,19 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 
   if (h0 < h1) fetch(h0);
   for (int h = h0; h < h1; ++h) {
-    __syncthreads();  // tiles free
+    lds_barrier();  // tiles free
     rx.store(sx, LV, threadIdx.x);
     ry.store(sy, LV, threadIdx.x);
     put_state(ss, rs);
     put_state(sd, rd);
     if (w == 0) {
-      const ChunkGate g = chunk_gate(a, tok, len, h, gate_rate(a, h), gate_bias(a, h));
-      sG[l] = g.G;
-      sdt[l] = g.dt;
-      seG[l] = fexp2(g.G);
-      seE[l] = fexp2(g.E);
+      sG[l] = tG[slot_of<T>(l)] = gt.G;
+      sGl[l] = tGl[slot_of<T>(l)] = gt.Glo;
+      sdt[l] = gt.dt;
+      seG[l] = fexp2(gt.G);
+      seE[l] = fexp2(gt.E);
     }
-    __syncthreads();
+    lds_barrier();
     if (h + 1 < h1) fetch(h + 1);
     float dd = 0.f;
 #pragma unroll
@@ -251,31 +257,36 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
         f32x4 p = zero4();
 #pragma unroll
         for (int q = 0; q < VQ; ++q)
-          mma16B<T>(p, frag_row<T>(sy, LV, 16 * I, q * KG<T>), frag_row<T>(sx, LV, 16 * J, q * KG<T>));
-        const int i0 = 16 * I + 4 * g4, j = 16 * J + r;
-        const f32x4 Gi = *reinterpret_cast<const f32x4*>(sG + i0);
-        const float Gj = sG[j], dj = sdt[j];
+          mma16B<T>(p, frag_row_slot<T>(sy, LV, 16 * I, q * KG<T>), frag_row<T>(sx, LV, 16 * J, q * KG<T>));
+        const int sl = slot_base4<T>(I, g4), j = 16 * J + r;
+        const f32x4 Gi = *reinterpret_cast<const f32x4*>(tG + sl), Gil = *reinterpret_cast<const f32x4*>(tGl + sl);
+        const float Gj = sG[j], Gjl = sGl[j], dj = sdt[j];
         f32x4 m;
         float col = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float dec = j <= i0 + e ? fexp2(Gi[e] - Gj) : 0.f;
-          if (j == i0 + e) dd += p[e];
+          const int i = 16 * I + slot_row<T>(4 * g4 + e);
+          const float dec = j <= i ? fexp2((Gi[e] - Gj) + (Gil[e] - Gjl)) : 0.f;
           m[e] = cb[b][e] * dec;
-          const float cm = m[e] * p[e];
+          float cm = m[e] * p[e];
+          if (j == i) {
+            dd += p[e];
+            scd[j] = cm;
+            cm = 0.f;
+          }
           col += cm;
           wsum[b][e] += p[e] * dec * dj;
           const float row = row16_sum(cm * dj);
-          if (r == 0) srp[J][i0 + e] = row;
+          if (r == 0) srp[J][i] = row;
         }
-        st4<T>(sm + j * LM + i0, m);
+        st4<T>(sm + j * LM + sl, m);
         col = rows_sum(col);
         if (g4 == 0) scp[I][j] = col;
       }
     }
     dd = rows_sum(row16_sum(dd));
     if (l == 0) sdd[w] = dd;
-    __syncthreads();
+    lds_barrier();
     if (w == 0 && l < len) {
       float rr = 0.f, cc = 0.f;
 #pragma unroll
@@ -285,6 +296,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       }
       a.ri[(int64_t)h * a.seq.total + tok + l] = rr;
       a.ci[(int64_t)h * a.seq.total + tok + l] = cc;
+      a.cd[(int64_t)h * a.seq.total + tok + l] = scd[l];
     }
     if (w == 1 && l == 0) {
       float s = 0.f;
@@ -299,13 +311,14 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       for (int pi = 0; pi < PTW; ++pi) {
         const int pt = half * PTW + pi;
         f32x4 u = zero4(), v = zero4();
+        const T* sdp = sd + slot_place<T>(16 * pt + r) * LK + VEC<T> * g4;
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
           if ((q + 1) * KG<T> > 16 * tb)
             mma16B<T>(u, frag_col<T>(sy, LV, q * KG<T>, 16 * pt), frag_row<T>(sm, LM, 16 * tb, q * KG<T>));
 #pragma unroll
         for (int q = 0; q < KQ; ++q)
-          mma16B<T>(v, frag_row<T>(sd, LK, 16 * pt, q * KG<T>), frag_row<T>(sb, LK, 16 * tb, q * KG<T>));
+          mma16B<T>(v, *reinterpret_cast<const uint4*>(sdp + q * KG<T>), frag_row<T>(sb, LK, 16 * tb, q * KG<T>));
         const int p = 16 * pt + 4 * g4;
         const f32x4 dyv = ld4<T>(sy + j * LV + p);
 #pragma unroll
@@ -341,17 +354,17 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       }
     }
   }
-  // the heads' W: as W^T [j][i] for dB, then as W [i][j] for dC
-  __syncthreads();
+  // the heads' W: as W^T [j][i] for dB, then as W [i][j] for dC (columns in slot order)
+  lds_barrier();
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int blk = b * CB_WAVES + w;
     if (blk < 10) {
       const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
-      st4<T>(sm + (16 * J + r) * LM + 16 * I + 4 * g4, wsum[b]);
+      st4<T>(sm + (16 * J + r) * LM + slot_base4<T>(I, g4), wsum[b]);
     }
   }
-  __syncthreads();
+  lds_barrier();
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
     if ((q + 1) * KG<T> > 16 * tb) {
@@ -359,10 +372,26 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 #pragma unroll
       for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dB[ni], wf, frag_col<T>(sc, LK, q * KG<T>, 16 * (half * NTW + ni)));
     }
+  lds_barrier();
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int blk = b * CB_WAVES + w;
+    if (blk < 10) {
+      const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        T* p = sm + (16 * I + slot_row<T>(4 * g4 + e)) * LM;
+        p[slot_of<T>(16 * J + r)] = (T)wsum[b][e];
+        // the block right of the diagonal that shares a contraction with it
+        if (I == J && (I & 1) == 0) p[slot_of<T>(16 * (J + 1) + r)] = (T)0.f;
+      }
+    }
+  }
+  lds_barrier();
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
     if (q * KG<T> <= 16 * tb) {
-      const uint4 wf = frag_col<T>(sm, LM, q * KG<T>, 16 * tb);  // column i of W^T, contraction j
+      const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row i, contraction j
 #pragma unroll
       for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dC[ni], wf, frag_col<T>(sb, LK, q * KG<T>, 16 * (half * NTW + ni)));
     }
@@ -404,12 +433,14 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
     for (int c = nch - 1; c >= 0; --c) {
       const int t = t0 + c * CH + l;
       const bool on = t < t1;
-      float dt = 0.f, cc = 0.f, diff = 0.f, z = 0.f;
+      float dt = 0.f, cc = 0.f, diff = 0.f, cross = 0.f, z = 0.f;
       if (on) {
         z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
         dt = softplus_full(z);
-        cc = a.cx[row + t] + a.ci[row + t];
-        diff = a.rx[row + t] + a.ri[row + t] - dt * cc;
+        const float cx = a.cx[row + t], ci = a.ci[row + t];
+        cross = a.rx[row + t] - dt * cx;
+        diff = cross + (a.ri[row + t] - dt * ci);
+        cc = cx + ci + a.cd[row + t];
       }
       float s = diff;
 #pragma unroll
@@ -418,7 +449,9 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
         if (l + d < 64) s += u;
       }
       const float dg = s + tail;
-      tail += __shfl(s, 0, 64);
+      // what the chunk adds for the earlier ones: over a whole chunk the pairs inside
+      // it cancel, so only the parts through the states are carried on
+      tail += rows_sum(row16_sum(cross));
       if (on) {
         const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
         const float dz = (cc + A * dg) * sg;
@@ -452,7 +485,7 @@ __global__ __launch_bounds__(256) void k_ssm_params(SsmArgs a) {
   }
   s = rows_sum(row16_sum(s));
   if (lane_id() == 0) buf[wave_id()] = s;
-  __syncthreads();
+  lds_barrier();
   if (threadIdx.x == 0) {
     float* o = what == 0 ? a.da_log : what == 1 ? a.ddt_bias : a.dd;
     if (o) o[h] = (buf[0] + buf[1]) + (buf[2] + buf[3]);
@@ -482,10 +515,10 @@ __global__ __launch_bounds__(256) void k_ssm_bcsum(SsmArgs a) {
 }  // namespace
 
 hipError_t launch_ssm_walk(const SsmArgs& a, bool f32, hipStream_t s) {
-  return ssm_kv(a.K, a.V, f32, [&](auto t, auto k, auto v) {
+  return ssm_kv_heads(a, f32, [&](auto t, auto k, auto v, auto hb) {
     using T = decltype(t);
-    constexpr int K = decltype(k)::value, V = decltype(v)::value;
-    REWY_LAUNCH((k_ssm_walk<T, K, V>), dim3(a.nslot * a.H, 2), dim3(4 * V), s, a);
+    constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
+    REWY_LAUNCH((k_ssm_walk<T, K, V, HB>), dim3(a.nslot * ssm_head_blocks(a, HB), 2), dim3(4 * HB * V), s, a);
     return hipGetLastError();
   });
 }

@@ -47,6 +47,7 @@ struct SsmArgs {
   float* ddt_bias;
   float* dh0;
   // workspace
+  void* gates;             // [nchunk, H, 64] Gate
   float* sf;               // [nslot, H, K, V] local end states, then the states that enter the segments
   float* sr;               // [nslot, H, K, V] local adjoints, then the adjoints of the states that leave them
   float* gsum;             // [nslot, H] sum of g (log2 units) over a segment
@@ -54,14 +55,17 @@ struct SsmArgs {
   void* hd;                // same: adjoint of the state leaving each chunk
   float* rx;               // [H, tokens] row part of the decay gradient through the entering state
   float* cx;               // [H, tokens] column part (per unit of dt) through the leaving state
-  float* ri;               // [H, tokens] row part inside the chunk
-  float* ci;               // [H, tokens] column part inside the chunk
+  float* ri;               // [H, tokens] row part inside the chunk (i > j)
+  float* ci;               // [H, tokens] column part inside the chunk (i > j)
+  float* cd;               // [H, tokens] the term i = j, which belongs to c and cancels in the decay gradient
   float* ends;             // [nslot, H] <state, adjoint> at each segment's end
   float* dpart;            // [nchunk, H] partial sums of dD
   float* apart;            // [nslot, 2, H] partial sums of dA_log and ddt_bias
   float* bcpart;           // [2, split, tokens, G, K] partial sums of dB and dC (split > 1)
 };
 
+int ssm_head_blocks(const SsmArgs& a, int hb);
+hipError_t launch_ssm_gates(const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_state(const SsmArgs& a, bool f32, bool both, hipStream_t s);
 hipError_t launch_ssm_pass(const SsmArgs& a, bool both, hipStream_t s);
 hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s);
@@ -113,33 +117,19 @@ __device__ __forceinline__ int xcd_range(int b, int n) {
 // softplus at full fp32 precision (small steps dt matter relative to themselves)
 __device__ __forceinline__ float softplus_full(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
-// The gates of a chunk, by one wave, lane t its token: dt, and in log2 units the
-// inclusive prefix G, the exclusive suffix E = G_L - G (summed on its own, so
-// that small ones are exact) and the total.  Rows past the end have dt = g = 0.
-struct ChunkGate {
-  float dt, G, E, GL;
+// The gates of one token, formed once per call by k_ssm_gates and read by every
+// walk: dt, the chunk's inclusive prefix sum G of g (log2 units) and the
+// exclusive suffix sum E = G_L - G.  The sums are taken in 64 bits.  G is kept as
+// hi + lo, so that a difference G_i - G_j of neighbours is as exact after a long,
+// strongly decaying stretch of the chunk as at its start (one float would be off by
+// a step of G there, and the exponential by as much relative to itself).  Rows
+// past the sequence's end have dt = g = 0, so G of row 63 is the chunk's total.
+struct Gate {
+  float dt, G, Glo, E;
 };
-__device__ __forceinline__ ChunkGate chunk_gate(const SsmArgs& a, int tok, int len, int h, float A2, float bias) {
-  const int t = lane_id();
-  ChunkGate r;
-  r.dt = 0.f;
-  if (t < len) r.dt = softplus_full(ld_beta(a.dt, a.dt_f32, (int64_t)(tok + t) * a.H + h) + bias);
-  const float g = A2 * r.dt;
-  float p = g, s = g;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const float u = __shfl_up(p, d, 64), v = __shfl_down(s, d, 64);
-    if (t >= d) p += u;
-    if (t + d < 64) s += v;
-  }
-  r.G = p;
-  r.E = __shfl_down(s, 1, 64);
-  if (t == 63) r.E = 0.f;
-  r.GL = __shfl(p, 63, 64);
-  return r;
+__device__ __forceinline__ const Gate* chunk_gates(const SsmArgs& a, int cslot, int h) {
+  return reinterpret_cast<const Gate*>(a.gates) + ((int64_t)cslot * a.H + h) * CH;
 }
-// -exp(A_log) log2(e)
-__device__ __forceinline__ float gate_rate(const SsmArgs& a, int h) { return -expf(a.a_log[h]) * LOG2E; }
 __device__ __forceinline__ float gate_bias(const SsmArgs& a, int h) { return a.dt_bias ? a.dt_bias[h] : 0.f; }
 
 // ---- operand fragments ------------------------------------------------------------
@@ -156,24 +146,62 @@ __device__ __forceinline__ uint4 frag_row(const T* p, int ld, int r0, int k0) {
   const int l = lane_id();
   return *reinterpret_cast<const uint4*>(p + (r0 + (l & 15)) * ld + k0 + VEC<T> * (l >> 4));
 }
+// the same with the rows of a 16-row block in slot order (below)
+template <typename T>
+__device__ __forceinline__ uint4 frag_row_slot(const T* p, int ld, int r0, int k0);
 // the same with the slot order of frag_acc
 template <typename T>
 __device__ __forceinline__ uint4 frag_row_acc(const T* p, int ld, int r0, int q) {
   const int l = lane_id();
   return perm_row<T>(p + (r0 + (l & 15)) * ld + 4 * (l >> 4), q);
 }
-// column c0 + (l & 15) of an LDS tile, contraction over its rows t0 + VEC (l >> 4)
-// + e.  bf16: two transposing reads, each giving lane l of a 16-lane group column
-// l of four rows that the group reads as 32 contiguous bytes each.
+// column c0 + (l & 15) of an LDS tile, contraction over its rows t0 .. t0 + KG - 1.
+// fp32: slot 4 (l >> 4) + e is row t0 + 4 (l >> 4) + e.  bf16: two transposing
+// reads, each of which gives lane l of a 16-lane group column l of the four rows
+// that the group reads as 32 contiguous bytes each.  A row's pitch is 16 bytes
+// past a multiple of the banks, so the eight rows that half a wave reads together
+// are taken two apart (32 bytes apart in the banks: no conflicts): slot 8 (l >> 4) +
+// 4 hf + e is row t0 + 16 hf + tr_row(l >> 4, e).  slot_of() gives a row's slot.
+__device__ __forceinline__ int tr_row(int g, int e) { return 8 * (g & 1) + 2 * e + (g >> 1); }
+template <typename T>
+__device__ __forceinline__ int slot_of(int t) {
+  if constexpr (std::is_same_v<T, bf16>)
+    return (t & 32) + 8 * (((t >> 3) & 1) + 2 * (t & 1)) + 4 * ((t >> 4) & 1) + ((t >> 1) & 3);
+  else return t;
+}
+// Row of a 16-row block whose slots a lane group finds together: rows in this order,
+// as the rows of a product, put its C fragment's four values into neighbouring slots.
+template <typename T>
+__device__ __forceinline__ int slot_row(int i) {
+  if constexpr (std::is_same_v<T, bf16>) return tr_row(i >> 2, i & 3);
+  else return i;
+}
+template <typename T>
+__device__ __forceinline__ uint4 frag_row_slot(const T* p, int ld, int r0, int k0) {
+  const int l = lane_id();
+  return *reinterpret_cast<const uint4*>(p + (r0 + slot_row<T>(l & 15)) * ld + k0 + VEC<T> * (l >> 4));
+}
+// LDS row for row i of a tile whose frag_col fragments shall have slot k at row k
+template <typename T>
+__device__ __forceinline__ int slot_place(int i) {
+  if constexpr (std::is_same_v<T, bf16>) return (i & ~31) + 16 * ((i >> 2) & 1) + tr_row((i >> 3) & 3, i & 3);
+  else return i;
+}
+// first of the four neighbouring slots of rows 16 J + slot_row(4 g + e)
+template <typename T>
+__device__ __forceinline__ int slot_base4(int J, int g) {
+  if constexpr (std::is_same_v<T, bf16>) return 32 * (J >> 1) + 8 * g + 4 * (J & 1);
+  else return 16 * J + 4 * g;
+}
 template <typename T>
 __device__ __forceinline__ uint4 frag_col(const T* p, int ld, int t0, int c0) {
   const int l = lane_id(), g = l >> 4, r = l & 15;
   if constexpr (std::is_same_v<T, bf16>) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-    const T* q = p + (t0 + 8 * g + (r >> 2)) * ld + c0 + 4 * (r & 3);
+    const T* q = p + (t0 + tr_row(g, r >> 2)) * ld + c0 + 4 * (r & 3);
     const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q));
-    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 4 * ld));
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 16 * ld));
     const uint2 x = __builtin_bit_cast(uint2, u), y = __builtin_bit_cast(uint2, v);
     return uint4{x.x, x.y, y.x, y.y};
   } else {
@@ -265,46 +293,55 @@ __device__ __forceinline__ f32x4 ld4(const T* p) {
   }
 }
 
-// a chunk's rows of a token-major tensor, columns col .. + C - 1 (rows past len: zeros)
+// A chunk's rows of a token-major tensor, columns col .. + C - 1, of which the first
+// cols belong to the caller (rows past len read as zeros; the others hold whatever
+// the row holds there, or zeros behind the last row's)
 template <typename T, int C, int NTH>
 __device__ __forceinline__ void load_tile(TileRegs<T, CH, C, NTH>& r, const void* base, int64_t tok, int64_t stride,
-                                          int col, int len) {
+                                          int col, int len, int cols) {
   const T* p = reinterpret_cast<const T*>(base) + tok * stride + col;
-  r.load(gbuf(p, tile_bytes<T>(len, stride, C)), stride, threadIdx.x);
+  r.load(gbuf(p, tile_bytes<T>(len, stride, cols)), stride, threadIdx.x);
 }
 
 // State update S = exp(G_L) S + sum_t K_t (al_t u_t)^T for the wave's 16 columns:
-// A operand K^T (columns of sk), B operand al u (columns of su, scaled and split).
+// A operand K^T (columns of sk), B operand al u (columns of su, scaled and split;
+// sal holds al in slot order).
 template <typename T, int K>
-__device__ __forceinline__ void state_update(f32x4 (&S)[K / 16], const T* sk, int ldk, const uint4 (&ut)[CH / KG<T>],
+__device__ __forceinline__ void state_update(f32x4 (&S)[K / 16], const T* sk, int ldk, const T* su, int ldu, int c0,
                                              const float* sal, float dec) {
   constexpr int NQ = CH / KG<T>, VE = VEC<T>, NS = SPLIT<T>;
   const int g = lane_id() >> 4;
-  uint4 uf[NQ][NS];
+#pragma unroll
+  for (int nt = 0; nt < K / 16; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[nt][i] *= dec;
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
+    uint4 uf[NS];
     float f[VE];
-    frag_get<T>(f, ut[q]);
+    frag_get<T>(f, frag_col<T>(su, ldu, q * KG<T>, c0));
 #pragma unroll
     for (int e = 0; e < VE; e += 4) {
       const f32x4 al = *reinterpret_cast<const f32x4*>(sal + q * KG<T> + VE * g + e);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[e + i] *= al[i];
     }
-    frag_split<T, NS>(uf[q], f);
-  }
+    frag_split<T, NS>(uf, f);
 #pragma unroll
-  for (int nt = 0; nt < K / 16; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) S[nt][i] *= dec;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
+    for (int nt = 0; nt < K / 16; ++nt) {
       const uint4 kf = frag_col<T>(sk, ldk, q * KG<T>, 16 * nt);
 #pragma unroll
-      for (int s = NS - 1; s >= 0; --s) mma16B<T>(S[nt], kf, uf[q][s]);
+      for (int s = NS - 1; s >= 0; --s) mma16B<T>(S[nt], kf, uf[s]);
     }
   }
 }
+
+// Heads side by side in one workgroup of the walks: with eight waves of 16 columns
+// (fp32: four) as many heads of a group as fit share its B and C tiles.
+template <typename T>
+constexpr int WALK_COLS = std::is_same_v<T, bf16> ? 128 : 64;
+// blocks of HB heads of all groups
+__device__ __forceinline__ int head_blocks(const SsmArgs& a, int HB) { return a.G * ((a.per + HB - 1) / HB); }
 
 // the (type, K, V) variants of a kernel
 template <typename F>
@@ -324,6 +361,17 @@ hipError_t ssm_kv(int K, int V, bool f32, F&& f) {
     return hipErrorInvalidValue;
   };
   return f32 ? k_of(float{}) : k_of(bf16{});
+}
+// the same with the heads of a workgroup: as many as fit, or one where a group
+// has no two heads to put side by side
+template <typename F>
+hipError_t ssm_kv_heads(const SsmArgs& a, bool f32, F&& f) {
+  return ssm_kv(a.K, a.V, f32, [&](auto t, auto k, auto v) -> hipError_t {
+    constexpr int HB = WALK_COLS<decltype(t)> / decltype(v)::value;
+    if constexpr (HB > 1)
+      if (a.per == 1) return f(t, k, v, std::integral_constant<int, 1>{});
+    return f(t, k, v, std::integral_constant<int, HB>{});
+  });
 }
 
 }  // namespace rewy

@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -32,13 +33,25 @@ CFLAGS = [
 ]
 
 
+def _closure(path: str, seen: dict) -> dict:
+    """The file and every project header it includes, directly or not."""
+    if path not in seen:
+        text = open(path, "rb").read()
+        seen[path] = text
+        for name in re.findall(rb'^\s*#\s*include\s+"([^"]+)"', text, re.M):
+            for d in (CSRC, INCLUDE):
+                p = os.path.join(d, name.decode())
+                if os.path.exists(p):
+                    _closure(p, seen)
+                    break
+    return seen
+
+
 def _digest(src: str) -> str:
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".hpp", ".h")):
-            h.update(open(os.path.join(CSRC, name), "rb").read())
-    h.update(open(os.path.join(INCLUDE, "rewy.h"), "rb").read())
-    h.update(open(src, "rb").read())
+    for path, text in sorted(_closure(src, {}).items()):
+        h.update(os.path.basename(path).encode())
+        h.update(text)
     h.update(" ".join(CFLAGS).encode())
     return h.hexdigest()[:16]
 

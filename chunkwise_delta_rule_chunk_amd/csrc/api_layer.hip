@@ -179,15 +179,27 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   a.seg = bwd ? 256 : ssm_segment(total, a.H, 512, 8192);
   if (!bwd && !a.seq.cu && (int64_t)a.seq.N * a.H >= 512) a.seg = std::max(CH, (int)up64(longest));
   a.two = longest > a.seg;
-  const int64_t nslot = total / a.seg + a.seq.N, nchunk = total / CH + a.seq.N;
+  auto slots = [&](int64_t L) {  // (ssm.hpp)
+    return a.seq.cu ? total / L + a.seq.N : a.seq.N * std::max<int64_t>((a.seq.T + L - 1) / L, 1);
+  };
+  const int64_t nslot = slots(a.seg), nchunk = slots(CH);
   if (nslot * a.H > INT32_MAX / 2 || nchunk * a.H > INT32_MAX / 2 || (int64_t)a.seq.N * a.H > INT32_MAX / 2)
     return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
                 (long long)total, a.H);
   a.nslot = (int)nslot;
   a.nchunk = (int)nchunk;
-  // head ranges that share a group's dB and dC: enough workgroups for two a CU
-  a.split = 1;
-  while (a.split < a.per && nchunk * a.G * a.split < 512) a.split = std::min(a.per, a.split * 2);
+  // Head ranges that share a group's dB and dC.  A workgroup of the chunk backward
+  // fills a CU and costs about its heads plus one (its B and C tiles, the joint
+  // products); the ranges are the ones with the shortest schedule on 256 CUs, and
+  // of those the fewest, as each range adds a partial sum to memory.
+  int64_t best = INT64_MAX;
+  for (int sp = 1; sp <= std::min(a.per, 32); ++sp) {
+    const int64_t rounds = (nchunk * a.G * sp + 255) / 256, cost = rounds * ((a.per + sp - 1) / sp + 1);
+    if (cost < best) {
+      best = cost;
+      a.split = sp;
+    }
+  }
   return REWY_OK;
 }
 
@@ -202,6 +214,7 @@ size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
   char* gates;
   take(gates, (size_t)a.nchunk * a.H * CH * sizeof(Gate));
   a.gates = gates;
+  take(a.cb, (size_t)a.nchunk * a.G * 10 * 256 * 4);
   if (a.two) {
     take(a.sf, a.nslot * kv * 4);
     if (bwd) take(a.sr, a.nslot * kv * 4);
@@ -395,7 +408,7 @@ REWY_API int rewy_ssm_fwd(const rewy_ssm_desc* d, const void* x, const void* dt,
     if (ht && ht == h0) return fail(REWY_EINVAL, "ht may not be h0");
     REWY_TRY(check_workspace(workspace, ws_bytes, ssm_layout(a, f32, false, static_cast<char*>(workspace))));
     a.y = y; a.ht = ht;
-    REWY_TRY(hip_check(traced("k_ssm_gates", s, [&] { return launch_ssm_gates(a, s); }), "scan gates"));
+    REWY_TRY(hip_check(traced("k_ssm_prep", s, [&] { return launch_ssm_prep(a, f32, false, s); }), "scan preparation"));
     if (a.two) {
       REWY_TRY(hip_check(traced("k_ssm_state", s, [&] { return launch_ssm_state(a, f32, false, s); }), "segment states"));
       REWY_TRY(hip_check(traced("k_ssm_pass", s, [&] { return launch_ssm_pass(a, false, s); }), "segment pass"));
@@ -447,7 +460,7 @@ REWY_API int rewy_ssm_bwd(const rewy_ssm_desc* d, const void* x, const void* dt,
     a.dy = dy; a.dht = dht; a.dx = dx; a.ddt = ddt; a.da_log = da_log; a.ddt_bias = ddt_bias;
     a.db = db; a.dc = dc; a.dd = dD; a.dh0 = dh0;
     if (some) {
-      REWY_TRY(hip_check(traced("k_ssm_gates", s, [&] { return launch_ssm_gates(a, s); }), "scan gates"));
+      REWY_TRY(hip_check(traced("k_ssm_prep", s, [&] { return launch_ssm_prep(a, f32, true, s); }), "scan preparation"));
       if (a.two) {
         REWY_TRY(hip_check(traced("k_ssm_state", s, [&] { return launch_ssm_state(a, f32, true, s); }), "segment states"));
         REWY_TRY(hip_check(traced("k_ssm_pass", s, [&] { return launch_ssm_pass(a, true, s); }), "segment pass"));

@@ -14,9 +14,6 @@
 // sums into a parameter's gradient stays fp32.
 #include "ssm.hpp"
 
-#ifndef SSM_WAVES
-#define SSM_WAVES 4
-#endif
 namespace rewy {
 
 namespace {
@@ -26,11 +23,12 @@ namespace {
 // C_t); reverse: the adjoint that leaves each chunk goes to hd, and cx_t =
 // exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds 16 columns of one head.
 template <typename T, int K, int V, int HB>
-__global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
-  constexpr int CW = HB * V, NTH = 4 * CW, NW = CW / 16, LK = pitch<T>(K), LV = pitch<T>(CW);
-  constexpr int NT = K / 16, KQ = K / KG<T>, NS = SPLIT<T>, WH = V / 16;
+__global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
+  constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, NW = NTH / 64;
+  constexpr int LK = pitch<T>(K), LV = pitch<T>(CW), NQ = CH / KG<T>;
+  constexpr int NT = K / 16, KQ = K / KG<T>, NS = SPLIT<T>, WH = V / (16 * CT);  // waves of a head
   __shared__ __align__(16) T sk[CH * LK];  // update: B (forward), C (reverse)
-  __shared__ __align__(16) T sq[CH * LK];  // probe: C, B
+  __shared__ __align__(16) T sq[CH * LK];  // probe: C, B (columns in the slot order of frag_acc)
   __shared__ __align__(16) T su[CH * LV];  // update: x, dy
   __shared__ __align__(16) T sp[CH * LV];  // probe: dy, x
   __shared__ __align__(16) float sal[HB][CH], sdot[NW][CH];
@@ -43,7 +41,7 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
   const int gb = (a.per + HB - 1) / HB, grp = hb / gb, h0 = grp * a.per + (hb - grp * gb) * HB;
   const int nh = min(HB, (grp + 1) * a.per - h0);  // heads of this block
   const int nch = (t1 - t0 + CH - 1) / CH, w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15;
-  const int hw = w / WH, h = min(h0 + hw, h0 + nh - 1), pc0 = 16 * w - hw * V;
+  const int hw = w / WH, h = min(h0 + hw, h0 + nh - 1), pc0 = 16 * CT * w - hw * V;
   const bool live = hw < nh;
   const int cbase = slot_base(a.seq, pc.n, CH) + pc.k * (a.seg / CH);
   const int64_t seqst = ((int64_t)pc.n * a.H + h) * K * V + pc0 + r;
@@ -51,11 +49,13 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
   const float* given = dir ? a.dht : a.h0;
   // (an empty sequence has no segment of its own: its state is given through)
   const float* init = a.two && nch > 0 ? (dir ? a.sr : a.sf) + segst : given ? given + seqst : nullptr;
-  f32x4 S[NT];
+  f32x4 S[CT][NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[nt][i] = init ? init[(int64_t)(16 * nt + 4 * g4 + i) * V] : 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[ct][nt][i] = init ? init[(16 * nt + 4 * g4 + i) * V + 16 * ct] : 0.f;
   TileRegs<T, CH, K, NTH> rk, rq;
   TileRegs<T, CH, CW, NTH> ru, rp;
   Gate gt = {};
@@ -72,11 +72,11 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
   for (int c = 0; c < nch; ++c) {
     const int ci = dir ? nch - 1 - c : c, tok = t0 + ci * CH, len = min(CH, t1 - tok);
     rk.store(sk, LK, threadIdx.x);
-    rq.store(sq, LK, threadIdx.x);
+    store_acc_order<T, K, NTH>(rq, sq, LK);
     ru.store(su, LV, threadIdx.x);
     rp.store(sp, LV, threadIdx.x);
     float be = 0.f;
-    if (w < HB) {
+    if (w < nh) {
       const float eG = fexp2(gt.G), eE = fexp2(gt.E);
       sal[w][slot_of<T>(l)] = dir ? eG : eE * gt.dt;
       be = dir ? eE : eG;
@@ -85,32 +85,49 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
     lds_barrier();
     if (c + 1 < nch) fetch(c + 1);
     if (live) {
-      T* hp = hand + (((int64_t)(cbase + ci) * a.H + h) * WH + pc0 / 16) * (K * 16) + l * 4;
+      T* hp = hand + (((int64_t)(cbase + ci) * a.H + h) * (V / 16) + pc0 / 16) * (K * 16) + l * 4;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) st4<T>(hp + nt * 256, S[nt]);
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) st4<T>(hp + ct * K * 16 + nt * 256, S[ct][nt]);
     }
-    f32x4 Y[4];
+    f32x4 Y[CT][4];
 #pragma unroll
-    for (int I = 0; I < 4; ++I) Y[I] = zero4();
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int I = 0; I < 4; ++I) Y[ct][I] = zero4();
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
-      uint4 sf[NS];
-      frag_acc<T, NS>(sf, S, q);
+      uint4 sf[CT][NS];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) frag_acc<T, NS>(sf[ct], S[ct], q);
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        const uint4 qf = frag_row_acc<T>(sq, LK, 16 * I, q);
+        const uint4 qf = frag_row<T>(sq, LK, 16 * I, q * KG<T>);
 #pragma unroll
-        for (int s = NS - 1; s >= 0; --s) mma16B<T>(Y[I], sf[s], qf);
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int s = NS - 1; s >= 0; --s) mma16B<T>(Y[ct][I], sf[ct][s], qf);
       }
     }
-    // Y[I] holds columns t = 16 I + r, rows (columns of the state) 4 g4 + i
+    // Y[.][I] holds columns t = 16 I + r, rows (columns of the state) 4 g4 + i
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
-      const f32x4 u = ld4<T>(sp + (16 * I + r) * LV + 16 * w + 4 * g4);
-      const float d = rows_sum((Y[I][0] * u[0] + Y[I][1] * u[1]) + (Y[I][2] * u[2] + Y[I][3] * u[3]));
+      float d = 0.f;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const f32x4 u = ld4<T>(sp + (16 * I + r) * LV + 16 * (CT * w + ct) + 4 * g4);
+        d += (Y[ct][I][0] * u[0] + Y[ct][I][1] * u[1]) + (Y[ct][I][2] * u[2] + Y[ct][I][3] * u[3]);
+      }
+      d = rows_sum(d);
       if (g4 == I) sdot[w][16 * I + r] = d;
     }
-    state_update<T, K>(S, sk, LK, su, LV, 16 * w, sal[hw], sdec[hw]);
+    uint4 ut[CT][NQ];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) ut[ct][q] = frag_col<T>(su, LV, q * KG<T>, 16 * (CT * w + ct));
+    state_update<T, K, CT, NS>(S, sk, LK, ut, sal[hw], sdec[hw]);
     lds_barrier();  // dots complete, tiles free
     if (w < nh && l < len) {
       float d = 0.f;
@@ -123,11 +140,14 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
     // <S, dS> at the segment's end
     const float* adj = a.two && nch > 0 ? a.sr + segst : a.dht ? a.dht + seqst : nullptr;
     float d = 0.f;
+    if (adj) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (adj) d += S[nt][i] * adj[(int64_t)(16 * nt + 4 * g4 + i) * V];
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d += S[ct][nt][i] * adj[(16 * nt + 4 * g4 + i) * V + 16 * ct];
+    }
     d = rows_sum(row16_sum(d));
     if (l == 0) sred[w] = d;
     lds_barrier();
@@ -137,10 +157,13 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_walk(SsmArgs a) {
       a.ends[(int64_t)slot * a.H + h0 + w] = d;
     }
   } else if (a.dh0 && live && pc.k == 0) {
+    float* o = a.dh0 + seqst;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a.dh0[seqst + (int64_t)(16 * nt + 4 * g4 + i) * V] = S[nt][i];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[(16 * nt + 4 * g4 + i) * V + 16 * ct] = S[ct][nt][i];
   }
 }
 
@@ -219,14 +242,8 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   f32x4 cb[NB], wsum[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    cb[b] = wsum[b] = zero4();
-    const int blk = b * CB_WAVES + w;
-    if (blk < 10) {
-      const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
-#pragma unroll
-      for (int q = 0; q < KQ; ++q)
-        mma16B<T>(cb[b], frag_row_slot<T>(sc, LK, 16 * I, q * KG<T>), frag_row<T>(sb, LK, 16 * J, q * KG<T>));
-    }
+    wsum[b] = zero4();
+    cb[b] = reinterpret_cast<const f32x4*>(a.cb)[((int64_t)(cslot * a.G + grp) * 10 + min(b * CB_WAVES + w, 9)) * 64 + l];
   }
   f32x4 dC[NTW], dB[NTW];
 #pragma unroll
@@ -253,7 +270,8 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
     for (int b = 0; b < NB; ++b) {
       const int blk = b * CB_WAVES + w;
       if (blk < 10) {
-        const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+        int I, J;
+        tri_block(blk, I, J);
         f32x4 p = zero4();
 #pragma unroll
         for (int q = 0; q < VQ; ++q)
@@ -360,7 +378,8 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   for (int b = 0; b < NB; ++b) {
     const int blk = b * CB_WAVES + w;
     if (blk < 10) {
-      const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+      int I, J;
+      tri_block(blk, I, J);
       st4<T>(sm + (16 * J + r) * LM + slot_base4<T>(I, g4), wsum[b]);
     }
   }
@@ -377,7 +396,8 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   for (int b = 0; b < NB; ++b) {
     const int blk = b * CB_WAVES + w;
     if (blk < 10) {
-      const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
+      int I, J;
+      tri_block(blk, I, J);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         T* p = sm + (16 * I + slot_row<T>(4 * g4 + e)) * LM;

@@ -3,16 +3,44 @@
 // form.
 #include "ssm.hpp"
 
-#ifndef SSM_WAVES
-#define SSM_WAVES 4
-#endif
 namespace rewy {
 
 namespace {
 
-// The gates of all chunks: one wave per chunk and head, lane t its token.
-__global__ __launch_bounds__(256) void k_ssm_gates(SsmArgs a) {
-  const int wk = blockIdx.x * 4 + wave_id(), t = lane_id();
+// What every walk of a call reads and no walk should form again.  Workgroups < ngate:
+// the gates, one wave per chunk and head, lane t its token.  The others: C B^T
+// of one chunk and group, the lower triangle's ten 16 x 16 blocks as C fragments,
+// shared by the heads of the group; forward: rows j in slot order, columns i
+// (what the coefficients' rows are made of); backward: rows i, columns j.
+template <typename T, int K>
+__global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int ngate, int bwd) {
+  const int t = lane_id(), w = wave_id();
+  if ((int)blockIdx.x >= ngate) {
+    const int wk = blockIdx.x - ngate, cslot = wk / a.G, grp = wk - cslot * a.G;
+    const Piece pc = find_piece(a.seq, cslot, CH);
+    const int tok = pc.bos + pc.k * CH, len = min(CH, pc.eos - tok);
+    if (!pc.on || len <= 0) return;
+    const T* bp = reinterpret_cast<const T*>(a.b) + (int64_t)tok * a.bs + grp * K;
+    const T* cp = reinterpret_cast<const T*>(a.c) + (int64_t)tok * a.cs + grp * K;
+    const GBuf gb = gbuf(bp, tile_bytes<T>(len, a.bs, K)), gc = gbuf(cp, tile_bytes<T>(len, a.cs, K));
+    for (int blk = w; blk < 10; blk += 4) {
+      int I, J;
+      tri_block(blk, I, J);
+      const int r = t & 15, k0 = VEC<T> * (t >> 4);
+      const int i = 16 * I + (bwd ? slot_row<T>(r) : r), j = 16 * J + (bwd ? r : slot_row<T>(r));
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int q = 0; q < K / KG<T>; ++q) {
+        const uint4 bf = gld16(gb, (uint32_t)((j * a.bs + k0 + q * KG<T>) * (int64_t)sizeof(T)));
+        const uint4 cf = gld16(gc, (uint32_t)((i * a.cs + k0 + q * KG<T>) * (int64_t)sizeof(T)));
+        if (bwd) mma16B<T>(acc, cf, bf);
+        else mma16B<T>(acc, bf, cf);
+      }
+      reinterpret_cast<f32x4*>(a.cb)[((int64_t)wk * 10 + blk) * 64 + t] = acc;
+    }
+    return;
+  }
+  const int wk = blockIdx.x * 4 + w;
   if (wk >= a.nchunk * a.H) return;
   const int cslot = wk / a.H, h = wk - cslot * a.H;
   const Piece pc = find_piece(a.seq, cslot, CH);
@@ -36,9 +64,10 @@ __global__ __launch_bounds__(256) void k_ssm_gates(SsmArgs a) {
 // Local state of one segment and HB heads: forward (dir 0), from zero, all but a
 // sequence's last segment; reverse (dir 1), the adjoint that the segment's own
 // tokens send to the state that enters it, all but the first.
-template <typename T, int K, int V, int HB>
-__global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_state(SsmArgs a) {
-  constexpr int CW = HB * V, NTH = 4 * CW, LK = pitch<T>(K), LV = pitch<T>(CW);
+template <typename T, int K, int V, int HB, int NS>
+__global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_state(SsmArgs a) {
+  constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, LK = pitch<T>(K), LV = pitch<T>(CW);
+  constexpr int NQ = CH / KG<T>, NT = K / 16;
   __shared__ __align__(16) T sk[CH * LK];
   __shared__ __align__(16) T su[CH * LV];
   __shared__ __align__(16) float sal[HB][CH];
@@ -51,11 +80,13 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_state(SsmArgs a) 
   if (dir == 0 ? t1 >= pc.eos : pc.k == 0) return;
   const int gb = (a.per + HB - 1) / HB, grp = hb / gb, h0 = grp * a.per + (hb - grp * gb) * HB;
   const int nh = min(HB, (grp + 1) * a.per - h0);  // heads of this block
-  const int nch = (t1 - t0 + CH - 1) / CH, w = wave_id(), l = lane_id(), hw = 16 * w / V;
+  const int nch = (t1 - t0 + CH - 1) / CH, w = wave_id(), l = lane_id(), hw = 16 * CT * w / V;
   const int cbase = slot_base(a.seq, pc.n, CH) + pc.k * (a.seg / CH);
-  f32x4 S[K / 16];
+  f32x4 S[CT][NT];
 #pragma unroll
-  for (int i = 0; i < K / 16; ++i) S[i] = zero4();
+  for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) S[ct][i] = zero4();
   float gs = 0.f;
   TileRegs<T, CH, K, NTH> rk;
   TileRegs<T, CH, CW, NTH> ru;
@@ -70,24 +101,31 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_state(SsmArgs a) 
   for (int c = 0; c < nch; ++c) {
     rk.store(sk, LK, threadIdx.x);
     ru.store(su, LV, threadIdx.x);
-    if (w < HB) {
+    if (w < nh) {
       sal[w][slot_of<T>(l)] = dir ? fexp2(gt.G) : fexp2(gt.E) * gt.dt;
       if (l == 63) sdec[w] = fexp2(gt.G);
       gs += gt.G;
     }
     lds_barrier();
     if (c + 1 < nch) fetch(c + 1);
-    state_update<T, K>(S, sk, LK, su, LV, 16 * w, sal[hw], sdec[hw]);
+    uint4 ut[CT][NQ];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) ut[ct][q] = frag_col<T>(su, LV, q * KG<T>, 16 * (CT * w + ct));
+    state_update<T, K, CT, NS>(S, sk, LK, ut, sal[hw], sdec[hw]);
     lds_barrier();
   }
   // (forward and reverse sum the same decays, each for the segments it takes)
   if (w < nh && l == 63) a.gsum[((int64_t)dir * a.nslot + slot) * a.H + h0 + w] = gs;
   if (hw >= nh) return;
-  float* o = (dir ? a.sr : a.sf) + ((int64_t)slot * a.H + h0 + hw) * K * V + 16 * w - hw * V + (l & 15);
+  float* o = (dir ? a.sr : a.sf) + ((int64_t)slot * a.H + h0 + hw) * K * V + 16 * CT * w - hw * V + (l & 15);
 #pragma unroll
-  for (int nt = 0; nt < K / 16; ++nt)
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[(int64_t)(16 * nt + 4 * (l >> 4) + i) * V] = S[nt][i];
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[(16 * nt + 4 * (l >> 4) + i) * V + 16 * ct] = S[ct][nt][i];
 }
 
 // In place: the local states of a sequence's segments become the states that
@@ -121,19 +159,24 @@ __global__ __launch_bounds__(256) void k_ssm_pass(SsmArgs a) {
 }
 
 // The walk of one segment and HB heads.  Wave w owns 16 columns of y and of the
-// state; the chunk's coefficients M, one 64 x 64 matrix a head, are formed block
-// by block by all waves (C B^T once for the heads) and shared through LDS.
-template <typename T, int K, int V, int HB>
-__global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_fwd(SsmArgs a) {
-  constexpr int CW = HB * V, NTH = 4 * CW, NW = CW / 16, LK = pitch<T>(K), LV = pitch<T>(CW), LM = pitch<T>(CH);
-  constexpr int NQ = CH / KG<T>, NT = K / 16, KQ = K / KG<T>;
+// state (with CT = 2, 32: a fragment read from LDS serves two products).  A chunk's
+// coefficients M (one 64 x 64 matrix a head, from C B^T and the gates, which are a
+// chunk ahead) are formed block by block by all waves and shared through LDS.  Two
+// barriers a chunk: tiles and M complete; tiles and M free.  y leaves through
+// the x tile, whole rows at a time.
+template <typename T, int K, int V, int HB, int CT, int NS>
+__global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
+  constexpr int CW = HB * V, NTH = 4 * CW / CT, NW = NTH / 64;
+  constexpr int LK = pitch<T>(K), LV = pitch<T>(CW), LM = pitch<T>(CH);
+  constexpr int NQ = CH / KG<T>, NT = K / 16, KQ = K / KG<T>, NB = (10 + NW - 1) / NW;
   __shared__ __align__(16) T sb[CH * LK];
-  __shared__ __align__(16) T sc[CH * LK];
+  __shared__ __align__(16) T sc[CH * LK];  // columns in the slot order of frag_acc
   __shared__ __align__(16) T sx[CH * LV];
   __shared__ __align__(16) T sm[HB][CH * LM];  // columns in slot order
-  // gates of each head: by token, and in slot order
-  __shared__ __align__(16) float sG[HB][CH], sGl[HB][CH], seq[HB][CH], tG[HB][CH], tGl[HB][CH], tdt[HB][CH], sal[HB][CH];
-  __shared__ float sdec[HB];
+  // gates of each head: by token, and (t) in slot order
+  __shared__ __align__(16) float sG[2][HB][CH], sGl[2][HB][CH], tG[2][HB][CH], tGl[2][HB][CH], tdt[2][HB][CH];
+  __shared__ __align__(16) float seq[2][HB][CH], sal[2][HB][CH];
+  __shared__ float sdec[2][HB];
   const int nhb = head_blocks(a, HB), wk = xcd_range(blockIdx.x, a.nslot * nhb), slot = wk / nhb, hb = wk - slot * nhb;
   const Piece pc = find_piece(a.seq, slot, a.seg);
   if (!pc.on) return;
@@ -141,7 +184,7 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_fwd(SsmArgs a) {
   const int gb = (a.per + HB - 1) / HB, grp = hb / gb, h0 = grp * a.per + (hb - grp * gb) * HB;
   const int nh = min(HB, (grp + 1) * a.per - h0);  // heads of this block
   const int nch = (t1 - t0 + CH - 1) / CH, w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15;
-  const int hw = 16 * w / V, h = min(h0 + hw, h0 + nh - 1), pc0 = 16 * w - hw * V;  // the wave's head, its columns
+  const int hw = 16 * CT * w / V, h = min(h0 + hw, h0 + nh - 1), pc0 = 16 * CT * w - hw * V;  // the wave's head, its columns
   const bool live = hw < nh;
   const int cbase = slot_base(a.seq, pc.n, CH) + pc.k * (a.seg / CH);
   const float D = a.d ? a.d[h] : 0.f;
@@ -150,111 +193,160 @@ __global__ __launch_bounds__(4 * HB * V, SSM_WAVES) void k_ssm_fwd(SsmArgs a) {
   const float* init = a.two && nch > 0 ? a.sf + ((int64_t)slot * a.H + h) * K * V + pc0 + r
                       : a.h0           ? a.h0 + head
                                        : nullptr;
-  f32x4 S[NT];
+  f32x4 S[CT][NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[nt][i] = init ? init[(int64_t)(16 * nt + 4 * g4 + i) * V] : 0.f;
-  // a pair of blocks above the diagonal lies inside a contraction of 32: zeros, written once
-  for (int i = threadIdx.x; i < HB * CH * LM; i += NTH) sm[0][i] = (T)0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[ct][nt][i] = init ? init[(16 * nt + 4 * g4 + i) * V + 16 * ct] : 0.f;
 
   TileRegs<T, CH, K, NTH> rb, rc;
   TileRegs<T, CH, CW, NTH> rx;
-  Gate gt = {};
+  f32x4 rcb[NB];
   auto fetch = [&](int c) {
     const int tok = t0 + c * CH, len = min(CH, t1 - tok);
-    if (w < nh) gt = chunk_gates(a, cbase + c, h0 + w)[l];
     load_tile<T, K, NTH>(rb, a.b, tok, a.bs, grp * K, len, K);
     load_tile<T, K, NTH>(rc, a.c, tok, a.cs, grp * K, len, K);
     load_tile<T, CW, NTH>(rx, a.x, tok, a.xs, h0 * V, len, nh * V);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      rcb[b] = reinterpret_cast<const f32x4*>(a.cb)[((int64_t)((cbase + c) * a.G + grp) * 10 + min(b * NW + w, 9)) * 64 + l];
   };
-  if (nch > 0) fetch(0);
-  for (int c = 0; c < nch; ++c) {
-    const int tok = t0 + c * CH, len = min(CH, t1 - tok);
+  auto put_tiles = [&]() {
     rb.store(sb, LK, threadIdx.x);
-    rc.store(sc, LK, threadIdx.x);
+    store_acc_order<T, K, NTH>(rc, sc, LK);
     rx.store(sx, LV, threadIdx.x);
-    if (w < HB) {
-      const float eG = fexp2(gt.G);
-      const int sl = slot_of<T>(l);
-      sG[w][l] = gt.G;
-      sGl[w][l] = gt.Glo;
-      seq[w][l] = eG;
-      tG[w][sl] = gt.G;
-      tGl[w][sl] = gt.Glo;
-      tdt[w][sl] = gt.dt;
-      sal[w][sl] = fexp2(gt.E) * gt.dt;
-      if (l == 63) sdec[w] = eG;
-    }
-    lds_barrier();
-    if (c + 1 < nch) fetch(c + 1);
-    // coefficients: block (I, J) of the lower triangle, as its transpose (rows j in
-    // slot order, columns i), so that a lane holds four neighbours of a row of M
+  };
+  auto put_gates = [&](const Gate& gt, int p) {
+    const int sl = slot_of<T>(l);
+    const float eG = fexp2(gt.G);
+    sG[p][w][l] = tG[p][w][sl] = gt.G;
+    sGl[p][w][l] = tGl[p][w][sl] = gt.Glo;
+    tdt[p][w][sl] = gt.dt;
+    seq[p][w][l] = eG;
+    sal[p][w][sl] = fexp2(gt.E) * gt.dt;
+    if (l == 63) sdec[p][w] = eG;
+  };
+  // coefficients of the chunk whose C B^T is in rcb, gates in set p: block (I, J) as its
+  // transpose (rows j in slot order, columns i), so that a lane holds four neighbours
+  // of a row of M
+  auto put_coefficients = [&](int p) {
 #pragma unroll
-    for (int b0 = 0; b0 < 10; b0 += NW) {
-      const int blk = b0 + w;
+    for (int b = 0; b < NB; ++b) {
+      const int blk = b * NW + w;
       if (blk < 10) {
-        const int I = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, J = blk - I * (I + 1) / 2;
-        f32x4 acc = zero4();
-#pragma unroll
-        for (int q = 0; q < KQ; ++q)
-          mma16B<T>(acc, frag_row_slot<T>(sb, LK, 16 * J, q * KG<T>), frag_row<T>(sc, LK, 16 * I, q * KG<T>));
+        int I, J;
+        tri_block(blk, I, J);
         const int i = 16 * I + r, sl = slot_base4<T>(J, g4);
 #pragma unroll
         for (int k = 0; k < HB; ++k) {
-          const float Gi = sG[k][i], Gil = sGl[k][i];
-          const f32x4 Gj = *reinterpret_cast<const f32x4*>(tG[k] + sl), Gjl = *reinterpret_cast<const f32x4*>(tGl[k] + sl);
-          const f32x4 dj = *reinterpret_cast<const f32x4*>(tdt[k] + sl);
+          const float Gi = sG[p][k][i], Gil = sGl[p][k][i];
+          const f32x4 Gj = *reinterpret_cast<const f32x4*>(tG[p][k] + sl), Gjl = *reinterpret_cast<const f32x4*>(tGl[p][k] + sl);
+          const f32x4 dj = *reinterpret_cast<const f32x4*>(tdt[p][k] + sl);
           f32x4 m;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            m[e] = 16 * J + slot_row<T>(4 * g4 + e) <= i ? acc[e] * fexp2((Gi - Gj[e]) + (Gil - Gjl[e])) * dj[e] : 0.f;
+            m[e] = 16 * J + slot_row<T>(4 * g4 + e) <= i ? rcb[b][e] * fexp2((Gi - Gj[e]) + (Gil - Gjl[e])) * dj[e] : 0.f;
           st4<T>(sm[k] + i * LM + sl, m);
         }
       }
     }
+  };
+  const bool gater = w < nh;
+  Gate gt = {};
+  if (nch > 0) {
+    fetch(0);
+    if (gater) {
+      put_gates(chunk_gates(a, cbase, h0 + w)[l], 0);
+      if (nch > 1) put_gates(chunk_gates(a, cbase + 1, h0 + w)[l], 1);
+    }
+    // a pair of blocks above the diagonal lies inside a contraction of 32: zeros, written once
+    for (int i = threadIdx.x; i < HB * CH * LM; i += NTH) sm[0][i] = (T)0.f;
+    lds_barrier();
+    put_coefficients(0);
+    put_tiles();
+  }
+  for (int c = 0; c < nch; ++c) {
+    const int tok = t0 + c * CH, len = min(CH, t1 - tok), p = c & 1;
+    lds_barrier();  // tiles, coefficients and gates complete
+    if (c + 1 < nch) fetch(c + 1);
+    if (gater && c + 2 < nch) gt = chunk_gates(a, cbase + c + 2, h0 + w)[l];
     // entering state: Y^T = S^T C^T, columns scaled by exp(G)
-    f32x4 Y[4];
+    f32x4 Y[CT][4];
 #pragma unroll
-    for (int I = 0; I < 4; ++I) Y[I] = zero4();
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int I = 0; I < 4; ++I) Y[ct][I] = zero4();
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
-      uint4 sf[1];
-      frag_acc<T, 1>(sf, S, q);
+      uint4 sf[CT][1];
 #pragma unroll
-      for (int I = 0; I < 4; ++I) mma16B<T>(Y[I], sf[0], frag_row_acc<T>(sc, LK, 16 * I, q));
+      for (int ct = 0; ct < CT; ++ct) frag_acc<T, 1>(sf[ct], S[ct], q);
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        const uint4 cf = frag_row<T>(sc, LK, 16 * I, q * KG<T>);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) mma16B<T>(Y[ct][I], sf[ct][0], cf);
+      }
     }
+    T* xw = sx + r * LV + 16 * CT * w + 4 * g4;  // the wave's own columns of the x tile
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
-      const float e = seq[hw][16 * I + r];
+      const float e = seq[p][hw][16 * I + r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) Y[I][i] *= e;
+      for (int ct = 0; ct < CT; ++ct) {
+        const f32x4 xv = ld4<T>(xw + 16 * I * LV + 16 * ct);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Y[ct][I][i] = Y[ct][I][i] * e + D * xv[i];
+      }
     }
-    lds_barrier();  // M complete
+    uint4 xt[CT][NQ];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const uint4 xt = frag_col<T>(sx, LV, q * KG<T>, 16 * w);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) xt[ct][q] = frag_col<T>(sx, LV, q * KG<T>, 16 * (CT * w + ct));
 #pragma unroll
       for (int I = 0; I < 4; ++I)
-        if (q * KG<T> <= 16 * I) mma16B<T>(Y[I], xt, frag_row<T>(sm[hw], LM, 16 * I, q * KG<T>));
-    }
+        if (q * KG<T> <= 16 * I) {
+          const uint4 mf = frag_row<T>(sm[hw], LM, 16 * I, q * KG<T>);
 #pragma unroll
-    for (int I = 0; I < 4; ++I) {
-      const int t = 16 * I + r;
-      const f32x4 xv = ld4<T>(sx + t * LV + 16 * w + 4 * g4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) Y[I][i] += D * xv[i];
-      if (live && t < len)
-        st4<T>(reinterpret_cast<T*>(a.y) + (int64_t)(tok + t) * a.ys + h * V + pc0 + 4 * g4, Y[I]);
+          for (int ct = 0; ct < CT; ++ct) mma16B<T>(Y[ct][I], xt[ct][q], mf);
+        }
     }
-    state_update<T, K>(S, sb, LK, sx, LV, 16 * w, sal[hw], sdec[hw]);
-    lds_barrier();  // tiles free
+    // (read above, and by no other wave)
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) st4<T>(xw + 16 * I * LV + 16 * ct, Y[ct][I]);
+    state_update<T, K, CT, NS>(S, sb, LK, xt, sal[p][hw], sdec[p][hw]);
+    lds_barrier();  // tiles and coefficients free, y complete
+    {
+      // each thread takes y from where its pieces of the next x tile go
+      using TR = TileRegs<T, CH, CW, NTH>;
+      const GBuf gy = gbuf(reinterpret_cast<T*>(a.y) + (int64_t)tok * a.ys + h0 * V, tile_bytes<T>(len, a.ys, nh * V));
+#pragma unroll
+      for (int j = 0; j < TR::N; ++j) {
+        const int idx = threadIdx.x + j * NTH, row = idx / TR::PER, col = (idx - row * TR::PER) * TR::VEC;
+        if (idx < TR::TOTAL)
+          gst16(gy, col < nh * V ? (uint32_t)((row * a.ys + col) * (int64_t)sizeof(T)) : OOB,
+                *reinterpret_cast<const uint4*>(sx + row * LV + col));
+      }
+    }
+    if (c + 1 < nch) {
+      put_tiles();
+      put_coefficients(p ^ 1);
+    }
+    if (gater && c + 2 < nch) put_gates(gt, p);
   }
   if (a.ht && live && t1 >= pc.eos) {
+    float* o = a.ht + head;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a.ht[head + (int64_t)(16 * nt + 4 * g4 + i) * V] = S[nt][i];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[(16 * nt + 4 * g4 + i) * V + 16 * ct] = S[ct][nt][i];
   }
 }
 
@@ -324,9 +416,14 @@ __global__ __launch_bounds__(256) void k_ssm_recurrent(SsmArgs a) {
 
 }  // namespace
 
-hipError_t launch_ssm_gates(const SsmArgs& a, hipStream_t s) {
-  REWY_LAUNCH(k_ssm_gates, dim3((a.nchunk * a.H + 3) / 4), dim3(256), s, a);
-  return hipGetLastError();
+hipError_t launch_ssm_prep(const SsmArgs& a, bool f32, bool bwd, hipStream_t s) {
+  return ssm_kv(a.K, 32, f32, [&](auto t, auto k, auto) {
+    using T = decltype(t);
+    constexpr int K = decltype(k)::value;
+    const int ngate = (a.nchunk * a.H + 3) / 4;
+    REWY_LAUNCH((k_ssm_prep<T, K>), dim3(ngate + a.nchunk * a.G), dim3(256), s, a, ngate, (int)bwd);
+    return hipGetLastError();
+  });
 }
 int ssm_head_blocks(const SsmArgs& a, int hb) { return a.G * ((a.per + hb - 1) / hb); }
 
@@ -334,7 +431,9 @@ hipError_t launch_ssm_state(const SsmArgs& a, bool f32, bool both, hipStream_t s
   return ssm_kv_heads(a, f32, [&](auto t, auto k, auto v, auto hb) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
-    REWY_LAUNCH((k_ssm_state<T, K, V, HB>), dim3(a.nslot * ssm_head_blocks(a, HB), both ? 2 : 1), dim3(4 * HB * V), s, a);
+    const dim3 grid(a.nslot * ssm_head_blocks(a, HB), both ? 2 : 1), block(4 * HB * V);
+    if (both || a.ht) REWY_LAUNCH((k_ssm_state<T, K, V, HB, SPLIT<T>>), grid, block, s, a);
+    else REWY_LAUNCH((k_ssm_state<T, K, V, HB, SPLIT_Y<T>>), grid, block, s, a);
     return hipGetLastError();
   });
 }
@@ -346,7 +445,10 @@ hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s) {
   return ssm_kv_heads(a, f32, [&](auto t, auto k, auto v, auto hb) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
-    REWY_LAUNCH((k_ssm_fwd<T, K, V, HB>), dim3(a.nslot * ssm_head_blocks(a, HB)), dim3(4 * HB * V), s, a);
+    constexpr int CT = V == 128 ? 2 : 1;
+    const dim3 grid(a.nslot * ssm_head_blocks(a, HB)), block(4 * HB * V / CT);
+    if (a.ht) REWY_LAUNCH((k_ssm_fwd<T, K, V, HB, CT, SPLIT<T>>), grid, block, s, a);
+    else REWY_LAUNCH((k_ssm_fwd<T, K, V, HB, CT, SPLIT_Y<T>>), grid, block, s, a);
     return hipGetLastError();
   });
 }

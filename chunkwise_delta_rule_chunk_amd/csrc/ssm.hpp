@@ -48,6 +48,7 @@ struct SsmArgs {
   float* dh0;
   // workspace
   void* gates;             // [nchunk, H, 64] Gate
+  float* cb;               // [nchunk, G, 10, 64 lanes, 4] C B^T, blocks of the lower triangle as C fragments
   float* sf;               // [nslot, H, K, V] local end states, then the states that enter the segments
   float* sr;               // [nslot, H, K, V] local adjoints, then the adjoints of the states that leave them
   float* gsum;             // [nslot, H] sum of g (log2 units) over a segment
@@ -65,7 +66,7 @@ struct SsmArgs {
 };
 
 int ssm_head_blocks(const SsmArgs& a, int hb);
-hipError_t launch_ssm_gates(const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_prep(const SsmArgs& a, bool f32, bool bwd, hipStream_t s);
 hipError_t launch_ssm_state(const SsmArgs& a, bool f32, bool both, hipStream_t s);
 hipError_t launch_ssm_pass(const SsmArgs& a, bool both, hipStream_t s);
 hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s);
@@ -77,21 +78,26 @@ hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_recurrent(const SsmArgs& a, bool f32, hipStream_t s);
 
 // ---- slots --------------------------------------------------------------------
-// Pieces of L tokens of every sequence, numbered without a table: the pieces of
-// sequence n take the slots start(n) / L + n, + 1, ...  Slots of different
-// sequences never meet (a sequence of len tokens moves start / L by at least
-// ceil(len / L) - 1), every sequence has at least one, and there are at most
-// total / L + N.
+// Pieces of L tokens of every sequence, numbered without a table.  Sequences of
+// one length take ceil(T / L) slots each (at least one), all in use.  Packed ones: the
+// pieces of sequence n take the slots start(n) / L + n, + 1, ...  Slots of
+// different sequences never meet (a sequence of len tokens moves start / L by at
+// least ceil(len / L) - 1), every sequence has at least one, and there are at
+// most total / L + N.
 struct Piece {
   int n;         // sequence
   int bos, eos;  // its tokens
   int k;         // piece of the sequence
   bool on;       // the slot is used
 };
-__device__ __forceinline__ int slot_base(const SeqArgs& q, int n, int L) { return seq_start(q, n) / L + n; }
+__device__ __forceinline__ int slots_each(const SeqArgs& q, int L) { return max((q.T + L - 1) / L, 1); }
+__device__ __forceinline__ int slot_base(const SeqArgs& q, int n, int L) {
+  return q.cu ? seq_start(q, n) / L + n : n * slots_each(q, L);
+}
 __device__ __forceinline__ Piece find_piece(const SeqArgs& q, int slot, int L) {
   int lo = 0, hi = q.N - 1;
-  while (lo < hi) {
+  if (!q.cu) lo = min(slot / slots_each(q, L), hi);
+  while (q.cu && lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (slot_base(q, mid, L) <= slot) lo = mid;
     else hi = mid - 1;
@@ -117,7 +123,7 @@ __device__ __forceinline__ int xcd_range(int b, int n) {
 // softplus at full fp32 precision (small steps dt matter relative to themselves)
 __device__ __forceinline__ float softplus_full(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
-// The gates of one token, formed once per call by k_ssm_gates and read by every
+// The gates of one token, formed once per call by k_ssm_prep and read by every
 // walk: dt, the chunk's inclusive prefix sum G of g (log2 units) and the
 // exclusive suffix sum E = G_L - G.  The sums are taken in 64 bits.  G is kept as
 // hi + lo, so that a difference G_i - G_j of neighbours is as exact after a long,
@@ -226,9 +232,13 @@ __device__ __forceinline__ void frag_get(float (&f)[VEC<T>], uint4 v) {
 }
 // An fp32 value that meets a 16-bit operand in a product whose sum is kept in fp32
 // (states, decay gradients) is given as the sum of SPLIT bf16 values, hi + mid +
-// lo: 24 bits, as many as fp32 has.  fp32 operands are one piece.
+// lo: 24 bits, as many as fp32 has.  Two (17 bits) do for a state that only a bf16
+// output reads (one would add as much error as the output's own rounding).  fp32
+// operands are one piece.
 template <typename T>
 constexpr int SPLIT = std::is_same_v<T, bf16> ? 3 : 1;
+template <typename T>
+constexpr int SPLIT_Y = std::is_same_v<T, bf16> ? 2 : 1;
 template <typename T, int NS>
 __device__ __forceinline__ void frag_split(uint4 (&out)[NS], const float (&f)[VEC<T>]) {
   if constexpr (std::is_same_v<T, bf16>) {
@@ -303,41 +313,72 @@ __device__ __forceinline__ void load_tile(TileRegs<T, CH, C, NTH>& r, const void
   r.load(gbuf(p, tile_bytes<T>(len, stride, cols)), stride, threadIdx.x);
 }
 
-// State update S = exp(G_L) S + sum_t K_t (al_t u_t)^T for the wave's 16 columns:
-// A operand K^T (columns of sk), B operand al u (columns of su, scaled and split;
-// sal holds al in slot order).
-template <typename T, int K>
-__device__ __forceinline__ void state_update(f32x4 (&S)[K / 16], const T* sk, int ldk, const T* su, int ldu, int c0,
-                                             const float* sal, float dec) {
-  constexpr int NQ = CH / KG<T>, VE = VEC<T>, NS = SPLIT<T>;
+// State update S = exp(G_L) S + sum_t K_t (al_t u_t)^T for the wave's CT tiles of 16
+// columns: A operand K^T (columns of sk, read once for the CT tiles), B operand al u
+// (ut: columns of the u tile; scaled and split; sal holds al in slot order).
+template <typename T, int K, int CT, int NS>
+__device__ __forceinline__ void state_update(f32x4 (&S)[CT][K / 16], const T* sk, int ldk,
+                                             const uint4 (&ut)[CT][CH / KG<T>], const float* sal, float dec) {
+  constexpr int NQ = CH / KG<T>, VE = VEC<T>;
   const int g = lane_id() >> 4;
 #pragma unroll
-  for (int nt = 0; nt < K / 16; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) S[nt][i] *= dec;
-#pragma unroll
   for (int q = 0; q < NQ; ++q) {
-    uint4 uf[NS];
-    float f[VE];
-    frag_get<T>(f, frag_col<T>(su, ldu, q * KG<T>, c0));
+    uint4 uf[CT][NS];
 #pragma unroll
-    for (int e = 0; e < VE; e += 4) {
-      const f32x4 al = *reinterpret_cast<const f32x4*>(sal + q * KG<T> + VE * g + e);
+    for (int ct = 0; ct < CT; ++ct) {
+      float f[VE];
+      frag_get<T>(f, ut[ct][q]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[e + i] *= al[i];
+      for (int e = 0; e < VE; e += 4) {
+        const f32x4 al = *reinterpret_cast<const f32x4*>(sal + q * KG<T> + VE * g + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[e + i] *= al[i];
+      }
+      frag_split<T, NS>(uf[ct], f);
     }
-    frag_split<T, NS>(uf, f);
 #pragma unroll
     for (int nt = 0; nt < K / 16; ++nt) {
       const uint4 kf = frag_col<T>(sk, ldk, q * KG<T>, 16 * nt);
 #pragma unroll
-      for (int s = NS - 1; s >= 0; --s) mma16B<T>(S[nt], kf, uf[s]);
+      for (int ct = 0; ct < CT; ++ct) {
+        if (q == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[ct][nt][i] *= dec;
+        }
+#pragma unroll
+        for (int s = NS - 1; s >= 0; --s) mma16B<T>(S[ct][nt], kf, uf[ct][s]);
+      }
     }
   }
 }
 
-// Heads side by side in one workgroup of the walks: with eight waves of 16 columns
-// (fp32: four) as many heads of a group as fit share its B and C tiles.
+// Block b = 0 .. 9 of the lower triangle of 4 x 4 blocks, row by row.
+__device__ __forceinline__ void tri_block(int b, int& I, int& J) {
+  I = b >= 6 ? 3 : b >= 3 ? 2 : b >= 1 ? 1 : 0;
+  J = b - I * (I + 1) / 2;
+}
+
+// A tile into LDS with the columns of each 32 in the slot order of frag_acc, so that
+// frag_row gives the partner of a fragment made of C fragments (fp32: as they are).
+template <typename T, int C, int NTH>
+__device__ __forceinline__ void store_acc_order(const TileRegs<T, CH, C, NTH>& t, T* s, int ls) {
+  if constexpr (std::is_same_v<T, bf16>) {
+#pragma unroll
+    for (int j = 0; j < TileRegs<T, CH, C, NTH>::N; ++j) {
+      const int idx = threadIdx.x + j * NTH, row = idx / (C / 8), c = (idx - row * (C / 8)) * 8;
+      if (idx < TileRegs<T, CH, C, NTH>::TOTAL) {
+        T* p = s + row * ls + (c & ~31) + 8 * ((c >> 2) & 3) + 4 * ((c >> 4) & 1);
+        *reinterpret_cast<uint2*>(p) = uint2{t.r[j].x, t.r[j].y};
+        *reinterpret_cast<uint2*>(p + 8) = uint2{t.r[j].z, t.r[j].w};
+      }
+    }
+  } else {
+    t.store(s, ls, threadIdx.x);
+  }
+}
+
+// Heads side by side in one workgroup of the walks: as many heads of a group as
+// fit in its columns share the B and C tiles.
 template <typename T>
 constexpr int WALK_COLS = std::is_same_v<T, bf16> ? 128 : 64;
 // blocks of HB heads of all groups

@@ -233,7 +233,7 @@ size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
     take(a.cd, tok);
     take(a.ends, (size_t)a.nslot * a.H * 4);
     take(a.dpart, (size_t)a.nchunk * a.H * 4);
-    take(a.apart, (size_t)a.nslot * 2 * a.H * 4);
+    take(a.apart, (size_t)a.nchunk * 2 * a.H * 8);
     if (a.split > 1) take(a.bcpart, (size_t)2 * a.split * a.seq.total * a.G * a.K * 4);
   }
   return std::max<size_t>(off, ALIGN);

@@ -91,35 +91,32 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) st4<T>(hp + ct * K * 16 + nt * 256, S[ct][nt]);
     }
-    f32x4 Y[CT][4];
+    // The probe's sums decide the decay gradient's accuracy (its terms cancel), so
+    // they are kept in two accumulators, which halves the roundings that meet the large
+    // part: bf16: the leading piece of the state apart from the others; fp32: every
+    // other step.
+    f32x4 Y[2][4];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int I = 0; I < 4; ++I) Y[ct][I] = zero4();
+    for (int I = 0; I < 4; ++I) Y[0][I] = Y[1][I] = zero4();
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
-      uint4 sf[CT][NS];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) frag_acc<T, NS>(sf[ct], S[ct], q);
+      uint4 sf[NS];
+      frag_acc<T, NS>(sf, S[0], q);
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         const uint4 qf = frag_row<T>(sq, LK, 16 * I, q * KG<T>);
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int s = NS - 1; s >= 0; --s) mma16B<T>(Y[ct][I], sf[ct][s], qf);
+        for (int s = NS - 1; s >= 0; --s) mma16B<T>(Y[NS > 1 ? s > 0 : q & 1][I], sf[s], qf);
       }
     }
     // Y[.][I] holds columns t = 16 I + r, rows (columns of the state) 4 g4 + i
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
-      float d = 0.f;
+      const f32x4 u = ld4<T>(sp + (16 * I + r) * LV + 16 * w + 4 * g4);
+      float v[4];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const f32x4 u = ld4<T>(sp + (16 * I + r) * LV + 16 * (CT * w + ct) + 4 * g4);
-        d += (Y[ct][I][0] * u[0] + Y[ct][I][1] * u[1]) + (Y[ct][I][2] * u[2] + Y[ct][I][3] * u[3]);
-      }
-      d = rows_sum(d);
+      for (int i = 0; i < 4; ++i) v[i] = Y[0][I][i] * u[i] + Y[1][I][i] * u[i];
+      const float d = rows_sum((v[0] + v[1]) + (v[2] + v[3]));
       if (g4 == I) sdot[w][16 * I + r] = d;
     }
     uint4 ut[CT][NQ];
@@ -372,49 +369,60 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       }
     }
   }
-  // the heads' W: as W^T [j][i] for dB, then as W [i][j] for dC (columns in slot order)
-  lds_barrier();
+  // The heads' W: as W^T [j][i] for dB, then as W [i][j] for dC (columns in slot order);
+  // for bf16 in two pieces, as it is rounded once for all heads at little cost.
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int blk = b * CB_WAVES + w;
-    if (blk < 10) {
-      int I, J;
-      tri_block(blk, I, J);
-      st4<T>(sm + (16 * J + r) * LM + slot_base4<T>(I, g4), wsum[b]);
-    }
-  }
-  lds_barrier();
+  for (int piece = 0; piece < (std::is_same_v<T, bf16> ? 2 : 1); ++piece) {
+    lds_barrier();
 #pragma unroll
-  for (int q = 0; q < NQ; ++q)
-    if ((q + 1) * KG<T> > 16 * tb) {
-      const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row j, contraction i
+    for (int b = 0; b < NB; ++b) {
+      const int blk = b * CB_WAVES + w;
+      if (blk < 10) {
+        int I, J;
+        tri_block(blk, I, J);
+        if (piece) {
 #pragma unroll
-      for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dB[ni], wf, frag_col<T>(sc, LK, q * KG<T>, 16 * (half * NTW + ni)));
-    }
-  lds_barrier();
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int blk = b * CB_WAVES + w;
-    if (blk < 10) {
-      int I, J;
-      tri_block(blk, I, J);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        T* p = sm + (16 * I + slot_row<T>(4 * g4 + e)) * LM;
-        p[slot_of<T>(16 * J + r)] = (T)wsum[b][e];
-        // the block right of the diagonal that shares a contraction with it
-        if (I == J && (I & 1) == 0) p[slot_of<T>(16 * (J + 1) + r)] = (T)0.f;
+          for (int e = 0; e < 4; ++e) wsum[b][e] -= (float)(T)wsum[b][e];
+        }
+        T* p = sm + (16 * J + r) * LM;
+        st4<T>(p + slot_base4<T>(I, g4), wsum[b]);
+        // the block left of the diagonal that shares a contraction with it
+        if (I == J && (I & 1)) st4<T>(p + slot_base4<T>(I - 1, g4), zero4());
       }
     }
-  }
-  lds_barrier();
+    lds_barrier();
 #pragma unroll
-  for (int q = 0; q < NQ; ++q)
-    if (q * KG<T> <= 16 * tb) {
-      const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row i, contraction j
+    for (int q = 0; q < NQ; ++q)
+      if ((q + 1) * KG<T> > 16 * tb) {
+        const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row j, contraction i
 #pragma unroll
-      for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dC[ni], wf, frag_col<T>(sb, LK, q * KG<T>, 16 * (half * NTW + ni)));
+        for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dB[ni], wf, frag_col<T>(sc, LK, q * KG<T>, 16 * (half * NTW + ni)));
+      }
+    lds_barrier();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int blk = b * CB_WAVES + w;
+      if (blk < 10) {
+        int I, J;
+        tri_block(blk, I, J);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          T* p = sm + (16 * I + slot_row<T>(4 * g4 + e)) * LM;
+          p[slot_of<T>(16 * J + r)] = (T)wsum[b][e];
+          // the block right of the diagonal that shares a contraction with it
+          if (I == J && (I & 1) == 0) p[slot_of<T>(16 * (J + 1) + r)] = (T)0.f;
+        }
+      }
     }
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      if (q * KG<T> <= 16 * tb) {
+        const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row i, contraction j
+#pragma unroll
+        for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dC[ni], wf, frag_col<T>(sb, LK, q * KG<T>, 16 * (half * NTW + ni)));
+      }
+  }
 #pragma unroll
   for (int ni = 0; ni < NTW; ++ni) {
     const int n = 16 * (half * NTW + ni) + r;
@@ -436,79 +444,89 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   }
 }
 
-// Gate gradients of one segment and head, one wave: the suffix sums of r - dt c
-// from the segment's end, 64 tokens a step.
+// Gate gradients of one chunk and head, one wave, lane t its token: the suffix sum
+// of r - dt c over the chunk, then over the rest of its segment what the later
+// chunks add through the states, then <S, dS> at the segment's end.  (Over a whole
+// chunk the pairs inside it cancel, so of later chunks only the parts through
+// the states count.)
 __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
   const int wk = blockIdx.x * 4 + wave_id(), l = lane_id();
-  if (wk >= a.nslot * a.H) return;
-  const int slot = wk / a.H, h = wk - slot * a.H;
-  const Piece pc = find_piece(a.seq, slot, a.seg);
-  float dA = 0.f, db = 0.f;
-  if (pc.on) {
-    const int t0 = pc.bos + pc.k * a.seg, t1 = min(t0 + a.seg, pc.eos);
-    const int nch = (t1 - t0 + CH - 1) / CH;
-    const float A = -expf(a.a_log[h]), bias = gate_bias(a, h);
-    const int64_t row = (int64_t)h * a.seq.total;
-    float tail = t1 > t0 ? a.ends[(int64_t)slot * a.H + h] : 0.f;
-    for (int c = nch - 1; c >= 0; --c) {
-      const int t = t0 + c * CH + l;
-      const bool on = t < t1;
-      float dt = 0.f, cc = 0.f, diff = 0.f, cross = 0.f, z = 0.f;
-      if (on) {
-        z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
-        dt = softplus_full(z);
-        const float cx = a.cx[row + t], ci = a.ci[row + t];
-        cross = a.rx[row + t] - dt * cx;
-        diff = cross + (a.ri[row + t] - dt * ci);
-        cc = cx + ci + a.cd[row + t];
-      }
-      float s = diff;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const float u = __shfl_down(s, d, 64);
-        if (l + d < 64) s += u;
-      }
-      const float dg = s + tail;
-      // what the chunk adds for the earlier ones: over a whole chunk the pairs inside
-      // it cancel, so only the parts through the states are carried on
-      tail += rows_sum(row16_sum(cross));
-      if (on) {
-        const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
-        const float dz = (cc + A * dg) * sg;
-        st_beta(a.ddt, a.dt_f32, (int64_t)t * a.H + h, dz);
-        dA += dg * (A * dt);
-        db += dz;
-      }
-    }
+  if (wk >= a.nchunk * a.H) return;
+  const int cslot = wk / a.H, h = wk - cslot * a.H;
+  const Piece pc = find_piece(a.seq, cslot, CH);
+  const int t0 = pc.bos + pc.k * CH, per = a.seg / CH, k = pc.k / per;  // segment of the chunk
+  if (!pc.on || t0 >= pc.eos) {
+    if (l < 2) a.apart[((int64_t)cslot * 2 + l) * a.H + h] = 0.;
+    return;
   }
-  dA = rows_sum(row16_sum(dA));
-  db = rows_sum(row16_sum(db));
+  const int t1 = min(t0 + CH, pc.eos), t2 = min(pc.bos + (k + 1) * a.seg, pc.eos);
+  const int64_t row = (int64_t)h * a.seq.total;
+  const float bias = gate_bias(a, h);
+  // (sums in 64 bits: their terms cancel, and what they leave is summed once more
+  // over the tokens)
+  auto wave_sum = [](double v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
+    return v;
+  };
+  double rest = 0.;
+  const Gate* g = chunk_gates(a, cslot, h);
+  for (int t = t0 + CH + l, c = 1; c < per; ++c, t += CH)
+    if (t < t2) rest += (double)a.rx[row + t] - (double)chunk_gates(a, cslot + c, h)[l].dt * a.cx[row + t];
+  const double tail = a.ends[((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h] + wave_sum(rest);
+  const int t = t0 + l;
+  const bool on = t < t1;
+  float dt = 0.f, z = 0.f;
+  double cc = 0., s = 0.;
+  if (on) {
+    z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
+    dt = g[l].dt;
+    cc = (double)a.cx[row + t] + a.ci[row + t];
+    s = (double)a.rx[row + t] + a.ri[row + t] - dt * cc;
+    cc += a.cd[row + t];
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const double u = __shfl_down(s, d, 64);
+    if (l + d < 64) s += u;
+  }
+  double dA = 0., db = 0.;
+  if (on) {
+    const double A = -exp((double)a.a_log[h]), dg = s + tail;
+    const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
+    db = (cc + A * dg) * sg;
+    st_beta(a.ddt, a.dt_f32, (int64_t)t * a.H + h, (float)db);
+    dA = dg * (A * dt);
+  }
+  dA = wave_sum(dA);
+  db = wave_sum(db);
   if (l == 0) {
-    a.apart[((int64_t)slot * 2 + 0) * a.H + h] = dA;
-    a.apart[((int64_t)slot * 2 + 1) * a.H + h] = db;
+    a.apart[((int64_t)cslot * 2 + 0) * a.H + h] = dA;
+    a.apart[((int64_t)cslot * 2 + 1) * a.H + h] = db;
   }
 }
 
-// dA_log, ddt_bias [H] over the segments and dD [H] over the chunks; a chunk
-// slot that no sequence uses holds nothing and is skipped.
+// dA_log, ddt_bias and dD [H], sums over the chunks (of dD's a slot that no sequence
+// uses holds nothing and is skipped).
 __global__ __launch_bounds__(256) void k_ssm_params(SsmArgs a) {
-  __shared__ float buf[4];
+  __shared__ double buf[4];
   const int h = blockIdx.x, what = blockIdx.y;
-  float s = 0.f;
+  double s = 0.;
   if (what < 2) {
-    for (int i = threadIdx.x; i < a.nslot; i += 256) s += a.apart[((int64_t)i * 2 + what) * a.H + h];
+    for (int i = threadIdx.x; i < a.nchunk; i += 256) s += a.apart[((int64_t)i * 2 + what) * a.H + h];
   } else {
     for (int i = threadIdx.x; i < a.nchunk; i += 256) {
       const Piece pc = find_piece(a.seq, i, CH);
       if (pc.on && pc.bos + pc.k * CH < pc.eos) s += a.dpart[(int64_t)i * a.H + h];
     }
   }
-  s = rows_sum(row16_sum(s));
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d, 64);
   if (lane_id() == 0) buf[wave_id()] = s;
-  lds_barrier();
+  __syncthreads();
   if (threadIdx.x == 0) {
     float* o = what == 0 ? a.da_log : what == 1 ? a.ddt_bias : a.dd;
-    if (o) o[h] = (buf[0] + buf[1]) + (buf[2] + buf[3]);
+    if (o) o[h] = (float)((buf[0] + buf[1]) + (buf[2] + buf[3]));
   }
 }
 
@@ -551,7 +569,7 @@ hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s) {
   });
 }
 hipError_t launch_ssm_gate(const SsmArgs& a, hipStream_t s) {
-  REWY_LAUNCH(k_ssm_gate, dim3((a.nslot * a.H + 3) / 4), dim3(256), s, a);
+  REWY_LAUNCH(k_ssm_gate, dim3((a.nchunk * a.H + 3) / 4), dim3(256), s, a);
   return hipGetLastError();
 }
 hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s) {

@@ -61,7 +61,7 @@ struct SsmArgs {
   float* cd;               // [H, tokens] the term i = j, which belongs to c and cancels in the decay gradient
   float* ends;             // [nslot, H] <state, adjoint> at each segment's end
   float* dpart;            // [nchunk, H] partial sums of dD
-  float* apart;            // [nslot, 2, H] partial sums of dA_log and ddt_bias
+  double* apart;           // [nchunk, 2, H] partial sums of dA_log and ddt_bias
   float* bcpart;           // [2, split, tokens, G, K] partial sums of dB and dC (split > 1)
 };
 

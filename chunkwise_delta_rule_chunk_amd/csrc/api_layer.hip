@@ -114,7 +114,7 @@ int conv_args(const rewy_conv_desc* d, ConvArgs& a) {
   REWY_TRY(check_stride("x_stride", d->x_stride, d->D, a.xs));
   REWY_TRY(check_stride("y_stride", d->y_stride, d->D, a.ys));
   REWY_TRY(check_stride("dx_stride", d->dx_stride, d->D, a.dxs));
-  conv_bwd_shape(a.seq.total, a.D, d->dtype == REWY_F32, a.run, a.tiles);
+  conv_bwd_shape(a.seq.total, a.D, a.run, a.tiles);
   return REWY_OK;
 }
 size_t conv_ws(const ConvArgs& a) { return up(std::max<size_t>((size_t)a.tiles * (a.W + 1) * a.D * 4, 1)); }

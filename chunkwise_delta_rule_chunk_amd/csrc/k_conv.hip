@@ -9,7 +9,8 @@
 //
 // Memory is all it costs.  A lane owns VE channels (16 bytes) and walks a run
 // of tokens with the last W - 1 rows in registers, so each row is read once
-// per run plus W - 1 rows at its start.  Tokens are packed; a run that meets
+// per run plus W - 1 rows at its start.  Workgroups that follow each other share
+// their tokens, so whole rows are streamed.  Tokens are packed; a run that meets
 // the end of a sequence takes up the next one's state.
 #include "layer.hpp"
 
@@ -17,7 +18,7 @@ namespace rewy {
 
 namespace {
 
-constexpr int CONV_WAVES = 4;  // runs (waves) of one block, side by side along the tokens
+constexpr int CONV_WAVES = 1;  // waves of one workgroup, side by side along the channels
 
 __device__ __forceinline__ float silu(float z) { return z * sigmoid_f(z); }
 
@@ -33,14 +34,18 @@ __device__ __forceinline__ int seq_of(const SeqArgs& q, int t) {
   return lo;
 }
 
+// Channels of a lane: 16 bytes of a row, in the backward at most four (its windows and
+// sums fill the registers).
+template <typename T, bool BWD>
+constexpr int CVE = BWD ? 4 : Vec<T>::VE;
+
 // Row p of sequence n counted from its first token; p < 0 reads the initial state.
-template <typename T, int W>
-__device__ __forceinline__ void conv_row(float (&f)[Vec<T>::VE], const ConvArgs& a, int n, int bos, int p, int c, int nv) {
-  constexpr int VE = Vec<T>::VE;
+template <typename T, int W, int VE>
+__device__ __forceinline__ void conv_row(float (&f)[VE], const ConvArgs& a, int n, int bos, int p, int c, int nv) {
   if (p >= 0) {
-    ldv<T>(f, reinterpret_cast<const T*>(a.x) + (int64_t)(bos + p) * a.xs + c, nv);
+    ldv<T, VE>(f, reinterpret_cast<const T*>(a.x) + (int64_t)(bos + p) * a.xs + c, nv);
   } else if (a.h0) {
-    ldv<T>(f, reinterpret_cast<const T*>(a.h0) + ((int64_t)n * (W - 1) + (W - 1) + p) * a.D + c, nv);
+    ldv<T, VE>(f, reinterpret_cast<const T*>(a.h0) + ((int64_t)n * (W - 1) + (W - 1) + p) * a.D + c, nv);
   } else {
 #pragma unroll
     for (int e = 0; e < VE; ++e) f[e] = 0.f;
@@ -51,79 +56,135 @@ __device__ __forceinline__ void conv_row(float (&f)[Vec<T>::VE], const ConvArgs&
 template <typename WT, int VE, int W>
 __device__ __forceinline__ void conv_taps(float (&wt)[W][VE], float (&b)[VE], const ConvArgs& a, int c, int nv) {
   const WT* w = reinterpret_cast<const WT*>(a.w) + (int64_t)c * W;
+  float f[VE * W];
 #pragma unroll
-  for (int e = 0; e < VE; ++e)
+  for (int k = 0; k < VE * W; k += 4) {
+    float g[4];
+    ldv<WT, 4>(g, w + k, nv * W - k);
 #pragma unroll
-    for (int j = 0; j < W; ++j) wt[j][e] = e < nv ? (float)w[e * W + j] : 0.f;
+    for (int e = 0; e < 4; ++e) f[k + e] = g[e];
+  }
 #pragma unroll
-  for (int e = 0; e < VE; ++e) b[e] = 0.f;
-  if (a.bias) ldw<VE, WT>(b, reinterpret_cast<const WT*>(a.bias) + c, nv);
+  for (int e = 0; e < VE; ++e) {
+    b[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) wt[j][e] = f[e * W + j];
+  }
+  if (a.bias) ldv<WT, VE>(b, reinterpret_cast<const WT*>(a.bias) + c, nv);
 }
 
 // Final state of sequence n (grid rows past the token tiles).
 template <typename T, int W>
 __device__ __forceinline__ void conv_final(const ConvArgs& a, int n, int c, int nv) {
-  constexpr int VE = Vec<T>::VE;
+  constexpr int VE = CVE<T, false>;
   int bos, eos;
   seq_range(a.seq, n, bos, eos);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
     float f[VE];
-    conv_row<T, W>(f, a, n, bos, eos - bos - (W - 1) + k, c, nv);
-    stv<T>(reinterpret_cast<T*>(a.ht) + ((int64_t)n * (W - 1) + k) * a.D + c, f, nv);
+    conv_row<T, W, VE>(f, a, n, bos, eos - bos - (W - 1) + k, c, nv);
+    stv<T, VE>(reinterpret_cast<T*>(a.ht) + ((int64_t)n * (W - 1) + k) * a.D + c, f, nv);
   }
 }
 
-template <typename T, typename WT, int W>
+// A row's VE channels on their way from memory.  FULL (every lane's channels exist
+// and rows keep 4-byte alignment): one unconditional load, kept in the operand type,
+// and stores through a buffer resource, whose range check drops the rows past the
+// run.  The compiler can then count the requests in flight (one counter serves
+// loads and stores) and a row's use waits for that row alone; with loads and stores
+// in branches it waited for all of them (3.2 instead of 4.5 TB/s forward).
+template <typename T, int VE, bool FULL>
+struct Row {
+  typename VecN<T, VE>::raw v;
+  float f[FULL ? 1 : VE];
+  __device__ __forceinline__ void load(const T* p, int nv) {
+    if constexpr (FULL) v = *reinterpret_cast<const typename VecN<T, VE>::type*>(p);
+    else ldv<T, VE>(f, p, nv);
+  }
+  __device__ __forceinline__ void get(float (&o)[VE]) const {
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      if constexpr (FULL) o[e] = (float)v[e];
+      else o[e] = f[e];
+    }
+  }
+};
+template <typename T, int VE, bool FULL>
+__device__ __forceinline__ void put_row(const GBuf& g, T* p, int row, int64_t stride, int c, bool on,
+                                        const float (&o)[VE], int nv) {
+  if constexpr (FULL) {
+    typename VecN<T, VE>::raw v;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) v[e] = (T)o[e];
+    const uint32_t off = on ? (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(T) : OOB;
+    if constexpr (VE * sizeof(T) == 16) gst16(g, off, __builtin_bit_cast(uint4, v));
+    else gst8(g, off, __builtin_bit_cast(uint2, v));
+  } else {
+    if (on) stv<T, VE>(p + row * stride + c, o, nv);
+  }
+}
+// values loaded in front of a loop: waited for here, so that the loop's uses need not
+template <int N>
+__device__ __forceinline__ void settle(float (&f)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+v"(f[e]));
+}
+// tokens worked on side by side: a multiple of W, so that the ring of the last W rows
+// turns at compile time
+constexpr int conv_group(int W) { return W == 3 ? 6 : 8; }
+
+// The rows of the next U tokens are in flight while one is worked on.
+template <typename T, typename WT, int W, bool FULL>
 __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
-  constexpr int VE = Vec<T>::VE;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (blockIdx.y * 64 + lane) * VE, nv = a.D - c;
+  constexpr int VE = CVE<T, false>, U = conv_group(W);
+  const int cb = blockIdx.x % a.cblocks, tile = blockIdx.x / a.cblocks;
+  const int c = (cb * 64 * CONV_WAVES + threadIdx.x) * VE, nv = a.D - c;
   if (nv <= 0) return;
-  if ((int)blockIdx.x >= a.tiles) {  // one sequence's final state per wave
-    const int n = (blockIdx.x - a.tiles) * CONV_WAVES + wave;
-    if (n < a.seq.N) conv_final<T, W>(a, n, c, nv);
+  if (tile >= a.tiles) {  // a sequence's final state
+    conv_final<T, W>(a, tile - a.tiles, c, nv);
     return;
   }
-  const int64_t first = (blockIdx.x * (int64_t)CONV_WAVES + wave) * a.run;
+  const int64_t first = (int64_t)tile * a.run;
   const int total = seq_start(a.seq, a.seq.N);  // rows behind the last sequence stay as they are
   if (first >= total) return;
-  int t = (int)first;
-  const int end = min(t + a.run, total);
-  float wt[W][VE], b[VE], h[W - 1][VE];  // h[k]: row t - (W-1) + k
-  conv_taps<WT, VE, W>(wt, b, a, c, nv);
-  int n = seq_of(a.seq, t), bos, eos;
+  int t0 = (int)first;
+  const int end = min(t0 + a.run, total);
+  int n = seq_of(a.seq, t0), bos, eos;
   seq_range(a.seq, n, bos, eos);
+  float wt[W][VE], b[VE];
+  conv_taps<WT, VE, W>(wt, b, a, c, nv);
   const T* x = reinterpret_cast<const T*>(a.x) + c;
-  T* y = reinterpret_cast<T*>(a.y) + c;
-  while (t < end) {
-    while (eos <= t && n + 1 < a.seq.N) seq_range(a.seq, ++n, bos, eos);  // (skips empty ones)
-    const int stop = eos > t ? min(end, eos) : end;
+  T* y = reinterpret_cast<T*>(a.y) + first * a.ys;
+  const GBuf gy = gbuf(y, tile_bytes<T>(end - (int)first, a.ys, a.D));
+  while (t0 < end) {
+    while (eos <= t0 && n + 1 < a.seq.N) seq_range(a.seq, ++n, bos, eos);  // (passes over empty ones)
+    const int stop = eos > t0 ? min(end, eos) : end;
+    Row<T, VE, FULL> in[U];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) conv_row<T, W>(h[k], a, n, bos, t - bos - (W - 1) + k, c, nv);
-    constexpr int U = 4;  // rows requested together
-    for (; t < stop; t += U) {
-      float xv[U][VE];
+    for (int u = 0; u < U; ++u) in[u].load(x + (int64_t)min(t0 + u, stop - 1) * a.xs, nv);
+    float h[W][VE];  // token t0 + u is in h[u % W]
 #pragma unroll
-      for (int u = 0; u < U; ++u) ldv<T>(xv[u], x + (int64_t)min(t + u, stop - 1) * a.xs, nv);
+    for (int k = 0; k < W - 1; ++k) {
+      conv_row<T, W, VE>(h[k + 1], a, n, bos, t0 - bos - (W - 1) + k, c, nv);
+      settle(h[k + 1]);
+    }
+    for (int t = t0; t < stop; t += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        in[u].get(h[u % W]);
+        in[u].load(x + (int64_t)min(t + u + U, stop - 1) * a.xs, nv);
         float o[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           float p = b[e];
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) p += wt[j][e] * h[j][e];
-          p += wt[W - 1][e] * xv[u][e];
+          for (int j = 0; j < W; ++j) p += wt[j][e] * h[(u + 1 + j) % W][e];
           o[e] = a.act == REWY_ACT_SILU ? silu(p) : p;
-#pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
-          h[W - 2][e] = xv[u][e];
         }
-        if (t + u < stop) stv<T>(y + (int64_t)(t + u) * a.ys, o, nv);
+        put_row<T, VE, FULL>(gy, y, t + u - (int)first, a.ys, c, t + u < stop, o, nv);
       }
     }
-    t = stop;
+    t0 = stop;
   }
 }
 
@@ -131,12 +192,12 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
 // the same lane, so the state may be updated in place.
 template <typename T, typename WT, int W>
 __global__ __launch_bounds__(64) void k_conv_step(ConvArgs a) {
-  constexpr int VE = Vec<T>::VE;
+  constexpr int VE = 4;  // latency counts: few bytes a lane, many lanes
   const int c = (blockIdx.y * 64 + threadIdx.x) * VE, nv = a.D - c, n = blockIdx.x;
   if (nv <= 0) return;
   float h[W][VE], wt[W][VE], b[VE];
 #pragma unroll
-  for (int k = 0; k < W; ++k) conv_row<T, W>(h[k], a, n, n, k - (W - 1), c, nv);
+  for (int k = 0; k < W; ++k) conv_row<T, W, VE>(h[k], a, n, n, k - (W - 1), c, nv);
   conv_taps<WT, VE, W>(wt, b, a, c, nv);
   float o[VE];
 #pragma unroll
@@ -146,26 +207,22 @@ __global__ __launch_bounds__(64) void k_conv_step(ConvArgs a) {
     for (int j = 0; j < W; ++j) p += wt[j][e] * h[j][e];
     o[e] = a.act == REWY_ACT_SILU ? silu(p) : p;
   }
-  stv<T>(reinterpret_cast<T*>(a.y) + (int64_t)n * a.ys + c, o, nv);
+  stv<T, VE>(reinterpret_cast<T*>(a.y) + (int64_t)n * a.ys + c, o, nv);
   if (a.ht) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
-      stv<T>(reinterpret_cast<T*>(a.ht) + ((int64_t)n * (W - 1) + k) * a.D + c, h[k + 1], nv);
+      stv<T, VE>(reinterpret_cast<T*>(a.ht) + ((int64_t)n * (W - 1) + k) * a.D + c, h[k + 1], nv);
   }
 }
 
-// dpre = dy act'(pre) of one row, h[j] = the row's taps
-template <typename T, int W>
-__device__ __forceinline__ void conv_dpre(float (&dp)[Vec<T>::VE], const float (&h)[W][Vec<T>::VE],
-                                          const float (&wt)[W][Vec<T>::VE], const float (&b)[Vec<T>::VE], int act) {
+// dp (dy of a row) becomes dy act'(pre); pre = the row before the activation
+template <int VE>
+__device__ __forceinline__ void conv_dpre(float (&dp)[VE], const float (&pre)[VE], int act) {
   if (act != REWY_ACT_SILU) return;
 #pragma unroll
-  for (int e = 0; e < Vec<T>::VE; ++e) {
-    float p = b[e];
-#pragma unroll
-    for (int j = 0; j < W; ++j) p += wt[j][e] * h[j][e];
-    const float s = sigmoid_f(p);
-    dp[e] *= s * (1.f + p * (1.f - s));
+  for (int e = 0; e < VE; ++e) {
+    const float s = sigmoid_f(pre[e]);
+    dp[e] *= s * (1.f + pre[e] * (1.f - s));
   }
 }
 
@@ -174,7 +231,7 @@ __device__ __forceinline__ void conv_dpre(float (&dp)[Vec<T>::VE], const float (
 // is shorter than the state.
 template <typename T, typename WT, int W>
 __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv) {
-  constexpr int VE = Vec<T>::VE;
+  constexpr int VE = CVE<T, true>;
   int bos, eos;
   seq_range(a.seq, n, bos, eos);
   const int L = eos - bos;
@@ -185,16 +242,23 @@ __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv
 #pragma unroll
     for (int e = 0; e < VE; ++e) g[k][e] = 0.f;
     const int f = k - L;  // row of the final state that this row is
-    if (a.dht && f >= 0) ldv<T>(g[k], reinterpret_cast<const T*>(a.dht) + ((int64_t)n * (W - 1) + f) * a.D + c, nv);
+    if (a.dht && f >= 0) ldv<T, VE>(g[k], reinterpret_cast<const T*>(a.dht) + ((int64_t)n * (W - 1) + f) * a.D + c, nv);
   }
 #pragma unroll
   for (int t = 0; t < W - 1; ++t) {
     if (t >= L) break;
-    float h[W][VE], dp[VE];
+    float pre[VE], dp[VE];
 #pragma unroll
-    for (int j = 0; j < W; ++j) conv_row<T, W>(h[j], a, n, bos, t - (W - 1) + j, c, nv);
-    ldv<T>(dp, reinterpret_cast<const T*>(a.dy) + (int64_t)(bos + t) * a.ys + c, nv);
-    conv_dpre<T, W>(dp, h, wt, b, a.act);
+    for (int e = 0; e < VE; ++e) pre[e] = b[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      float h[VE];
+      conv_row<T, W, VE>(h, a, n, bos, t - (W - 1) + j, c, nv);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) pre[e] += wt[j][e] * h[e];
+    }
+    ldv<T, VE>(dp, reinterpret_cast<const T*>(a.dy) + (int64_t)(bos + t) * a.ys + c, nv);
+    conv_dpre<VE>(dp, pre, a.act);
 #pragma unroll
     for (int k = t; k < W - 1; ++k)
 #pragma unroll
@@ -202,18 +266,20 @@ __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv
   }
 #pragma unroll
   for (int k = 0; k < W - 1; ++k)
-    stv<T>(reinterpret_cast<T*>(a.dh0) + ((int64_t)n * (W - 1) + k) * a.D + c, g[k], nv);
+    stv<T, VE>(reinterpret_cast<T*>(a.dh0) + ((int64_t)n * (W - 1) + k) * a.D + c, g[k], nv);
 }
 
-template <typename T, typename WT, int W>
+// A run's part of each sequence it meets: tokens enter one by one (the rows of the next
+// U in flight); a token's dpre meets the W rows that it reached, and a row leaves
+// when the W - 1 tokens behind it have entered.
+template <typename T, typename WT, int W, bool FULL>
 __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
-  constexpr int VE = Vec<T>::VE;
-  __shared__ float red[CONV_WAVES - 1][VE][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (blockIdx.y * 64 + lane) * VE, nv = a.D - c;
-  if ((int)blockIdx.x >= a.tiles) {
-    const int n = (blockIdx.x - a.tiles) * CONV_WAVES + wave;
-    if (n < a.seq.N && nv > 0) conv_dh0<T, WT, W>(a, n, c, nv);
+  constexpr int VE = CVE<T, true>, U = conv_group(W);
+  const int cb = blockIdx.x % a.cblocks, tile = blockIdx.x / a.cblocks;
+  const int c = (cb * 64 * CONV_WAVES + threadIdx.x) * VE, nv = a.D - c;
+  if (nv <= 0) return;
+  if (tile >= a.tiles) {  // a sequence's initial state
+    conv_dh0<T, WT, W>(a, tile - a.tiles, c, nv);
     return;
   }
   float wt[W][VE], b[VE], dw[W][VE], db[VE];
@@ -224,97 +290,88 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
   }
-  const int64_t first = (blockIdx.x * (int64_t)CONV_WAVES + wave) * a.run;
+  const int64_t first = (int64_t)tile * a.run;
   const int total = seq_start(a.seq, a.seq.N);  // rows behind the last sequence stay as they are
-  if (first < total && nv > 0) {
+  if (first < total) {
     int t0 = (int)first;
     const int end = min(t0 + a.run, total);
     int n = seq_of(a.seq, t0), bos, eos;
     seq_range(a.seq, n, bos, eos);
+    const T* x = reinterpret_cast<const T*>(a.x) + c;
     const T* dy = reinterpret_cast<const T*>(a.dy) + c;
-    T* dx = reinterpret_cast<T*>(a.dx) + c;
+    T* dx = reinterpret_cast<T*>(a.dx) + first * a.dxs;
+    const GBuf gx = gbuf(dx, tile_bytes<T>(end - (int)first, a.dxs, a.D));
     while (t0 < end) {
       while (eos <= t0 && n + 1 < a.seq.N) seq_range(a.seq, ++n, bos, eos);
-      // this run's tokens of the sequence: [t0, stop)
-      const int stop = eos > t0 ? min(end, eos) : end, last = max(eos, stop);
-      float h[W][VE], d[W][VE];  // h[j]: row t - (W-1) + j;  d[j]: dpre of the same row
+      // this run's tokens of the sequence: [t0, stop); the tokens that reach them: [t0, last)
+      const int stop = eos > t0 ? min(end, eos) : end, eoq = max(eos, stop), last = min(stop + W - 1, eoq);
+      Row<T, VE, FULL> xin[U], din[U];
+      auto fetch = [&](int u, int t) {
+        const int64_t tt = min(t, last - 1);
+        xin[u].load(x + tt * a.xs, nv);
+        din[u].load(dy + tt * a.ys, nv);
+      };
 #pragma unroll
-      for (int j = 1; j < W; ++j) conv_row<T, W>(h[j], a, n, bos, t0 - bos - W + j, c, nv);
+      for (int u = 0; u < U; ++u) fetch(u, t0 + u);
+      float h[W][VE], d[W][VE];  // token t0 + u and its dpre are in h[u % W], d[u % W]
 #pragma unroll
-      for (int j = 0; j < W; ++j)
+      for (int k = 0; k < W - 1; ++k) {
+        conv_row<T, W, VE>(h[k + 1], a, n, bos, t0 - bos - (W - 1) + k, c, nv);
+        settle(h[k + 1]);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) d[j][e] = 0.f;
-      // token t enters; the row t - (W-1) has met all its taps and leaves
-      for (int t = t0; t < stop + W - 1; ++t) {
+        for (int e = 0; e < VE; ++e) d[k + 1][e] = 0.f;
+      }
+      for (int t = t0; t < stop + W - 1; t += U) {
 #pragma unroll
-        for (int j = 0; j + 1 < W; ++j)
+        for (int u = 0; u < U; ++u) {
+          constexpr int R = W;
+          float(&hn)[VE] = h[u % R];
+          float(&dn)[VE] = d[u % R];
+          xin[u].get(hn);
+          din[u].get(dn);
+          fetch(u, t + u + U);
+          float pre[VE];
+          const float live = t + u < last ? 1.f : 0.f, own = t + u < stop ? 1.f : 0.f;
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
-            h[j][e] = h[j + 1][e];
-            d[j][e] = d[j + 1][e];
+            pre[e] = b[e];
+#pragma unroll
+            for (int j = 0; j < W; ++j) pre[e] += wt[j][e] * h[(u + 1 + j) % R][e];
           }
-        float dp[VE];
-        if (t < last) {
-          conv_row<T, W>(h[W - 1], a, n, bos, t - bos, c, nv);
-          ldv<T>(dp, dy + (int64_t)t * a.ys, nv);
-          conv_dpre<T, W>(dp, h, wt, b, a.act);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VE; ++e) dp[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < VE; ++e) d[W - 1][e] = dp[e];
-        if (t < stop) {
+          conv_dpre<VE>(dn, pre, a.act);
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
-            db[e] += dp[e];
+            dn[e] = live != 0.f ? dn[e] : 0.f;
+            const float m = own != 0.f ? dn[e] : 0.f;
+            db[e] += m;
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][e] += dp[e] * h[j][e];
+            for (int j = 0; j < W; ++j) dw[j][e] += m * h[(u + 1 + j) % R][e];
           }
-        }
-        const int o = t - (W - 1);
-        if (o >= t0) {
+          const int o = t + u - (W - 1);  // the row that leaves
           float g[VE];
-          const int f = o - (last - (W - 1));  // its row of the final state
-          if (a.dht && f >= 0) {
-            ldv<T>(g, reinterpret_cast<const T*>(a.dht) + ((int64_t)n * (W - 1) + f) * a.D + c, nv);
-          } else {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) g[e] = 0.f;
+          for (int e = 0; e < VE; ++e) {
+            g[e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) g[e] += wt[W - 1 - j][e] * d[(u + 1 + j) % R][e];
           }
+          const int f = o - (eoq - (W - 1));  // its row of the final state
+          if (a.dht && f >= 0 && o < stop && o >= t0) {
+            float q[VE];
+            ldv<T, VE>(q, reinterpret_cast<const T*>(a.dht) + ((int64_t)n * (W - 1) + f) * a.D + c, nv);
+            settle(q);
 #pragma unroll
-          for (int e = 0; e < VE; ++e)
-#pragma unroll
-            for (int j = 0; j < W; ++j) g[e] += wt[W - 1 - j][e] * d[j][e];
-          stv<T>(dx + (int64_t)o * a.dxs, g, nv);
+            for (int e = 0; e < VE; ++e) g[e] += q[e];
+          }
+          put_row<T, VE, FULL>(gx, dx, o - (int)first, a.dxs, c, o >= t0 && o < stop, g, nv);
         }
       }
       t0 = stop;
     }
   }
-  // the block's runs, joined in their order
 #pragma unroll
-  for (int j = 0; j <= W; ++j) {
-    float v[VE];
-#pragma unroll
-    for (int e = 0; e < VE; ++e) v[e] = j < W ? dw[j < W ? j : 0][e] : db[e];
-    __syncthreads();
-    if (wave > 0) {
-#pragma unroll
-      for (int e = 0; e < VE; ++e) red[wave - 1][e][lane] = v[e];
-    }
-    __syncthreads();
-    if (wave == 0 && nv > 0) {
-#pragma unroll
-      for (int k = 0; k < CONV_WAVES - 1; ++k)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v[e] += red[k][e][lane];
-      stv<float>(a.part + ((int64_t)blockIdx.x * (W + 1) + j) * a.D + c, *reinterpret_cast<float(*)[4]>(v), min(nv, 4));
-      if constexpr (VE == 8)
-        stv<float>(a.part + ((int64_t)blockIdx.x * (W + 1) + j) * a.D + c + 4, *reinterpret_cast<float(*)[4]>(v + 4),
-                   min(nv - 4, 4));
-    }
-  }
+  for (int j = 0; j <= W; ++j)
+    stv<float, VE>(a.part + ((int64_t)tile * (W + 1) + j) * a.D + c, j < W ? dw[j < W ? j : 0] : db, nv);
 }
 
 // dw [D, W] and dbias [D] from the partial sums [tiles, W + 1, D]: 16
@@ -349,13 +406,16 @@ hipError_t conv_taps_of(int W, F&& f) {
     default: return hipErrorInvalidValue;
   }
 }
-int conv_cblocks(int D, bool f32) { return (D + 64 * (f32 ? 4 : 8) - 1) / (64 * (f32 ? 4 : 8)); }
+// waves along the channels
+int conv_cblocks(int D, int ve) { return (D + 64 * ve - 1) / (64 * ve); }
 
 template <typename T, typename WT>
-hipError_t conv_fwd_t(const ConvArgs& a, int cb, hipStream_t s) {
+hipError_t conv_fwd_t(const ConvArgs& a, hipStream_t s) {
   return conv_taps_of(a.W, [&](auto w) {
-    const int fin = a.ht ? (a.seq.N + CONV_WAVES - 1) / CONV_WAVES : 0;
-    REWY_LAUNCH((k_conv_fwd<T, WT, decltype(w)::value>), dim3(a.tiles + fin, cb), dim3(64 * CONV_WAVES), s, a);
+    const int fin = a.ht ? a.seq.N : 0;
+    const dim3 grid((a.tiles + fin) * a.cblocks), block(64 * CONV_WAVES);
+    if (a.full) REWY_LAUNCH((k_conv_fwd<T, WT, decltype(w)::value, true>), grid, block, s, a);
+    else REWY_LAUNCH((k_conv_fwd<T, WT, decltype(w)::value, false>), grid, block, s, a);
     return hipGetLastError();
   });
 }
@@ -367,12 +427,15 @@ hipError_t conv_step_t(const ConvArgs& a, int cb, hipStream_t s) {
   });
 }
 template <typename T, typename WT>
-hipError_t conv_bwd_t(const ConvArgs& a, int cb, hipStream_t s) {
+hipError_t conv_bwd_t(const ConvArgs& a, hipStream_t s) {
   return conv_taps_of(a.W, [&](auto w) {
     constexpr int W = decltype(w)::value;
-    const int fin = a.dh0 ? (a.seq.N + CONV_WAVES - 1) / CONV_WAVES : 0;
-    if (a.tiles + fin > 0)
-      REWY_LAUNCH((k_conv_bwd<T, WT, W>), dim3(a.tiles + fin, cb), dim3(64 * CONV_WAVES), s, a);
+    const int fin = a.dh0 ? a.seq.N : 0;
+    const dim3 grid((a.tiles + fin) * a.cblocks), block(64 * CONV_WAVES);
+    if (a.tiles + fin > 0) {
+      if (a.full) REWY_LAUNCH((k_conv_bwd<T, WT, W, true>), grid, block, s, a);
+      else REWY_LAUNCH((k_conv_bwd<T, WT, W, false>), grid, block, s, a);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     REWY_LAUNCH((k_conv_reduce<WT, W>), dim3((a.D + 15) / 16, W + 1), dim3(256), s, a);
@@ -382,36 +445,48 @@ hipError_t conv_bwd_t(const ConvArgs& a, int cb, hipStream_t s) {
 
 // Tokens of a run: the longest of 4 .. most whose runs still give each SIMD two
 // waves or so; a longer run reads fewer rows twice.
-int conv_run(int total, int cb, int most) {
+int conv_run(int total, int cw, int most) {
   int run = most;
-  while (run > 4 && (int64_t)((total + run - 1) / run) * cb < 2048) run /= 2;
+  while (run > 4 && (int64_t)((total + run - 1) / run) * cw < 2048) run /= 2;
   return run;
 }
-int conv_tiles(int total, int run) { return (int)(((int64_t)total + (int64_t)run * CONV_WAVES - 1) / ((int64_t)run * CONV_WAVES)); }
+int conv_tiles(int total, int run) { return (int)(((int64_t)total + run - 1) / run); }
+int conv_gblocks(int cw) { return (cw + CONV_WAVES - 1) / CONV_WAVES; }
 
 }  // namespace
 
-void conv_bwd_shape(int total, int D, bool f32, int& run, int& tiles) {
-  run = conv_run(total, conv_cblocks(D, f32), 64);
+void conv_bwd_shape(int total, int D, int& run, int& tiles) {
+  run = conv_run(total, conv_cblocks(D, 4), 64);
   tiles = conv_tiles(total, run);
 }
 
+namespace {
+// whether every lane's channels exist and the rows that are written keep 4-byte alignment
+// (and their offsets within a run 32 bits)
+bool conv_full(const ConvArgs& a, int ve, size_t e, const void* out, int64_t stride) {
+  return a.D % ve == 0 && (uintptr_t)out % 4 == 0 && stride * e % 4 == 0 && stride <= (1 << 22);
+}
+}  // namespace
+
 hipError_t launch_conv_fwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
-  const int cb = conv_cblocks(a.D, f32);
-  a.run = conv_run(a.seq.total, cb, 32);
+  const int cw = conv_cblocks(a.D, f32 ? CVE<float, false> : CVE<bf16, false>);
+  a.run = conv_run(a.seq.total, cw, 32);
   a.tiles = conv_tiles(a.seq.total, a.run);
-  if (f32) return wf32 ? conv_fwd_t<float, float>(a, cb, s) : conv_fwd_t<float, bf16>(a, cb, s);
-  return wf32 ? conv_fwd_t<bf16, float>(a, cb, s) : conv_fwd_t<bf16, bf16>(a, cb, s);
+  a.cblocks = conv_gblocks(cw);
+  a.full = conv_full(a, f32 ? CVE<float, false> : CVE<bf16, false>, f32 ? 4 : 2, a.y, a.ys);
+  if (f32) return wf32 ? conv_fwd_t<float, float>(a, s) : conv_fwd_t<float, bf16>(a, s);
+  return wf32 ? conv_fwd_t<bf16, float>(a, s) : conv_fwd_t<bf16, bf16>(a, s);
 }
 hipError_t launch_conv_step(const ConvArgs& a, bool f32, bool wf32, hipStream_t s) {
-  const int cb = conv_cblocks(a.D, f32);
+  const int cb = conv_cblocks(a.D, 4);
   if (f32) return wf32 ? conv_step_t<float, float>(a, cb, s) : conv_step_t<float, bf16>(a, cb, s);
   return wf32 ? conv_step_t<bf16, float>(a, cb, s) : conv_step_t<bf16, bf16>(a, cb, s);
 }
-hipError_t launch_conv_bwd(const ConvArgs& a, bool f32, bool wf32, hipStream_t s) {
-  const int cb = conv_cblocks(a.D, f32);
-  if (f32) return wf32 ? conv_bwd_t<float, float>(a, cb, s) : conv_bwd_t<float, bf16>(a, cb, s);
-  return wf32 ? conv_bwd_t<bf16, float>(a, cb, s) : conv_bwd_t<bf16, bf16>(a, cb, s);
+hipError_t launch_conv_bwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
+  a.cblocks = conv_gblocks(conv_cblocks(a.D, 4));
+  a.full = conv_full(a, 4, f32 ? 4 : 2, a.dx, a.dxs);
+  if (f32) return wf32 ? conv_bwd_t<float, float>(a, s) : conv_bwd_t<float, bf16>(a, s);
+  return wf32 ? conv_bwd_t<bf16, float>(a, s) : conv_bwd_t<bf16, bf16>(a, s);
 }
 
 }  // namespace rewy

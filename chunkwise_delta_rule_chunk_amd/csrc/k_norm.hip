@@ -104,14 +104,14 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int j = (c * TPR + t) * VE;
-    ldv<T>(s[c], x + j, D - j);
+    ldv<T, VE>(s[c], x + j, D - j);
   }
   if (r) {
     float rv[NC][VE];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
-      ldv<T>(rv[c], r + j, D - j);
+      ldv<T, VE>(rv[c], r + j, D - j);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
-      stv<T>(o + j, s[c], D - j);
+      stv<T, VE>(o + j, s[c], D - j);
     }
   }
 #pragma unroll
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
   for (int c = 0; c < NC; ++c) {
     const int j = (c * TPR + t) * VE;
     float wv[VE];
-    if (w) ldw<VE, W>(wv, w + j, D - j);
+    if (w) ldv<W, VE>(wv, w + j, D - j);
 #pragma unroll
     for (int e = 0; e < VE; ++e) s[c][e] = s[c][e] * rstd * (w ? wv[e] : 1.f);
   }
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
-      stv<T>(o + j, s[c], D - j);
+      stv<T, VE>(o + j, s[c], D - j);
     }
   }
   if (!a.quant) return;
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bw
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int j = (c * TPR + t) * VE;
-    if (w) ldw<VE, W>(wv[c], w + j, D - j);
+    if (w) ldv<W, VE>(wv[c], w + j, D - j);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       if (!w) wv[c][e] = 1.f;
@@ -227,8 +227,8 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bw
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
-      ldv<T>(s[c], sp + j, n - j);
-      ldv<T>(dy[c], dp + j, n - j);
+      ldv<T, VE>(s[c], sp + j, n - j);
+      ldv<T, VE>(dy[c], dp + j, n - j);
     }
     const float rstd = a.rstd[m];
     float dot = 0.f;
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bw
       for (int c = 0; c < NC; ++c) {
         const int j = (c * TPR + t) * VE;
         float ds[VE];
-        ldv<T>(ds, gp + j, n - j);
+        ldv<T, VE>(ds, gp + j, n - j);
 #pragma unroll
         for (int e = 0; e < VE; ++e) dy[c][e] = rstd * (dy[c][e] - s[c][e] * k) + ds[e];
       }
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bw
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
-      stv<T>(o + j, dy[c], n - j);
+      stv<T, VE>(o + j, dy[c], n - j);
     }
   }
   if (!a.part) return;
@@ -362,7 +362,7 @@ int norm_bwd_blocks(int64_t M, int D, bool f32) {
     return hipSuccess;
   };
   (void)(f32 ? norm_shape<float>(D, take) : norm_shape<bf16>(D, take));
-  // four blocks a CU: enough rows in flight, and few partial rows to join
+  // four blocks a CU (8192 x 4096 bf16: 58 + 9 us with 1024, 84 + 7 us with 512 blocks)
   return (int)std::min<int64_t>((M + rpb - 1) / rpb, 1024);
 }
 

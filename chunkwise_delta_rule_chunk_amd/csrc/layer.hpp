@@ -14,62 +14,48 @@ namespace rewy {
 // (gfx950 in its unaligned access mode, the mode of HSA queues), so rows of an
 // odd length or stride take the same wide accesses as aligned ones and only a
 // row's last, partial vector is read element by element.
+template <typename T, int N>
+struct VecN {
+  typedef T raw __attribute__((ext_vector_type(N)));
+  typedef raw type __attribute__((aligned(sizeof(T))));
+};
 template <typename T>
 struct Vec {
   static constexpr int VE = 16 / (int)sizeof(T);
-  typedef T raw __attribute__((ext_vector_type(VE)));
-  typedef raw type __attribute__((aligned(sizeof(T))));
 };
 
-// p[0 .. VE) as fp32; only the first n are read (the others are zero)
-template <typename T>
-__device__ __forceinline__ void ldv(float (&f)[Vec<T>::VE], const T* p, int n) {
-  constexpr int VE = Vec<T>::VE;
+// p[0 .. VE) as fp32, of which the first n exist (the others are zero), in loads of at
+// most 16 bytes
+template <typename T, int VE>
+__device__ __forceinline__ void ldv(float (&f)[VE], const T* p, int n) {
+  constexpr int N = VE < Vec<T>::VE ? VE : Vec<T>::VE;
   if (n >= VE) {
-    const typename Vec<T>::raw v = *reinterpret_cast<const typename Vec<T>::type*>(p);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) f[e] = (float)v[e];
-  } else {
+    for (int j = 0; j < VE; j += N) {
+      const typename VecN<T, N>::raw v = *reinterpret_cast<const typename VecN<T, N>::type*>(p + j);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) f[e] = e < n ? (float)p[e] : 0.f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void stv(T* p, const float (&f)[Vec<T>::VE], int n) {
-  constexpr int VE = Vec<T>::VE;
-  if (n >= VE) {
-    typename Vec<T>::raw v;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) v[e] = (T)f[e];
-    *reinterpret_cast<typename Vec<T>::type*>(p) = v;
-  } else {
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (e < n) p[e] = (T)f[e];
-  }
-}
-// VE consecutive parameters stored as bf16 or fp32 (VE = 4 or 8)
-template <int VE, typename W>
-__device__ __forceinline__ void ldw(float (&f)[VE], const W* p, int n) {
-  constexpr int WV = Vec<W>::VE;
-  if (n >= VE) {
-    if constexpr (VE >= WV) {
-#pragma unroll
-      for (int j = 0; j < VE / WV; ++j) {
-        const typename Vec<W>::raw v = *reinterpret_cast<const typename Vec<W>::type*>(p + j * WV);
-#pragma unroll
-        for (int e = 0; e < WV; ++e) f[j * WV + e] = (float)v[e];
-      }
-    } else {
-      typedef W half __attribute__((ext_vector_type(VE)));
-      typedef half half_u __attribute__((aligned(sizeof(W))));
-      const half v = *reinterpret_cast<const half_u*>(p);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) f[e] = (float)v[e];
+      for (int e = 0; e < N; ++e) f[j + e] = (float)v[e];
     }
   } else {
 #pragma unroll
     for (int e = 0; e < VE; ++e) f[e] = e < n ? (float)p[e] : 0.f;
+  }
+}
+template <typename T, int VE>
+__device__ __forceinline__ void stv(T* p, const float (&f)[VE], int n) {
+  constexpr int N = VE < Vec<T>::VE ? VE : Vec<T>::VE;
+  if (n >= VE) {
+#pragma unroll
+    for (int j = 0; j < VE; j += N) {
+      typename VecN<T, N>::raw v;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = (T)f[j + e];
+      *reinterpret_cast<typename VecN<T, N>::type*>(p + j) = v;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (e < n) p[e] = (T)f[e];
   }
 }
 
@@ -148,12 +134,14 @@ struct ConvArgs {
   void* dw;
   void* dbias;
   int run;              // tokens of one wave's run
-  int tiles;            // blocks along the tokens
+  int tiles;            // runs
+  int cblocks;          // workgroups along the channels
+  int full;             // no lane has a partial vector (k_conv.hip)
 };
-// tokens of one wave's run, and blocks along the tokens, of the backward
-void conv_bwd_shape(int total, int D, bool f32, int& run, int& tiles);
+// tokens of one wave's run, and runs, of the backward
+void conv_bwd_shape(int total, int D, int& run, int& tiles);
 hipError_t launch_conv_fwd(ConvArgs a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs& a, bool f32, bool wf32, hipStream_t s);
-hipError_t launch_conv_bwd(const ConvArgs& a, bool f32, bool wf32, hipStream_t s);
+hipError_t launch_conv_bwd(ConvArgs a, bool f32, bool wf32, hipStream_t s);
 
 }  // namespace rewy

@@ -7,7 +7,7 @@
 //   dx_t = sum_{o < W} w_{W-1-o} dpre_{t+o} (+ the final state's adjoint on the
 //   last W - 1 rows),   dw_j = sum_t dpre_t x_{t-(W-1)+j},   dbias = sum_t dpre_t.
 //
-// Memory is all it costs.  A lane owns VE channels (16 bytes) and walks a run
+// Memory is all it costs.  A lane owns four channels and walks a run
 // of tokens with the last W - 1 rows in registers, so each row is read once
 // per run plus W - 1 rows at its start.  Workgroups that follow each other share
 // their tokens, so whole rows are streamed.  Tokens are packed; a run that meets
@@ -34,13 +34,12 @@ __device__ __forceinline__ int seq_of(const SeqArgs& q, int t) {
   return lo;
 }
 
-// Channels of a lane: 16 bytes of a row, in the backward at most four (its windows and
-// sums fill the registers).
-template <typename T, bool BWD>
-constexpr int CVE = BWD ? 4 : Vec<T>::VE;
+// Channels of a lane: four, in either type.  With 16 bytes of bf16 (eight) fewer waves
+// fit and fewer rows are in flight: 34 instead of 30 us for 8192 x 4352.
+constexpr int VE = 4;
 
 // Row p of sequence n counted from its first token; p < 0 reads the initial state.
-template <typename T, int W, int VE>
+template <typename T, int W>
 __device__ __forceinline__ void conv_row(float (&f)[VE], const ConvArgs& a, int n, int bos, int p, int c, int nv) {
   if (p >= 0) {
     ldv<T, VE>(f, reinterpret_cast<const T*>(a.x) + (int64_t)(bos + p) * a.xs + c, nv);
@@ -53,7 +52,7 @@ __device__ __forceinline__ void conv_row(float (&f)[VE], const ConvArgs& a, int 
 }
 
 // taps as wt[j][e] for channels c .. c + VE - 1
-template <typename WT, int VE, int W>
+template <typename WT, int W>
 __device__ __forceinline__ void conv_taps(float (&wt)[W][VE], float (&b)[VE], const ConvArgs& a, int c, int nv) {
   const WT* w = reinterpret_cast<const WT*>(a.w) + (int64_t)c * W;
   float f[VE * W];
@@ -76,13 +75,12 @@ __device__ __forceinline__ void conv_taps(float (&wt)[W][VE], float (&b)[VE], co
 // Final state of sequence n (grid rows past the token tiles).
 template <typename T, int W>
 __device__ __forceinline__ void conv_final(const ConvArgs& a, int n, int c, int nv) {
-  constexpr int VE = CVE<T, false>;
   int bos, eos;
   seq_range(a.seq, n, bos, eos);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
     float f[VE];
-    conv_row<T, W, VE>(f, a, n, bos, eos - bos - (W - 1) + k, c, nv);
+    conv_row<T, W>(f, a, n, bos, eos - bos - (W - 1) + k, c, nv);
     stv<T, VE>(reinterpret_cast<T*>(a.ht) + ((int64_t)n * (W - 1) + k) * a.D + c, f, nv);
   }
 }
@@ -93,7 +91,7 @@ __device__ __forceinline__ void conv_final(const ConvArgs& a, int n, int c, int 
 // run.  The compiler can then count the requests in flight (one counter serves
 // loads and stores) and a row's use waits for that row alone; with loads and stores
 // in branches it waited for all of them (3.2 instead of 4.5 TB/s forward).
-template <typename T, int VE, bool FULL>
+template <typename T, bool FULL>
 struct Row {
   typename VecN<T, VE>::raw v;
   float f[FULL ? 1 : VE];
@@ -109,7 +107,7 @@ struct Row {
     }
   }
 };
-template <typename T, int VE, bool FULL>
+template <typename T, bool FULL>
 __device__ __forceinline__ void put_row(const GBuf& g, T* p, int row, int64_t stride, int c, bool on,
                                         const float (&o)[VE], int nv) {
   if constexpr (FULL) {
@@ -117,17 +115,16 @@ __device__ __forceinline__ void put_row(const GBuf& g, T* p, int row, int64_t st
 #pragma unroll
     for (int e = 0; e < VE; ++e) v[e] = (T)o[e];
     const uint32_t off = on ? (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(T) : OOB;
-    if constexpr (VE * sizeof(T) == 16) gst16(g, off, __builtin_bit_cast(uint4, v));
+    if constexpr (sizeof(T) == 4) gst16(g, off, __builtin_bit_cast(uint4, v));
     else gst8(g, off, __builtin_bit_cast(uint2, v));
   } else {
     if (on) stv<T, VE>(p + row * stride + c, o, nv);
   }
 }
 // values loaded in front of a loop: waited for here, so that the loop's uses need not
-template <int N>
-__device__ __forceinline__ void settle(float (&f)[N]) {
+__device__ __forceinline__ void settle(float (&f)[VE]) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) asm volatile("" : "+v"(f[e]));
+  for (int e = 0; e < VE; ++e) asm volatile("" : "+v"(f[e]));
 }
 // tokens worked on side by side: a multiple of W, so that the ring of the last W rows
 // turns at compile time
@@ -136,7 +133,7 @@ constexpr int conv_group(int W) { return W == 3 ? 6 : 8; }
 // The rows of the next U tokens are in flight while one is worked on.
 template <typename T, typename WT, int W, bool FULL>
 __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
-  constexpr int VE = CVE<T, false>, U = conv_group(W);
+  constexpr int U = conv_group(W);
   const int cb = blockIdx.x % a.cblocks, tile = blockIdx.x / a.cblocks;
   const int c = (cb * 64 * CONV_WAVES + threadIdx.x) * VE, nv = a.D - c;
   if (nv <= 0) return;
@@ -152,20 +149,20 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
   int n = seq_of(a.seq, t0), bos, eos;
   seq_range(a.seq, n, bos, eos);
   float wt[W][VE], b[VE];
-  conv_taps<WT, VE, W>(wt, b, a, c, nv);
+  conv_taps<WT, W>(wt, b, a, c, nv);
   const T* x = reinterpret_cast<const T*>(a.x) + c;
   T* y = reinterpret_cast<T*>(a.y) + first * a.ys;
   const GBuf gy = gbuf(y, tile_bytes<T>(end - (int)first, a.ys, a.D));
   while (t0 < end) {
     while (eos <= t0 && n + 1 < a.seq.N) seq_range(a.seq, ++n, bos, eos);  // (passes over empty ones)
     const int stop = eos > t0 ? min(end, eos) : end;
-    Row<T, VE, FULL> in[U];
+    Row<T, FULL> in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) in[u].load(x + (int64_t)min(t0 + u, stop - 1) * a.xs, nv);
     float h[W][VE];  // token t0 + u is in h[u % W]
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-      conv_row<T, W, VE>(h[k + 1], a, n, bos, t0 - bos - (W - 1) + k, c, nv);
+      conv_row<T, W>(h[k + 1], a, n, bos, t0 - bos - (W - 1) + k, c, nv);
       settle(h[k + 1]);
     }
     for (int t = t0; t < stop; t += U) {
@@ -181,7 +178,7 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
           for (int j = 0; j < W; ++j) p += wt[j][e] * h[(u + 1 + j) % W][e];
           o[e] = a.act == REWY_ACT_SILU ? silu(p) : p;
         }
-        put_row<T, VE, FULL>(gy, y, t + u - (int)first, a.ys, c, t + u < stop, o, nv);
+        put_row<T, FULL>(gy, y, t + u - (int)first, a.ys, c, t + u < stop, o, nv);
       }
     }
     t0 = stop;
@@ -192,13 +189,12 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
 // the same lane, so the state may be updated in place.
 template <typename T, typename WT, int W>
 __global__ __launch_bounds__(64) void k_conv_step(ConvArgs a) {
-  constexpr int VE = 4;  // latency counts: few bytes a lane, many lanes
   const int c = (blockIdx.y * 64 + threadIdx.x) * VE, nv = a.D - c, n = blockIdx.x;
   if (nv <= 0) return;
   float h[W][VE], wt[W][VE], b[VE];
 #pragma unroll
-  for (int k = 0; k < W; ++k) conv_row<T, W, VE>(h[k], a, n, n, k - (W - 1), c, nv);
-  conv_taps<WT, VE, W>(wt, b, a, c, nv);
+  for (int k = 0; k < W; ++k) conv_row<T, W>(h[k], a, n, n, k - (W - 1), c, nv);
+  conv_taps<WT, W>(wt, b, a, c, nv);
   float o[VE];
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
@@ -216,7 +212,6 @@ __global__ __launch_bounds__(64) void k_conv_step(ConvArgs a) {
 }
 
 // dp (dy of a row) becomes dy act'(pre); pre = the row before the activation
-template <int VE>
 __device__ __forceinline__ void conv_dpre(float (&dp)[VE], const float (&pre)[VE], int act) {
   if (act != REWY_ACT_SILU) return;
 #pragma unroll
@@ -231,12 +226,11 @@ __device__ __forceinline__ void conv_dpre(float (&dp)[VE], const float (&pre)[VE
 // is shorter than the state.
 template <typename T, typename WT, int W>
 __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv) {
-  constexpr int VE = CVE<T, true>;
   int bos, eos;
   seq_range(a.seq, n, bos, eos);
   const int L = eos - bos;
   float wt[W][VE], b[VE], g[W - 1][VE];
-  conv_taps<WT, VE, W>(wt, b, a, c, nv);
+  conv_taps<WT, W>(wt, b, a, c, nv);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
 #pragma unroll
@@ -253,12 +247,12 @@ __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float h[VE];
-      conv_row<T, W, VE>(h, a, n, bos, t - (W - 1) + j, c, nv);
+      conv_row<T, W>(h, a, n, bos, t - (W - 1) + j, c, nv);
 #pragma unroll
       for (int e = 0; e < VE; ++e) pre[e] += wt[j][e] * h[e];
     }
     ldv<T, VE>(dp, reinterpret_cast<const T*>(a.dy) + (int64_t)(bos + t) * a.ys + c, nv);
-    conv_dpre<VE>(dp, pre, a.act);
+    conv_dpre(dp, pre, a.act);
 #pragma unroll
     for (int k = t; k < W - 1; ++k)
 #pragma unroll
@@ -274,7 +268,7 @@ __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv
 // when the W - 1 tokens behind it have entered.
 template <typename T, typename WT, int W, bool FULL>
 __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
-  constexpr int VE = CVE<T, true>, U = conv_group(W);
+  constexpr int U = W == 3 ? 3 : 4;  // (more do not fit beside the windows and sums)
   const int cb = blockIdx.x % a.cblocks, tile = blockIdx.x / a.cblocks;
   const int c = (cb * 64 * CONV_WAVES + threadIdx.x) * VE, nv = a.D - c;
   if (nv <= 0) return;
@@ -283,7 +277,7 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
     return;
   }
   float wt[W][VE], b[VE], dw[W][VE], db[VE];
-  conv_taps<WT, VE, W>(wt, b, a, c, nv);
+  conv_taps<WT, W>(wt, b, a, c, nv);
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
     db[e] = 0.f;
@@ -305,7 +299,7 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
       while (eos <= t0 && n + 1 < a.seq.N) seq_range(a.seq, ++n, bos, eos);
       // this run's tokens of the sequence: [t0, stop); the tokens that reach them: [t0, last)
       const int stop = eos > t0 ? min(end, eos) : end, eoq = max(eos, stop), last = min(stop + W - 1, eoq);
-      Row<T, VE, FULL> xin[U], din[U];
+      Row<T, FULL> xin[U], din[U];
       auto fetch = [&](int u, int t) {
         const int64_t tt = min(t, last - 1);
         xin[u].load(x + tt * a.xs, nv);
@@ -316,7 +310,7 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
       float h[W][VE], d[W][VE];  // token t0 + u and its dpre are in h[u % W], d[u % W]
 #pragma unroll
       for (int k = 0; k < W - 1; ++k) {
-        conv_row<T, W, VE>(h[k + 1], a, n, bos, t0 - bos - (W - 1) + k, c, nv);
+        conv_row<T, W>(h[k + 1], a, n, bos, t0 - bos - (W - 1) + k, c, nv);
         settle(h[k + 1]);
 #pragma unroll
         for (int e = 0; e < VE; ++e) d[k + 1][e] = 0.f;
@@ -324,9 +318,8 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
       for (int t = t0; t < stop + W - 1; t += U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          constexpr int R = W;
-          float(&hn)[VE] = h[u % R];
-          float(&dn)[VE] = d[u % R];
+          float(&hn)[VE] = h[u % W];
+          float(&dn)[VE] = d[u % W];
           xin[u].get(hn);
           din[u].get(dn);
           fetch(u, t + u + U);
@@ -336,16 +329,16 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
           for (int e = 0; e < VE; ++e) {
             pre[e] = b[e];
 #pragma unroll
-            for (int j = 0; j < W; ++j) pre[e] += wt[j][e] * h[(u + 1 + j) % R][e];
+            for (int j = 0; j < W; ++j) pre[e] += wt[j][e] * h[(u + 1 + j) % W][e];
           }
-          conv_dpre<VE>(dn, pre, a.act);
+          conv_dpre(dn, pre, a.act);
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
             dn[e] = live != 0.f ? dn[e] : 0.f;
             const float m = own != 0.f ? dn[e] : 0.f;
             db[e] += m;
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][e] += m * h[(u + 1 + j) % R][e];
+            for (int j = 0; j < W; ++j) dw[j][e] += m * h[(u + 1 + j) % W][e];
           }
           const int o = t + u - (W - 1);  // the row that leaves
           float g[VE];
@@ -353,7 +346,7 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
           for (int e = 0; e < VE; ++e) {
             g[e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < W; ++j) g[e] += wt[W - 1 - j][e] * d[(u + 1 + j) % R][e];
+            for (int j = 0; j < W; ++j) g[e] += wt[W - 1 - j][e] * d[(u + 1 + j) % W][e];
           }
           const int f = o - (eoq - (W - 1));  // its row of the final state
           if (a.dht && f >= 0 && o < stop && o >= t0) {
@@ -363,7 +356,7 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) g[e] += q[e];
           }
-          put_row<T, VE, FULL>(gx, dx, o - (int)first, a.dxs, c, o >= t0 && o < stop, g, nv);
+          put_row<T, FULL>(gx, dx, o - (int)first, a.dxs, c, o >= t0 && o < stop, g, nv);
         }
       }
       t0 = stop;
@@ -407,7 +400,7 @@ hipError_t conv_taps_of(int W, F&& f) {
   }
 }
 // waves along the channels
-int conv_cblocks(int D, int ve) { return (D + 64 * ve - 1) / (64 * ve); }
+int conv_cblocks(int D) { return (D + 64 * VE - 1) / (64 * VE); }
 
 template <typename T, typename WT>
 hipError_t conv_fwd_t(const ConvArgs& a, hipStream_t s) {
@@ -456,35 +449,35 @@ int conv_gblocks(int cw) { return (cw + CONV_WAVES - 1) / CONV_WAVES; }
 }  // namespace
 
 void conv_bwd_shape(int total, int D, int& run, int& tiles) {
-  run = conv_run(total, conv_cblocks(D, 4), 64);
+  run = conv_run(total, conv_cblocks(D), 64);
   tiles = conv_tiles(total, run);
 }
 
 namespace {
 // whether every lane's channels exist and the rows that are written keep 4-byte alignment
 // (and their offsets within a run 32 bits)
-bool conv_full(const ConvArgs& a, int ve, size_t e, const void* out, int64_t stride) {
-  return a.D % ve == 0 && (uintptr_t)out % 4 == 0 && stride * e % 4 == 0 && stride <= (1 << 22);
+bool conv_full(const ConvArgs& a, size_t e, const void* out, int64_t stride) {
+  return a.D % VE == 0 && (uintptr_t)out % 4 == 0 && stride * e % 4 == 0 && stride <= (1 << 22);
 }
 }  // namespace
 
 hipError_t launch_conv_fwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
-  const int cw = conv_cblocks(a.D, f32 ? CVE<float, false> : CVE<bf16, false>);
+  const int cw = conv_cblocks(a.D);
   a.run = conv_run(a.seq.total, cw, 32);
   a.tiles = conv_tiles(a.seq.total, a.run);
   a.cblocks = conv_gblocks(cw);
-  a.full = conv_full(a, f32 ? CVE<float, false> : CVE<bf16, false>, f32 ? 4 : 2, a.y, a.ys);
+  a.full = conv_full(a, f32 ? 4 : 2, a.y, a.ys);
   if (f32) return wf32 ? conv_fwd_t<float, float>(a, s) : conv_fwd_t<float, bf16>(a, s);
   return wf32 ? conv_fwd_t<bf16, float>(a, s) : conv_fwd_t<bf16, bf16>(a, s);
 }
 hipError_t launch_conv_step(const ConvArgs& a, bool f32, bool wf32, hipStream_t s) {
-  const int cb = conv_cblocks(a.D, 4);
+  const int cb = conv_cblocks(a.D);
   if (f32) return wf32 ? conv_step_t<float, float>(a, cb, s) : conv_step_t<float, bf16>(a, cb, s);
   return wf32 ? conv_step_t<bf16, float>(a, cb, s) : conv_step_t<bf16, bf16>(a, cb, s);
 }
 hipError_t launch_conv_bwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
-  a.cblocks = conv_gblocks(conv_cblocks(a.D, 4));
-  a.full = conv_full(a, 4, f32 ? 4 : 2, a.dx, a.dxs);
+  a.cblocks = conv_gblocks(conv_cblocks(a.D));
+  a.full = conv_full(a, f32 ? 4 : 2, a.dx, a.dxs);
   if (f32) return wf32 ? conv_bwd_t<float, float>(a, s) : conv_bwd_t<float, bf16>(a, s);
   return wf32 ? conv_bwd_t<bf16, float>(a, s) : conv_bwd_t<bf16, bf16>(a, s);
 }

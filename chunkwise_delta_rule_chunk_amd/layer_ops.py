@@ -43,9 +43,9 @@ def _like(t, ref, shape, what, dtype=None):
     """A given tensor is on ref's device, with this shape and type, and contiguous."""
     if t is None:
         return
-    if t.device != ref.device:
+    if t.get_device() != ref.get_device():
         raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype} (got {t.dtype})")
@@ -81,29 +81,32 @@ def _row_stride(t, what, inner):
 
 class _On:
     """Device and stream of one call: allocations inside belong to the stream."""
+    __slots__ = ("handle", "stack")
 
     def __init__(self, ref, stream, inputs):
-        if ref.device.type != "cuda":
+        if not ref.is_cuda:
             raise ValueError(f"tensors must be on a GPU (got {ref.device})")
+        idx = ref.get_device()
         for t in inputs:
-            if t is not None and t.device != ref.device:
+            if t is not None and t.get_device() != idx:
                 raise ValueError(f"all tensors must be on {ref.device} (got one on {t.device})")
         self.stack = None
-        idx = ref.device.index
+        if stream is None and torch._C._cuda_getDevice() == idx:  # the usual call, kept short
+            self.handle = torch._C._cuda_getCurrentRawStream(idx)
+            return
         cur = torch.cuda.current_stream(idx)
         if stream is None:
             stream = cur
         elif stream.device != ref.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {ref.device}")
         self.handle = stream.cuda_stream
-        if torch.cuda.current_device() != idx or stream != cur:
-            self.stack = contextlib.ExitStack()
-            self.stack.enter_context(torch.cuda.device(ref.device))
-            self.stack.enter_context(torch.cuda.stream(stream))
-            if stream != cur:
-                for t in inputs:
-                    if t is not None:
-                        t.record_stream(stream)
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(ref.device))
+        self.stack.enter_context(torch.cuda.stream(stream))
+        if stream != cur:
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
 
     def __enter__(self):
         return self.handle
@@ -115,7 +118,7 @@ class _On:
 
 
 def _workspace(nbytes, ref, ws):
-    if nbytes == 0:
+    if nbytes == 0:  # (the call itself would refuse the descriptor)
         raise B.RewyError(B.REWY_EINVAL, "workspace size")
     return torch.empty(nbytes, dtype=torch.uint8, device=ref.device) if ws is None else ws
 

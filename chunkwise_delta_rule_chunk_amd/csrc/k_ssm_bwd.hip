@@ -6,7 +6,7 @@
 //   dC_i  = sum_heads [ sum_j W_ij B_j + exp(G_i) S_in dy_i ]
 //   dB_j  = sum_heads [ sum_i W_ij C_i + exp(G_L - G_j) dt_j dS x_j ]
 // and the decay's gradient from r_i = dy_i . (y_i - D x_i) and c_j = x_j . dv_j,
-//   dg_t = sum_{i >= t} (r_i - dt_i c_i) + <S, dS> at the segment's end,
+//   dg_t = sum_{i >= t} (r_i - dt_i c_i) + <S, dS> behind the last i,
 //   d raw_t = (c_t - exp(A_log) dg_t) sigmoid(raw_t + dt_bias),   dA_log = sum dg_t g_t.
 // r and c split into parts inside the chunk (formed where W is) and parts through
 // the states (formed by the walks, whose states are fp32); the states that the
@@ -444,11 +444,15 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   }
 }
 
-// Gate gradients of one chunk and head, one wave, lane t its token: the suffix sum
-// of r - dt c over the chunk, then over the rest of its segment what the later
-// chunks add through the states, then <S, dS> at the segment's end.  (Over a whole
-// chunk the pairs inside it cancel, so of later chunks only the parts through
-// the states count.)
+// Gate gradients of one chunk and head, one wave, lane t its token.  dg_t is the sum
+// over what passes token t's decay: the entering state into the rows i >= t (rx), the
+// rows j < t into the leaving state (dt cx), the pairs j < t <= i of the chunk (the
+// suffix sum of ri - dt ci, in which pairs on one side cancel), and what goes from the
+// entering into the leaving state, H = exp(G_L) <S_in, dS>.  With E = <S, dS> at a
+// chunk's end, H = E - sum dt cx, and E one chunk earlier is H + sum rx: from the
+// segment's end, where E is known, to this chunk.  Where the chunk's decay is
+// under 2^-30, H is nothing beside the rounding of E and is taken as 0, so that heads
+// with a strong decay, whose dg is far smaller than E, do not inherit that rounding.
 __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
   const int wk = blockIdx.x * 4 + wave_id(), l = lane_id();
   if (wk >= a.nchunk * a.H) return;
@@ -469,30 +473,41 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
     return v;
   };
-  double rest = 0.;
-  const Gate* g = chunk_gates(a, cslot, h);
-  for (int t = t0 + CH + l, c = 1; c < per; ++c, t += CH)
-    if (t < t2) rest += (double)a.rx[row + t] - (double)chunk_gates(a, cslot + c, h)[l].dt * a.cx[row + t];
-  const double tail = a.ends[((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h] + wave_sum(rest);
+  double E = a.ends[((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h];
+  float dt = 0.f, z = 0.f;
+  double rx = 0., dcx = 0., H = 0.;  // this chunk's own at the loop's end
+  for (int c = (t2 - t0 - 1) / CH; c >= 0; --c) {
+    const int t = t0 + c * CH + l;
+    const Gate* g = chunk_gates(a, cslot + c, h);
+    dt = 0.f;
+    rx = dcx = 0.;
+    if (t < t2) {
+      dt = g[l].dt;
+      rx = a.rx[row + t];
+      dcx = (double)dt * a.cx[row + t];
+    }
+    H = g[CH - 1].G < -30.f ? 0. : E - wave_sum(dcx);
+    E = H + wave_sum(rx);
+  }
   const int t = t0 + l;
   const bool on = t < t1;
-  float dt = 0.f, z = 0.f;
-  double cc = 0., s = 0.;
+  double cc = 0., s = rx, before = dcx;
   if (on) {
     z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
-    dt = g[l].dt;
-    cc = (double)a.cx[row + t] + a.ci[row + t];
-    s = (double)a.rx[row + t] + a.ri[row + t] - dt * cc;
-    cc += a.cd[row + t];
+    const float ci = a.ci[row + t];
+    s += a.ri[row + t] - (double)dt * ci;
+    cc = (double)a.cx[row + t] + ci + a.cd[row + t];
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    const double u = __shfl_down(s, d, 64);
+    const double u = __shfl_down(s, d, 64), v = __shfl_up(before, d, 64);
     if (l + d < 64) s += u;
+    if (l >= d) before += v;
   }
+  before -= dcx;
   double dA = 0., db = 0.;
   if (on) {
-    const double A = -exp((double)a.a_log[h]), dg = s + tail;
+    const double A = -exp((double)a.a_log[h]), dg = H + s + before;
     const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
     db = (cc + A * dg) * sg;
     st_beta(a.ddt, a.dt_f32, (int64_t)t * a.H + h, (float)db);

@@ -177,6 +177,7 @@ __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
   __shared__ __align__(16) float sG[2][HB][CH], sGl[2][HB][CH], tG[2][HB][CH], tGl[2][HB][CH], tdt[2][HB][CH];
   __shared__ __align__(16) float seq[2][HB][CH], sal[2][HB][CH];
   __shared__ float sdec[2][HB];
+  __shared__ int sodd;  // the last chunk, counted from 1, whose x tile holds an infinity or NaN
   const int nhb = head_blocks(a, HB), wk = xcd_range(blockIdx.x, a.nslot * nhb), slot = wk / nhb, hb = wk - slot * nhb;
   const Piece pc = find_piece(a.seq, slot, a.seg);
   if (!pc.on) return;
@@ -213,7 +214,8 @@ __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
     for (int b = 0; b < NB; ++b)
       rcb[b] = reinterpret_cast<const f32x4*>(a.cb)[((int64_t)((cbase + c) * a.G + grp) * 10 + min(b * NW + w, 9)) * 64 + l];
   };
-  auto put_tiles = [&]() {
+  auto put_tiles = [&](int c) {
+    if (tile_not_finite<T, CW, NTH>(rx)) sodd = c + 1;
     rb.store(sb, LK, threadIdx.x);
     store_acc_order<T, K, NTH>(rc, sc, LK);
     rx.store(sx, LV, threadIdx.x);
@@ -263,15 +265,37 @@ __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
     }
     // a pair of blocks above the diagonal lies inside a contraction of 32: zeros, written once
     for (int i = threadIdx.x; i < HB * CH * LM; i += NTH) sm[0][i] = (T)0.f;
+    if (threadIdx.x == 0) sodd = 0;
     lds_barrier();
     put_coefficients(0);
-    put_tiles();
+    put_tiles(0);
   }
   for (int c = 0; c < nch; ++c) {
     const int tok = t0 + c * CH, len = min(CH, t1 - tok), p = c & 1;
     lds_barrier();  // tiles, coefficients and gates complete
     if (c + 1 < nch) fetch(c + 1);
     if (gater && c + 2 < nch) gt = chunk_gates(a, cbase + c + 2, h0 + w)[l];
+    // An infinity or NaN of x would reach earlier tokens through the product's zeros
+    // right of the diagonal: it leaves the tile (each wave its own columns), and y from
+    // its token on and the column's state are set to NaN below.
+    const bool odd = __builtin_amdgcn_readfirstlane(sodd) == c + 1;
+    int first[CT];
+    if (odd) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        T* xc = sx + 16 * (CT * w + ct) + r;
+        first[ct] = CH;
+#pragma unroll 1
+        for (int j = CH - 4 + g4; j >= 0; j -= 4)
+          if (!(fabsf((float)xc[j * LV]) <= 3.4028235e38f)) {
+            xc[j * LV] = (T)0.f;
+            first[ct] = j;
+          }
+        first[ct] = min(first[ct], __shfl_xor(first[ct], 16, 64));
+        first[ct] = min(first[ct], __shfl_xor(first[ct], 32, 64));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
     // entering state: Y^T = S^T C^T, columns scaled by exp(G)
     f32x4 Y[CT][4];
 #pragma unroll
@@ -320,6 +344,21 @@ __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) st4<T>(xw + 16 * I * LV + 16 * ct, Y[ct][I]);
     state_update<T, K, CT, NS>(S, sb, LK, xt, sal[p][hw], sdec[p][hw]);
+    if (odd) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        T* yc = sx + 16 * (CT * w + ct) + r;
+#pragma unroll 1
+        for (int j = first[ct] + g4; j < CH; j += 4) yc[j * LV] = (T)__builtin_nanf("");
+        if (first[ct] < CH) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[ct][nt][i] = __builtin_nanf("");
+        }
+      }
+    }
     lds_barrier();  // tiles and coefficients free, y complete
     {
       // each thread takes y from where its pieces of the next x tile go
@@ -334,7 +373,7 @@ __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
       }
     }
     if (c + 1 < nch) {
-      put_tiles();
+      put_tiles(c + 1);
       put_coefficients(p ^ 1);
     }
     if (gater && c + 2 < nch) put_gates(gt, p);

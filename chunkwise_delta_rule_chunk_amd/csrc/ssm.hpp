@@ -155,12 +155,6 @@ __device__ __forceinline__ uint4 frag_row(const T* p, int ld, int r0, int k0) {
 // the same with the rows of a 16-row block in slot order (below)
 template <typename T>
 __device__ __forceinline__ uint4 frag_row_slot(const T* p, int ld, int r0, int k0);
-// the same with the slot order of frag_acc
-template <typename T>
-__device__ __forceinline__ uint4 frag_row_acc(const T* p, int ld, int r0, int q) {
-  const int l = lane_id();
-  return perm_row<T>(p + (r0 + (l & 15)) * ld + 4 * (l >> 4), q);
-}
 // column c0 + (l & 15) of an LDS tile, contraction over its rows t0 .. t0 + KG - 1.
 // fp32: slot 4 (l >> 4) + e is row t0 + 4 (l >> 4) + e.  bf16: two transposing
 // reads, each of which gives lane l of a 16-lane group column l of the four rows
@@ -265,7 +259,8 @@ __device__ __forceinline__ void frag_split(uint4 (&out)[NS], const float (&f)[VE
   }
 }
 // Fragment q of a contraction over the rows of a matrix held as C fragments, acc[i]
-// = rows 16 i + 4 (l >> 4) .. + 3 (partner: frag_row_acc).
+// = rows 16 i + 4 (l >> 4) .. + 3 (partner: frag_row of a tile
+// that store_acc_order wrote).
 template <typename T, int NS, int NT>
 __device__ __forceinline__ void frag_acc(uint4 (&out)[NS], const f32x4 (&acc)[NT], int q) {
   float f[VEC<T>];
@@ -350,6 +345,18 @@ __device__ __forceinline__ void state_update(f32x4 (&S)[CT][K / 16], const T* sk
       }
     }
   }
+}
+
+// Whether a register tile holds an infinity or NaN (an exponent of ones).
+template <typename T, int C, int NTH>
+__device__ __forceinline__ bool tile_not_finite(const TileRegs<T, CH, C, NTH>& t) {
+  constexpr uint32_t EXP = std::is_same_v<T, bf16> ? 0x7f807f80u : 0x7f800000u;
+  constexpr uint32_t ONE = std::is_same_v<T, bf16> ? 0x00800080u : 0x00800000u;
+  uint32_t s = 0;  // (the largest exponent plus one reaches the sign's place)
+#pragma unroll
+  for (int j = 0; j < TileRegs<T, CH, C, NTH>::N; ++j)
+    s |= ((t.r[j].x & EXP) + ONE) | ((t.r[j].y & EXP) + ONE) | ((t.r[j].z & EXP) + ONE) | ((t.r[j].w & EXP) + ONE);
+  return (s & ((EXP + ONE) & 0x80008000u)) != 0;
 }
 
 // Block b = 0 .. 9 of the lower triangle of 4 x 4 blocks, row by row.

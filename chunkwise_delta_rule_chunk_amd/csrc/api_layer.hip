@@ -105,7 +105,7 @@ int conv_args(const rewy_conv_desc* d, ConvArgs& a) {
   if (!d) return fail(REWY_EINVAL, "desc is NULL");
   memset(&a, 0, sizeof(a));
   REWY_TRY(seq_args(d->B, d->T, d->N, d->cu_seqlens, d->cu_seqlens_host, a.seq));
-  if (d->D <= 0 || d->D > 1 << 24) return fail(REWY_EINVAL, "bad shape D=%d", d->D);
+  if (d->D <= 0 || d->D > 1 << 23) return fail(REWY_EINVAL, "bad shape D=%d", d->D);
   if (d->W < 2 || d->W > 4) return fail(d->W < 1 ? REWY_EINVAL : REWY_EUNSUPPORTED, "W=%d not supported (2 to 4 taps)", d->W);
   REWY_TRY(check_dtype("dtype", d->dtype));
   REWY_TRY(check_dtype("w_dtype", d->w_dtype));
@@ -115,6 +115,9 @@ int conv_args(const rewy_conv_desc* d, ConvArgs& a) {
   REWY_TRY(check_stride("y_stride", d->y_stride, d->D, a.ys));
   REWY_TRY(check_stride("dx_stride", d->dx_stride, d->D, a.dxs));
   conv_bwd_shape(a.seq.total, a.D, a.run, a.tiles);
+  // waves of the forward (runs half as long) and of a step: under 2^32 threads a launch
+  if ((2 * (int64_t)a.tiles + a.seq.N) * conv_cblocks(a.D) >= 1 << 26)
+    return fail(REWY_EUNSUPPORTED, "%d sequences and %d tokens of %d channels are too many", a.seq.N, a.seq.total, a.D);
   return REWY_OK;
 }
 size_t conv_ws(const ConvArgs& a) { return up(std::max<size_t>((size_t)a.tiles * (a.W + 1) * a.D * 4, 1)); }
@@ -132,6 +135,8 @@ int conv_forward(const rewy_conv_desc* d, bool step, const void* x, const void* 
   REWY_TRY(check_ptr("h0", h0, e, false));
   REWY_TRY(check_ptr("y", y, e, some));
   REWY_TRY(check_ptr("ht", ht, e, false));
+  if (!step && ht && ht == h0) return fail(REWY_EINVAL, "ht may not be h0");
+  if (!step && some && y == x) return fail(REWY_EINVAL, "y may not be x");
   if (!some && !ht) return REWY_OK;
   a.x = x; a.w = w; a.bias = bias; a.h0 = h0; a.y = y; a.ht = ht;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -183,11 +188,8 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
     return a.seq.cu ? total / L + a.seq.N : a.seq.N * std::max<int64_t>((a.seq.T + L - 1) / L, 1);
   };
   const int64_t nslot = slots(a.seg), nchunk = slots(CH);
-  if (nslot * a.H > INT32_MAX / 2 || nchunk * a.H > INT32_MAX / 2 || (int64_t)a.seq.N * a.H > INT32_MAX / 2)
-    return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
-                (long long)total, a.H);
-  a.nslot = (int)nslot;
-  a.nchunk = (int)nchunk;
+  a.nslot = (int)std::min<int64_t>(nslot, INT32_MAX);
+  a.nchunk = (int)std::min<int64_t>(nchunk, INT32_MAX);
   // Head ranges that share a group's dB and dC.  A workgroup of the chunk backward
   // fills a CU and costs about its heads plus one (its B and C tiles, the joint
   // products); the ranges are the ones with the shortest schedule on 256 CUs, and
@@ -200,6 +202,14 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
       a.split = sp;
     }
   }
+  // a launch takes fewer than 2^32 threads: gates and C B^T, the walks, the token-serial
+  // form and the pass, and the backward's chunks and sums
+  const int64_t threads[] = {(nchunk * a.H / 4 + nchunk * a.G + 1) * 256, nslot * a.H * 512, (int64_t)a.seq.N * a.H * 256,
+                             bwd ? nchunk * a.G * a.split * 512 : 0, bwd ? total * a.G * a.K / 4 + 256 : 0};
+  for (int64_t n : threads)
+    if (n >= (int64_t)1 << 32)
+      return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
+                  (long long)total, a.H);
   return REWY_OK;
 }
 
@@ -373,6 +383,8 @@ REWY_API int rewy_conv_bwd(const rewy_conv_desc* d, const void* x, const void* w
     REWY_TRY(check_ptr("dh0", dh0, e, h0 != nullptr));
     if ((bias != nullptr) != (dbias != nullptr)) return fail(REWY_EINVAL, "dbias must be given exactly when bias is");
     REWY_TRY(check_workspace(workspace, ws_bytes, conv_ws(a)));
+    if (some && (dx == x || dx == dy)) return fail(REWY_EINVAL, "dx may not be x or dy");
+    if (dh0 && (dh0 == h0 || dh0 == dht)) return fail(REWY_EINVAL, "dh0 may not be h0 or dht");
     a.x = x; a.w = w; a.bias = bias; a.h0 = h0; a.dy = dy; a.dht = dht;
     a.dx = dx; a.dw = dw; a.dbias = dbias; a.dh0 = dh0;
     a.part = static_cast<float*>(workspace);
@@ -457,6 +469,7 @@ REWY_API int rewy_ssm_bwd(const rewy_ssm_desc* d, const void* x, const void* dt,
     const bool f32 = d->dtype == REWY_F32;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     REWY_TRY(check_workspace(workspace, ws_bytes, ssm_layout(a, f32, true, static_cast<char*>(workspace))));
+    if (dh0 && (dh0 == h0 || dh0 == dht)) return fail(REWY_EINVAL, "dh0 may not be h0 or dht");
     a.dy = dy; a.dht = dht; a.dx = dx; a.ddt = ddt; a.da_log = da_log; a.ddt_bias = ddt_bias;
     a.db = db; a.dc = dc; a.dd = dD; a.dh0 = dh0;
     if (some) {

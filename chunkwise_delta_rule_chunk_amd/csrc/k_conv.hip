@@ -18,8 +18,6 @@ namespace rewy {
 
 namespace {
 
-constexpr int CONV_WAVES = 1;  // waves of one workgroup, side by side along the channels
-
 __device__ __forceinline__ float silu(float z) { return z * sigmoid_f(z); }
 
 // The sequence that token t < total belongs to: the largest n with start(n) <= t.
@@ -90,7 +88,7 @@ __device__ __forceinline__ void conv_final(const ConvArgs& a, int n, int c, int 
 // and stores through a buffer resource, whose range check drops the rows past the
 // run.  The compiler can then count the requests in flight (one counter serves
 // loads and stores) and a row's use waits for that row alone; with loads and stores
-// in branches it waited for all of them (3.2 instead of 4.5 TB/s forward).
+// in branches it waited for all of them (45 instead of 30 us for 8192 x 4352).
 template <typename T, bool FULL>
 struct Row {
   typename VecN<T, VE>::raw v;
@@ -132,10 +130,10 @@ constexpr int conv_group(int W) { return W == 3 ? 6 : 8; }
 
 // The rows of the next U tokens are in flight while one is worked on.
 template <typename T, typename WT, int W, bool FULL>
-__global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_fwd(ConvArgs a) {
+__global__ __launch_bounds__(64) void k_conv_fwd(ConvArgs a) {
   constexpr int U = conv_group(W);
   const int cb = blockIdx.x % a.cblocks, tile = blockIdx.x / a.cblocks;
-  const int c = (cb * 64 * CONV_WAVES + threadIdx.x) * VE, nv = a.D - c;
+  const int c = (cb * 64 + threadIdx.x) * VE, nv = a.D - c;
   if (nv <= 0) return;
   if (tile >= a.tiles) {  // a sequence's final state
     conv_final<T, W>(a, tile - a.tiles, c, nv);
@@ -267,10 +265,10 @@ __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv
 // U in flight); a token's dpre meets the W rows that it reached, and a row leaves
 // when the W - 1 tokens behind it have entered.
 template <typename T, typename WT, int W, bool FULL>
-__global__ __launch_bounds__(64 * CONV_WAVES) void k_conv_bwd(ConvArgs a) {
+__global__ __launch_bounds__(64) void k_conv_bwd(ConvArgs a) {
   constexpr int U = W == 3 ? 3 : 4;  // (more do not fit beside the windows and sums)
   const int cb = blockIdx.x % a.cblocks, tile = blockIdx.x / a.cblocks;
-  const int c = (cb * 64 * CONV_WAVES + threadIdx.x) * VE, nv = a.D - c;
+  const int c = (cb * 64 + threadIdx.x) * VE, nv = a.D - c;
   if (nv <= 0) return;
   if (tile >= a.tiles) {  // a sequence's initial state
     conv_dh0<T, WT, W>(a, tile - a.tiles, c, nv);
@@ -399,14 +397,12 @@ hipError_t conv_taps_of(int W, F&& f) {
     default: return hipErrorInvalidValue;
   }
 }
-// waves along the channels
-int conv_cblocks(int D) { return (D + 64 * VE - 1) / (64 * VE); }
 
 template <typename T, typename WT>
 hipError_t conv_fwd_t(const ConvArgs& a, hipStream_t s) {
   return conv_taps_of(a.W, [&](auto w) {
     const int fin = a.ht ? a.seq.N : 0;
-    const dim3 grid((a.tiles + fin) * a.cblocks), block(64 * CONV_WAVES);
+    const dim3 grid((a.tiles + fin) * a.cblocks), block(64);
     if (a.full) REWY_LAUNCH((k_conv_fwd<T, WT, decltype(w)::value, true>), grid, block, s, a);
     else REWY_LAUNCH((k_conv_fwd<T, WT, decltype(w)::value, false>), grid, block, s, a);
     return hipGetLastError();
@@ -424,7 +420,7 @@ hipError_t conv_bwd_t(const ConvArgs& a, hipStream_t s) {
   return conv_taps_of(a.W, [&](auto w) {
     constexpr int W = decltype(w)::value;
     const int fin = a.dh0 ? a.seq.N : 0;
-    const dim3 grid((a.tiles + fin) * a.cblocks), block(64 * CONV_WAVES);
+    const dim3 grid((a.tiles + fin) * a.cblocks), block(64);
     if (a.tiles + fin > 0) {
       if (a.full) REWY_LAUNCH((k_conv_bwd<T, WT, W, true>), grid, block, s, a);
       else REWY_LAUNCH((k_conv_bwd<T, WT, W, false>), grid, block, s, a);
@@ -444,9 +440,11 @@ int conv_run(int total, int cw, int most) {
   return run;
 }
 int conv_tiles(int total, int run) { return (int)(((int64_t)total + run - 1) / run); }
-int conv_gblocks(int cw) { return (cw + CONV_WAVES - 1) / CONV_WAVES; }
 
 }  // namespace
+
+// waves (workgroups) along the channels
+int conv_cblocks(int D) { return (D + 64 * VE - 1) / (64 * VE); }
 
 void conv_bwd_shape(int total, int D, int& run, int& tiles) {
   run = conv_run(total, conv_cblocks(D), 64);
@@ -465,7 +463,7 @@ hipError_t launch_conv_fwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
   const int cw = conv_cblocks(a.D);
   a.run = conv_run(a.seq.total, cw, 32);
   a.tiles = conv_tiles(a.seq.total, a.run);
-  a.cblocks = conv_gblocks(cw);
+  a.cblocks = cw;
   a.full = conv_full(a, f32 ? 4 : 2, a.y, a.ys);
   if (f32) return wf32 ? conv_fwd_t<float, float>(a, s) : conv_fwd_t<float, bf16>(a, s);
   return wf32 ? conv_fwd_t<bf16, float>(a, s) : conv_fwd_t<bf16, bf16>(a, s);
@@ -476,7 +474,7 @@ hipError_t launch_conv_step(const ConvArgs& a, bool f32, bool wf32, hipStream_t 
   return wf32 ? conv_step_t<bf16, float>(a, cb, s) : conv_step_t<bf16, bf16>(a, cb, s);
 }
 hipError_t launch_conv_bwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
-  a.cblocks = conv_gblocks(conv_cblocks(a.D));
+  a.cblocks = conv_cblocks(a.D);
   a.full = conv_full(a, f32 ? 4 : 2, a.dx, a.dxs);
   if (f32) return wf32 ? conv_bwd_t<float, float>(a, s) : conv_bwd_t<float, bf16>(a, s);
   return wf32 ? conv_bwd_t<bf16, float>(a, s) : conv_bwd_t<bf16, bf16>(a, s);

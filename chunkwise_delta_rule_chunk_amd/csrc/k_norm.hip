@@ -92,7 +92,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
   __shared__ float sbuf[BLOCK / 64];
   __shared__ uint32_t mbuf[BLOCK / 64];
   const int t = threadIdx.x % TPR;
-  const int64_t row = blockIdx.x * (int64_t)RPB + threadIdx.x / TPR;
+  const int64_t row = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
   const bool on = row < a.M;
   const int D = on ? a.D : 0;  // threads past the last row hold nothing and write nothing
   const int64_t m = on ? row : 0;
@@ -339,7 +339,9 @@ hipError_t norm_fwd_t(const NormArgs& a, hipStream_t s) {
   return norm_shape<T>(a.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
     constexpr int BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
-    REWY_LAUNCH((k_norm_fwd<T, W, TPR, NC>), dim3((unsigned)((a.M + RPB - 1) / RPB)), dim3(BLOCK), s, a);
+    // (a launch takes fewer than 2^32 threads along x)
+    const int64_t n = (a.M + RPB - 1) / RPB, gx = std::min<int64_t>(n, 1 << 20);
+    REWY_LAUNCH((k_norm_fwd<T, W, TPR, NC>), dim3((unsigned)gx, (unsigned)((n + gx - 1) / gx)), dim3(BLOCK), s, a);
     return hipGetLastError();
   });
 }

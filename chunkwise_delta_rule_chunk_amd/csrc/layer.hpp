@@ -114,7 +114,6 @@ __device__ __forceinline__ void seq_range(const SeqArgs& q, int n, int& bos, int
   eos = max(seq_start(q, n + 1), bos);
 }
 
-
 // ---- short convolution ------------------------------------------------------------
 struct ConvArgs {
   SeqArgs seq;
@@ -135,10 +134,11 @@ struct ConvArgs {
   void* dbias;
   int run;              // tokens of one wave's run
   int tiles;            // runs
-  int cblocks;          // workgroups along the channels
+  int cblocks;          // waves along the channels
   int full;             // no lane has a partial vector (k_conv.hip)
 };
-// tokens of one wave's run, and runs, of the backward
+// waves along the channels; tokens of one wave's run, and runs, of the backward
+int conv_cblocks(int D);
 void conv_bwd_shape(int total, int D, int& run, int& tiles);
 hipError_t launch_conv_fwd(ConvArgs a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs& a, bool f32, bool wf32, hipStream_t s);

@@ -14,6 +14,7 @@ import contextlib
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -120,7 +121,11 @@ class _On:
 def _workspace(nbytes, ref, ws):
     if nbytes == 0:  # (the call itself would refuse the descriptor)
         raise B.RewyError(B.REWY_EINVAL, "workspace size")
-    return torch.empty(nbytes, dtype=torch.uint8, device=ref.device) if ws is None else ws
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+    if ws.dtype != torch.uint8 or ws.get_device() != ref.get_device() or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {ref.device}")
+    return ws
 
 
 # ---- RMS norm -----------------------------------------------------------------
@@ -136,6 +141,8 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0, ou
     dt = _dtype(x, "x")
     if quant not in _QUANT:
         raise ValueError(f"quant must be None, 'e4m3' or 'int8' (got {quant!r})")
+    if group not in (0, 32, 64, 128, 256):
+        raise ValueError(f"group must be 0, 32, 64, 128 or 256 (got {group})")
     D = x.shape[-1]
     M = x.numel() // D if D else 0
     wdt = dt
@@ -199,6 +206,7 @@ class RMSNormFunction(torch.autograd.Function):
         return y, (s if residual is not None else x.view_as(x))
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dy, ds):
         s, weight, rstd = fctx.saved_tensors
         g = rms_norm_backward(dict(s=s, weight=weight, rstd=rstd, eps=fctx.eps), dy.contiguous(),
@@ -232,6 +240,13 @@ def _sequences(x, cu_seqlens, T):
     return len(vals) - 1, torch.tensor(vals, dtype=torch.int32, device=x.device), host
 
 
+def _rows(shape, ref, clear):
+    """A new tensor of ref's type on its device; ``clear``: of zeros.  (Autograd
+    clears where rows may follow the last sequence, with offsets that only the
+    GPU holds: their gradients go on into other products.)"""
+    return (torch.zeros if clear else torch.empty)(shape, dtype=ref.dtype, device=ref.device)
+
+
 # ---- short convolution ------------------------------------------------------------
 def _conv_problem(x, weight, bias, h0, activation, cu_seqlens):
     if x.dim() != 3:
@@ -254,15 +269,16 @@ def _conv_problem(x, weight, bias, h0, activation, cu_seqlens):
 
 
 def short_conv(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=None,
-               output_final_state=False, stream=None):
+               output_final_state=False, clear=False, stream=None):
     """Causal convolution of x [B, T, D] with weight [D, W] (W = 2 .. 4) along the
     tokens, bias [D] and SiLU (``activation=None``: none).  h0 [N, W-1, D] holds
     the rows before each sequence (oldest first).  Returns (y, ht or None,
     ctx); ht is the next call's h0, ctx feeds ``short_conv_backward``.  x may be
-    a slice of longer rows."""
+    a slice of longer rows.  A GPU cu_seqlens may end before T: y's rows behind
+    the last sequence are then not written, or zeros with ``clear``."""
     desc, hshape, cu, host = _conv_problem(x, weight, bias, h0, activation, cu_seqlens)
     with _On(x, stream, (x, weight, bias, h0, cu)) as handle:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _rows(x.shape, x, clear)
         ht = torch.empty(hshape, dtype=x.dtype, device=x.device) if output_final_state else None
         _check(B.rewy_conv_fwd(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(ht), handle),
                "rewy_conv_fwd")
@@ -288,9 +304,10 @@ def short_conv_step(x, h0, weight, bias=None, *, activation="silu", ht=None, str
     return y, ht
 
 
-def short_conv_backward(ctx, dy, dht=None, *, stream=None, ws=None):
+def short_conv_backward(ctx, dy, dht=None, *, clear=False, stream=None, ws=None):
     """Gradients of the convolution: dict(dx, dweight, dbias, dh0).  dy [B, T, D]
-    may have a token stride; dht [N, W-1, D] is the final state's adjoint."""
+    may have a token stride; dht [N, W-1, D] is the final state's adjoint; ``clear``
+    as in the forward, for dx."""
     x, weight, bias, h0 = (ctx[k] for k in ("x", "weight", "bias", "h0"))
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must have x's shape and type")
@@ -300,7 +317,7 @@ def short_conv_backward(ctx, dy, dht=None, *, stream=None, ws=None):
     desc = B.RewyConvDesc(d.B, d.T, d.D, d.W, d.N, d.cu_seqlens, d.cu_seqlens_host, d.dtype, d.w_dtype,
                           d.act, d.x_stride, _row_stride(dy, "dy", 1), 0)
     with _On(x, stream, (x, weight, bias, h0, ctx["cu"], dy, dht)) as handle:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _rows(x.shape, x, clear)
         dw = torch.empty_like(weight)
         db = None if bias is None else torch.empty_like(bias)
         dh0 = None if h0 is None else torch.empty_like(h0)
@@ -315,16 +332,18 @@ class ShortConvFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(fctx, x, weight, bias, h0, activation, cu_seqlens):
-        y, ht, ctx = short_conv(x, weight, bias, activation=activation, h0=h0,
-                                cu_seqlens=cu_seqlens, output_final_state=True)
+        fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
+        y, ht, ctx = short_conv(x, weight, bias, activation=activation, h0=h0, cu_seqlens=cu_seqlens,
+                                output_final_state=True, clear=fctx.clear)
         fctx.save_for_backward(x, weight, bias, h0)
         fctx.rewy = {k: ctx[k] for k in ("desc", "cu", "host")}
         return y, ht
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dy, dht):
         ctx = dict(fctx.rewy, **dict(zip(("x", "weight", "bias", "h0"), fctx.saved_tensors)))
-        g = short_conv_backward(ctx, dy.contiguous(), dht.contiguous())
+        g = short_conv_backward(ctx, dy.contiguous(), dht.contiguous(), clear=fctx.clear)
         return g["dx"], g["dweight"], g["dbias"], g["dh0"], None, None
 
 
@@ -360,16 +379,18 @@ def _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens):
 
 
 def selective_scan(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seqlens=None,
-                   output_final_state=True, stream=None, ws=None):
+                   output_final_state=True, clear=False, stream=None, ws=None):
     """y_t = S_t^T C_t + d x_t with S_t = exp(-exp(a_log) dt_t) S_{t-1} + dt_t B_t x_t^T
     and dt_t = softplus(dt + dt_bias), in chunks (prompts, training).
 
     x [B, T, H, V], b and c [B, T, G, K] (slices of longer rows allowed), dt [B, T, H]
     (before the softplus), a_log, d, dt_bias [H] fp32, h0 [N, H, K, V] fp32.
-    Returns (y, ht or None, ctx); ctx feeds ``selective_scan_backward``."""
+    Returns (y, ht or None, ctx); ctx feeds ``selective_scan_backward``.  A GPU
+    cu_seqlens may end before T: y's rows behind the last sequence are then not
+    written, or zeros with ``clear``."""
     desc, shape, cu, host = _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)
     with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, cu)) as handle:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _rows(x.shape, x, clear)
         ht = torch.empty(shape, dtype=torch.float32, device=x.device) if output_final_state else None
         ws = _workspace(B.rewy_ssm_workspace_bytes(desc, 0), x, ws)
         _check(B.rewy_ssm_fwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
@@ -393,10 +414,11 @@ def selective_scan_recurrent(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=Non
     return y, ht
 
 
-def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, stream=None, ws=None):
+def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, clear=False, stream=None, ws=None):
     """Gradients of the scan: dict(dx, ddt, da_log, db, dc, dd, ddt_bias, dh0).
     dy may be a slice of longer rows.  ``out=(dx, db, dc)`` gives the places of
-    those three (slices of one row, for the convolution's backward)."""
+    those three (slices of one row, for the convolution's backward); ``clear`` as in
+    the forward, for the gradients that are made here."""
     x, dt, a_log, b, c, d, dt_bias, h0 = (ctx[k] for k in ("x", "dt", "a_log", "b", "c", "d", "dt_bias",
                                                            "h0"))
     if dy.shape != x.shape or dy.dtype != x.dtype:
@@ -412,12 +434,12 @@ def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, strea
                 raise ValueError(f"{name} must have the shape and type of its input")
     with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, ctx["cu"], dy, dht, *(out or ()))) as handle:
         if out is None:
-            out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (x, b, c))
+            out = tuple(_rows(t.shape, t, clear) for t in (x, b, c))
         dx, db, dc = out
         desc = B.RewySsmDesc(f.B, f.T, f.H, f.G, f.K, f.V, f.N, f.cu_seqlens, f.cu_seqlens_host, f.dtype,
                              f.dt_dtype, f.x_stride, f.b_stride, f.c_stride, _row_stride(dy, "dy", 2),
                              _row_stride(dx, "dx", 2), _row_stride(db, "db", 2), _row_stride(dc, "dc", 2))
-        ddt, da_log = torch.empty_like(dt), torch.empty_like(a_log)
+        ddt, da_log = _rows(dt.shape, dt, clear), torch.empty_like(a_log)
         dd = None if d is None else torch.empty_like(d)
         ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
         dh0 = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dh0 else None
@@ -433,16 +455,19 @@ class SelectiveScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(fctx, x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens):
-        y, ht, ctx = selective_scan(x, dt, a_log, b, c, d=d, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens)
+        fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
+        y, ht, ctx = selective_scan(x, dt, a_log, b, c, d=d, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
+                                    clear=fctx.clear)
         fctx.save_for_backward(x, dt, a_log, b, c, d, dt_bias, h0)
         fctx.rewy = {k: ctx[k] for k in ("desc", "cu", "host")}
         return y, ht
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dy, dht):
         names = ("x", "dt", "a_log", "b", "c", "d", "dt_bias", "h0")
         g = selective_scan_backward(dict(fctx.rewy, **dict(zip(names, fctx.saved_tensors))), dy.contiguous(),
-                                    dht.contiguous())
+                                    dht.contiguous(), clear=fctx.clear)
         return (g["dx"], g["ddt"], g["da_log"], g["db"], g["dc"], g["dd"], g["ddt_bias"], g["dh0"], None)
 
 

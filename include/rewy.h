@@ -234,8 +234,9 @@ int rewy_bwd_schedule(int schedule);
  * (weights, biases, A_log, D) are small contiguous tensors.  Sums, statistics
  * and states are fp32; every output is rounded once, to nearest even.  With
  * cu_seqlens, rows behind the last sequence (cu_seqlens[N] < T) belong to none:
- * they are not read, and what an output holds there stays.  No atomics: results
- * are bitwise reproducible for a given shape and device. */
+ * they are not read, and what an output holds there stays.  An output may
+ * overlap an input or another output only where that is said.  No atomics:
+ * results are bitwise reproducible for a given shape and device. */
 
 /* RMS norm with the residual's addition and an 8-bit output:
  *     s = x + res,  rstd = (mean(s^2) + eps)^-1/2,  y = s * rstd * w,
@@ -297,13 +298,12 @@ typedef struct {
     int64_t x_stride, y_stride, dx_stride; /* between tokens, in elements; 0 = D (y_stride: y and dy) */
 } rewy_conv_desc;
 
-/* Forward.  w is [D, W]; bias [D], h0 and ht may be NULL.  ht may not overlap
- * an input. */
+/* Forward.  w is [D, W]; bias [D], h0 and ht may be NULL. */
 int rewy_conv_fwd(const rewy_conv_desc *d, const void *x, const void *w, const void *bias,
                   const void *h0, void *y, void *ht, void *stream);
 
 /* One token for each of N = B sequences (T == 1, no cu_seqlens): the forward
- * with the state read and written in one pass; ht may be h0 itself. */
+ * with the state read and written in one pass; ht may be h0 itself, y x. */
 int rewy_conv_step(const rewy_conv_desc *d, const void *x, const void *w, const void *bias,
                    const void *h0, void *y, void *ht, void *stream);
 
@@ -353,7 +353,8 @@ typedef struct {
 size_t rewy_ssm_workspace_bytes(const rewy_ssm_desc *d, int phase);
 
 /* Forward in chunks of 64 tokens, for prompts and training.  h0 and ht may be
- * NULL; ht may not overlap h0. */
+ * NULL.  An infinity or NaN in a token's row reaches that token and the ones
+ * behind it, as in the recurrence. */
 int rewy_ssm_fwd(const rewy_ssm_desc *d, const void *x, const void *dt, const float *a_log,
                  const float *dt_bias, const void *b, const void *c, const float *D,
                  const float *h0, void *y, float *ht,
@@ -361,7 +362,8 @@ int rewy_ssm_fwd(const rewy_ssm_desc *d, const void *x, const void *dt, const fl
 
 /* Backward (the forward's states are formed again; nothing is kept between the
  * calls).  dht may be NULL; dh0 must be given when h0 is; ddt_bias and dD are given
- * exactly when dt_bias and D are.  Outputs are overwritten. */
+ * exactly when dt_bias and D are.  Outputs are overwritten.  Inputs are finite: an
+ * infinity or NaN may reach every gradient of its sequence. */
 int rewy_ssm_bwd(const rewy_ssm_desc *d, const void *x, const void *dt, const float *a_log,
                  const float *dt_bias, const void *b, const void *c, const float *D,
                  const float *h0, const void *dy, const float *dht,

@@ -110,6 +110,35 @@ def test_conv_pointers():
     assert bwd(n=need - 1) == B.REWY_EWORKSPACE and bwd(ws=None) == B.REWY_EWORKSPACE
 
 
+def test_conv_overlaps_and_sizes():
+    """Runs read their neighbours' rows, so nothing is formed in place but a step's."""
+    A = [P(256 * (i + 1)) for i in range(12)]
+    assert B.rewy_conv_fwd(_conv(), A[0], A[1], None, A[2], A[0], None, None) == B.REWY_EINVAL and "y may not" in B.rewy_last_error()
+    assert B.rewy_conv_fwd(_conv(), A[0], A[1], None, A[2], A[3], A[2], None) == B.REWY_EINVAL and "ht may not" in B.rewy_last_error()
+    need = B.rewy_conv_workspace_bytes(_conv())
+    for dx, dh0, msg in ((0, 7, "dx may not"), (4, 7, "dx may not"), (6, 2, "dh0 may not"), (6, 5, "dh0 may not")):
+        rc = B.rewy_conv_bwd(_conv(), A[0], A[1], A[3], A[2], A[4], A[5], A[dx], A[8], A[9], A[dh0], A[10], need, None)
+        assert rc == B.REWY_EINVAL and msg in B.rewy_last_error(), msg
+    for kw in (dict(B=1 << 26, T=1, D=1), dict(B=1 << 20, T=1, D=1 << 14), dict(D=(1 << 23) + 1)):
+        assert B.rewy_conv_workspace_bytes(_conv(**kw)) == 0, kw
+    assert B.rewy_conv_workspace_bytes(_conv(B=1, T=1 << 30, D=1)) > 0
+
+
+def test_ssm_sizes_and_overlaps():
+    """More workgroups than a launch takes are refused, not left to the launch."""
+    for kw in (dict(B=1 << 22, T=1, H=8, G=8, K=32, V=32), dict(B=1, T=1 << 30, H=64, G=64, K=32, V=32)):
+        for phase in (0, 1):
+            assert B.rewy_ssm_workspace_bytes(_ssm(**kw), phase) == 0 and "too many" in B.rewy_last_error()
+    assert B.rewy_ssm_workspace_bytes(_ssm(B=1, T=1 << 24, H=32, G=1, K=128, V=64), 0) > 0
+    assert B.rewy_ssm_workspace_bytes(_ssm(B=1, T=1 << 20, H=64, G=8, K=128, V=64), 1) > 0
+    A = [P(256 * (i + 1)) for i in range(24)]
+    need = B.rewy_ssm_workspace_bytes(_ssm(), 1)
+    for dh0 in (7, 9):
+        # x dt a_log dt_bias b c D h0, dy dht, dx ddt da_log ddt_bias db dc dD dh0
+        rc = B.rewy_ssm_bwd(_ssm(), *A[:8], A[8], A[9], *A[10:17], A[dh0], A[20], need, None)
+        assert rc == B.REWY_EINVAL and "dh0 may not" in B.rewy_last_error()
+
+
 def _ssm(**kw):
     d = dict(B=2, T=100, H=4, G=2, K=64, V=32, N=0, cu=None, host=None, dtype=B.REWY_BF16, dt_dtype=B.REWY_F32,
              x_stride=0, b_stride=0, c_stride=0, y_stride=0, dx_stride=0, db_stride=0, dc_stride=0)
@@ -179,6 +208,8 @@ def test_wrappers_refuse():
         L.rms_norm(x.half(), w)
     with pytest.raises(ValueError, match="quant"):
         L.rms_norm(x, w, quant="int4")
+    with pytest.raises(ValueError, match="group"):
+        L.rms_norm(x, w, quant="int8", group=-1)
     with pytest.raises(ValueError, match="weight must have shape"):
         L.rms_norm(x, torch.zeros(7))
     with pytest.raises(ValueError, match="residual"):

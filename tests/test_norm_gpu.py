@@ -201,3 +201,17 @@ def test_autograd():
     (yd.square().sum() + sd.sum()).backward()
     for a, b in ((x, xd), (r, rd), (w, wd)):
         assert (a.grad.double() - b.grad).norm() <= 1e-5 * b.grad.norm()
+
+
+def test_more_rows_than_a_launch_has_threads():
+    """2^28 + 5 short rows (over 2^32 threads): the first and the last rows are what they are alone."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    M = (1 << 28) + 5
+    x = torch.empty(M, 2, dtype=torch.bfloat16, device="cuda")
+    x[:1000], x[-1000:] = 1.0, 3.0
+    x[-1, 1] = -2.0
+    y, _, _, _, ctx = ops.rms_norm(x)
+    for cut in (slice(0, 1000), slice(M - 1000, M)):
+        part = x[cut].contiguous()
+        yp, _, _, _, cp = ops.rms_norm(part)
+        assert torch.equal(y[cut], yp) and torch.equal(ctx["rstd"][cut], cp["rstd"])

@@ -117,6 +117,12 @@ CASES = [
     (1, 600, 2, 2, 32, 32, "bf16", "fp32", [0, 1, 64, 65, 0, 0, 300, 127, 43, 0], True, "usual"),
     (1, 900, 3, 1, 64, 64, "fp32", "fp32", [299, 1, 600], True, "usual"),
     (1, 40, 4, 4, 128, 64, "bf16", "bf16", [1] * 40, False, "usual"),
+    # one head a workgroup, and head blocks that a group does not fill, of every width
+    (1, 100, 2, 2, 128, 32, "bf16", "fp32", None, True, "usual"),
+    (1, 300, 5, 1, 32, 32, "bf16", "bf16", None, True, "usual"),
+    (1, 300, 9, 3, 64, 64, "bf16", "fp32", None, True, "usual"),
+    (2, 300, 3, 1, 32, 32, "fp32", "bf16", None, True, "usual"),
+    (1, 520, 2, 2, 64, 32, "fp32", "fp32", [520], False, "none"),
 ]
 
 
@@ -284,3 +290,74 @@ def test_no_tokens_and_one_long_sequence():
     yr, htr = ops.selective_scan_recurrent(*args, **kw)
     assert (ht - htr).norm() <= 1e-5 * htr.norm()
     assert (y.float() - yr.float()).norm() <= 2.0 ** -7 * yr.float().norm()
+
+
+@pytest.mark.parametrize("K,V,H,dtype", [(128, 128, 2, "bf16"), (64, 64, 3, "bf16"), (32, 32, 5, "bf16"), (64, 32, 3, "fp32")])
+def test_not_finite_values_reach_no_earlier_token(K, V, H, dtype):
+    """A padded batch whose rows behind a row's tokens hold anything: y before them as without; y of the
+    column from the first such x on is not finite."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    B, T = 3, 150
+    args, kw, _, _ = _inputs(B, T, H, 1, K, V, dtype, "fp32", 11, B)
+    y0, _, _ = ops.selective_scan(*args, **kw)
+    x, dt, al, b, c = (t.clone() for t in args)
+    ends = [149, 65, 3]
+    for n, (e, bad) in enumerate(zip(ends, (float("nan"), float("inf"), -float("inf")))):
+        for t in (x, dt, b, c):
+            t[n, e:] = bad
+    y1, _, _ = ops.selective_scan(x, dt, al, b, c, **kw)
+    for n, e in enumerate(ends):
+        assert torch.equal(y0[n, :e], y1[n, :e])
+    # one value of x only: its column from its token on, and nothing else
+    x = args[0].clone()
+    x[1, 70, 1, 5], x[1, 20, 1, 6] = float("inf"), float("nan")
+    y2, h2, _ = ops.selective_scan(x, *args[1:], **kw)
+    same = torch.ones_like(y0, dtype=torch.bool)
+    same[1, 70:, 1, 5] = same[1, 20:, 1, 6] = False
+    assert torch.equal(y2[same], y0[same]) and not torch.isfinite(y2[~same]).any()
+    bad = torch.zeros_like(h2, dtype=torch.bool)
+    bad[1, 1, :, 5:7] = True
+    assert torch.equal(~torch.isfinite(h2), bad)
+
+
+def test_autograd_clears_rows_behind_the_last_sequence():
+    """Offsets that only the GPU holds may end before T: such rows have zero gradients, whatever the
+    allocator's memory held."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    args, kw, _, _ = _inputs(1, 90, 2, 1, 32, 32, "bf16", "fp32", 5, 1)
+    cu = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    leaves = [t.requires_grad_(True) for t in (*args, kw["h0"])]
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]
+    del junk
+    y, ht = ops.selective_scan_autograd(*args, **kw, cu_seqlens=cu)
+    assert (y[:, 70:] == 0).all()
+    (y.float().sum() + ht.sum()).backward()
+    for t in leaves:
+        assert torch.isfinite(t.grad).all()
+    for t in (args[0], args[1], args[3], args[4]):
+        assert (t.grad[:, 70:] == 0).all() and (t.grad[:, :70] != 0).any()
+    x = torch.randn(1, 50, 24, device="cuda").requires_grad_(True)
+    w = torch.randn(24, 4, device="cuda").requires_grad_(True)
+    cu = torch.tensor([0, 20, 31], dtype=torch.int32, device="cuda")
+    y, _ = ops.short_conv_autograd(x, w, cu_seqlens=cu)
+    assert (y[:, 31:] == 0).all()
+    y.sum().backward()
+    assert (x.grad[:, 31:] == 0).all() and torch.isfinite(x.grad).all() and torch.isfinite(w.grad).all()
+
+
+def test_second_derivatives_and_workspaces_are_refused():
+    from chunkwise_delta_rule_chunk_amd import ops
+    args, kw, dy, dht = _inputs(1, 70, 2, 1, 32, 32, "bf16", "fp32", 5, 1)
+    x = args[0].requires_grad_(True)
+    y, _ = ops.selective_scan_autograd(x, *args[1:], **kw)
+    g, = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.float().sum().backward()
+    ctx = ops.selective_scan(*(t.detach() for t in args), **kw)[2]
+    with pytest.raises(ValueError, match="ws must be"):
+        ops.selective_scan_backward(ctx, dy, dht, ws=torch.empty(1 << 24, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="ws must be"):
+        ops.selective_scan(*(t.detach() for t in args), **kw, ws=torch.empty(1 << 24, device="cuda"))
+    from chunkwise_delta_rule_chunk_amd.binding import RewyError
+    with pytest.raises(RewyError, match="workspace"):
+        ops.selective_scan(*(t.detach() for t in args), **kw, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))

@@ -241,7 +241,8 @@ size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
     take(a.ri, tok);
     take(a.ci, tok);
     take(a.cd, tok);
-    take(a.ends, (size_t)a.nslot * a.H * 4);
+    take(a.ends, (size_t)a.nslot * a.H * 8);
+    take(a.hdot, (size_t)a.nchunk * a.H * 4);
     take(a.dpart, (size_t)a.nchunk * a.H * 4);
     take(a.apart, (size_t)a.nchunk * 2 * a.H * 8);
     if (a.split > 1) take(a.bcpart, (size_t)2 * a.split * a.seq.total * a.G * a.K * 4);
@@ -485,7 +486,7 @@ REWY_API int rewy_ssm_bwd(const rewy_ssm_desc* d, const void* x, const void* dt,
     } else {
       REWY_TRY(state_through(a, dh0, dht, s));
     }
-    REWY_TRY(hip_check(traced("k_ssm_gate", s, [&] { return launch_ssm_gate(a, s); }), "scan gate backward"));
+    REWY_TRY(hip_check(traced("k_ssm_gate", s, [&] { return launch_ssm_gate(a, f32, s); }), "scan gate backward"));
     return hip_check(traced("k_ssm_params", s, [&] { return launch_ssm_params(a, s); }), "parameter gradients");
   });
 }

@@ -32,7 +32,8 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
   __shared__ __align__(16) T su[CH * LV];  // update: x, dy
   __shared__ __align__(16) T sp[CH * LV];  // probe: dy, x
   __shared__ __align__(16) float sal[HB][CH], sdot[NW][CH];
-  __shared__ float sdec[HB], sred[NW];
+  __shared__ float sdec[HB];
+  __shared__ double sred[NW];
   const int dir = blockIdx.y;
   const int nhb = head_blocks(a, HB), wk = xcd_range(blockIdx.x, a.nslot * nhb), slot = wk / nhb, hb = wk - slot * nhb;
   const Piece pc = find_piece(a.seq, slot, a.seg);
@@ -136,20 +137,21 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
   if (dir == 0) {
     // <S, dS> at the segment's end
     const float* adj = a.two && nch > 0 ? a.sr + segst : a.dht ? a.dht + seqst : nullptr;
-    float d = 0.f;
+    double d = 0.;
     if (adj) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d += S[ct][nt][i] * adj[(16 * nt + 4 * g4 + i) * V + 16 * ct];
+          for (int i = 0; i < 4; ++i) d += (double)S[ct][nt][i] * adj[(16 * nt + 4 * g4 + i) * V + 16 * ct];
     }
-    d = rows_sum(row16_sum(d));
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) d += __shfl_xor(d, m, 64);
     if (l == 0) sred[w] = d;
     lds_barrier();
     if (w < nh && l == 0) {
-      d = 0.f;
+      d = 0.;
       for (int i = 0; i < WH; ++i) d += sred[w * WH + i];
       a.ends[(int64_t)slot * a.H + h0 + w] = d;
     }
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   __shared__ __align__(16) T sd[V * LK];   // dS^T, the same
   __shared__ __align__(16) T sm[CH * LM];  // M0^T (columns in slot order), at the end W^T, then W
   __shared__ __align__(16) float sG[CH], sGl[CH], sdt[CH], seG[CH], seE[CH], tG[CH], tGl[CH];  // t: in slot order
-  __shared__ float srp[4][CH], scp[4][CH], scd[CH], sdd[CB_WAVES];
+  __shared__ float srp[4][CH], scp[4][CH], scd[CH], sdd[CB_WAVES], shd[CB_WAVES];
   const int nwork = a.nchunk * a.G * a.split;
   int wk = xcd_range(blockIdx.x, nwork);
   const int part = wk % a.split;
@@ -253,6 +255,21 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
     ry.store(sy, LV, threadIdx.x);
     put_state(ss, rs);
     put_state(sd, rd);
+    {
+      float hd = 0.f;
+#pragma unroll
+      for (int j = 0; j < TileRegs<T, V, K, NTH>::N; ++j) {
+        float u[VEC<T>], v[VEC<T>];
+        frag_get<T>(u, rs.r[j]);
+        frag_get<T>(v, rd.r[j]);
+        if (threadIdx.x + j * NTH < TileRegs<T, V, K, NTH>::TOTAL) {
+#pragma unroll
+          for (int e = 0; e < VEC<T>; ++e) hd += u[e] * v[e];
+        }
+      }
+      hd = rows_sum(row16_sum(hd));
+      if (l == 0) shd[w] = hd;
+    }
     if (w == 0) {
       sG[l] = tG[slot_of<T>(l)] = gt.G;
       sGl[l] = tGl[slot_of<T>(l)] = gt.Glo;
@@ -317,6 +334,11 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       float s = 0.f;
       for (int i = 0; i < CB_WAVES; ++i) s += sdd[i];
       a.dpart[(int64_t)cslot * a.H + h] = s;
+    }
+    if (w == 2 && l == 0) {
+      float s = 0.f;
+      for (int i = 0; i < CB_WAVES; ++i) s += shd[i];
+      a.hdot[(int64_t)cslot * a.H + h] = s;
     }
     // dX^T, rows p of this wave's half, columns j = 16 tb + r
     {
@@ -448,12 +470,17 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 // over what passes token t's decay: the entering state into the rows i >= t (rx), the
 // rows j < t into the leaving state (dt cx), the pairs j < t <= i of the chunk (the
 // suffix sum of ri - dt ci, in which pairs on one side cancel), and what goes from the
-// entering into the leaving state, H = exp(G_L) <S_in, dS>.  With E = <S, dS> at a
-// chunk's end, H = E - sum dt cx, and E one chunk earlier is H + sum rx: from the
-// segment's end, where E is known, to this chunk.  Where the chunk's decay is
-// under 2^-30, H is nothing beside the rounding of E and is taken as 0, so that heads
-// with a strong decay, whose dg is far smaller than E, do not inherit that rounding.
+// entering into the leaving state, H = exp(G_L) <S_in, dS>.
+// H is small beside E = <S_out, dS> where a chunk decays strongly, and dg_t is
+// multiplied by a g_t that is large there, so it may not inherit the rounding of E: it
+// is formed from the states that the chunk backward read (fp32: always).  As bf16
+// these give it to about 2^-9, so a decay over DIRECT takes it as E - sum dt cx
+// instead; E one chunk earlier is H + sum rx: from the next chunk that needs no E,
+// or from the segment's end, where the walk formed E, to this chunk.
+template <typename T>
 __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
+  // log2 of the decay: 2^-12 2^-9 is about the rounding of E and of the sum
+  constexpr float DIRECT = std::is_same_v<T, bf16> ? -12.f : 1.f;
   const int wk = blockIdx.x * 4 + wave_id(), l = lane_id();
   if (wk >= a.nchunk * a.H) return;
   const int cslot = wk / a.H, h = wk - cslot * a.H;
@@ -473,10 +500,13 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
     return v;
   };
-  double E = a.ends[((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h];
+  const int most = (t2 - t0 - 1) / CH;
+  int c = 0;
+  while (c < most && chunk_gates(a, cslot + c, h)[CH - 1].G >= DIRECT) ++c;
+  double E = a.ends[((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h];  // (used if no chunk up to the end needs none)
   float dt = 0.f, z = 0.f;
   double rx = 0., dcx = 0., H = 0.;  // this chunk's own at the loop's end
-  for (int c = (t2 - t0 - 1) / CH; c >= 0; --c) {
+  for (; c >= 0; --c) {
     const int t = t0 + c * CH + l;
     const Gate* g = chunk_gates(a, cslot + c, h);
     dt = 0.f;
@@ -486,7 +516,8 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
       rx = a.rx[row + t];
       dcx = (double)dt * a.cx[row + t];
     }
-    H = g[CH - 1].G < -30.f ? 0. : E - wave_sum(dcx);
+    const float GL = g[CH - 1].G;
+    H = GL < DIRECT ? (double)fexp2(GL) * a.hdot[(int64_t)(cslot + c) * a.H + h] : E - wave_sum(dcx);
     E = H + wave_sum(rx);
   }
   const int t = t0 + l;
@@ -583,8 +614,10 @@ hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s) {
     return hipGetLastError();
   });
 }
-hipError_t launch_ssm_gate(const SsmArgs& a, hipStream_t s) {
-  REWY_LAUNCH(k_ssm_gate, dim3((a.nchunk * a.H + 3) / 4), dim3(256), s, a);
+hipError_t launch_ssm_gate(const SsmArgs& a, bool f32, hipStream_t s) {
+  const dim3 grid((a.nchunk * a.H + 3) / 4);
+  if (f32) REWY_LAUNCH((k_ssm_gate<float>), grid, dim3(256), s, a);
+  else REWY_LAUNCH((k_ssm_gate<bf16>), grid, dim3(256), s, a);
   return hipGetLastError();
 }
 hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s) {

@@ -59,7 +59,8 @@ struct SsmArgs {
   float* ri;               // [H, tokens] row part inside the chunk (i > j)
   float* ci;               // [H, tokens] column part inside the chunk (i > j)
   float* cd;               // [H, tokens] the term i = j, which belongs to c and cancels in the decay gradient
-  float* ends;             // [nslot, H] <state, adjoint> at each segment's end
+  double* ends;            // [nslot, H] <state, adjoint> at each segment's end
+  float* hdot;             // [nchunk, H] <S_in, dS> of the handed-over states
   float* dpart;            // [nchunk, H] partial sums of dD
   double* apart;           // [nchunk, 2, H] partial sums of dA_log and ddt_bias
   float* bcpart;           // [2, split, tokens, G, K] partial sums of dB and dC (split > 1)
@@ -72,7 +73,7 @@ hipError_t launch_ssm_pass(const SsmArgs& a, bool both, hipStream_t s);
 hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_walk(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s);
-hipError_t launch_ssm_gate(const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_gate(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_recurrent(const SsmArgs& a, bool f32, hipStream_t s);
@@ -316,9 +317,9 @@ __device__ __forceinline__ void state_update(f32x4 (&S)[CT][K / 16], const T* sk
                                              const uint4 (&ut)[CT][CH / KG<T>], const float* sal, float dec) {
   constexpr int NQ = CH / KG<T>, VE = VEC<T>;
   const int g = lane_id() >> 4;
+  uint4 uf[CT][NQ][NS];
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    uint4 uf[CT][NS];
+  for (int q = 0; q < NQ; ++q)
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       float f[VE];
@@ -329,21 +330,26 @@ __device__ __forceinline__ void state_update(f32x4 (&S)[CT][K / 16], const T* sk
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[e + i] *= al[i];
       }
-      frag_split<T, NS>(uf[ct], f);
+      frag_split<T, NS>(uf[ct][q], f);
     }
 #pragma unroll
-    for (int nt = 0; nt < K / 16; ++nt) {
-      const uint4 kf = frag_col<T>(sk, ldk, q * KG<T>, 16 * nt);
+  for (int nt = 0; nt < K / 16; ++nt) {
+    f32x4 u[CT];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        if (q == 0) {
+    for (int ct = 0; ct < CT; ++ct) u[ct] = zero4();
+    uint4 kf[NQ];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[ct][nt][i] *= dec;
-        }
+    for (int q = 0; q < NQ; ++q) kf[q] = frag_col<T>(sk, ldk, q * KG<T>, 16 * nt);
 #pragma unroll
-        for (int s = NS - 1; s >= 0; --s) mma16B<T>(S[ct][nt], kf, uf[ct][s]);
-      }
-    }
+    for (int s = NS - 1; s >= 0; --s)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) mma16B<T>(u[ct], kf[q], uf[ct][q][s]);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[ct][nt][i] = dec * S[ct][nt][i] + u[ct][i];
   }
 }
 

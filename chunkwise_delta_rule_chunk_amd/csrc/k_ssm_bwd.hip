@@ -135,7 +135,8 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
     }
   }
   if (dir == 0) {
-    // <S, dS> at the segment's end
+    if constexpr (!std::is_same_v<T, bf16>) return;  // (k_ssm_gate needs no E)
+    // E = <S, dS> at the segment's end
     const float* adj = a.two && nch > 0 ? a.sr + segst : a.dht ? a.dht + seqst : nullptr;
     double d = 0.;
     if (adj) {
@@ -474,9 +475,11 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 // H is small beside E = <S_out, dS> where a chunk decays strongly, and dg_t is
 // multiplied by a g_t that is large there, so it may not inherit the rounding of E: it
 // is formed from the states that the chunk backward read (fp32: always).  As bf16
-// these give it to about 2^-9, so a decay over DIRECT takes it as E - sum dt cx
-// instead; E one chunk earlier is H + sum rx: from the next chunk that needs no E,
-// or from the segment's end, where the walk formed E, to this chunk.
+// these give it to about 2^-9, so a decay over DIRECT takes it from E instead: H = E -
+// sum dt cx, and E one chunk earlier is H + sum rx, or the other way round.  E is
+// known where the walks meet, at the ends of the segments, and behind and before a
+// chunk that needs no E; the nearest of these is taken, as every chunk in between adds
+// its rounding.
 template <typename T>
 __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
   // log2 of the decay: 2^-12 2^-9 is about the rounding of E and of the sum
@@ -500,29 +503,57 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
     return v;
   };
-  const int most = (t2 - t0 - 1) / CH;
-  int c = 0;
-  while (c < most && chunk_gates(a, cslot + c, h)[CH - 1].G >= DIRECT) ++c;
-  double E = a.ends[((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h];  // (used if no chunk up to the end needs none)
   float dt = 0.f, z = 0.f;
-  double rx = 0., dcx = 0., H = 0.;  // this chunk's own at the loop's end
-  for (; c >= 0; --c) {
+  double rx = 0., dcx = 0., srx = 0., sdcx = 0.;  // a chunk's, by token and summed; last this chunk's
+  auto sums = [&](int c) {  // of chunk ci + c
     const int t = t0 + c * CH + l;
-    const Gate* g = chunk_gates(a, cslot + c, h);
     dt = 0.f;
     rx = dcx = 0.;
     if (t < t2) {
-      dt = g[l].dt;
+      dt = chunk_gates(a, cslot + c, h)[l].dt;
       rx = a.rx[row + t];
       dcx = (double)dt * a.cx[row + t];
     }
-    const float GL = g[CH - 1].G;
-    H = GL < DIRECT ? (double)fexp2(GL) * a.hdot[(int64_t)(cslot + c) * a.H + h] : E - wave_sum(dcx);
-    E = H + wave_sum(rx);
+    srx = wave_sum(rx);
+    sdcx = wave_sum(dcx);
+  };
+  auto direct = [&](int c) {
+    return (double)fexp2(chunk_gates(a, cslot + c, h)[CH - 1].G) * a.hdot[(int64_t)(cslot + c) * a.H + h];
+  };
+  double H;
+  if constexpr (std::is_same_v<T, bf16>) {
+    const int ci = pc.k - k * per, nc = ci + (t2 - t0 + CH - 1) / CH;  // this chunk, chunks of the segment
+    const uint64_t none = __ballot(l < nc && chunk_gates(a, cslot - ci + min(l, nc - 1), h)[CH - 1].G < DIRECT);
+    const uint64_t later = none >> ci, before = none << (63 - ci);
+    const double* ends = a.ends + ((int64_t)slot_base(a.seq, pc.n, a.seg) + k) * a.H + h;
+    const int up = later ? __builtin_ctzll(later) : nc - 1 - ci;
+    const int down = before ? __builtin_clzll(before) : k > 0 || !a.h0 ? ci : SEG_CHUNKS;
+    double E = 0.;
+    bool known = true;
+    if (up <= down) {
+      if (later) H = direct(up);
+      else E = *ends, known = false;
+      for (int c = up; c >= 0; --c) {
+        sums(c);
+        if (c < up || !known) H = E - sdcx;
+        E = H + srx;
+      }
+    } else {
+      if (before) H = direct(-down);
+      else E = k > 0 ? ends[-a.H] : 0., known = false;
+      for (int c = -down; c <= 0; ++c) {
+        sums(c);
+        if (c > -down || !known) H = E - srx;
+        E = H + sdcx;
+      }
+    }
+  } else {
+    sums(0);
+    H = direct(0);
   }
   const int t = t0 + l;
   const bool on = t < t1;
-  double cc = 0., s = rx, before = dcx;
+  double cc = 0., s = rx, pre = dcx;
   if (on) {
     z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
     const float ci = a.ci[row + t];
@@ -531,14 +562,14 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    const double u = __shfl_down(s, d, 64), v = __shfl_up(before, d, 64);
+    const double u = __shfl_down(s, d, 64), v = __shfl_up(pre, d, 64);
     if (l + d < 64) s += u;
-    if (l >= d) before += v;
+    if (l >= d) pre += v;
   }
-  before -= dcx;
+  pre -= dcx;
   double dA = 0., db = 0.;
   if (on) {
-    const double A = -exp((double)a.a_log[h]), dg = H + s + before;
+    const double A = -exp((double)a.a_log[h]), dg = H + s + pre;
     const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
     db = (cc + A * dg) * sg;
     st_beta(a.ddt, a.dt_f32, (int64_t)t * a.H + h, (float)db);

@@ -78,6 +78,9 @@ hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_recurrent(const SsmArgs& a, bool f32, hipStream_t s);
 
+// chunks of a segment of the bf16 backward: 512 tokens (k_ssm_gate's chains)
+constexpr int SEG_CHUNKS = 8;
+
 // ---- slots --------------------------------------------------------------------
 // Pieces of L tokens of every sequence, numbered without a table.  Sequences of
 // one length take ceil(T / L) slots each (at least one), all in use.  Packed ones: the

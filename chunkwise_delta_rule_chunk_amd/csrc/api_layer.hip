@@ -238,8 +238,9 @@ size_t ssm_layout(SsmArgs& a, bool f32, bool bwd, char* ws) {
     a.hd = hd;
     take(a.rx, tok);
     take(a.cx, tok);
-    take(a.ri, tok);
-    take(a.ci, tok);
+    take(a.ri, 2 * tok);
+    take(a.ci, 2 * tok);
+    take(a.tot, (size_t)a.nchunk * a.H * 16);
     take(a.cd, tok);
     take(a.ends, (size_t)a.nslot * a.H * 8);
     take(a.hdot, (size_t)a.nchunk * a.H * 4);

@@ -320,16 +320,26 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
     dd = rows_sum(row16_sum(dd));
     if (l == 0) sdd[w] = dd;
     lds_barrier();
-    if (w == 0 && l < len) {
+    if (w == 0) {
+      const int I = l >> 4;
       float rr = 0.f, cc = 0.f;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b <= (l >> 4)) rr += srp[b][l];
-        if (b >= (l >> 4)) cc += scp[b][l];
+      for (int b = 0; b < 3; ++b) {
+        if (b < I) rr += srp[b][l];
+        if (b + 1 > I) cc += scp[b + 1][l];
       }
-      a.ri[(int64_t)h * a.seq.total + tok + l] = rr;
-      a.ci[(int64_t)h * a.seq.total + tok + l] = cc;
-      a.cd[(int64_t)h * a.seq.total + tok + l] = scd[l];
+      const float u = row16_sum(I >= 2 ? srp[0][l] : 0.f), v = row16_sum(I == 3 ? srp[1][l] : 0.f);
+      float* tot = a.tot + ((int64_t)cslot * a.H + h) * 4;
+      if (l == 32 || l == 48) tot[I - 2] = u;
+      if (l == 48) tot[2] = v;
+      if (l < len) {
+        const int64_t o = (int64_t)h * a.seq.total + tok + l, in = (int64_t)a.H * a.seq.total;
+        a.ri[o] = rr;
+        a.ri[in + o] = srp[I][l];
+        a.ci[o] = cc;
+        a.ci[in + o] = scp[I][l];
+        a.cd[o] = scd[l];
+      }
     }
     if (w == 1 && l == 0) {
       float s = 0.f;
@@ -469,9 +479,8 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 
 // Gate gradients of one chunk and head, one wave, lane t its token.  dg_t is the sum
 // over what passes token t's decay: the entering state into the rows i >= t (rx), the
-// rows j < t into the leaving state (dt cx), the pairs j < t <= i of the chunk (the
-// suffix sum of ri - dt ci, in which pairs on one side cancel), and what goes from the
-// entering into the leaving state, H = exp(G_L) <S_in, dS>.
+// rows j < t into the leaving state (dt cx), the pairs j < t <= i of the chunk, and what
+// goes from the entering into the leaving state, H = exp(G_L) <S_in, dS>.
 // H is small beside E = <S_out, dS> where a chunk decays strongly, and dg_t is
 // multiplied by a g_t that is large there, so it may not inherit the rounding of E: it
 // is formed from the states that the chunk backward read (fp32: always).  As bf16
@@ -551,25 +560,38 @@ __global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
     sums(0);
     H = direct(0);
   }
-  const int t = t0 + l;
+  // Pairs j < t <= i: with b the block of 16 that t lies in, the blocks right below and
+  // left of it whole (tot), the rows i >= t of b left of it, the columns j < t of b below
+  // it, and in its own block the suffix sum of ri - dt ci, in which the pairs on one
+  // side of t cancel (over the whole chunk they would cancel 64 tokens' roundings).
+  const int t = t0 + l, blk = l >> 4;
   const bool on = t < t1;
-  double cc = 0., s = rx, pre = dcx;
+  const int64_t in = (int64_t)a.H * a.seq.total;
+  double cc = 0., s = rx, pre = dcx, rb = 0., cb = 0.;  // suffix and prefix over the chunk; over the block
   if (on) {
     z = ld_beta(a.dt, a.dt_f32, (int64_t)t * a.H + h) + bias;
-    const float ci = a.ci[row + t];
-    s += a.ri[row + t] - (double)dt * ci;
-    cc = (double)a.cx[row + t] + ci + a.cd[row + t];
+    const float co = a.ci[row + t], ci = a.ci[in + row + t];
+    rb = (double)a.ri[row + t] + a.ri[in + row + t] - (double)dt * ci;
+    cb = (double)dt * co;
+    cc = (double)a.cx[row + t] + co + ci + a.cd[row + t];
   }
+  const double cb0 = cb;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const double u = __shfl_down(s, d, 64), v = __shfl_up(pre, d, 64);
     if (l + d < 64) s += u;
     if (l >= d) pre += v;
+    if (d < 16) {
+      const double p = __shfl_down(rb, d, 16), q = __shfl_up(cb, d, 16);
+      if ((l & 15) + d < 16) rb += p;
+      if ((l & 15) >= d) cb += q;
+    }
   }
-  pre -= dcx;
+  const f32x4 tot = *reinterpret_cast<const f32x4*>(a.tot + ((int64_t)cslot * a.H + h) * 4);
+  const double far = blk == 1 ? (double)tot[0] + tot[1] : blk == 2 ? (double)tot[1] + tot[2] : 0.;
   double dA = 0., db = 0.;
   if (on) {
-    const double A = -exp((double)a.a_log[h]), dg = H + s + pre;
+    const double A = -exp((double)a.a_log[h]), dg = H + s + (pre - dcx) + rb + (cb - cb0) + far;
     const float e = expf(-fabsf(z)), sg = (z >= 0.f ? 1.f : e) / (1.f + e);
     db = (cc + A * dg) * sg;
     st_beta(a.ddt, a.dt_f32, (int64_t)t * a.H + h, (float)db);

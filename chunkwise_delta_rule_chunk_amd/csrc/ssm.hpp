@@ -56,8 +56,9 @@ struct SsmArgs {
   void* hd;                // same: adjoint of the state leaving each chunk
   float* rx;               // [H, tokens] row part of the decay gradient through the entering state
   float* cx;               // [H, tokens] column part (per unit of dt) through the leaving state
-  float* ri;               // [H, tokens] row part inside the chunk (i > j)
-  float* ci;               // [H, tokens] column part inside the chunk (i > j)
+  float* ri;               // [2, H, tokens] row part inside the chunk (i > j): left of the diagonal's block of 16, in it
+  float* ci;               // [2, H, tokens] column part inside the chunk (i > j): below the block, in it
+  float* tot;              // [nchunk, H, 4] sums of the blocks (2, 0), (3, 0), (3, 1)
   float* cd;               // [H, tokens] the term i = j, which belongs to c and cancels in the decay gradient
   double* ends;            // [nslot, H] <state, adjoint> at each segment's end
   float* hdot;             // [nchunk, H] <S_in, dS> of the handed-over states

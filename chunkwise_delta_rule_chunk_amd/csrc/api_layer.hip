@@ -180,8 +180,8 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   const int64_t total = a.seq.total;
   const int longest = a.seq.cu ? a.seq.total : a.seq.T;
   // (the bf16 backward's decay gradient is summed from the ends of the segments, and its
-  // error grows with their length)
-  a.seg = bwd && d->dtype == REWY_BF16 ? SEG_CHUNKS * CH : ssm_segment(total, a.H, 512, 8192);
+  // error grows with their length: 1024 tokens would double it)
+  a.seg = ssm_segment(total, a.H, 512, bwd && d->dtype == REWY_BF16 ? SEG_CHUNKS * CH : 8192);
   if (!bwd && !a.seq.cu && (int64_t)a.seq.N * a.H >= 512) a.seg = std::max(CH, (int)up64(longest));
   a.two = longest > a.seg;
   auto slots = [&](int64_t L) {  // (ssm.hpp)

@@ -79,7 +79,7 @@ hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_recurrent(const SsmArgs& a, bool f32, hipStream_t s);
 
-// chunks of a segment of the bf16 backward: 512 tokens (k_ssm_gate's chains)
+// most chunks of a segment of the bf16 backward: 512 tokens (k_ssm_gate's chains)
 constexpr int SEG_CHUNKS = 8;
 
 // ---- slots --------------------------------------------------------------------

@@ -146,10 +146,12 @@ int conv_forward(const rewy_conv_desc* d, bool step, const void* x, const void* 
 }
 
 // ---- selective state space scan ---------------------------------------------------
-// Tokens of a segment: as long as the segments of all heads still fill the chip
-// (a longer segment means fewer states to join), and whole chunks.
-int ssm_segment(int64_t total, int H, int target, int most) {
-  const int64_t want = (total * H + target - 1) / target;
+// Tokens of a segment: as long as the segments of all heads still fill the chip with
+// `target` (a longer segment means fewer states to join), and whole chunks.  A sequence
+// ends with half a segment on average, so N sequences count N / 2 more; where that
+// leaves little of the target, half of it stays.
+int ssm_segment(int64_t total, int64_t N, int H, int target, int most) {
+  const int64_t whole = std::max<int64_t>(target - N * H / 2, target / 2), want = (total * H + whole - 1) / whole;
   return (int)std::min<int64_t>(most, std::max<int64_t>(256, (want + CH - 1) / CH * CH));
 }
 
@@ -181,7 +183,7 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   const int longest = a.seq.cu ? a.seq.total : a.seq.T;
   // (the bf16 backward's decay gradient is summed from the ends of the segments, and its
   // error grows with their length: 1024 tokens would double it)
-  a.seg = ssm_segment(total, a.H, 512, bwd && d->dtype == REWY_BF16 ? SEG_CHUNKS * CH : 8192);
+  a.seg = ssm_segment(total, a.seq.N, a.H, 512, bwd && d->dtype == REWY_BF16 ? SEG_CHUNKS * CH : 8192);
   if (!bwd && !a.seq.cu && (int64_t)a.seq.N * a.H >= 512) a.seg = std::max(CH, (int)up64(longest));
   a.two = longest > a.seg;
   auto slots = [&](int64_t L) {  // (ssm.hpp)

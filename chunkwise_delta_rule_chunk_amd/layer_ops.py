@@ -248,12 +248,12 @@ def _rows(shape, ref, clear):
 
 
 # ---- short convolution ------------------------------------------------------------
-def _conv_problem(x, weight, bias, h0, activation, cu_seqlens):
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, D]")
+def _conv_problem(x, weight, bias, h0, activation, cu_seqlens, step=False):
+    if x.dim() != (2 if step else 3):
+        raise ValueError("x must be [N, D]" if step else "x must be [B, T, D]")
     if activation not in _ACT:
         raise ValueError(f"activation must be None or 'silu' (got {activation!r})")
-    Bsz, T, D = x.shape
+    Bsz, T, D = (x.shape[0], 1, x.shape[1]) if step else x.shape
     if weight.dim() != 2:
         raise ValueError("weight must be [D, W]")
     W = weight.shape[1]
@@ -288,13 +288,10 @@ def short_conv(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=N
 def short_conv_step(x, h0, weight, bias=None, *, activation="silu", ht=None, stream=None):
     """One new token x [N, D] for each sequence with state h0 [N, W-1, D].
     Returns (y, ht); ``ht`` may be h0 itself (updated in place)."""
-    if x.dim() != 2:
-        raise ValueError("x must be [N, D]")
-    desc, hshape, _, _ = _conv_problem(x[:, None], weight, bias, h0, activation, None)
+    desc, hshape, _, _ = _conv_problem(x, weight, bias, h0, activation, None, step=True)
     _like(ht, x, hshape, "ht", x.dtype)
     if h0 is None:
         raise ValueError("h0 must be given")
-    desc.x_stride = _row_stride(x, "x", 1)
     with _On(x, stream, (x, weight, bias, h0, ht)) as handle:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         if ht is None:

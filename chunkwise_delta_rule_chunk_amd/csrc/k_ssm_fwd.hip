@@ -476,7 +476,7 @@ hipError_t launch_ssm_prep(const SsmArgs& a, bool f32, bool bwd, hipStream_t s) 
 int ssm_head_blocks(const SsmArgs& a, int hb) { return a.G * ((a.per + hb - 1) / hb); }
 
 hipError_t launch_ssm_state(const SsmArgs& a, bool f32, bool both, hipStream_t s) {
-  return ssm_kv_heads(a, f32, [&](auto t, auto k, auto v, auto hb) {
+  return ssm_kv_heads<128>(a, f32, [&](auto t, auto k, auto v, auto hb) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
     const dim3 grid(a.nslot * ssm_head_blocks(a, HB), both ? 2 : 1), block(4 * HB * V);
@@ -490,7 +490,7 @@ hipError_t launch_ssm_pass(const SsmArgs& a, bool both, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s) {
-  return ssm_kv_heads(a, f32, [&](auto t, auto k, auto v, auto hb) {
+  return ssm_kv_heads<128>(a, f32, [&](auto t, auto k, auto v, auto hb) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
     constexpr int CT = V == 128 ? 2 : 1;

@@ -76,7 +76,6 @@ hipError_t launch_ssm_walk(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_gate(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_params(const SsmArgs& a, hipStream_t s);
-hipError_t launch_ssm_bcsum(const SsmArgs& a, bool f32, hipStream_t s);
 hipError_t launch_ssm_recurrent(const SsmArgs& a, bool f32, hipStream_t s);
 
 // most chunks of a segment of the bf16 backward: 512 tokens (k_ssm_gate's chains)
@@ -394,10 +393,10 @@ __device__ __forceinline__ void store_acc_order(const TileRegs<T, CH, C, NTH>& t
   }
 }
 
-// Heads side by side in one workgroup of the walks: as many heads of a group as
-// fit in its columns share the B and C tiles.
+// Heads side by side in one workgroup: as many heads of a group as fit in its columns
+// share the B and C tiles.
 template <typename T>
-constexpr int WALK_COLS = std::is_same_v<T, bf16> ? 128 : 64;
+constexpr int HEAD_COLS = std::is_same_v<T, bf16> ? 128 : 64;
 // blocks of HB heads of all groups
 __device__ __forceinline__ int head_blocks(const SsmArgs& a, int HB) { return a.G * ((a.per + HB - 1) / HB); }
 
@@ -420,12 +419,12 @@ hipError_t ssm_kv(int K, int V, bool f32, F&& f) {
   };
   return f32 ? k_of(float{}) : k_of(bf16{});
 }
-// the same with the heads of a workgroup: as many as fit, or one where a group
-// has no two heads to put side by side
-template <typename F>
+// the same with the heads of a workgroup: as many as fit in COLS columns, or one where a
+// group has no two heads to put side by side
+template <int COLS, typename F>
 hipError_t ssm_kv_heads(const SsmArgs& a, bool f32, F&& f) {
   return ssm_kv(a.K, a.V, f32, [&](auto t, auto k, auto v) -> hipError_t {
-    constexpr int HB = WALK_COLS<decltype(t)> / decltype(v)::value;
+    constexpr int HB = std::max(std::min(COLS, HEAD_COLS<decltype(t)>) / decltype(v)::value, 1);
     if constexpr (HB > 1)
       if (a.per == 1) return f(t, k, v, std::integral_constant<int, 1>{});
     return f(t, k, v, std::integral_constant<int, HB>{});

@@ -7,41 +7,39 @@ namespace rewy {
 
 namespace {
 
-// What every walk of a call reads and no walk should form again.  Workgroups < ngate:
-// the gates, one wave per chunk and head, lane t its token.  The others: C B^T
-// of one chunk and group, the lower triangle's ten 16 x 16 blocks as C fragments,
-// shared by the heads of the group; forward: rows j in slot order, columns i
-// (what the coefficients' rows are made of); backward: rows i, columns j.  8192 x 32 heads,
-// K = 128: 9 us, most of it latency.
+// What every walk of a call reads and no walk should form again.  Workgroups < nblk:
+// C B^T of the chunks and groups, one wave for each of the lower triangle's ten 16 x 16
+// blocks, as C fragments shared by the heads of the group; forward: rows j in slot
+// order, columns i (what the coefficients' rows are made of); backward: rows i, columns
+// j.  The others: the gates, one wave per chunk and head, lane t its token.
 template <typename T, int K>
-__global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int ngate, int bwd) {
+__global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int nblk, int bwd) {
   const int t = lane_id(), w = wave_id();
-  if ((int)blockIdx.x >= ngate) {
-    const int wk = blockIdx.x - ngate, cslot = wk / a.G, grp = wk - cslot * a.G;
+  if ((int)blockIdx.x < nblk) {
+    const int wb = blockIdx.x * 4 + w, wk = wb / 10, cslot = wk / a.G, grp = wk - cslot * a.G;
+    if (cslot >= a.nchunk) return;
     const Piece pc = find_piece(a.seq, cslot, CH);
     const int tok = pc.bos + pc.k * CH, len = min(CH, pc.eos - tok);
     if (!pc.on || len <= 0) return;
     const T* bp = reinterpret_cast<const T*>(a.b) + (int64_t)tok * a.bs + grp * K;
     const T* cp = reinterpret_cast<const T*>(a.c) + (int64_t)tok * a.cs + grp * K;
     const GBuf gb = gbuf(bp, tile_bytes<T>(len, a.bs, K)), gc = gbuf(cp, tile_bytes<T>(len, a.cs, K));
-    for (int blk = w; blk < 10; blk += 4) {
-      int I, J;
-      tri_block(blk, I, J);
-      const int r = t & 15, k0 = VEC<T> * (t >> 4);
-      const int i = 16 * I + (bwd ? slot_row<T>(r) : r), j = 16 * J + (bwd ? r : slot_row<T>(r));
-      f32x4 acc = zero4();
+    int I, J;
+    tri_block(wb - wk * 10, I, J);
+    const int r = t & 15, k0 = VEC<T> * (t >> 4);
+    const int i = 16 * I + (bwd ? slot_row<T>(r) : r), j = 16 * J + (bwd ? r : slot_row<T>(r));
+    f32x4 acc = zero4();
 #pragma unroll
-      for (int q = 0; q < K / KG<T>; ++q) {
-        const uint4 bf = gld16(gb, (uint32_t)((j * a.bs + k0 + q * KG<T>) * (int64_t)sizeof(T)));
-        const uint4 cf = gld16(gc, (uint32_t)((i * a.cs + k0 + q * KG<T>) * (int64_t)sizeof(T)));
-        if (bwd) mma16B<T>(acc, cf, bf);
-        else mma16B<T>(acc, bf, cf);
-      }
-      reinterpret_cast<f32x4*>(a.cb)[((int64_t)wk * 10 + blk) * 64 + t] = acc;
+    for (int q = 0; q < K / KG<T>; ++q) {
+      const uint4 bf = gld16(gb, (uint32_t)((j * a.bs + k0 + q * KG<T>) * (int64_t)sizeof(T)));
+      const uint4 cf = gld16(gc, (uint32_t)((i * a.cs + k0 + q * KG<T>) * (int64_t)sizeof(T)));
+      if (bwd) mma16B<T>(acc, cf, bf);
+      else mma16B<T>(acc, bf, cf);
     }
+    reinterpret_cast<f32x4*>(a.cb)[(int64_t)wb * 64 + t] = acc;
     return;
   }
-  const int wk = blockIdx.x * 4 + w;
+  const int wk = (blockIdx.x - nblk) * 4 + w;
   if (wk >= a.nchunk * a.H) return;
   const int cslot = wk / a.H, h = wk - cslot * a.H;
   const Piece pc = find_piece(a.seq, cslot, CH);
@@ -468,8 +466,8 @@ hipError_t launch_ssm_prep(const SsmArgs& a, bool f32, bool bwd, hipStream_t s) 
   return ssm_kv(a.K, 32, f32, [&](auto t, auto k, auto) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value;
-    const int ngate = (a.nchunk * a.H + 3) / 4;
-    REWY_LAUNCH((k_ssm_prep<T, K>), dim3(ngate + a.nchunk * a.G), dim3(256), s, a, ngate, (int)bwd);
+    const int nblk = (int)(((int64_t)a.nchunk * a.G * 10 + 3) / 4), ngate = (a.nchunk * a.H + 3) / 4;
+    REWY_LAUNCH((k_ssm_prep<T, K>), dim3(nblk + ngate), dim3(256), s, a, nblk, (int)bwd);
     return hipGetLastError();
   });
 }

@@ -146,13 +146,22 @@ int conv_forward(const rewy_conv_desc* d, bool step, const void* x, const void* 
 }
 
 // ---- selective state space scan ---------------------------------------------------
-// Tokens of a segment: as long as the segments of all heads still fill the chip with
-// `target` (a longer segment means fewer states to join), and whole chunks.  A sequence
-// ends with half a segment on average, so N sequences count N / 2 more; where that
-// leaves little of the target, half of it stays.
-int ssm_segment(int64_t total, int64_t N, int H, int target, int most) {
-  const int64_t whole = std::max<int64_t>(target - N * H / 2, target / 2), want = (total * H + whole - 1) / whole;
-  return (int)std::min<int64_t>(most, std::max<int64_t>(256, (want + CH - 1) / CH * CH));
+// Tokens of a segment, whole chunks: as long as the segments of all heads still fill
+// the chip with SEGMENTS of them, two workgroups a CU (a longer segment means fewer
+// states to join).  Sequences of equal length: ceil(T / segment) each.  Packed ones end
+// with half a segment on average, which leaves the target (N - 1) / 2 a head less, at
+// least half of it.
+int ssm_segment(const SeqArgs& q, int H, int most) {
+  constexpr int64_t SEGMENTS = 512;
+  int64_t want;
+  if (q.cu) {
+    const int64_t whole = std::max(SEGMENTS - (int64_t)(q.N - 1) * H / 2, SEGMENTS / 2);
+    want = ((int64_t)q.total * H + whole - 1) / whole;
+  } else {
+    const int64_t each = std::max<int64_t>(SEGMENTS / ((int64_t)q.N * H), 1);
+    want = (q.T + each - 1) / each;
+  }
+  return (int)std::min<int64_t>(most, std::max<int64_t>(256, up64(want)));
 }
 
 int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
@@ -183,8 +192,7 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   const int longest = a.seq.cu ? a.seq.total : a.seq.T;
   // (the bf16 backward's decay gradient is summed from the ends of the segments, and its
   // error grows with their length: 1024 tokens would double it)
-  a.seg = ssm_segment(total, a.seq.N, a.H, 512, bwd && d->dtype == REWY_BF16 ? SEG_CHUNKS * CH : 8192);
-  if (!bwd && !a.seq.cu && (int64_t)a.seq.N * a.H >= 512) a.seg = std::max(CH, (int)up64(longest));
+  a.seg = ssm_segment(a.seq, a.H, bwd && d->dtype == REWY_BF16 ? SEG_CHUNKS * CH : INT32_MAX / CH * CH);
   a.two = longest > a.seg;
   auto slots = [&](int64_t L) {  // (ssm.hpp)
     return a.seq.cu ? total / L + a.seq.N : a.seq.N * std::max<int64_t>((a.seq.T + L - 1) / L, 1);

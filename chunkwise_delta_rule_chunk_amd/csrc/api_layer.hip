@@ -205,7 +205,8 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   // products); the ranges are the ones with the shortest schedule on 256 CUs, and
   // of those the fewest, as each range adds a partial sum to memory.
   int64_t best = INT64_MAX;
-  for (int sp = 1; sp <= std::min(a.per, 32); ++sp) {
+  a.split = 1;
+  for (int sp = 1; bwd && sp <= std::min(a.per, 32); ++sp) {
     const int64_t rounds = (nchunk * a.G * sp + 255) / 256, cost = rounds * ((a.per + sp - 1) / sp + 1);
     if (cost < best) {
       best = cost;

@@ -122,10 +122,19 @@ def _workspace(nbytes, ref, ws):
     if nbytes == 0:  # (the call itself would refuse the descriptor)
         raise B.RewyError(B.REWY_EINVAL, "workspace size")
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+        return ref.new_empty(nbytes, dtype=torch.uint8)
     if ws.dtype != torch.uint8 or ws.get_device() != ref.get_device() or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {ref.device}")
     return ws
+
+
+def _like_new(ref, clear=False):
+    """A new contiguous tensor of ref's shape and type on its device; ``clear``: of
+    zeros.  (Autograd clears where rows may follow the last sequence, with offsets
+    that only the GPU holds: their gradients go on into other products.)"""
+    if clear:
+        return ref.new_zeros(ref.shape)
+    return torch.empty_like(ref) if ref.is_contiguous() else ref.new_empty(ref.shape)
 
 
 # ---- RMS norm -----------------------------------------------------------------
@@ -156,13 +165,13 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0, ou
             raise ValueError("residual must have x's shape and type")
         rs = _row_stride(residual, "residual", 1)
     with _On(x, stream, (x, weight, residual)) as handle:
-        s = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if output else None
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+        s = _like_new(x) if residual is not None else None
+        y = _like_new(x) if output else None
+        rstd = x.new_empty(M, dtype=torch.float32)
         q = scale = None
         if quant is not None:
-            q = torch.empty(x.shape, dtype=_QDT[quant], device=x.device)
-            scale = torch.empty(M, -(-D // group) if group else 1, dtype=torch.float32, device=x.device)
+            q = x.new_empty(x.shape, dtype=_QDT[quant])
+            scale = x.new_empty((M, -(-D // group) if group else 1), dtype=torch.float32)
         desc = B.RewyNormDesc(M, D, dt, wdt, _QUANT[quant], group, eps, xs, rs, 0, 0)
         _check(B.rewy_norm_fwd(desc, _p(x), _p(residual), _p(weight), _p(s), _p(y), _p(q), _p(scale),
                                _p(rstd), handle), "rewy_norm_fwd")
@@ -185,7 +194,7 @@ def rms_norm_backward(ctx, dy, ds=None, *, stream=None, ws=None):
                           _row_stride(s, "s", 1), 0 if ds is None else _row_stride(ds, "ds", 1), 0,
                           _row_stride(dy, "dy", 1))
     with _On(s, stream, (s, weight, ctx["rstd"], dy, ds)) as handle:
-        dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
+        dx = _like_new(s)
         dw = None if weight is None else torch.empty_like(weight)
         if dw is not None:
             ws = _workspace(B.rewy_norm_workspace_bytes(desc), s, ws)
@@ -240,13 +249,6 @@ def _sequences(x, cu_seqlens, T):
     return len(vals) - 1, torch.tensor(vals, dtype=torch.int32, device=x.device), host
 
 
-def _rows(shape, ref, clear):
-    """A new tensor of ref's type on its device; ``clear``: of zeros.  (Autograd
-    clears where rows may follow the last sequence, with offsets that only the
-    GPU holds: their gradients go on into other products.)"""
-    return (torch.zeros if clear else torch.empty)(shape, dtype=ref.dtype, device=ref.device)
-
-
 # ---- short convolution ------------------------------------------------------------
 def _conv_problem(x, weight, bias, h0, activation, cu_seqlens, step=False):
     if x.dim() != (2 if step else 3):
@@ -278,8 +280,8 @@ def short_conv(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=N
     the last sequence are then not written, or zeros with ``clear``."""
     desc, hshape, cu, host = _conv_problem(x, weight, bias, h0, activation, cu_seqlens)
     with _On(x, stream, (x, weight, bias, h0, cu)) as handle:
-        y = _rows(x.shape, x, clear)
-        ht = torch.empty(hshape, dtype=x.dtype, device=x.device) if output_final_state else None
+        y = _like_new(x, clear)
+        ht = x.new_empty(hshape) if output_final_state else None
         _check(B.rewy_conv_fwd(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(ht), handle),
                "rewy_conv_fwd")
     return y, ht, dict(desc=desc, x=x, weight=weight, bias=bias, h0=h0, cu=cu, host=host)
@@ -293,9 +295,9 @@ def short_conv_step(x, h0, weight, bias=None, *, activation="silu", ht=None, str
     if h0 is None:
         raise ValueError("h0 must be given")
     with _On(x, stream, (x, weight, bias, h0, ht)) as handle:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like_new(x)
         if ht is None:
-            ht = torch.empty(hshape, dtype=x.dtype, device=x.device)
+            ht = x.new_empty(hshape)
         _check(B.rewy_conv_step(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(ht), handle),
                "rewy_conv_step")
     return y, ht
@@ -314,7 +316,7 @@ def short_conv_backward(ctx, dy, dht=None, *, clear=False, stream=None, ws=None)
     desc = B.RewyConvDesc(d.B, d.T, d.D, d.W, d.N, d.cu_seqlens, d.cu_seqlens_host, d.dtype, d.w_dtype,
                           d.act, d.x_stride, _row_stride(dy, "dy", 1), 0)
     with _On(x, stream, (x, weight, bias, h0, ctx["cu"], dy, dht)) as handle:
-        dx = _rows(x.shape, x, clear)
+        dx = _like_new(x, clear)
         dw = torch.empty_like(weight)
         db = None if bias is None else torch.empty_like(bias)
         dh0 = None if h0 is None else torch.empty_like(h0)
@@ -387,8 +389,8 @@ def selective_scan(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seql
     written, or zeros with ``clear``."""
     desc, shape, cu, host = _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)
     with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, cu)) as handle:
-        y = _rows(x.shape, x, clear)
-        ht = torch.empty(shape, dtype=torch.float32, device=x.device) if output_final_state else None
+        y = _like_new(x, clear)
+        ht = x.new_empty(shape, dtype=torch.float32) if output_final_state else None
         ws = _workspace(B.rewy_ssm_workspace_bytes(desc, 0), x, ws)
         _check(B.rewy_ssm_fwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
                               _p(y), _p(ht), _p(ws), ws.numel(), handle), "rewy_ssm_fwd")
@@ -403,9 +405,9 @@ def selective_scan_recurrent(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=Non
     desc, shape, cu, host = _scan_problem(x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens)
     _like(ht, x, shape, "ht", torch.float32)
     with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, cu, ht)) as handle:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like_new(x)
         if ht is None:
-            ht = torch.empty(shape, dtype=torch.float32, device=x.device)
+            ht = x.new_empty(shape, dtype=torch.float32)
         _check(B.rewy_ssm_recurrent_fwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d),
                                         _p(h0), _p(y), _p(ht), handle), "rewy_ssm_recurrent_fwd")
     return y, ht
@@ -431,15 +433,15 @@ def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, clear
                 raise ValueError(f"{name} must have the shape and type of its input")
     with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, ctx["cu"], dy, dht, *(out or ()))) as handle:
         if out is None:
-            out = tuple(_rows(t.shape, t, clear) for t in (x, b, c))
+            out = tuple(_like_new(t, clear) for t in (x, b, c))
         dx, db, dc = out
         desc = B.RewySsmDesc(f.B, f.T, f.H, f.G, f.K, f.V, f.N, f.cu_seqlens, f.cu_seqlens_host, f.dtype,
                              f.dt_dtype, f.x_stride, f.b_stride, f.c_stride, _row_stride(dy, "dy", 2),
                              _row_stride(dx, "dx", 2), _row_stride(db, "db", 2), _row_stride(dc, "dc", 2))
-        ddt, da_log = _rows(dt.shape, dt, clear), torch.empty_like(a_log)
+        ddt, da_log = _like_new(dt, clear), torch.empty_like(a_log)
         dd = None if d is None else torch.empty_like(d)
         ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
-        dh0 = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dh0 else None
+        dh0 = x.new_empty(shape, dtype=torch.float32) if want_dh0 else None
         ws = _workspace(B.rewy_ssm_workspace_bytes(desc, 1), x, ws)
         _check(B.rewy_ssm_bwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
                               _p(dy), _p(dht), _p(dx), _p(ddt), _p(da_log), _p(ddt_bias), _p(db), _p(dc),

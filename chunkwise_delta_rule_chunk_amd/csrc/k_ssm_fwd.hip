@@ -11,7 +11,8 @@ namespace {
 // C B^T of the chunks and groups, one wave for each of the lower triangle's ten 16 x 16
 // blocks, as C fragments shared by the heads of the group; forward: rows j in slot
 // order, columns i (what the coefficients' rows are made of); backward: rows i, columns
-// j.  The others: the gates, one wave per chunk and head, lane t its token.
+// j.  The others: the gates, one wave per chunk and head, lane t its token.  8192 x 32 heads,
+// K = 128: 7 us, most of it latency.
 template <typename T, int K>
 __global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int nblk, int bwd) {
   const int t = lane_id(), w = wave_id();
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int nblk, int bwd) 
 // sequence's last segment; reverse (dir 1), the adjoint that the segment's own
 // tokens send to the state that enters it, all but the first.  Wave w holds 16 columns
 // of one head's state.  8192 x 32 heads, K = V = 128 in segments of 512: x read and 31 MB
-// of states written, 31.8 us (3.2 TB/s).  Both directions of K = 128, V = 64: 34.8 us.
+// of states written, 28.8 us (3.4 TB/s).  Both directions of K = 128, V = 64: 33 us.
 template <typename T, int K, int V, int HB, int NS>
 __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_state(SsmArgs a) {
   constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, LK = pitch<T>(K), LV = pitch<T>(CW);

@@ -123,6 +123,10 @@ CASES = [
     (1, 300, 9, 3, 64, 64, "bf16", "fp32", None, True, "usual"),
     (2, 300, 3, 1, 32, 32, "fp32", "bf16", None, True, "usual"),
     (1, 520, 2, 2, 64, 32, "fp32", "fp32", [520], False, "none"),
+    # several segments without a chunk that decays strongly, so that the decay gradient's
+    # chains start at segment ends, from behind and from the front, with and without a state
+    (1, 1100, 2, 1, 64, 64, "bf16", "fp32", None, False, "none"),
+    (1, 1200, 2, 1, 32, 32, "bf16", "fp32", [700, 500], True, "none"),
 ]
 
 

@@ -125,6 +125,7 @@ def _workspace(nbytes, ref, ws):
         return ref.new_empty(nbytes, dtype=torch.uint8)
     if ws.dtype != torch.uint8 or ws.get_device() != ref.get_device() or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {ref.device}")
+    ws.record_stream(torch.cuda.current_stream(ref.device))  # (the call's)
     return ws
 
 
@@ -135,6 +136,11 @@ def _like_new(ref, clear=False):
     if clear:
         return ref.new_zeros(ref.shape)
     return torch.empty_like(ref) if ref.is_contiguous() else ref.new_empty(ref.shape)
+
+
+def _adjoint(dy, ref):
+    """The adjoint of an output of ref's shape, zeros if nothing used the output."""
+    return ref.new_zeros(ref.shape) if dy is None else dy.contiguous()
 
 
 # ---- RMS norm -----------------------------------------------------------------
@@ -209,6 +215,7 @@ class RMSNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(fctx, x, weight, residual, eps):
+        fctx.set_materialize_grads(False)
         y, s, _, _, ctx = rms_norm(x, weight, residual, eps=eps)
         fctx.save_for_backward(s, weight, ctx["rstd"])
         fctx.eps, fctx.residual = eps, residual is not None
@@ -218,8 +225,8 @@ class RMSNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(fctx, dy, ds):
         s, weight, rstd = fctx.saved_tensors
-        g = rms_norm_backward(dict(s=s, weight=weight, rstd=rstd, eps=fctx.eps), dy.contiguous(),
-                              ds.contiguous())
+        g = rms_norm_backward(dict(s=s, weight=weight, rstd=rstd, eps=fctx.eps), _adjoint(dy, s),
+                              None if ds is None else ds.contiguous())
         return g["dx"], g["dweight"], g["dx"] if fctx.residual else None, None
 
 
@@ -331,6 +338,7 @@ class ShortConvFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(fctx, x, weight, bias, h0, activation, cu_seqlens):
+        fctx.set_materialize_grads(False)
         fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
         y, ht, ctx = short_conv(x, weight, bias, activation=activation, h0=h0, cu_seqlens=cu_seqlens,
                                 output_final_state=True, clear=fctx.clear)
@@ -342,7 +350,8 @@ class ShortConvFunction(torch.autograd.Function):
     @once_differentiable
     def backward(fctx, dy, dht):
         ctx = dict(fctx.rewy, **dict(zip(("x", "weight", "bias", "h0"), fctx.saved_tensors)))
-        g = short_conv_backward(ctx, dy.contiguous(), dht.contiguous(), clear=fctx.clear)
+        g = short_conv_backward(ctx, _adjoint(dy, ctx["x"]), None if dht is None else dht.contiguous(),
+                                clear=fctx.clear)
         return g["dx"], g["dweight"], g["dbias"], g["dh0"], None, None
 
 
@@ -454,6 +463,7 @@ class SelectiveScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(fctx, x, dt, a_log, b, c, d, dt_bias, h0, cu_seqlens):
+        fctx.set_materialize_grads(False)
         fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
         y, ht, ctx = selective_scan(x, dt, a_log, b, c, d=d, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
                                     clear=fctx.clear)
@@ -465,8 +475,9 @@ class SelectiveScanFunction(torch.autograd.Function):
     @once_differentiable
     def backward(fctx, dy, dht):
         names = ("x", "dt", "a_log", "b", "c", "d", "dt_bias", "h0")
-        g = selective_scan_backward(dict(fctx.rewy, **dict(zip(names, fctx.saved_tensors))), dy.contiguous(),
-                                    dht.contiguous(), clear=fctx.clear)
+        ctx = dict(fctx.rewy, **dict(zip(names, fctx.saved_tensors)))
+        g = selective_scan_backward(ctx, _adjoint(dy, ctx["x"]), None if dht is None else dht.contiguous(),
+                                    clear=fctx.clear)
         return (g["dx"], g["ddt"], g["da_log"], g["db"], g["dc"], g["dd"], g["ddt_bias"], g["dh0"], None)
 
 

@@ -216,7 +216,7 @@ int ssm_args(const rewy_ssm_desc* d, bool bwd, SsmArgs& a) {
   // a launch takes fewer than 2^32 threads: gates and C B^T, the walks, the token-serial
   // form and the pass, and the backward's chunks and sums
   const int64_t threads[] = {(nchunk * a.H + nchunk * a.G * 10 + 8) * 64, nslot * a.H * 512, (int64_t)a.seq.N * a.H * 256,
-                             bwd ? nchunk * a.G * a.split * 512 : 0, bwd ? nchunk * a.H * 64 + total * a.G * a.K / 2 + 1024 : 0};
+                             bwd ? nchunk * a.G * a.split * 1024 : 0, bwd ? nchunk * a.H * 64 + total * a.G * a.K / 2 + 1024 : 0};
   for (int64_t n : threads)
     if (n >= (int64_t)1 << 32)
       return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,

@@ -170,17 +170,20 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
   }
 }
 
-constexpr int CB_WAVES = 8;
+// Waves of a chunk's workgroup: 16 where a wave's part fits in 128 registers (K = 64, V = 64
+// and 128: 63 -> 59 and 92 -> 85 us for 8192 x 32 heads bf16, 149 -> 130 fp32), else 8 (K = 128
+// spills with 16: 122 instead of 77 us; K or V = 32 has no 16 parts).
+constexpr int cb_waves(int K, int V) { return K == 64 && V >= 64 ? 16 : 8; }
 
 // One chunk, one group, a range of its heads: dx, the parts of r and c inside
 // the chunk, and dB, dC summed over the heads in registers.  Wave w owns rows
-// 16 (w & 3) .. + 15 of the chunk and half w >> 2 of the state rows (dB, dC) or
-// of the columns (dx).  The size above: 78.9 us, 262 MB (3.3 TB/s; the states half of
+// 16 (w & 3) .. + 15 of the chunk and share w >> 2 of the state rows (dB, dC) or
+// of the columns (dx).  The size above: 77 us, 262 MB (3.3 TB/s; the states half of
 // them) and 16 GFLOP; eight waves a CU, as its tiles take most of the LDS.
 template <typename T, int K, int V>
-__global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
-  constexpr int NTH = 64 * CB_WAVES, LK = pitch<T>(K), LV = pitch<T>(V), LM = pitch<T>(CH), NQ = CH / KG<T>;
-  constexpr int KQ = K / KG<T>, VQ = V / KG<T>, NTW = K / 32, PTW = V / 32;  // tiles of a half
+__global__ __launch_bounds__(64 * cb_waves(K, V)) void k_ssm_chunk(SsmArgs a) {
+  constexpr int NW = cb_waves(K, V), NTH = 64 * NW, LK = pitch<T>(K), LV = pitch<T>(V), LM = pitch<T>(CH), NQ = CH / KG<T>;
+  constexpr int KQ = K / KG<T>, VQ = V / KG<T>, NTW = K / 4 / NW, PTW = V / 4 / NW;  // tiles of a wave
   __shared__ __align__(16) T sb[CH * LK];
   __shared__ __align__(16) T sc[CH * LK];
   __shared__ __align__(16) T sx[CH * LV];
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   __shared__ __align__(16) T sd[V * LK];   // dS^T, the same
   __shared__ __align__(16) T sm[CH * LM];  // M0^T (columns in slot order), at the end W^T, then W
   __shared__ __align__(16) float sG[CH], sGl[CH], sdt[CH], seG[CH], seE[CH], tG[CH], tGl[CH];  // t: in slot order
-  __shared__ float srp[4][CH], scp[4][CH], scd[CH], sdd[CB_WAVES], shd[CB_WAVES];
+  __shared__ float srp[4][CH], scp[4][CH], scd[CH], sdd[NW], shd[NW];
   const int nwork = a.nchunk * a.G * a.split;
   int wk = xcd_range(blockIdx.x, nwork);
   const int part = wk % a.split;
@@ -199,7 +202,8 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   const int tok = pc.bos + pc.k * CH, len = min(CH, pc.eos - tok);
   if (!pc.on || len <= 0) return;
   const int h0 = grp * a.per + part * a.per / a.split, h1 = grp * a.per + (part + 1) * a.per / a.split;
-  const int w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15, tb = w & 3, half = w >> 2;
+  // (the wave's number in a scalar register: with 16 waves every one of the 128 others counts)
+  const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), g4 = l >> 4, r = l & 15, tb = w & 3, sh = w >> 2;
 
   TileRegs<T, CH, V, NTH> rx, ry;
   TileRegs<T, V, K, NTH> rs, rd;  // pieces of the handed-over states, 16 bytes = two lanes' fragments
@@ -240,14 +244,14 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
   }
   for (int i = threadIdx.x; i < CH * LM; i += NTH) sm[i] = (T)0.f;
   lds_barrier();
-  // blocks (I, J) of the lower triangle: 10 over 8 waves.  C B^T and the sum of W over
+  // blocks (I, J) of the lower triangle: 10 over the waves.  C B^T and the sum of W over
   // the heads stay in registers (rows i = 16 I + slot_row(4 g4 + e), column j = 16 J + r).
-  constexpr int NB = (10 + CB_WAVES - 1) / CB_WAVES;
+  constexpr int NB = (10 + NW - 1) / NW;
   f32x4 cb[NB], wsum[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     wsum[b] = zero4();
-    cb[b] = reinterpret_cast<const f32x4*>(a.cb)[((int64_t)(cslot * a.G + grp) * 10 + min(b * CB_WAVES + w, 9)) * 64 + l];
+    cb[b] = reinterpret_cast<const f32x4*>(a.cb)[((int64_t)(cslot * a.G + grp) * 10 + min(b * NW + w, 9)) * 64 + l];
   }
   f32x4 dC[NTW], dB[NTW];
 #pragma unroll
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
     float dd = 0.f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int blk = b * CB_WAVES + w;
+      const int blk = b * NW + w;
       if (blk < 10) {
         int I, J;
         tri_block(blk, I, J);
@@ -347,21 +351,21 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
     }
     if (w == 1 && l == 0) {
       float s = 0.f;
-      for (int i = 0; i < CB_WAVES; ++i) s += sdd[i];
+      for (int i = 0; i < NW; ++i) s += sdd[i];
       a.dpart[(int64_t)cslot * a.H + h] = s;
     }
     if (w == 2 && l == 0) {
       float s = 0.f;
-      for (int i = 0; i < CB_WAVES; ++i) s += shd[i];
+      for (int i = 0; i < NW; ++i) s += shd[i];
       a.hdot[(int64_t)cslot * a.H + h] = s;
     }
-    // dX^T, rows p of this wave's half, columns j = 16 tb + r
+    // dX^T, rows p of this wave's share, columns j = 16 tb + r
     {
       const int j = 16 * tb + r;
       const float eE = seE[j], dt = sdt[j], D = a.d ? a.d[h] : 0.f;
 #pragma unroll
       for (int pi = 0; pi < PTW; ++pi) {
-        const int pt = half * PTW + pi;
+        const int pt = sh * PTW + pi;
         f32x4 u = zero4(), v = zero4();
         const T* sdp = sd + slot_place<T>(16 * pt + r) * LK + VEC<T> * g4;
 #pragma unroll
@@ -391,7 +395,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       const f32x4 dt = *reinterpret_cast<const f32x4*>(sdt + 16 * tb + 4 * g4);
 #pragma unroll
       for (int ni = 0; ni < NTW; ++ni) {
-        const int nt = half * NTW + ni;
+        const int nt = sh * NTW + ni;
         f32x4 u = zero4(), v = zero4();
 #pragma unroll
         for (int q = 0; q < VQ; ++q) {
@@ -413,7 +417,7 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
     lds_barrier();
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int blk = b * CB_WAVES + w;
+      const int blk = b * NW + w;
       if (blk < 10) {
         int I, J;
         tri_block(blk, I, J);
@@ -433,12 +437,12 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       if ((q + 1) * KG<T> > 16 * tb) {
         const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row j, contraction i
 #pragma unroll
-        for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dB[ni], wf, frag_col<T>(sc, LK, q * KG<T>, 16 * (half * NTW + ni)));
+        for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dB[ni], wf, frag_col<T>(sc, LK, q * KG<T>, 16 * (sh * NTW + ni)));
       }
     lds_barrier();
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int blk = b * CB_WAVES + w;
+      const int blk = b * NW + w;
       if (blk < 10) {
         int I, J;
         tri_block(blk, I, J);
@@ -457,12 +461,12 @@ __global__ __launch_bounds__(64 * CB_WAVES) void k_ssm_chunk(SsmArgs a) {
       if (q * KG<T> <= 16 * tb) {
         const uint4 wf = frag_row<T>(sm, LM, 16 * tb, q * KG<T>);  // row i, contraction j
 #pragma unroll
-        for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dC[ni], wf, frag_col<T>(sb, LK, q * KG<T>, 16 * (half * NTW + ni)));
+        for (int ni = 0; ni < NTW; ++ni) mma16B<T>(dC[ni], wf, frag_col<T>(sb, LK, q * KG<T>, 16 * (sh * NTW + ni)));
       }
   }
 #pragma unroll
   for (int ni = 0; ni < NTW; ++ni) {
-    const int n = 16 * (half * NTW + ni) + r;
+    const int n = 16 * (sh * NTW + ni) + r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * tb + 4 * g4 + e;
@@ -669,7 +673,7 @@ hipError_t launch_ssm_chunk(const SsmArgs& a, bool f32, hipStream_t s) {
   return ssm_kv(a.K, a.V, f32, [&](auto t, auto k, auto v) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value;
-    REWY_LAUNCH((k_ssm_chunk<T, K, V>), dim3(a.nchunk * a.G * a.split), dim3(64 * CB_WAVES), s, a);
+    REWY_LAUNCH((k_ssm_chunk<T, K, V>), dim3(a.nchunk * a.G * a.split), dim3(64 * cb_waves(K, V)), s, a);
     return hipGetLastError();
   });
 }

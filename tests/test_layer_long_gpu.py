@@ -99,3 +99,34 @@ def test_one_of_two_outputs():
     full = torch.autograd.grad((y * 0).sum() + ht.sum(), args)
     for a, b in zip(some, full):
         assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Forward and backward of the three on two streams that overlap: each as alone."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    sets = []
+    for T in (700, 1300):
+        x, r, w = rn(T, 512).bfloat16(), rn(T, 512).bfloat16(), rn(512)
+        cw = rn(512, 4)
+        scan = (rn(1, T, 4, 64).bfloat16(), rn(1, T, 4) - 3, rn(4), rn(1, T, 1, 128).bfloat16(), rn(1, T, 1, 128).bfloat16())
+        sets.append((x, r, w, cw, scan))
+
+    def run(x, r, w, cw, scan, stream=None):
+        y, s, _, _, nc = ops.rms_norm(x, w, r, stream=stream)
+        n = ops.rms_norm_backward(nc, r, stream=stream)
+        z, _, cc = ops.short_conv(x[None], cw, stream=stream)
+        c = ops.short_conv_backward(cc, r[None], stream=stream)
+        o, ht, sc = ops.selective_scan(*scan, stream=stream)
+        b = ops.selective_scan_backward(sc, scan[0], stream=stream)
+        return [y, s, n["dx"], n["dweight"], z, c["dx"], c["dweight"], o, ht] + [b[k] for k in ("dx", "ddt", "da_log", "db", "dc")]
+
+    alone = [run(*a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[run(*a, stream=s) for a, s in zip(sets, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(alone, pair):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))

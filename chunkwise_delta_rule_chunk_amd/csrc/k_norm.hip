@@ -66,13 +66,11 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* buf) {
   }
 }
 
-// scale and its inverse from the largest magnitude's bits: 1 where there is
-// nothing to scale (all zeros, or magnitudes whose inverse would overflow)
-__device__ __forceinline__ void make_scale(uint32_t bits, float qmax, float& scale, float& inv) {
+// scale from the largest magnitude's bits: 1 where there is nothing to scale (all zeros,
+// or magnitudes so small that a step of the scale would be lost)
+__device__ __forceinline__ float make_scale(uint32_t bits, float qmax) {
   const float m = __uint_as_float(bits);
-  const bool none = m < 0x1p-100f;
-  scale = none ? 1.f : m / qmax;
-  inv = none ? 1.f : qmax / m;
+  return m < 0x1p-100f ? 1.f : m / qmax;
 }
 // four values to four bytes
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
@@ -171,8 +169,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int j = (c * TPR + t) * VE;
-    float scale, inv;
-    make_scale(a.group ? lanes_max_n(mx[c], lanes) : all, qmax, scale, inv);
+    const float scale = make_scale(a.group ? lanes_max_n(mx[c], lanes) : all, qmax);
     if (a.group) {
       if (j < D && j % a.group == 0) a.scale[m * a.ng + j / a.group] = scale;
     } else if (c == 0 && t == 0 && on) {
@@ -181,9 +178,11 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
     uint32_t b[VE / 4];
 #pragma unroll
     for (int k = 0; k < VE / 4; ++k) {
+      // (divided: a product with a rounded inverse takes the neighbouring code beside a tie;
+      // the same 58 us for 8192 x 4096 bf16, 2 us more for 10007 x 1537 fp32)
       const float* v = s[c] + 4 * k;
-      b[k] = a.quant == REWY_QUANT_E4M3 ? pack_e4m3(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv)
-                                        : pack_int8(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      b[k] = a.quant == REWY_QUANT_E4M3 ? pack_e4m3(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale)
+                                        : pack_int8(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale);
     }
     if (D - j >= VE) {
       typedef uint32_t words __attribute__((ext_vector_type(VE / 4)));

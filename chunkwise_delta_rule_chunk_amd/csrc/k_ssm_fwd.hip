@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int nblk, int bwd) 
 // tokens send to the state that enters it, all but the first.  Wave w holds 16 columns
 // of one head's state.  8192 x 32 heads, K = V = 128 in segments of 512: x read and 31 MB
 // of states written, 28.8 us (3.4 TB/s).  Both directions of K = 128, V = 64: 33 us.
-template <typename T, int K, int V, int HB, int NS>
+template <typename T, int K, int V, int HB>
 __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_state(SsmArgs a) {
   constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, LK = pitch<T>(K), LV = pitch<T>(CW);
   constexpr int NQ = CH / KG<T>, NT = K / 16;
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_state(SsmArgs a) {
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int q = 0; q < NQ; ++q) ut[ct][q] = frag_col<T>(su, LV, q * KG<T>, 16 * (CT * w + ct));
-    state_update<T, K, CT, NS>(S, sk, LK, ut, sal[hw], sdec[hw]);
+    state_update<T, K, CT, SPLIT<T>>(S, sk, LK, ut, sal[hw], sdec[hw]);
     lds_barrier();
   }
   // (forward and reverse sum the same decays, each for the segments it takes)
@@ -166,12 +166,13 @@ __global__ __launch_bounds__(256) void k_ssm_pass(SsmArgs a) {
 // coefficients M (one 64 x 64 matrix a head, from C B^T and the gates, which are a
 // chunk ahead) are formed block by block by all waves and shared through LDS.  Two
 // barriers a chunk: tiles and M complete; tiles and M free.  y leaves through
-// the x tile, whole rows at a time.  8192 x 32 heads, K = V = 128: 67.5 us, 196 MB (2.9
-// TB/s) and 28 GFLOP (420 TFLOP/s): two waves a SIMD, whose matrix instructions (a
-// quarter of the time), coefficients and LDS traffic leave each other gaps.  V = 64: 42.6
-// us; fp32, 9000 x 16 heads, K = V = 64 in 16 sequences: 62.8 us, where the fp32
+// the x tile, whole rows at a time.  8192 x 32 heads, K = V = 128: 78 us, 196 MB (2.5
+// TB/s) and 38 GFLOP (480 TFLOP/s): two waves a SIMD, whose matrix instructions,
+// coefficients and LDS traffic leave each other gaps (64 us with updates of the state in two
+// pieces, ssm.hpp).  V = 64: 43 us;
+// fp32, 9000 x 16 heads, K = V = 64 in 16 sequences: 62.8 us, where the fp32
 // matrix instructions take half of the time.
-template <typename T, int K, int V, int HB, int CT, int NS>
+template <typename T, int K, int V, int HB, int CT>
 __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
   constexpr int CW = HB * V, NTH = 4 * CW / CT, NW = NTH / 64;
   constexpr int LK = pitch<T>(K), LV = pitch<T>(CW), LM = pitch<T>(CH);
@@ -350,7 +351,7 @@ __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
     for (int I = 0; I < 4; ++I)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) st4<T>(xw + 16 * I * LV + 16 * ct, Y[ct][I]);
-    state_update<T, K, CT, NS>(S, sb, LK, xt, sal[p][hw], sdec[p][hw]);
+    state_update<T, K, CT, SPLIT<T>>(S, sb, LK, xt, sal[p][hw], sdec[p][hw]);
     if (odd) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
@@ -479,8 +480,7 @@ hipError_t launch_ssm_state(const SsmArgs& a, bool f32, bool both, hipStream_t s
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
     const dim3 grid(a.nslot * ssm_head_blocks(a, HB), both ? 2 : 1), block(4 * HB * V);
-    if (both || a.ht) REWY_LAUNCH((k_ssm_state<T, K, V, HB, SPLIT<T>>), grid, block, s, a);
-    else REWY_LAUNCH((k_ssm_state<T, K, V, HB, SPLIT_Y<T>>), grid, block, s, a);
+    REWY_LAUNCH((k_ssm_state<T, K, V, HB>), grid, block, s, a);
     return hipGetLastError();
   });
 }
@@ -494,8 +494,7 @@ hipError_t launch_ssm_fwd(const SsmArgs& a, bool f32, hipStream_t s) {
     constexpr int K = decltype(k)::value, V = decltype(v)::value, HB = decltype(hb)::value;
     constexpr int CT = V == 128 ? 2 : 1;
     const dim3 grid(a.nslot * ssm_head_blocks(a, HB)), block(4 * HB * V / CT);
-    if (a.ht) REWY_LAUNCH((k_ssm_fwd<T, K, V, HB, CT, SPLIT<T>>), grid, block, s, a);
-    else REWY_LAUNCH((k_ssm_fwd<T, K, V, HB, CT, SPLIT_Y<T>>), grid, block, s, a);
+    REWY_LAUNCH((k_ssm_fwd<T, K, V, HB, CT>), grid, block, s, a);
     return hipGetLastError();
   });
 }

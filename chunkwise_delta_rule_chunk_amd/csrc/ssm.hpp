@@ -230,13 +230,10 @@ __device__ __forceinline__ void frag_get(float (&f)[VEC<T>], uint4 v) {
 }
 // An fp32 value that meets a 16-bit operand in a product whose sum is kept in fp32
 // (states, decay gradients) is given as the sum of SPLIT bf16 values, hi + mid +
-// lo: 24 bits, as many as fp32 has.  Two (17 bits) do for a state that only a bf16
-// output reads (one would add as much error as the output's own rounding).  fp32
-// operands are one piece.
+// lo: 24 bits, as many as fp32 has, whether or not the call hands out the final state (two
+// pieces, 17 bits, would make a prompt's y depend on that).  fp32 operands are one piece.
 template <typename T>
 constexpr int SPLIT = std::is_same_v<T, bf16> ? 3 : 1;
-template <typename T>
-constexpr int SPLIT_Y = std::is_same_v<T, bf16> ? 2 : 1;
 template <typename T, int NS>
 __device__ __forceinline__ void frag_split(uint4 (&out)[NS], const float (&f)[VEC<T>]) {
   if constexpr (std::is_same_v<T, bf16>) {

@@ -353,7 +353,7 @@ typedef struct {
 size_t rewy_ssm_workspace_bytes(const rewy_ssm_desc *d, int phase);
 
 /* Forward in chunks of 64 tokens, for prompts and training.  h0 and ht may be
- * NULL.  An infinity or NaN in a token's row reaches that token and the ones
+ * NULL; y does not depend on whether ht is given.  An infinity or NaN in a token's row reaches that token and the ones
  * behind it, as in the recurrence. */
 int rewy_ssm_fwd(const rewy_ssm_desc *d, const void *x, const void *dt, const float *a_log,
                  const float *dt_bias, const void *b, const void *c, const float *D,

@@ -143,6 +143,15 @@ def _adjoint(dy, ref):
     return ref.new_zeros(ref.shape) if dy is None else dy.contiguous()
 
 
+def _aligned(t):
+    """t, contiguous, at a multiple of 16 bytes: autograd may send back a view at any
+    offset of a larger buffer."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 # ---- RMS norm -----------------------------------------------------------------
 def rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0, output=True,
              stream=None):
@@ -476,8 +485,7 @@ class SelectiveScanFunction(torch.autograd.Function):
     def backward(fctx, dy, dht):
         names = ("x", "dt", "a_log", "b", "c", "d", "dt_bias", "h0")
         ctx = dict(fctx.rewy, **dict(zip(names, fctx.saved_tensors)))
-        g = selective_scan_backward(ctx, _adjoint(dy, ctx["x"]), None if dht is None else dht.contiguous(),
-                                    clear=fctx.clear)
+        g = selective_scan_backward(ctx, _aligned(_adjoint(dy, ctx["x"])), _aligned(dht), clear=fctx.clear)
         return (g["dx"], g["ddt"], g["da_log"], g["db"], g["dc"], g["dd"], g["ddt_bias"], g["dh0"], None)
 
 

@@ -233,7 +233,9 @@ class RMSNormFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(fctx, dy, ds):
-        s, weight, rstd = fctx.saved_tensors
+        s, weight, rstd = fctx.saved_tensors  # (checked again: _saved_problem)
+        _like(weight, s, s.shape[-1:], "weight")
+        _like(rstd, s, (s.shape[:-1].numel(),), "rstd", torch.float32)
         g = rms_norm_backward(dict(s=s, weight=weight, rstd=rstd, eps=fctx.eps), _adjoint(dy, s),
                               None if ds is None else ds.contiguous())
         return g["dx"], g["dweight"], g["dx"] if fctx.residual else None, None
@@ -263,6 +265,16 @@ def _sequences(x, cu_seqlens, T):
         raise ValueError(f"cu_seqlens must end at T={T}")
     host = (ctypes.c_int32 * len(vals))(*vals)
     return len(vals) - 1, torch.tensor(vals, dtype=torch.int32, device=x.device), host
+
+
+def _saved_problem(problem, host):
+    """The problem of tensors that autograd saved, with the forward's host copy of the
+    offsets.  Hooks on saved tensors may return them in another layout (contiguous, from
+    the host), so strides, types and shapes are those of what came back, not the forward's."""
+    desc, shape, cu, own = problem
+    if host is not None:
+        desc.cu_seqlens_host, own = ctypes.addressof(host), host
+    return desc, shape, cu, own
 
 
 # ---- short convolution ------------------------------------------------------------
@@ -352,13 +364,15 @@ class ShortConvFunction(torch.autograd.Function):
         y, ht, ctx = short_conv(x, weight, bias, activation=activation, h0=h0, cu_seqlens=cu_seqlens,
                                 output_final_state=True, clear=fctx.clear)
         fctx.save_for_backward(x, weight, bias, h0)
-        fctx.rewy = {k: ctx[k] for k in ("desc", "cu", "host")}
+        fctx.activation, fctx.cu, fctx.host = activation, ctx["cu"], ctx["host"]
         return y, ht
 
     @staticmethod
     @once_differentiable
     def backward(fctx, dy, dht):
-        ctx = dict(fctx.rewy, **dict(zip(("x", "weight", "bias", "h0"), fctx.saved_tensors)))
+        x, weight, bias, h0 = fctx.saved_tensors
+        desc, _, cu, host = _saved_problem(_conv_problem(x, weight, bias, h0, fctx.activation, fctx.cu), fctx.host)
+        ctx = dict(desc=desc, x=x, weight=weight, bias=bias, h0=h0, cu=cu, host=host)
         g = short_conv_backward(ctx, _adjoint(dy, ctx["x"]), None if dht is None else dht.contiguous(),
                                 clear=fctx.clear)
         return g["dx"], g["dweight"], g["dbias"], g["dh0"], None, None
@@ -477,14 +491,16 @@ class SelectiveScanFunction(torch.autograd.Function):
         y, ht, ctx = selective_scan(x, dt, a_log, b, c, d=d, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
                                     clear=fctx.clear)
         fctx.save_for_backward(x, dt, a_log, b, c, d, dt_bias, h0)
-        fctx.rewy = {k: ctx[k] for k in ("desc", "cu", "host")}
+        fctx.cu, fctx.host = ctx["cu"], ctx["host"]
         return y, ht
 
     @staticmethod
     @once_differentiable
     def backward(fctx, dy, dht):
         names = ("x", "dt", "a_log", "b", "c", "d", "dt_bias", "h0")
-        ctx = dict(fctx.rewy, **dict(zip(names, fctx.saved_tensors)))
+        saved = fctx.saved_tensors
+        desc, _, cu, host = _saved_problem(_scan_problem(*saved, fctx.cu), fctx.host)
+        ctx = dict(zip(names, saved), desc=desc, cu=cu, host=host)
         g = selective_scan_backward(ctx, _aligned(_adjoint(dy, ctx["x"])), _aligned(dht), clear=fctx.clear)
         return (g["dx"], g["ddt"], g["da_log"], g["db"], g["dc"], g["dd"], g["ddt_bias"], g["dh0"], None)
 

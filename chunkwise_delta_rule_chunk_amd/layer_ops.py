@@ -363,15 +363,15 @@ class ShortConvFunction(torch.autograd.Function):
         fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
         y, ht, ctx = short_conv(x, weight, bias, activation=activation, h0=h0, cu_seqlens=cu_seqlens,
                                 output_final_state=True, clear=fctx.clear)
-        fctx.save_for_backward(x, weight, bias, h0)
-        fctx.activation, fctx.cu, fctx.host = activation, ctx["cu"], ctx["host"]
+        fctx.save_for_backward(x, weight, bias, h0, ctx["cu"])
+        fctx.activation, fctx.host = activation, ctx["host"]
         return y, ht
 
     @staticmethod
     @once_differentiable
     def backward(fctx, dy, dht):
-        x, weight, bias, h0 = fctx.saved_tensors
-        desc, _, cu, host = _saved_problem(_conv_problem(x, weight, bias, h0, fctx.activation, fctx.cu), fctx.host)
+        x, weight, bias, h0, cu = fctx.saved_tensors
+        desc, _, cu, host = _saved_problem(_conv_problem(x, weight, bias, h0, fctx.activation, cu), fctx.host)
         ctx = dict(desc=desc, x=x, weight=weight, bias=bias, h0=h0, cu=cu, host=host)
         g = short_conv_backward(ctx, _adjoint(dy, ctx["x"]), None if dht is None else dht.contiguous(),
                                 clear=fctx.clear)
@@ -490,8 +490,8 @@ class SelectiveScanFunction(torch.autograd.Function):
         fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
         y, ht, ctx = selective_scan(x, dt, a_log, b, c, d=d, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
                                     clear=fctx.clear)
-        fctx.save_for_backward(x, dt, a_log, b, c, d, dt_bias, h0)
-        fctx.cu, fctx.host = ctx["cu"], ctx["host"]
+        fctx.save_for_backward(x, dt, a_log, b, c, d, dt_bias, h0, ctx["cu"])
+        fctx.host = ctx["host"]
         return y, ht
 
     @staticmethod
@@ -499,7 +499,7 @@ class SelectiveScanFunction(torch.autograd.Function):
     def backward(fctx, dy, dht):
         names = ("x", "dt", "a_log", "b", "c", "d", "dt_bias", "h0")
         saved = fctx.saved_tensors
-        desc, _, cu, host = _saved_problem(_scan_problem(*saved, fctx.cu), fctx.host)
+        desc, _, cu, host = _saved_problem(_scan_problem(*saved), fctx.host)
         ctx = dict(zip(names, saved), desc=desc, cu=cu, host=host)
         g = selective_scan_backward(ctx, _aligned(_adjoint(dy, ctx["x"])), _aligned(dht), clear=fctx.clear)
         return (g["dx"], g["ddt"], g["da_log"], g["db"], g["dc"], g["dd"], g["ddt_bias"], g["dh0"], None)

@@ -37,3 +37,21 @@ def test_saved_on_the_host(packed):
         out = loss()
     got = torch.autograd.grad(out, leaves)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_offsets_changed_before_the_backward():
+    """Offsets that only the GPU holds are part of what the backward reads: overwritten in place
+    between the forward and the backward, they are refused as any saved tensor is."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    g = torch.Generator(device="cuda").manual_seed(7)
+    leaf = lambda *s: torch.randn(*s, generator=g, device="cuda").requires_grad_(True)  # noqa: E731
+    x, w = leaf(1, 90, 24), leaf(24, 4)
+    args = (leaf(1, 90, 2, 32), leaf(1, 90, 2), leaf(2), leaf(1, 90, 1, 32), leaf(1, 90, 1, 32))
+    cu = torch.tensor([0, 40, 90], dtype=torch.int32, device="cuda")
+    for call in (lambda: ops.short_conv_autograd(x, w, cu_seqlens=cu), lambda: ops.selective_scan_autograd(*args, cu_seqlens=cu)):
+        y, _ = call()
+        cu[1] += 5
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            y.sum().backward()
+        y, _ = call()
+        y.sum().backward()

@@ -449,7 +449,8 @@ def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, clear
     """Gradients of the scan: dict(dx, ddt, da_log, db, dc, dd, ddt_bias, dh0).
     dy may be a slice of longer rows.  ``out=(dx, db, dc)`` gives the places of
     those three (slices of one row, for the convolution's backward); ``clear`` as in
-    the forward, for the gradients that are made here."""
+    the forward, for the gradients that are made here.  dh0 is handed out where h0 was
+    given, or as ``want_dh0`` says."""
     x, dt, a_log, b, c, d, dt_bias, h0 = (ctx[k] for k in ("x", "dt", "a_log", "b", "c", "d", "dt_bias",
                                                            "h0"))
     if dy.shape != x.shape or dy.dtype != x.dtype:
@@ -473,12 +474,14 @@ def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, clear
         ddt, da_log = _like_new(dt, clear), torch.empty_like(a_log)
         dd = None if d is None else torch.empty_like(d)
         ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
-        dh0 = x.new_empty(shape, dtype=torch.float32) if want_dh0 else None
+        # (the entry writes it wherever there is a state)
+        dh0 = x.new_empty(shape, dtype=torch.float32) if want_dh0 or h0 is not None else None
         ws = _workspace(B.rewy_ssm_workspace_bytes(desc, 1), x, ws)
         _check(B.rewy_ssm_bwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
                               _p(dy), _p(dht), _p(dx), _p(ddt), _p(da_log), _p(ddt_bias), _p(db), _p(dc),
                               _p(dd), _p(dh0), _p(ws), ws.numel(), handle), "rewy_ssm_bwd")
-    return dict(dx=dx, ddt=ddt, da_log=da_log, db=db, dc=dc, dd=dd, ddt_bias=ddt_bias, dh0=dh0)
+    return dict(dx=dx, ddt=ddt, da_log=da_log, db=db, dc=dc, dd=dd, ddt_bias=ddt_bias,
+                dh0=dh0 if want_dh0 else None)
 
 
 class SelectiveScanFunction(torch.autograd.Function):

@@ -291,9 +291,13 @@ __global__ __launch_bounds__(256) void k_state_through(f32x4* dst, const f32x4* 
 int state_through(const SsmArgs& a, float* dst, const float* src, hipStream_t s) {
   if (!dst || dst == src) return REWY_OK;
   const int64_t n = (int64_t)a.seq.N * a.H * a.K * a.V / 4;
-  REWY_LAUNCH(k_state_through, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256), s,
-              reinterpret_cast<f32x4*>(dst), reinterpret_cast<const f32x4*>(src), n);
-  return hip_check(hipGetLastError(), "state copy");
+  return hip_check(traced("k_state_through", s,
+                          [&] {
+                            REWY_LAUNCH(k_state_through, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256),
+                                        s, reinterpret_cast<f32x4*>(dst), reinterpret_cast<const f32x4*>(src), n);
+                            return hipGetLastError();
+                          }),
+                   "state copy");
 }
 
 }  // namespace
@@ -402,9 +406,11 @@ REWY_API int rewy_conv_bwd(const rewy_conv_desc* d, const void* x, const void* w
     a.dx = dx; a.dw = dw; a.dbias = dbias; a.dh0 = dh0;
     a.part = static_cast<float*>(workspace);
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return hip_check(traced("k_conv_bwd", s,
-                            [&] { return launch_conv_bwd(a, d->dtype == REWY_F32, d->w_dtype == REWY_F32, s); }),
-                     "convolution backward");
+    const bool wf32 = d->w_dtype == REWY_F32;
+    if (a.tiles > 0 || dh0)  // (otherwise no kernel runs, and none is to be named)
+      REWY_TRY(hip_check(traced("k_conv_bwd", s, [&] { return launch_conv_bwd(a, d->dtype == REWY_F32, wf32, s); }),
+                         "convolution backward"));
+    return hip_check(traced("k_conv_reduce", s, [&] { return launch_conv_reduce(a, wf32, s); }), "weight gradient");
   });
 }
 

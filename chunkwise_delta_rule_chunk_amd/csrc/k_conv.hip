@@ -427,12 +427,15 @@ hipError_t conv_bwd_t(const ConvArgs& a, hipStream_t s) {
     constexpr int W = decltype(w)::value;
     const int fin = a.dh0 ? a.seq.N : 0;
     const dim3 grid((a.tiles + fin) * a.cblocks), block(64);
-    if (a.tiles + fin > 0) {
-      if (a.full) REWY_LAUNCH((k_conv_bwd<T, WT, W, true>), grid, block, s, a);
-      else REWY_LAUNCH((k_conv_bwd<T, WT, W, false>), grid, block, s, a);
-    }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (a.full) REWY_LAUNCH((k_conv_bwd<T, WT, W, true>), grid, block, s, a);
+    else REWY_LAUNCH((k_conv_bwd<T, WT, W, false>), grid, block, s, a);
+    return hipGetLastError();
+  });
+}
+template <typename WT>
+hipError_t conv_reduce_t(const ConvArgs& a, hipStream_t s) {
+  return conv_taps_of(a.W, [&](auto w) {
+    constexpr int W = decltype(w)::value;
     REWY_LAUNCH((k_conv_reduce<WT, W>), dim3((a.D + 15) / 16, W + 1), dim3(256), s, a);
     return hipGetLastError();
   });
@@ -484,6 +487,9 @@ hipError_t launch_conv_bwd(ConvArgs a, bool f32, bool wf32, hipStream_t s) {
   a.full = conv_full(a, f32 ? 4 : 2, a.dx, a.dxs);
   if (f32) return wf32 ? conv_bwd_t<float, float>(a, s) : conv_bwd_t<float, bf16>(a, s);
   return wf32 ? conv_bwd_t<bf16, float>(a, s) : conv_bwd_t<bf16, bf16>(a, s);
+}
+hipError_t launch_conv_reduce(const ConvArgs& a, bool wf32, hipStream_t s) {
+  return wf32 ? conv_reduce_t<float>(a, s) : conv_reduce_t<bf16>(a, s);
 }
 
 }  // namespace rewy

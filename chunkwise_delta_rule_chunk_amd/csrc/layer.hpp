@@ -143,5 +143,6 @@ void conv_bwd_shape(int total, int D, int& run, int& tiles);
 hipError_t launch_conv_fwd(ConvArgs a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs& a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_conv_bwd(ConvArgs a, bool f32, bool wf32, hipStream_t s);
+hipError_t launch_conv_reduce(const ConvArgs& a, bool wf32, hipStream_t s);
 
 }  // namespace rewy

@@ -74,6 +74,12 @@ int norm_args(const rewy_norm_desc* d, NormArgs& a) {
   a.nblk = norm_bwd_blocks(d->M, d->D, d->dtype == REWY_F32);
   return REWY_OK;
 }
+// An output over an input row by row: with another stride a row would be written before
+// another workgroup has read it.
+int norm_in_place(const NormArgs& a, const char* out, const void* o, int64_t os, const char* in, const void* i, int64_t is) {
+  if (a.M > 1 && o && o == i && os != is) return fail(REWY_EINVAL, "%s over %s needs the same stride", out, in);
+  return REWY_OK;
+}
 size_t norm_ws(const NormArgs& a) { return up(std::max<size_t>((size_t)a.nblk * a.D * 4, 1)); }
 
 // ---- sequences ------------------------------------------------------------------
@@ -321,6 +327,10 @@ REWY_API int rewy_norm_fwd(const rewy_norm_desc* d, const void* x, const void* r
     REWY_TRY(check_ptr("scale", scale, 4, some && d->quant != REWY_QUANT_NONE));
     REWY_TRY(check_ptr("q", q, 1, some && d->quant != REWY_QUANT_NONE));
     if (d->quant == REWY_QUANT_NONE && (q || scale)) return fail(REWY_EINVAL, "q and scale are given only when quant != NONE");
+    REWY_TRY(norm_in_place(a, "sum", sum, a.ss, "x", x, a.xs));
+    REWY_TRY(norm_in_place(a, "sum", sum, a.ss, "res", res, a.rs));
+    REWY_TRY(norm_in_place(a, "y", y, a.ys, "x", x, a.xs));
+    REWY_TRY(norm_in_place(a, "y", y, a.ys, "res", res, a.rs));
     if (!some) return REWY_OK;
     a.x = x; a.res = res; a.w = w; a.sum = sum; a.y = y; a.q = q; a.scale = scale; a.rstd = rstd;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -350,6 +360,9 @@ REWY_API int rewy_norm_bwd(const rewy_norm_desc* d, const void* sv, const void* 
     REWY_TRY(check_ptr("dx", dx, e, some));
     REWY_TRY(check_ptr("dw", dw, we, false));
     if (dw && !w) return fail(REWY_EINVAL, "dw is given without w");
+    REWY_TRY(norm_in_place(a, "dx", dx, a.ss, "s", sv, a.xs));
+    REWY_TRY(norm_in_place(a, "dx", dx, a.ss, "dy", dy, a.ys));
+    REWY_TRY(norm_in_place(a, "dx", dx, a.ss, "ds", ds, a.rs));
     if (dw) REWY_TRY(check_workspace(workspace, ws_bytes, norm_ws(a)));
     a.x = sv; a.w = w; a.rstd = const_cast<float*>(rstd); a.dy = dy; a.res = ds; a.sum = dx; a.dw = dw;
     a.part = dw ? static_cast<float*>(workspace) : nullptr;

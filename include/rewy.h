@@ -273,7 +273,7 @@ size_t rewy_norm_workspace_bytes(const rewy_norm_desc *d);
  * stored sum (x itself without a residual; x_stride), rstd what the forward
  * wrote, dy [M, D] (y_stride), ds the adjoint of the sum's other use
  * (res_stride) or NULL.  dx (sum_stride) is the gradient of x and of res
- * alike and may be ds itself; dw ([D], w_dtype) may be NULL, and must be NULL when
+ * alike and may be ds itself (same stride); dw ([D], w_dtype) may be NULL, and must be NULL when
  * w is.  The workspace is 256-byte aligned. */
 int rewy_norm_bwd(const rewy_norm_desc *d, const void *s, const void *w, const float *rstd,
                   const void *dy, const void *ds, void *dx, void *dw,

@@ -152,11 +152,12 @@ int conv_forward(const rewy_conv_desc* d, bool step, const void* x, const void* 
 }
 
 // ---- selective state space scan ---------------------------------------------------
-// Tokens of a segment, whole chunks: as long as the segments of all heads still fill
-// the chip with SEGMENTS of them, two workgroups a CU (a longer segment means fewer
-// states to join).  Sequences of equal length: ceil(T / segment) each.  Packed ones end
-// with half a segment on average, which leaves the target (N - 1) / 2 a head less, at
-// least half of it.
+// Tokens of a segment, whole chunks, at least 256: as long as there are SEGMENTS pairs of a
+// segment and a head (a longer segment means fewer states to join).  With one head a
+// workgroup (V = 128, the walks of V = 64) that is two workgroups for each CU; where heads
+// share one (V = 64 and 32 of the forward) it is half or a quarter as many.  Sequences of equal
+// length: ceil(T / segment) each.  Packed ones end with half a segment on average, which
+// leaves the target (N - 1) / 2 a head less, at least half of it.
 int ssm_segment(const SeqArgs& q, int H, int most) {
   constexpr int64_t SEGMENTS = 512;
   int64_t want;

@@ -88,7 +88,9 @@ __device__ __forceinline__ void conv_final(const ConvArgs& a, int n, int c, int 
 // and stores through a buffer resource, whose range check drops the rows past the
 // run.  The compiler can then count the requests in flight (one counter serves
 // loads and stores) and a row's use waits for that row alone; with loads and stores
-// in branches it waited for all of them (45 instead of 30 us for 8192 x 4352).
+// in branches, as other channel numbers and alignments take them, it waits for all of
+// them (8192 x 4352: 28 us, x 4354: 46, x 4351, whose vectors are also unaligned: 60;
+// backward of 32768 x 2304: 111 us, x 2306: 243).
 template <typename T, bool FULL>
 struct Row {
   typename VecN<T, VE>::raw v;
@@ -268,8 +270,8 @@ __device__ __forceinline__ void conv_dh0(const ConvArgs& a, int n, int c, int nv
 // U in flight); a token's dpre meets the W rows that it reached, and a row leaves
 // when the W - 1 tokens behind it have entered.  One pass: the convolution is formed
 // again from x, so x, dy and dx pass memory once.  32768 x 2304 bf16 in 16 sequences:
-// 453 MB, 500 with the partial sums and the runs' shared rows, in 115 us (4.3 TB/s;
-// the forward of the same rows 62.8 us, 4.8 TB/s).
+// 453 MB, 500 with the partial sums and the runs' shared rows, in 113 us (4.4 TB/s;
+// the forward of the same rows 62 us, 5.1 TB/s).
 template <typename T, typename WT, int W, bool FULL>
 __global__ __launch_bounds__(64) void k_conv_bwd(ConvArgs a) {
   constexpr int U = W == 3 ? 3 : 4;  // (more do not fit beside the windows and sums)

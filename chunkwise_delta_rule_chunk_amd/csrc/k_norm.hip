@@ -87,9 +87,9 @@ __device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d
 
 // One row a group of TPR threads: all loads first, one join for the mean, one for the
 // scale (a group of columns lies in neighbouring lanes: no LDS).  Bound by HBM:
-// 8192 x 4096 bf16 with the sum, e4m3 in groups of 128: 302 MB in 56.5 us (5.3 TB/s);
-// without the 8-bit output but with y 49.5 us (5.4 TB/s); 10007 x 1537 fp32 to int8 30.7
-// us; 16 rows of 4096: 5.5 us, a launch and two trips to memory.
+// 8192 x 4096 bf16 with the sum, e4m3 in groups of 128: 304 MB in 55 us (5.5 TB/s);
+// without the 8-bit output but with y 49 us (5.5 TB/s); 10007 x 1537 fp32 to int8 33
+// us; 16 rows of 4096: 6 us, a launch and two trips to memory.
 template <typename T, typename W, int TPR, int NC>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fwd(NormArgs a) {
   constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
 #pragma unroll
     for (int k = 0; k < VE / 4; ++k) {
       // (divided: a product with a rounded inverse takes the neighbouring code beside a tie;
-      // the same 58 us for 8192 x 4096 bf16, 2 us more for 10007 x 1537 fp32)
+      // no slower for 8192 x 4096 bf16, 33 instead of 30.5 us for 10007 x 1537 fp32)
       const float* v = s[c] + 4 * k;
       b[k] = a.quant == REWY_QUANT_E4M3 ? pack_e4m3(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale)
                                         : pack_int8(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale);

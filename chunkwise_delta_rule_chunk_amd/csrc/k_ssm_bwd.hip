@@ -22,9 +22,10 @@ namespace {
 // state that enters each chunk goes to hs, and rx_t = exp(G_t) dy_t . (S_in^T
 // C_t); reverse: the adjoint that leaves each chunk goes to hd, and cx_t =
 // exp(G_L - G_t) x_t . (dS^T B_t).  Wave w holds 16 columns of one head.  Heads of 64
-// columns in workgroups of their own (two a CU, which fill each other's waits: 85 us,
-// two heads in one workgroup 93).  8192 x 32 heads, K = 128, V = 64: 85 us; 313 MB (134 of them the handed-over states; 3.7 TB/s)
-// and 52 GFLOP, as the states meet the 16-bit operands in three pieces (610 TFLOP/s).
+// columns in workgroups of their own (two a CU, which fill each other's waits: 85 us in a row
+// of calls, two heads in one workgroup 93).  8192 x 32 heads, K = 128, V = 64, alone: 97 us, 90 at
+// least; 321 MB (134 of them the handed-over states; 3.3 TB/s) and 52 GFLOP, as the states
+// meet the 16-bit operands in three pieces (540 TFLOP/s).
 template <typename T, int K, int V, int HB>
 __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_walk(SsmArgs a) {
   constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, NW = NTH / 64;
@@ -178,8 +179,9 @@ constexpr int cb_waves(int K, int V) { return K == 64 && V >= 64 ? 16 : 8; }
 // One chunk, one group, a range of its heads: dx, the parts of r and c inside
 // the chunk, and dB, dC summed over the heads in registers.  Wave w owns rows
 // 16 (w & 3) .. + 15 of the chunk and share w >> 2 of the state rows (dB, dC) or
-// of the columns (dx).  The size above: 77 us, 262 MB (3.3 TB/s; the states half of
-// them) and 16 GFLOP; eight waves a CU, as its tiles take most of the LDS.
+// of the columns (dx).  The size above, alone: 85 us, 79 at least (77 in a row of calls), 267
+// MB (3.1 TB/s; the states half of them) and 16 GFLOP; one workgroup a CU, as its tiles take
+// most of the LDS.
 template <typename T, int K, int V>
 __global__ __launch_bounds__(64 * cb_waves(K, V)) void k_ssm_chunk(SsmArgs a) {
   constexpr int NW = cb_waves(K, V), NTH = 64 * NW, LK = pitch<T>(K), LV = pitch<T>(V), LM = pitch<T>(CH), NQ = CH / KG<T>;

@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void k_ssm_prep(SsmArgs a, int nblk, int bwd) 
 // sequence's last segment; reverse (dir 1), the adjoint that the segment's own
 // tokens send to the state that enters it, all but the first.  Wave w holds 16 columns
 // of one head's state.  8192 x 32 heads, K = V = 128 in segments of 512: x read and 31 MB
-// of states written, 28.8 us (3.4 TB/s).  Both directions of K = 128, V = 64: 33 us.
+// of states written, 34 us (3.0 TB/s).  Both directions of K = 128, V = 64: 35 us.
 template <typename T, int K, int V, int HB>
 __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_state(SsmArgs a) {
   constexpr int CW = HB * V, CT = 1, NTH = 4 * CW, LK = pitch<T>(K), LV = pitch<T>(CW);
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(4 * HB * V, 2) void k_ssm_state(SsmArgs a) {
 // In place: the local states of a sequence's segments become the states that
 // enter them (forward; from h0) or the adjoints of the states that leave them
 // (reverse; from dht).  Bound by HBM (the 15 states of 64 KB and 32 heads above:
-// 11.1 us, 5.5 TB/s).
+// 11.7 us, 5.6 TB/s).
 __global__ __launch_bounds__(256) void k_ssm_pass(SsmArgs a) {
   const int kv = a.K * a.V, n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, dir = blockIdx.z;
   const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
@@ -166,12 +166,16 @@ __global__ __launch_bounds__(256) void k_ssm_pass(SsmArgs a) {
 // coefficients M (one 64 x 64 matrix a head, from C B^T and the gates, which are a
 // chunk ahead) are formed block by block by all waves and shared through LDS.  Two
 // barriers a chunk: tiles and M complete; tiles and M free.  y leaves through
-// the x tile, whole rows at a time.  8192 x 32 heads, K = V = 128: 78 us, 196 MB (2.5
-// TB/s) and 38 GFLOP (480 TFLOP/s): two waves a SIMD, whose matrix instructions,
-// coefficients and LDS traffic leave each other gaps (64 us with updates of the state in two
-// pieces, ssm.hpp).  V = 64: 43 us;
-// fp32, 9000 x 16 heads, K = V = 64 in 16 sequences: 62.8 us, where the fp32
-// matrix instructions take half of the time.
+// the x tile, whole rows at a time.
+// With bf16 operands M and the entering state are rounded to bf16 once each as operands of
+// y's products, which y's own rounding covers (8192 x 32 heads, K = V = 128: y is off by
+// 1.8e-3 in norm, by 1.7e-3 if it is formed in 32 bits and only rounded at the end); two
+// pieces each would double those products.  The carried state meets no such rounding.
+// The size above: 80 us, 225 MB (2.8 TB/s; 18 MB of it registers that do not fit) and 38
+// GFLOP (470 TFLOP/s): two waves a SIMD, whose matrix instructions, coefficients and LDS
+// traffic leave each other gaps (66 us if the state's updates come in two pieces,
+// ssm.hpp).  V = 64: 46 us; fp32, 9000 x 16 heads, K = V = 64 in 16 sequences: 63 us,
+// where the fp32 matrix instructions take half of the time.
 template <typename T, int K, int V, int HB, int CT>
 __global__ __launch_bounds__(4 * HB * V / CT, 2) void k_ssm_fwd(SsmArgs a) {
   constexpr int CW = HB * V, NTH = 4 * CW / CT, NW = NTH / 64;

@@ -51,7 +51,7 @@ struct SsmArgs {
   float* cb;               // [nchunk, G, 10, 64 lanes, 4] C B^T, blocks of the lower triangle as C fragments
   float* sf;               // [nslot, H, K, V] local end states, then the states that enter the segments
   float* sr;               // [nslot, H, K, V] local adjoints, then the adjoints of the states that leave them
-  float* gsum;             // [nslot, H] sum of g (log2 units) over a segment
+  float* gsum;             // [2, nslot, H] sum of g (log2 units) over a segment, for each direction
   void* hs;                // [nchunk, H, V/16, K/16, 64 lanes, 4] state entering each chunk (operand type)
   void* hd;                // same: adjoint of the state leaving each chunk
   float* rx;               // [H, tokens] row part of the decay gradient through the entering state

@@ -139,3 +139,67 @@ def test_a_graph_of_autograd_used_twice():
     once = torch.autograd.grad(z.sum(), leaves, retain_graph=True)
     again = torch.autograd.grad(z.sum(), leaves)
     assert _same(once, again)
+
+
+def test_states_and_their_adjoints_left_out():
+    """No initial state is a state of zeros, no adjoint one of zeros; dh0 may be asked for without h0."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    rn = _gen(6)
+    for T, dt in ((600, torch.bfloat16), (70, torch.float32)):
+        a = (rn(2, T, 2, 64).to(dt), rn(2, T, 2) - 3, rn(2), rn(2, T, 1, 32).to(dt), rn(2, T, 1, 32).to(dt))
+        z, dy = torch.zeros(2, 2, 32, 64, device="cuda"), rn(2, T, 2, 64).to(dt)
+        y, ht, c = ops.selective_scan(*a)
+        y0, ht0, c0 = ops.selective_scan(*a, h0=z)
+        assert torch.equal(y, y0) and torch.equal(ht, ht0)
+        g, g0 = ops.selective_scan_backward(c, dy, want_dh0=True), ops.selective_scan_backward(c0, dy, z)
+        for k in ("dx", "db", "dc", "dh0"):
+            assert torch.equal(g[k], g0[k]), k
+        for k in ("ddt", "da_log"):  # (a state that is given ends the decay gradient's chains elsewhere)
+            assert (g[k].double() - g0[k].double()).norm() <= 1e-5 * g0[k].double().norm(), k
+        assert ops.selective_scan_backward(c0, dy, z, want_dh0=False)["dh0"] is None
+    x, w, dy = rn(2, 50, 36), rn(36, 4), rn(2, 50, 36)
+    z = torch.zeros(2, 3, 36, device="cuda")
+    y, ht, c = ops.short_conv(x, w, output_final_state=True)
+    y0, ht0, c0 = ops.short_conv(x, w, h0=z, output_final_state=True)
+    assert torch.equal(y, y0) and torch.equal(ht, ht0)
+    g, g0 = ops.short_conv_backward(c, dy), ops.short_conv_backward(c0, dy, z)
+    assert torch.equal(g["dx"], g0["dx"]) and torch.equal(g["dweight"], g0["dweight"]) and g["dh0"] is None
+
+
+def test_two_threads_at_once():
+    """Each thread on a stream of its own; errors of one are not the other's."""
+    import threading
+
+    from chunkwise_delta_rule_chunk_amd import binding as B
+    from chunkwise_delta_rule_chunk_amd import ops
+    rn = _gen(7)
+    sets = [(rn(1, T, 4, 64).bfloat16(), rn(1, T, 4) - 3, rn(4), rn(1, T, 1, 64).bfloat16(), rn(1, T, 1, 64).bfloat16())
+            for T in (500, 900)]
+
+    def once(a):
+        y, ht, c = ops.selective_scan(*a)
+        return [y, ht, *ops.selective_scan_backward(c, a[0], ht).values()]
+
+    want = [once(a) for a in sets]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    out = once(sets[i])
+                    s.synchronize()
+                    assert _same(out, want[i])
+                    with pytest.raises(B.RewyError, match="bad eps"):
+                        ops.rms_norm(sets[i][0], eps=-1.0)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed

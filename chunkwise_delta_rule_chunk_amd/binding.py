@@ -29,6 +29,7 @@ EXPORTS = ("rewy_workspace_bytes", "rewy_saved_bytes", "rewy_fwd", "rewy_bwd", "
            "rewy_norm_fwd", "rewy_norm_workspace_bytes", "rewy_norm_bwd",
            "rewy_conv_fwd", "rewy_conv_step", "rewy_conv_workspace_bytes", "rewy_conv_bwd",
            "rewy_ssm_workspace_bytes", "rewy_ssm_fwd", "rewy_ssm_bwd", "rewy_ssm_recurrent_fwd",
+           "rewy_decay_workspace_bytes", "rewy_decay_fwd", "rewy_decay_bwd", "rewy_decay_recurrent_fwd",
            "rewy_bwd_schedule", "rewy_trace_begin", "rewy_trace_end", "rewy_trace_select",
            "rewy_status_string",
            "rewy_last_error")
@@ -71,6 +72,18 @@ class RewySsmDesc(ctypes.Structure):
         ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
         ("y_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64), ("db_stride", ctypes.c_int64),
         ("dc_stride", ctypes.c_int64),
+    ]
+
+
+class RewyDecayDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("o_stride", ctypes.c_int64), ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64),
+        ("dv_stride", ctypes.c_int64),
     ]
 
 
@@ -124,7 +137,7 @@ def load():
         lib.rewy_recurrent_fwd_gdn2.argtypes = [D] + [P] * 10
         lib.rewy_recurrent_fwd_gdn2.restype = ctypes.c_int
         ND, CD = ctypes.POINTER(RewyNormDesc), ctypes.POINTER(RewyConvDesc)
-        SD = ctypes.POINTER(RewySsmDesc)
+        SD, LD = ctypes.POINTER(RewySsmDesc), ctypes.POINTER(RewyDecayDesc)
         for name, args, res in (
                 ("rewy_norm_fwd", [ND] + [P] * 9, ctypes.c_int),
                 ("rewy_norm_workspace_bytes", [ND], S),
@@ -136,7 +149,11 @@ def load():
                 ("rewy_ssm_workspace_bytes", [SD, ctypes.c_int], S),
                 ("rewy_ssm_fwd", [SD] + [P] * 11 + [S, P], ctypes.c_int),
                 ("rewy_ssm_bwd", [SD] + [P] * 19 + [S, P], ctypes.c_int),
-                ("rewy_ssm_recurrent_fwd", [SD] + [P] * 11, ctypes.c_int)):
+                ("rewy_ssm_recurrent_fwd", [SD] + [P] * 11, ctypes.c_int),
+                ("rewy_decay_workspace_bytes", [LD, ctypes.c_int], S),
+                ("rewy_decay_fwd", [LD] + [P] * 8 + [S, P], ctypes.c_int),
+                ("rewy_decay_bwd", [LD] + [P] * 12 + [S, P], ctypes.c_int),
+                ("rewy_decay_recurrent_fwd", [LD] + [P] * 8, ctypes.c_int)):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = res
         lib.rewy_bwd_schedule.argtypes = [ctypes.c_int]
@@ -259,6 +276,23 @@ def rewy_ssm_bwd(desc, x, dt, a_log, dt_bias, b, c, D, h0, dy, dht, dx, ddt, da_
 def rewy_ssm_recurrent_fwd(desc, x, dt, a_log, dt_bias, b, c, D, h0, y, ht, stream) -> int:
     return load().rewy_ssm_recurrent_fwd(ctypes.byref(desc), x, dt, a_log, dt_bias, b, c, D, h0, y,
                                          ht, stream)
+
+
+def rewy_decay_workspace_bytes(desc, phase) -> int:
+    return load().rewy_decay_workspace_bytes(ctypes.byref(desc), phase)
+
+
+def rewy_decay_fwd(desc, q, k, v, g, h0, o, ht, workspace, ws_bytes, stream) -> int:
+    return load().rewy_decay_fwd(ctypes.byref(desc), q, k, v, g, h0, o, ht, workspace, ws_bytes, stream)
+
+
+def rewy_decay_bwd(desc, q, k, v, g, h0, dO, dht, dq, dk, dv, dh0, workspace, ws_bytes, stream) -> int:
+    return load().rewy_decay_bwd(ctypes.byref(desc), q, k, v, g, h0, dO, dht, dq, dk, dv, dh0, workspace,
+                                 ws_bytes, stream)
+
+
+def rewy_decay_recurrent_fwd(desc, q, k, v, g, h0, o, ht, stream) -> int:
+    return load().rewy_decay_recurrent_fwd(ctypes.byref(desc), q, k, v, g, h0, o, ht, stream)
 
 
 def rewy_bwd_schedule(schedule: int) -> int:

@@ -1,0 +1,183 @@
+// Host side of the linear attention with one constant decay for each head
+// (include/rewy.h): argument checks, workspace sizes and launches.  Nothing here
+// allocates device memory or waits for the device.
+#include "decay.hpp"
+#include "layer_host.hpp"
+
+namespace rewy {
+namespace {
+
+// Tokens of a segment, whole chunks, at least 256: as long as there are 512 pairs of a
+// segment and a head, two workgroups for each CU (a longer segment means fewer states to
+// join).  Packed sequences end with half a segment on average, which leaves the target
+// (N - 1) / 2 a head less, at least half of it.
+int decay_segment(const SeqArgs& q, int H) {
+  constexpr int64_t SEGMENTS = 512;
+  int64_t want;
+  if (q.cu) {
+    const int64_t whole = std::max(SEGMENTS - (int64_t)(q.N - 1) * H / 2, SEGMENTS / 2);
+    want = ((int64_t)q.total * H + whole - 1) / whole;
+  } else {
+    const int64_t each = std::max<int64_t>(SEGMENTS / ((int64_t)q.N * H), 1);
+    want = (q.T + each - 1) / each;
+  }
+  return (int)std::min<int64_t>(INT32_MAX / CH * CH, std::max<int64_t>(256, up64(want)));
+}
+
+int decay_args(const rewy_decay_desc* d, bool bwd, DecayArgs& a) {
+  if (!d) return fail(REWY_EINVAL, "desc is NULL");
+  memset(&a, 0, sizeof(a));
+  REWY_TRY(seq_args(d->B, d->T, d->N, d->cu_seqlens, d->cu_seqlens_host, a.seq));
+  if (d->H <= 0 || d->G <= 0 || d->H > 65536 || d->H % d->G)
+    return fail(REWY_EINVAL, "bad heads H=%d G=%d (H must be a multiple of G)", d->H, d->G);
+  REWY_TRY(check_dtype("dtype", d->dtype));
+  auto ok = [](int v) { return v == 32 || v == 64 || v == 128; };
+  if (d->K <= 0 || d->V <= 0) return fail(REWY_EINVAL, "bad shape K=%d V=%d", d->K, d->V);
+  if (!ok(d->K) || !ok(d->V)) return fail(REWY_EUNSUPPORTED, "K=%d V=%d not supported (32, 64 or 128)", d->K, d->V);
+  if (!(d->scale - d->scale == 0.f)) return fail(REWY_EINVAL, "scale is not finite");
+  a.H = d->H; a.G = d->G; a.K = d->K; a.V = d->V; a.per = d->H / d->G; a.scale = d->scale;
+  const int64_t qr = (int64_t)d->H * d->K, kr = (int64_t)d->G * d->K, vr = (int64_t)d->G * d->V, orow = (int64_t)d->H * d->V;
+  struct { const char* name; int64_t given, row; int64_t* out; } st[] = {
+      {"q_stride", d->q_stride, qr, &a.qs},    {"k_stride", d->k_stride, kr, &a.ks},    {"v_stride", d->v_stride, vr, &a.vs},
+      {"o_stride", d->o_stride, orow, &a.os},  {"dq_stride", d->dq_stride, qr, &a.dqs}, {"dk_stride", d->dk_stride, kr, &a.dks},
+      {"dv_stride", d->dv_stride, vr, &a.dvs}};
+  for (const auto& e : st) {
+    REWY_TRY(check_stride(e.name, e.given, e.row, *e.out));
+    if (*e.out * esize(d->dtype) % 16) return fail(REWY_EINVAL, "%s is not a multiple of 16 bytes", e.name);
+    if (*e.out > 1 << 22) return fail(REWY_EUNSUPPORTED, "%s %lld exceeds 2^22 elements", e.name, (long long)*e.out);
+  }
+  a.seg = decay_segment(a.seq, a.H);
+  a.two = (a.seq.cu ? a.seq.total : a.seq.T) > a.seg;
+  const int64_t L = a.seg, total = a.seq.total;
+  const int64_t nslot = a.seq.cu ? total / L + a.seq.N : a.seq.N * std::max<int64_t>((a.seq.T + L - 1) / L, 1);
+  a.nslot = (int)std::min<int64_t>(nslot, INT32_MAX);
+  // a launch takes fewer than 2^32 threads along x: the segments' states and walks, the
+  // token-serial form and the pass, the heads' sums
+  const int64_t threads[] = {nslot * a.H * 512, (int64_t)a.seq.N * a.H * 256, bwd ? total * a.G * 32 + 256 : 0};
+  for (int64_t n : threads)
+    if (n >= (int64_t)1 << 32)
+      return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
+                  (long long)total, a.H);
+  return REWY_OK;
+}
+
+size_t decay_layout(DecayArgs& a, bool bwd, char* ws) {
+  size_t off = 0;
+  auto take = [&](float*& p, size_t n) {
+    p = reinterpret_cast<float*>(ws + off);
+    off += up(n * 4);
+  };
+  const size_t kv = (size_t)a.H * a.K * a.V;
+  if (a.two) {
+    take(a.sf, a.nslot * kv);
+    if (bwd) take(a.sr, a.nslot * kv);
+  }
+  if (bwd && a.per > 1) {
+    take(a.kpart, (size_t)a.seq.total * a.H * a.K);
+    take(a.vpart, (size_t)a.seq.total * a.H * a.V);
+  }
+  return std::max<size_t>(off, ALIGN);
+}
+
+int decay_inputs(const void* q, const void* k, const void* v, const float* g, const float* h0, DecayArgs& a) {
+  const bool some = a.seq.total > 0;
+  REWY_TRY(check_ptr("q", q, 16, some));
+  REWY_TRY(check_ptr("k", k, 16, some));
+  REWY_TRY(check_ptr("v", v, 16, some));
+  REWY_TRY(check_ptr("g", g, 4, true));
+  REWY_TRY(check_ptr("h0", h0, 16, false));
+  a.q = q; a.k = k; a.v = v; a.g = g; a.h0 = h0;
+  return REWY_OK;
+}
+
+int decay_walk(const DecayArgs& a, int what, bool f32, hipStream_t s) {
+  return hip_check(traced("k_decay_walk", s, [&] { return launch_decay_walk(a, what, f32, s); }), "attention");
+}
+// The states of the segments that the walks need, and those that are handed out.
+int decay_states(const DecayArgs& a, int dirs, bool f32, hipStream_t s) {
+  if (!dirs) return REWY_OK;
+  REWY_TRY(hip_check(traced("k_decay_state", s, [&] { return launch_decay_state(a, f32, dirs, s); }), "segment states"));
+  if (!a.two) return REWY_OK;
+  return hip_check(traced("k_decay_pass", s, [&] { return launch_decay_pass(a, dirs, s); }), "segment pass");
+}
+
+}  // namespace
+}  // namespace rewy
+
+using namespace rewy;
+
+REWY_API size_t rewy_decay_workspace_bytes(const rewy_decay_desc* d, int phase) {
+  DecayArgs a;
+  if (phase != 0 && phase != 1) {
+    fail(REWY_EINVAL, "bad phase %d", phase);
+    return 0;
+  }
+  if (decay_args(d, phase == 1, a) != REWY_OK) return 0;
+  return decay_layout(a, phase == 1, nullptr);
+}
+
+REWY_API int rewy_decay_fwd(const rewy_decay_desc* d, const void* q, const void* k, const void* v, const float* g,
+                            const float* h0, void* o, float* ht, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> int {
+    DecayArgs a;
+    REWY_TRY(decay_args(d, false, a));
+    REWY_TRY(decay_inputs(q, k, v, g, h0, a));
+    const bool some = a.seq.total > 0, f32 = d->dtype == REWY_F32;
+    REWY_TRY(check_ptr("o", o, 16, some));
+    REWY_TRY(check_ptr("ht", ht, 16, false));
+    REWY_TRY(check_workspace(workspace, ws_bytes, decay_layout(a, false, static_cast<char*>(workspace))));
+    if (ht && ht == h0) return fail(REWY_EINVAL, "ht may not be h0");
+    if (some && (o == q || o == k || o == v)) return fail(REWY_EINVAL, "o may not be q, k or v");
+    a.o = o; a.ht = ht;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    REWY_TRY(decay_states(a, a.two || ht ? 1 : 0, f32, s));
+    return some ? decay_walk(a, DECAY_O, f32, s) : (int)REWY_OK;
+  });
+}
+
+REWY_API int rewy_decay_bwd(const rewy_decay_desc* d, const void* q, const void* k, const void* v, const float* g,
+                            const float* h0, const void* dO, const float* dht, void* dq, void* dk, void* dv, float* dh0,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> int {
+    DecayArgs a;
+    REWY_TRY(decay_args(d, true, a));
+    REWY_TRY(decay_inputs(q, k, v, g, h0, a));
+    const bool some = a.seq.total > 0, f32 = d->dtype == REWY_F32;
+    REWY_TRY(check_ptr("dO", dO, 16, some));
+    REWY_TRY(check_ptr("dht", dht, 16, false));
+    REWY_TRY(check_ptr("dq", dq, 16, some));
+    REWY_TRY(check_ptr("dk", dk, 16, some));
+    REWY_TRY(check_ptr("dv", dv, 16, some));
+    REWY_TRY(check_ptr("dh0", dh0, 16, h0 != nullptr));
+    REWY_TRY(check_workspace(workspace, ws_bytes, decay_layout(a, true, static_cast<char*>(workspace))));
+    if (dh0 && (dh0 == h0 || dh0 == dht)) return fail(REWY_EINVAL, "dh0 may not be h0 or dht");
+    for (const void* out : {dq, dk, dv})
+      if (some && (out == q || out == k || out == v || out == dO)) return fail(REWY_EINVAL, "a gradient may not be an input");
+    a.dO = dO; a.dht = dht; a.dq = dq; a.dk = dk; a.dv = dv; a.dh0 = dh0;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    REWY_TRY(decay_states(a, (a.two ? 3 : 0) | (dh0 ? 2 : 0), f32, s));
+    if (!some) return REWY_OK;
+    REWY_TRY(decay_walk(a, DECAY_DQ, f32, s));
+    REWY_TRY(decay_walk(a, DECAY_DV, f32, s));
+    REWY_TRY(decay_walk(a, DECAY_DK, f32, s));
+    if (a.per == 1) return REWY_OK;
+    return hip_check(traced("k_decay_sum", s, [&] { return launch_decay_sum(a, f32, s); }), "head sums");
+  });
+}
+
+REWY_API int rewy_decay_recurrent_fwd(const rewy_decay_desc* d, const void* q, const void* k, const void* v,
+                                      const float* g, const float* h0, void* o, float* ht, void* stream) {
+  return guarded([&]() -> int {
+    DecayArgs a;
+    REWY_TRY(decay_args(d, false, a));
+    REWY_TRY(decay_inputs(q, k, v, g, h0, a));
+    REWY_TRY(check_ptr("o", o, 16, a.seq.total > 0));
+    REWY_TRY(check_ptr("ht", ht, 16, false));
+    if (a.seq.total == 0 && !ht) return REWY_OK;
+    if (a.seq.total > 0 && (o == q || o == k || o == v)) return fail(REWY_EINVAL, "o may not be q, k or v");
+    a.o = o; a.ht = ht;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    return hip_check(traced("k_decay_recurrent", s, [&] { return launch_decay_recurrent(a, d->dtype == REWY_F32, s); }),
+                     "recurrent attention");
+  });
+}

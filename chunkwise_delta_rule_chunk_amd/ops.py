@@ -11,6 +11,8 @@ from typing import Optional
 import torch
 
 from . import binding as B
+from .decay_ops import (decay_attention, decay_attention_autograd, decay_attention_backward,  # noqa: F401
+                        decay_attention_recurrent)
 from .layer_ops import (rms_norm, rms_norm_autograd, rms_norm_backward,  # noqa: F401
                         selective_scan, selective_scan_autograd, selective_scan_backward,
                         selective_scan_recurrent, short_conv, short_conv_autograd,

@@ -378,6 +378,63 @@ int rewy_ssm_recurrent_fwd(const rewy_ssm_desc *d, const void *x, const void *dt
                            const float *a_log, const float *dt_bias, const void *b, const void *c,
                            const float *D, const float *h0, void *y, float *ht, void *stream);
 
+/* Linear attention with one constant decay for each head: per sequence n and head
+ * h the fp32 state S [K, V], token by token, with lam_h = exp(g[h]),
+ *     S = lam S + k_t v_t^T,   o_t = scale S^T q_t,
+ * the matrix-state recurrence whose decay is a parameter of the model and not of
+ * the token.  H / G neighbouring heads share a key and value head (G = H: each has its
+ * own).  g is finite or -infinity (lam = 0) and not positive; it has no gradient.
+ *
+ * Layouts (token-major):
+ *   q, dq              [B, T, H, K]   dtype
+ *   k, dk              [B, T, G, K]   dtype
+ *   v, dv              [B, T, G, V]   dtype
+ *   o, dO              [B, T, H, V]   dtype
+ *   g                  [H]            fp32
+ *   h0, ht, dht, dh0   [N, H, K, V]   fp32, contiguous
+ * Tensors of dtype may be slices of longer rows (a joint projection's output, for
+ * one): token strides in elements, 0 = contiguous; dO has o's stride.  Pointers of
+ * dtype tensors and states are 16-byte aligned and strides a multiple of 16 bytes, at
+ * most 2^22 elements.  K and V are 32, 64 or 128.  With bf16 operands the coefficients
+ * inside a chunk and the states that only 16-bit outputs read are rounded to bf16 as
+ * operands; the states that are handed out keep 24 bits. */
+typedef struct {
+    int32_t B, T, H, G, K, V;
+    int32_t N;                      /* sequences: B (or 0) without cu_seqlens */
+    const int32_t *cu_seqlens;      /* device [N+1] or NULL; needs B == 1 */
+    const int32_t *cu_seqlens_host; /* optional host copy, validated if given */
+    int32_t dtype;                  /* rewy_dtype of q, k, v, o and their gradients */
+    float scale;                    /* query scale, usually K^-1/2 */
+    int64_t q_stride, k_stride, v_stride, o_stride;
+    int64_t dq_stride, dk_stride, dv_stride;
+} rewy_decay_desc;
+
+/* Bytes of workspace: phase 0 = rewy_decay_fwd, 1 = rewy_decay_bwd (256-byte
+ * aligned).  Returns 0 for an invalid descriptor or phase. */
+size_t rewy_decay_workspace_bytes(const rewy_decay_desc *d, int phase);
+
+/* Forward in chunks of 64 tokens, for prompts and training.  h0 and ht may be NULL;
+ * o does not depend on whether ht is given.  An infinity or NaN in a token's row
+ * reaches that token and the ones behind it, as in the recurrence. */
+int rewy_decay_fwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
+                   const float *g, const float *h0, void *o, float *ht,
+                   void *workspace, size_t ws_bytes, void *stream);
+
+/* Backward (nothing is kept between the calls).  dht may be NULL; dh0 must be given
+ * when h0 is.  dk and dv are summed over the heads that share them.  Outputs are
+ * overwritten.  Inputs are finite: an infinity or NaN may reach every gradient of its
+ * sequence. */
+int rewy_decay_bwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
+                   const float *g, const float *h0, const void *dO, const float *dht,
+                   void *dq, void *dk, void *dv, float *dh0,
+                   void *workspace, size_t ws_bytes, void *stream);
+
+/* Token-serial forward for decoding: the same recurrence, no workspace, the state on
+ * chip from h0 to ht; ht may be h0 itself.  Meant for one or a few new tokens per
+ * sequence. */
+int rewy_decay_recurrent_fwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
+                             const float *g, const float *h0, void *o, float *ht, void *stream);
+
 /* Per-kernel timing (a tracing aid: device events, as in the ReWY paper's timing
  * protocol).  After rewy_trace_begin(), calls made by this thread
  * record a HIP event pair on the call's stream around every kernel they

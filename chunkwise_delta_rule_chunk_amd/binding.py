@@ -18,7 +18,7 @@ REWY_BF16, REWY_F32 = 0, 1
 REWY_RECOMPUTE, REWY_SAVE = 0, 1
 REWY_SCHEDULE_JOINT, REWY_SCHEDULE_SEPARATE = 0, 1
 REWY_QUANT_NONE, REWY_QUANT_E4M3, REWY_QUANT_INT8 = 0, 1, 2
-REWY_ACT_NONE, REWY_ACT_SILU = 0, 1
+REWY_ACT_NONE, REWY_ACT_SILU, REWY_ACT_SIGMOID = 0, 1, 2
 
 NOALLOC_SCRATCH_BYTES = 128 << 20  # REWY_NOALLOC_SCRATCH_BYTES
 
@@ -30,6 +30,7 @@ EXPORTS = ("rewy_workspace_bytes", "rewy_saved_bytes", "rewy_fwd", "rewy_bwd", "
            "rewy_conv_fwd", "rewy_conv_step", "rewy_conv_workspace_bytes", "rewy_conv_bwd",
            "rewy_ssm_workspace_bytes", "rewy_ssm_fwd", "rewy_ssm_bwd", "rewy_ssm_recurrent_fwd",
            "rewy_decay_workspace_bytes", "rewy_decay_fwd", "rewy_decay_bwd", "rewy_decay_recurrent_fwd",
+           "rewy_gnorm_fwd", "rewy_gnorm_workspace_bytes", "rewy_gnorm_bwd", "rewy_e4m3_linear",
            "rewy_bwd_schedule", "rewy_trace_begin", "rewy_trace_end", "rewy_trace_select",
            "rewy_status_string",
            "rewy_last_error")
@@ -87,6 +88,24 @@ class RewyDecayDesc(ctypes.Structure):
     ]
 
 
+class RewyGnormDesc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("D", ctypes.c_int32), ("G", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("center", ctypes.c_int32),
+        ("quant", ctypes.c_int32), ("group", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
+    ]
+
+
+class RewyE4m3Desc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("a_block", ctypes.c_int32),
+        ("w_rows", ctypes.c_int32), ("dtype", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
+        ("a_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+    ]
+
+
 class RewyTraceEntry(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_char * 96), ("total_ms", ctypes.c_double),
                 ("launches", ctypes.c_int)]
@@ -138,6 +157,7 @@ def load():
         lib.rewy_recurrent_fwd_gdn2.restype = ctypes.c_int
         ND, CD = ctypes.POINTER(RewyNormDesc), ctypes.POINTER(RewyConvDesc)
         SD, LD = ctypes.POINTER(RewySsmDesc), ctypes.POINTER(RewyDecayDesc)
+        GD, ED = ctypes.POINTER(RewyGnormDesc), ctypes.POINTER(RewyE4m3Desc)
         for name, args, res in (
                 ("rewy_norm_fwd", [ND] + [P] * 9, ctypes.c_int),
                 ("rewy_norm_workspace_bytes", [ND], S),
@@ -153,7 +173,11 @@ def load():
                 ("rewy_decay_workspace_bytes", [LD, ctypes.c_int], S),
                 ("rewy_decay_fwd", [LD] + [P] * 8 + [S, P], ctypes.c_int),
                 ("rewy_decay_bwd", [LD] + [P] * 12 + [S, P], ctypes.c_int),
-                ("rewy_decay_recurrent_fwd", [LD] + [P] * 8, ctypes.c_int)):
+                ("rewy_decay_recurrent_fwd", [LD] + [P] * 8, ctypes.c_int),
+                ("rewy_gnorm_fwd", [GD] + [P] * 10, ctypes.c_int),
+                ("rewy_gnorm_workspace_bytes", [GD], S),
+                ("rewy_gnorm_bwd", [GD] + [P] * 12 + [S, P], ctypes.c_int),
+                ("rewy_e4m3_linear", [ED] + [P] * 7, ctypes.c_int)):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = res
         lib.rewy_bwd_schedule.argtypes = [ctypes.c_int]
@@ -293,6 +317,23 @@ def rewy_decay_bwd(desc, q, k, v, g, h0, dO, dht, dq, dk, dv, dh0, workspace, ws
 
 def rewy_decay_recurrent_fwd(desc, q, k, v, g, h0, o, ht, stream) -> int:
     return load().rewy_decay_recurrent_fwd(ctypes.byref(desc), q, k, v, g, h0, o, ht, stream)
+
+
+def rewy_gnorm_fwd(desc, x, z, w, b, y, q, scale, mean, rstd, stream) -> int:
+    return load().rewy_gnorm_fwd(ctypes.byref(desc), x, z, w, b, y, q, scale, mean, rstd, stream)
+
+
+def rewy_gnorm_workspace_bytes(desc) -> int:
+    return load().rewy_gnorm_workspace_bytes(ctypes.byref(desc))
+
+
+def rewy_gnorm_bwd(desc, x, z, w, b, mean, rstd, dy, dx, dz, dw, db, workspace, ws_bytes, stream) -> int:
+    return load().rewy_gnorm_bwd(ctypes.byref(desc), x, z, w, b, mean, rstd, dy, dx, dz, dw, db, workspace,
+                                 ws_bytes, stream)
+
+
+def rewy_e4m3_linear(desc, a, a_scale, w, w_scale, bias, y, stream) -> int:
+    return load().rewy_e4m3_linear(ctypes.byref(desc), a, a_scale, w, w_scale, bias, y, stream)
 
 
 def rewy_bwd_schedule(schedule: int) -> int:

@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "librewy.so")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "k_fwd_prep.hip", "k_scan.hip", "k_bwd_chunk.hip", "k_recurrent.hip",
            "api_layer.hip", "k_norm.hip", "k_conv.hip", "k_ssm_fwd.hip", "k_ssm_bwd.hip",
-           "api_decay.hip", "k_decay.hip"]
+           "api_decay.hip", "k_decay.hip", "api_gnorm.hip", "k_gnorm.hip", "api_mm8.hip", "k_mm8.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 CFLAGS = [

@@ -1,0 +1,439 @@
+// Group norm over a token's channels, with a gate or an activation behind it and an
+// 8-bit output.  Row by row, for each of G groups of L channels,
+//   mean = avg x (or 0),  rstd = (avg (x - mean)^2 + eps)^-1/2,
+//   n = (x - mean) rstd w + b,   y = n act(z)  or  y = act(n)  without a gate z,
+// and scales and codes of y as the RMS norm's.  Everything is formed from the
+// unrounded fp32 values; y and q are rounded once each.  Backward, with xh = (x -
+// mean) rstd, dn = dy act(z) or dy act'(n), u = dn w:
+//   dx = rstd (u - avg u - xh avg(u xh)),  dz = dy n act'(z),
+//   dw = sum_rows dn xh,  db = sum_rows dn
+// (avg u only with a mean).
+//
+// Memory is all it costs: each input is read once and each output written once.  A
+// row is held by TPR threads in registers (NC vectors of 16 bytes a thread).  Where a
+// group is a power of two of whole vectors, at most a wave, its lanes are neighbours
+// and its statistics a few lane moves; any other group length takes them from a pass
+// of its own (k_gnorm_stats), which reads the row a second time.
+#include "gnorm.hpp"
+
+namespace rewy {
+
+namespace {
+
+// Sum over aligned groups of `lanes` lanes (a power of two up to 64), in every lane.
+__device__ __forceinline__ float group_sum(float x, int lanes) {
+  if (lanes > 1) x += dpp_mov<0xB1>(x);   // quad_perm [1,0,3,2]
+  if (lanes > 2) x += dpp_mov<0x4E>(x);   // quad_perm [2,3,0,1]
+  if (lanes > 4) x += dpp_mov<0x141>(x);  // row_half_mirror
+  if (lanes > 8) x += dpp_mov<0x140>(x);  // row_mirror
+  if (lanes > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (lanes > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return x;
+}
+
+// the activation's value, and its derivative
+__device__ __forceinline__ float act_value(float t, int act) {
+  return act == REWY_ACT_NONE ? t : act == REWY_ACT_SILU ? t * sigmoid_f(t) : sigmoid_f(t);
+}
+__device__ __forceinline__ float act_both(float t, int act, float& d) {
+  const float s = sigmoid_f(t);
+  if (act == REWY_ACT_SILU) {
+    d = s * (1.f + t * (1.f - s));
+    return t * s;
+  }
+  d = act == REWY_ACT_NONE ? 1.f : s * (1.f - s);
+  return act == REWY_ACT_NONE ? t : s;
+}
+
+// The groups' statistics of a vector of a row, from memory: element e of columns j ..
+template <int VE>
+struct GroupOf {
+  int g[VE];
+  __device__ __forceinline__ GroupOf(int j, int L, int G) {
+    int k = j / L, r = j - k * L;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      g[e] = min(k, G - 1);
+      if (++r == L) {
+        r = 0;
+        ++k;
+      }
+    }
+  }
+};
+
+// Statistics of every (row, group), P lanes each (a power of two): mean and rstd, or
+// for the backward the means of u and of u xh.
+template <typename T, typename W, bool BWD>
+__global__ __launch_bounds__(256) void k_gnorm_stats(GnormArgs a, int P) {
+  const int p = threadIdx.x & (P - 1), per = 256 / P;
+  const int64_t n = a.M * a.G;
+  for (int64_t i0 = blockIdx.x * (int64_t)per; i0 < n; i0 += (int64_t)gridDim.x * per) {
+    const int64_t i = min(i0 + threadIdx.x / P, n - 1), m = i / a.G;  // (whole waves stay together for the lane moves)
+    const int g = (int)(i - m * a.G), j0 = g * a.L;
+    const T* x = reinterpret_cast<const T*>(a.x) + m * a.xs + j0;
+    if constexpr (!BWD) {
+      float s = 0.f, mean = 0.f;
+      if (a.center) {
+        for (int j = p; j < a.L; j += P) s += (float)x[j];
+        mean = group_sum(s, P) / (float)a.L;
+        s = 0.f;
+      }
+      for (int j = p; j < a.L; j += P) {
+        const float d = (float)x[j] - mean;
+        s += d * d;
+      }
+      const float rstd = 1.f / sqrtf(group_sum(s, P) / (float)a.L + a.eps);
+      if (p == 0) {
+        if (a.center) a.mean[i] = mean;
+        a.rstd[i] = rstd;
+      }
+    } else {
+      const T* z = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs + j0 : nullptr;
+      const T* dy = reinterpret_cast<const T*>(a.dy) + m * a.ys + j0;
+      const W* w = a.w ? reinterpret_cast<const W*>(a.w) + j0 : nullptr;
+      const W* b = a.b ? reinterpret_cast<const W*>(a.b) + j0 : nullptr;
+      const float mean = a.center ? a.mean[i] : 0.f, rstd = a.rstd[i];
+      float s1 = 0.f, s2 = 0.f;
+      for (int j = p; j < a.L; j += P) {
+        const float xh = ((float)x[j] - mean) * rstd, wv = w ? (float)w[j] : 1.f;
+        float d, act = act_both(z ? (float)z[j] : xh * wv + (b ? (float)b[j] : 0.f), a.act, d);
+        const float u = (float)dy[j] * (z ? act : d) * wv;
+        s1 += u;
+        s2 += u * xh;
+      }
+      s1 = group_sum(s1, P) / (float)a.L;
+      s2 = group_sum(s2, P) / (float)a.L;
+      if (p == 0) {
+        a.sums[2 * i] = a.center ? s1 : 0.f;
+        a.sums[2 * i + 1] = s2;
+      }
+    }
+  }
+}
+
+template <typename T, typename W, int TPR, int NC, bool GIVEN>
+__global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_fwd(GnormArgs a) {
+  constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
+  __shared__ uint32_t mbuf[BLOCK / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
+  const bool on = row < a.M;
+  const int D = on ? a.D : 0;  // threads past the last row hold nothing and write nothing
+  const int64_t m = on ? row : 0;
+  const T* x = reinterpret_cast<const T*>(a.x) + m * a.xs;
+  const T* z = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs : nullptr;
+  const W* w = reinterpret_cast<const W*>(a.w);
+  const W* b = reinterpret_cast<const W*>(a.b);
+
+  float s[NC][VE], zv[NC][VE];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = (c * TPR + t) * VE;
+    ldv<T, VE>(s[c], x + j, D - j);
+  }
+  if (z) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = (c * TPR + t) * VE;
+      ldv<T, VE>(zv[c], z + j, D - j);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = (c * TPR + t) * VE;
+    if constexpr (GIVEN) {
+      const GroupOf<VE> of(j, a.L, a.G);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const int64_t i = m * a.G + of.g[e];
+        s[c][e] = (s[c][e] - (a.center ? a.mean[i] : 0.f)) * a.rstd[i];
+      }
+    } else {
+      // (a vector lies in one group, and a group's lanes in one wave)
+      float mean = 0.f, ss = 0.f;
+      if (a.center) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) mean += s[c][e];
+        mean = group_sum(mean, a.lanes) / (float)a.L;
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        s[c][e] -= mean;
+        ss += s[c][e] * s[c][e];
+      }
+      const float rstd = 1.f / sqrtf(group_sum(ss, a.lanes) / (float)a.L + a.eps);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s[c][e] *= rstd;
+      if (j < D && (t & (a.lanes - 1)) == 0) {
+        const int64_t i = m * a.G + j / a.L;
+        if (a.center) a.mean[i] = mean;
+        a.rstd[i] = rstd;
+      }
+    }
+    float wv[VE], bv[VE];
+    if (w) ldv<W, VE>(wv, w + j, D - j);
+    if (b) ldv<W, VE>(bv, b + j, D - j);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      float n = s[c][e];
+      if (w) n *= wv[e];
+      if (b) n += bv[e];
+      s[c][e] = z ? n * act_value(zv[c][e], a.act) : act_value(n, a.act);
+    }
+  }
+  if (a.y) {
+    T* o = reinterpret_cast<T*>(a.y) + m * a.ys;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = (c * TPR + t) * VE;
+      stv<T, VE>(o + j, s[c], D - j);
+    }
+  }
+  if (!a.quant) return;
+  const float qmax = a.quant == REWY_QUANT_E4M3 ? 448.f : 127.f;
+  uint32_t mx[NC], all = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = (c * TPR + t) * VE;
+    mx[c] = 0;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (j + e < D) mx[c] = max(mx[c], mag(s[c][e]));
+    all = max(all, mx[c]);
+  }
+  if (!a.group) all = row_max<TPR>(all, mbuf);
+  const int lanes = a.group ? min(a.group / VE, TPR) : 0;  // lanes that share a scale
+  uint8_t* q = reinterpret_cast<uint8_t*>(a.q) + m * a.D;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = (c * TPR + t) * VE;
+    const float scale = make_scale(a.group ? lanes_max_n(mx[c], lanes) : all, qmax);
+    if (a.group) {
+      if (j < D && j % a.group == 0) a.scale[m * a.ng + j / a.group] = scale;
+    } else if (c == 0 && t == 0 && on) {
+      a.scale[m] = scale;
+    }
+    store_codes<VE>(q + j, s[c], scale, a.quant == REWY_QUANT_E4M3, D - j);
+  }
+}
+
+// Each block takes rows blockIdx, + gridDim, ... and keeps dw and db of its columns in
+// registers; one partial row of each per block goes to the workspace (no atomics: the
+// same sums every time).
+template <typename T, typename W, int TPR, int NC, bool GIVEN>
+__global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_bwd(GnormArgs a) {
+  constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
+  __shared__ float wbuf[RPB > 1 ? BLOCK * NC * VE : 1];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, D = a.D;
+  const W* w = reinterpret_cast<const W*>(a.w);
+  const W* b = reinterpret_cast<const W*>(a.b);
+  float wv[NC][VE], bv[NC][VE], dw[NC][VE], db[NC][VE];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = (c * TPR + t) * VE;
+    if (w) ldv<W, VE>(wv[c], w + j, D - j);
+    if (b) ldv<W, VE>(bv[c], b + j, D - j);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      if (!w) wv[c][e] = 1.f;
+      if (!b) bv[c][e] = 0.f;
+      dw[c][e] = db[c][e] = 0.f;
+    }
+  }
+  for (int64_t r0 = blockIdx.x * (int64_t)RPB; r0 < a.M; r0 += (int64_t)gridDim.x * RPB) {
+    const bool on = r0 + sub < a.M;
+    const int64_t m = on ? r0 + sub : 0;
+    const int n = on ? D : 0;
+    const T* xp = reinterpret_cast<const T*>(a.x) + m * a.xs;
+    const T* zp = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs : nullptr;
+    const T* dp = reinterpret_cast<const T*>(a.dy) + m * a.ys;
+    float x[NC][VE], dy[NC][VE], zv[NC][VE];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = (c * TPR + t) * VE;
+      ldv<T, VE>(x[c], xp + j, n - j);
+      ldv<T, VE>(dy[c], dp + j, n - j);
+      if (zp) ldv<T, VE>(zv[c], zp + j, n - j);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = (c * TPR + t) * VE;
+      float rs[VE], c1[VE], c2[VE];
+      if constexpr (GIVEN) {
+        const GroupOf<VE> of(j, a.L, a.G);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int64_t i = m * a.G + of.g[e];
+          rs[e] = a.rstd[i];
+          x[c][e] = j + e < n ? (x[c][e] - (a.center ? a.mean[i] : 0.f)) * rs[e] : 0.f;
+          c1[e] = a.sums[2 * i];
+          c2[e] = a.sums[2 * i + 1];
+        }
+      } else {
+        const int64_t i = m * a.G + (j < n ? j / a.L : 0);
+        const float r = a.rstd[i], mean = a.center ? a.mean[i] : 0.f;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          rs[e] = r;
+          x[c][e] = j < n ? (x[c][e] - mean) * r : 0.f;
+        }
+      }
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float nv = x[c][e] * wv[c][e] + bv[c][e];
+        float d, act = act_both(zp ? zv[c][e] : nv, a.act, d);
+        const float dn = dy[c][e] * (zp ? act : d);  // (rows and columns past the end: zero)
+        zv[c][e] = dy[c][e] * nv * d;
+        dw[c][e] += dn * x[c][e];
+        db[c][e] += dn;
+        dy[c][e] = dn * wv[c][e];
+        s1 += dy[c][e];
+        s2 += dy[c][e] * x[c][e];
+      }
+      if constexpr (!GIVEN) {
+        s1 = a.center ? group_sum(s1, a.lanes) / (float)a.L : 0.f;
+        s2 = group_sum(s2, a.lanes) / (float)a.L;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          c1[e] = s1;
+          c2[e] = s2;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) dy[c][e] = rs[e] * (dy[c][e] - c1[e] - x[c][e] * c2[e]);
+      stv<T, VE>(reinterpret_cast<T*>(a.dx) + m * a.dxs + j, dy[c], n - j);
+      if (zp) stv<T, VE>(reinterpret_cast<T*>(a.dz) + m * a.dzs + j, zv[c], n - j);
+    }
+  }
+  if (!a.part) return;
+  // dw, then db
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* part = a.part + ((int64_t)blockIdx.x * 2 + k) * D;
+    float(&d)[NC][VE] = k ? db : dw;
+    if constexpr (RPB > 1) {  // the block's row groups, joined in their order
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) wbuf[(sub * NC * VE + c * VE + e) * TPR + t] = d[c][e];
+      __syncthreads();
+      for (int i = threadIdx.x; i < TPR * NC * VE; i += BLOCK) {
+        // entry i is element e of vector c of thread tt
+        const int tt = i % TPR, ce = i / TPR, j = ((ce / VE) * TPR + tt) * VE + ce % VE;
+        float v = 0.f;
+#pragma unroll
+        for (int q = 0; q < RPB; ++q) v += wbuf[(q * NC * VE + ce) * TPR + tt];
+        if (j < D) part[j] = v;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int j = (c * TPR + t) * VE;
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (j + e < D) part[j + e] = d[c][e];
+      }
+    }
+  }
+}
+
+// The row shape of a length: the fewest threads that hold it in at most 16 elements
+// each (x, z, dy and the parameters and their sums stay in registers).
+template <typename T, typename F>
+hipError_t gnorm_shape(int D, F&& f) {
+  constexpr int VE = Vec<T>::VE;
+  const int v = (D + VE - 1) / VE;  // vectors of a row
+#define REWY_GNORM_SHAPE(TPR, NC) \
+  if (v <= (TPR) * (NC)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NC>{})
+  REWY_GNORM_SHAPE(16, 1);
+  REWY_GNORM_SHAPE(64, 1);
+  REWY_GNORM_SHAPE(64, 2);
+  REWY_GNORM_SHAPE(256, 1);
+  REWY_GNORM_SHAPE(256, 2);
+  REWY_GNORM_SHAPE(1024, 1);
+  REWY_GNORM_SHAPE(1024, 2);
+  if constexpr (VE == 4) REWY_GNORM_SHAPE(1024, 4);
+#undef REWY_GNORM_SHAPE
+  return hipErrorInvalidValue;
+}
+
+template <typename T, typename W, bool GIVEN>
+hipError_t gnorm_fwd_t(const GnormArgs& a, hipStream_t s) {
+  return gnorm_shape<T>(a.D, [&](auto tpr, auto nc) {
+    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
+    constexpr int BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
+    // (a launch takes fewer than 2^32 threads along x)
+    const int64_t n = (a.M + RPB - 1) / RPB, gx = std::min<int64_t>(n, 1 << 20);
+    REWY_LAUNCH((k_gnorm_fwd<T, W, TPR, NC, GIVEN>), dim3((unsigned)gx, (unsigned)((n + gx - 1) / gx)), dim3(BLOCK), s, a);
+    return hipGetLastError();
+  });
+}
+template <typename T, typename W, bool GIVEN>
+hipError_t gnorm_bwd_t(const GnormArgs& a, hipStream_t s) {
+  return gnorm_shape<T>(a.D, [&](auto tpr, auto nc) {
+    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
+    REWY_LAUNCH((k_gnorm_bwd<T, W, TPR, NC, GIVEN>), dim3(a.nblk), dim3(TPR > NORM_BLOCK ? TPR : NORM_BLOCK), s, a);
+    return hipGetLastError();
+  });
+}
+// the (T, W) variants
+template <typename F>
+hipError_t gnorm_types(bool f32, bool wf32, F&& f) {
+  if (f32) return wf32 ? f(float{}, float{}) : f(float{}, bf16{});
+  return wf32 ? f(bf16{}, float{}) : f(bf16{}, bf16{});
+}
+
+}  // namespace
+
+int gnorm_lanes(int L, bool f32) {
+  const int ve = f32 ? 4 : 8, n = L / ve;
+  return L % ve == 0 && n <= 64 && (n & (n - 1)) == 0 ? n : 0;
+}
+int gnorm_bwd_blocks(int64_t M, int D, bool f32) {
+  int rpb = 1;
+  auto take = [&](auto tpr, auto) {
+    rpb = std::max(1, NORM_BLOCK / decltype(tpr)::value);
+    return hipSuccess;
+  };
+  (void)(f32 ? gnorm_shape<float>(D, take) : gnorm_shape<bf16>(D, take));
+  return (int)std::min<int64_t>((M + rpb - 1) / rpb, 1024);
+}
+
+hipError_t launch_gnorm_stats(const GnormArgs& a, bool f32, bool wf32, bool bwd, hipStream_t s) {
+  int P = 1;  // about four channels a lane
+  while (P < 64 && 4 * P < a.L) P *= 2;
+  const int64_t n = (a.M * a.G * P + 255) / 256;
+  const dim3 grid((unsigned)std::min<int64_t>(n, 1 << 20));
+  return gnorm_types(f32, wf32, [&](auto t, auto w) {
+    using T = decltype(t);
+    using W = decltype(w);
+    if (bwd) REWY_LAUNCH((k_gnorm_stats<T, W, true>), grid, dim3(256), s, a, P);
+    else REWY_LAUNCH((k_gnorm_stats<T, T, false>), grid, dim3(256), s, a, P);
+    return hipGetLastError();
+  });
+}
+hipError_t launch_gnorm_fwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s) {
+  return gnorm_types(f32, wf32, [&](auto t, auto w) {
+    using T = decltype(t);
+    using W = decltype(w);
+    return a.lanes ? gnorm_fwd_t<T, W, false>(a, s) : gnorm_fwd_t<T, W, true>(a, s);
+  });
+}
+hipError_t launch_gnorm_bwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s) {
+  return gnorm_types(f32, wf32, [&](auto t, auto w) {
+    using T = decltype(t);
+    using W = decltype(w);
+    return a.lanes ? gnorm_bwd_t<T, W, false>(a, s) : gnorm_bwd_t<T, W, true>(a, s);
+  });
+}
+
+}  // namespace rewy

@@ -12,78 +12,11 @@
 // once.  A row is held by TPR threads in registers (NC vectors of 16 bytes a
 // thread), so nothing is read twice and sum may overwrite x or res.  (A square over
 // 3e38 makes the sum of squares infinite and the row zero, as in any fp32 norm.)
-#include "layer.hpp"
+#include "row.hpp"
 
 namespace rewy {
 
 namespace {
-
-constexpr int NORM_BLOCK = 256;
-
-// Largest magnitude by its bits: NaN > infinity > every number, so a row that
-// holds one keeps it in its scale.
-__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-template <int LANES>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
-#pragma unroll
-  for (int m = 1; m < LANES; m *= 2) x = max(x, (uint32_t)__shfl_xor((int)x, m, 64));
-  return x;
-}
-__device__ __forceinline__ uint32_t lanes_max_n(uint32_t x, int lanes) {
-  for (int m = 1; m < lanes; m *= 2) x = max(x, (uint32_t)__shfl_xor((int)x, m, 64));
-  return x;
-}
-
-// Sum (and maximum) over the TPR threads of a row; `buf` holds one word per
-// wave of the block and is used once per call site.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float* buf) {
-  if constexpr (TPR <= 64) {
-    return lanes_sum<TPR>(x);
-  } else {
-    x = lanes_sum<64>(x);
-    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
-    __syncthreads();
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) t += buf[i];
-    return t;
-  }
-}
-template <int TPR>
-__device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* buf) {
-  if constexpr (TPR <= 64) {
-    return lanes_max<TPR>(x);
-  } else {
-    x = lanes_max<64>(x);
-    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
-    __syncthreads();
-    uint32_t t = 0;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) t = max(t, buf[i]);
-    return t;
-  }
-}
-
-// scale from the largest magnitude's bits: 1 where there is nothing to scale (all zeros,
-// or magnitudes so small that a step of the scale would be lost)
-__device__ __forceinline__ float make_scale(uint32_t bits, float qmax) {
-  const float m = __uint_as_float(bits);
-  return m < 0x1p-100f ? 1.f : m / qmax;
-}
-// four values to four bytes
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  // (a value that rounding left just above the largest stays the largest; NaN stays NaN)
-  auto lim = [](float v) { return v > 448.f ? 448.f : v < -448.f ? -448.f : v; };
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(lim(a), lim(b), 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lim(c), lim(d), r, true);
-}
-__device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d) {
-  // NaN (a row whose scale says so) becomes 0
-  auto cv = [](float v) { return (uint32_t)(int)fminf(fmaxf(v != v ? 0.f : rintf(v), -127.f), 127.f) & 255u; };
-  return cv(a) | cv(b) << 8 | cv(c) << 16 | cv(d) << 24;
-}
 
 // One row a group of TPR threads: all loads first, one join for the mean, one for the
 // scale (a group of columns lies in neighbouring lanes: no LDS).  Bound by HBM:
@@ -175,29 +108,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_fw
     } else if (c == 0 && t == 0 && on) {
       a.scale[m] = scale;
     }
-    uint32_t b[VE / 4];
-#pragma unroll
-    for (int k = 0; k < VE / 4; ++k) {
-      // (divided: a product with a rounded inverse takes the neighbouring code beside a tie;
-      // no slower for 8192 x 4096 bf16, 33 instead of 30.5 us for 10007 x 1537 fp32)
-      const float* v = s[c] + 4 * k;
-      b[k] = a.quant == REWY_QUANT_E4M3 ? pack_e4m3(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale)
-                                        : pack_int8(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale);
-    }
-    if (D - j >= VE) {
-      typedef uint32_t words __attribute__((ext_vector_type(VE / 4)));
-      typedef words words_u __attribute__((aligned(1)));
-      if constexpr (VE == 8) {
-        *reinterpret_cast<words_u*>(q + j) = words{b[0], b[1]};
-      } else {
-        typedef uint32_t word_u __attribute__((aligned(1)));
-        *reinterpret_cast<word_u*>(q + j) = b[0];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (j + e < D) q[j + e] = (uint8_t)(b[e / 4] >> (8 * (e & 3)));
-    }
+    store_codes<VE>(q + j, s[c], scale, a.quant == REWY_QUANT_E4M3, D - j);
   }
 }
 

@@ -67,6 +67,13 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return LANES == 64 ? rows_sum(x) : x;
 }
 
+// Workgroup b of n in an order that gives each XCD (workgroups go to the 8 XCDs
+// in turn) one contiguous range, so that neighbours, which share operands, share an L2.
+__device__ __forceinline__ int xcd_range(int b, int n) {
+  const int x = b & 7, per = n >> 3, rem = n & 7;
+  return x * per + min(x, rem) + (b >> 3);
+}
+
 // ---- RMS norm -----------------------------------------------------------------
 struct NormArgs {
   int64_t M;

@@ -115,14 +115,6 @@ __device__ __forceinline__ Piece find_piece(const SeqArgs& q, int slot, int L) {
   return p;
 }
 
-// Workgroup b of n in an order that gives each XCD (workgroups go to the 8 XCDs
-// in turn) one contiguous range, so that neighbours, which share B and C, share
-// an L2.
-__device__ __forceinline__ int xcd_range(int b, int n) {
-  const int x = b & 7, per = n >> 3, rem = n & 7;
-  return x * per + min(x, rem) + (b >> 3);
-}
-
 // ---- gates ----------------------------------------------------------------------
 // softplus at full fp32 precision (small steps dt matter relative to themselves)
 __device__ __forceinline__ float softplus_full(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }

@@ -13,6 +13,8 @@ import torch
 from . import binding as B
 from .decay_ops import (decay_attention, decay_attention_autograd, decay_attention_backward,  # noqa: F401
                         decay_attention_recurrent)
+from .output_ops import (e4m3_linear, group_norm, group_norm_autograd,  # noqa: F401
+                         group_norm_backward)
 from .layer_ops import (rms_norm, rms_norm_autograd, rms_norm_backward,  # noqa: F401
                         selective_scan, selective_scan_autograd, selective_scan_backward,
                         selective_scan_recurrent, short_conv, short_conv_autograd,

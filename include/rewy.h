@@ -284,7 +284,7 @@ int rewy_norm_bwd(const rewy_norm_desc *d, const void *s, const void *w, const f
  * the rows before a sequence's first token being its initial state h0
  * [N, W-1, D] (oldest first; zeros without one).  The final state ht is the last
  * W-1 rows of [h0 ; x] and is h0 for the sequence's continuation. */
-typedef enum { REWY_ACT_NONE = 0, REWY_ACT_SILU = 1 } rewy_act;
+typedef enum { REWY_ACT_NONE = 0, REWY_ACT_SILU = 1, REWY_ACT_SIGMOID = 2 /* group norm only */ } rewy_act;
 
 typedef struct {
     int32_t B, T, D;                /* batch rows, tokens of a row, channels */
@@ -434,6 +434,69 @@ int rewy_decay_bwd(const rewy_decay_desc *d, const void *q, const void *k, const
  * sequence. */
 int rewy_decay_recurrent_fwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
                              const float *g, const float *h0, void *o, float *ht, void *stream);
+
+/* Group norm over a token's channels, with a gate or an activation and an 8-bit
+ * output: row by row, for each of G groups of L = D / G neighbouring channels,
+ *     mean = avg x (0 without center),  rstd = (avg (x - mean)^2 + eps)^-1/2,
+ *     n = (x - mean) rstd w + b,   y = n act(z),  or  y = act(n) without a gate z,
+ * and scale and q from the unrounded y as for the RMS norm.  With the heads of a
+ * token mixer as the groups this is the norm behind it; q and scale (group 128) are
+ * what rewy_e4m3_linear reads. */
+typedef struct {
+    int64_t M;                      /* rows, 0 .. 2^31 - 1 */
+    int32_t D;                      /* row length, 1 .. 16384 */
+    int32_t G;                      /* groups, a divisor of D */
+    int32_t dtype;                  /* rewy_dtype of x, z, y (and of dy, dx, dz) */
+    int32_t w_dtype;                /* rewy_dtype of w, b, dw and db */
+    int32_t act;                    /* rewy_act */
+    int32_t center;                 /* 1: the mean is taken off; 0: it is not (an RMS norm by group) */
+    int32_t quant;                  /* rewy_quant of q (forward) */
+    int32_t group;                  /* columns per scale: 0 = the whole row, else 32, 64, 128 or 256 */
+    float eps;                      /* >= 0 */
+    int64_t x_stride, z_stride, y_stride, dx_stride, dz_stride; /* between rows, in elements; 0 = D (y_stride: y and dy) */
+} rewy_gnorm_desc;
+
+/* Forward.  z, w (1) and b (0) may be NULL; y may be NULL and is then not written; q
+ * ([M, D], contiguous) and scale (fp32 [M, ceil(D / group)], or [M] for group 0) are
+ * given exactly when quant != NONE; mean (exactly with center) and rstd, fp32
+ * [M, G], are written. */
+int rewy_gnorm_fwd(const rewy_gnorm_desc *d, const void *x, const void *z, const void *w,
+                   const void *b, void *y, void *q, float *scale, float *mean, float *rstd,
+                   void *stream);
+
+/* Bytes of workspace of the backward (0 for an invalid descriptor). */
+size_t rewy_gnorm_workspace_bytes(const rewy_gnorm_desc *d);
+
+/* Backward for y (gradients pass an 8-bit output straight through): mean and rstd are
+ * what the forward wrote.  dz is given exactly when z is; dw and db ([D], w_dtype) may be
+ * NULL, and must be NULL when w and b are.  The workspace is 256-byte aligned. */
+int rewy_gnorm_bwd(const rewy_gnorm_desc *d, const void *x, const void *z, const void *w,
+                   const void *b, const float *mean, const float *rstd, const void *dy,
+                   void *dx, void *dz, void *dw, void *db,
+                   void *workspace, size_t ws_bytes, void *stream);
+
+/* Product of e4m3 operands (the OCP format without infinities) with fp32 scales for
+ * blocks of 128 columns:
+ *     y[m, n] = sum_b sa[m, b] sw[n, b] (sum_{k in b} a[m, k] w[n, k]) + bias[n],
+ * b the blocks of 128 of the K columns (the last may be shorter).  a is what the norms
+ * hand out as q, w a weight [N, K] as it is stored.  Products of codes are exact, sums
+ * are fp32, y is rounded once.  A NaN code or scale reaches the outputs of its row of a
+ * or w (and, for a scale that 128 rows of w share, of those rows). */
+typedef struct {
+    int32_t M;                      /* rows of a, >= 0 */
+    int32_t N, K;                   /* rows of w; columns, a multiple of 16 */
+    int32_t a_block;                /* columns per scale of a: 128, or 0 = the whole row */
+    int32_t w_rows;                 /* rows per scale of w: 128, or 1 */
+    int32_t dtype;                  /* rewy_dtype of y */
+    int32_t bias_dtype;             /* rewy_dtype of bias */
+    int64_t a_stride, w_stride, y_stride; /* between rows, in elements; 0 = K, K, N */
+} rewy_e4m3_desc;
+
+/* a [M, K] and w [N, K] are 16-byte aligned, a_stride and w_stride multiples of 16 and at
+ * most 2^22; a_scale is [M, ceil(K / 128)] (a_block 0: [M]), w_scale [ceil(N / 128) (w_rows 1:
+ * N), ceil(K / 128)], both contiguous; bias [N] may be NULL.  No workspace. */
+int rewy_e4m3_linear(const rewy_e4m3_desc *d, const void *a, const float *a_scale, const void *w,
+                     const float *w_scale, const void *bias, void *y, void *stream);
 
 /* Per-kernel timing (a tracing aid: device events, as in the ReWY paper's timing
  * protocol).  After rewy_trace_begin(), calls made by this thread

@@ -1,0 +1,132 @@
+"""Product of e4m3 operands with scales for blocks of 128, against the sum in 64 bits.
+
+Bounds, U = 2^-24.  Products of codes are exact in fp32.  A block's 128 terms are summed
+in fp32 (at most 128 U of their magnitudes), meet the product of two scales (3 roundings)
+and at most K / 128 others (one rounding each), then the bias: (133 + K / 128) U of the
+sum of magnitudes covers them.  Outputs add half a step of their type.
+
+A 16-bit y of more than 64 rows comes from the 8-bit matrix instructions, which line up
+at most eight neighbouring products on a grid 13 bits under the largest of them (a pair of
+codes 0 and 1 keeps 2^-13 of the larger product and no less; a code eight places away
+keeps everything): seven terms lose less than 2^-13 of the largest each, 2^-10 of the
+sum of magnitudes.  In norm what is dropped is under 1e-4 (measured: 5e-5 where all codes
+are equally frequent), and the rounding of y at most 2^-8, which values just over a power
+of two reach."""
+import pytest
+import torch
+
+from layer_util import DT, U32, close
+from parity_util import gpu_available, say
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a GPU and librewy.so")]
+
+F8 = torch.float8_e4m3fn
+
+
+def codes(g, *shape):
+    """Every finite code, with the frequencies of a normal distribution, and some at the ends."""
+    t = (torch.randn(*shape, generator=g) * 40).clamp(-448, 448)
+    t.view(-1)[::97] = 448.0
+    t.view(-1)[1::101] = 2.0 ** -9
+    return t.to(F8).cuda()
+
+
+def scales(g, *shape):
+    return torch.exp(1.5 * torch.randn(*shape, generator=g) - 4).cuda()
+
+
+def formula(a, sa, w, sw, bias):
+    """y, and the sum of its terms' magnitudes."""
+    K, N = a.shape[1], w.shape[0]
+    wide = lambda s: s.double() if s.shape[1] == 1 else s.double().repeat_interleave(128, 1)[:, :K]  # noqa: E731
+    full = sw.double() if sw.shape[0] == N else sw.double().repeat_interleave(128, 0)[:N]
+    A, W = a.double() * wide(sa), w.double() * wide(full)
+    b = 0 if bias is None else bias.double()
+    return A @ W.t() + b, A.abs() @ W.abs().t() + (0 if bias is None else b.abs())
+
+
+def check(y, a, sa, w, sw, bias):
+    ref, mag = formula(a, sa, w, sw, bias)
+    wide = y.dtype == torch.float32 or y.shape[0] <= 64
+    close(y, ref, ((133 + a.shape[1] / 128) * U32 + (0 if wide else 2.0 ** -10)) * mag, "y")
+    if y.numel() > 1000:
+        rel = ((y.double() - ref).norm() / ref.norm()).item()
+        say(f"[layer] y norm error {rel:.2e}")
+        assert rel <= (1e-6 if y.dtype == torch.float32 else 2.0 ** -8 + 1e-4)
+
+
+SHAPES = [
+    # M, N, K
+    (1, 1, 16), (1, 4096, 4096), (3, 17, 144), (16, 128, 128), (17, 130, 2320), (33, 100, 1024), (64, 33, 2048),
+    (65, 64, 128), (100, 300, 400), (128, 128, 256), (129, 257, 640), (300, 1000, 1040), (513, 385, 16), (1000, 4354, 2320),
+    (2049, 8192, 272), (4100, 4100, 384),
+]
+
+
+@pytest.mark.parametrize("rows", [False, True])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(M, N, K, rows):
+    from chunkwise_delta_rule_chunk_amd import ops
+    g = torch.Generator().manual_seed(M + N + K)
+    nb = -(-K // 128)
+    v = M + N + K // 16 + rows
+    whole, dtype = v % 3 == 0, ("bf16", "fp32")[v % 2]
+    a, w = codes(g, M, K), codes(g, N, K)
+    sa, sw = scales(g, M, 1 if whole else nb), scales(g, N if rows else -(-N // 128), nb)
+    bias = torch.randn(N, generator=g).to(DT[("fp32", "bf16")[v % 4 % 2]]).cuda() if v % 4 < 2 else None
+    y = ops.e4m3_linear(a, sa, w, sw, bias, dtype=DT[dtype])
+    assert y.shape == (M, N) and y.dtype == DT[dtype]
+    check(y, a, sa, w, sw, bias)
+    assert torch.equal(y, ops.e4m3_linear(a, sa, w, sw, bias, dtype=DT[dtype]))
+
+
+@pytest.mark.parametrize("M", [5, 200, 4097])
+def test_strided_operands_leave_their_neighbours_alone(M):
+    """a and w as slices of longer rows (whose other columns are NaN codes), and a tail
+    block whose missing columns would be read from the next row."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    K, N = 400, 4100 if M > 4000 else 200
+    g = torch.Generator().manual_seed(M)
+    hold = lambda r: torch.full((r, 496), 0x7f, dtype=torch.uint8, device="cuda").view(F8)  # noqa: E731
+    A, W = hold(M), hold(N)
+    A.view(torch.uint8)[:, 32:32 + K] = codes(g, M, K).view(torch.uint8)
+    W.view(torch.uint8)[:, 32:32 + K] = codes(g, N, K).view(torch.uint8)
+    a, w = A[:, 32:32 + K], W[:, 32:32 + K]
+    sa, sw = scales(g, M, 4), scales(g, -(-N // 128), 4)
+    y = ops.e4m3_linear(a, sa, w, sw, dtype=torch.float32)
+    assert torch.equal(y, ops.e4m3_linear(a.contiguous(), sa, w.contiguous(), sw, dtype=torch.float32))
+    check(y, a.contiguous(), sa, w.contiguous(), sw, None)
+
+
+@pytest.mark.parametrize("M,N", [(9, 70), (300, 300)])
+def test_nan_reaches_its_row_only(M, N):
+    from chunkwise_delta_rule_chunk_amd import ops
+    g = torch.Generator().manual_seed(1)
+    a, w = codes(g, M, 256), codes(g, N, 256)
+    sa, sw = scales(g, M, 2), scales(g, N, 2)
+    y0 = ops.e4m3_linear(a, sa, w, sw)
+    a.view(torch.uint8)[4, 130] = 0x7f
+    sa[2, 1] = float("inf")
+    w.view(torch.uint8)[60, 3] = 0xff
+    y = ops.e4m3_linear(a, sa, w, sw)
+    hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    hit[4] = hit[2] = True
+    hit[:, 60] = True
+    assert torch.equal(y[~hit], y0[~hit])
+    assert torch.isnan(y[4]).all() and torch.isnan(y[:, 60]).all() and not torch.isfinite(y[2]).any()
+
+
+def test_reads_what_the_norms_hand_out():
+    """rms_norm's and group_norm's codes and scales, without a copy in between."""
+    from chunkwise_delta_rule_chunk_amd import ops
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(3, 50, 512, generator=g).to(torch.bfloat16).cuda()
+    w, sw = codes(g, 384, 512), scales(g, 3, 4)
+    for group in (0, 128):
+        _, _, q, s, _ = ops.rms_norm(x, quant="e4m3", group=group, output=False)
+        y = ops.e4m3_linear(q, s, w, sw)
+        assert y.shape == (3, 50, 384)
+        check(y.flatten(0, 1), q.flatten(0, 1), s, w, sw, None)
+        _, q, s, _ = ops.group_norm(x, groups=4, quant="e4m3", group=group, output=False)
+        check(ops.e4m3_linear(q, s, w, sw).flatten(0, 1), q.flatten(0, 1), s, w, sw, None)

@@ -172,7 +172,7 @@ def load():
                 ("rewy_ssm_recurrent_fwd", [SD] + [P] * 11, ctypes.c_int),
                 ("rewy_decay_workspace_bytes", [LD, ctypes.c_int], S),
                 ("rewy_decay_fwd", [LD] + [P] * 8 + [S, P], ctypes.c_int),
-                ("rewy_decay_bwd", [LD] + [P] * 12 + [S, P], ctypes.c_int),
+                ("rewy_decay_bwd", [LD] + [P] * 8 + [S] + [P] * 5 + [S, P], ctypes.c_int),
                 ("rewy_decay_recurrent_fwd", [LD] + [P] * 8, ctypes.c_int),
                 ("rewy_gnorm_fwd", [GD] + [P] * 10, ctypes.c_int),
                 ("rewy_gnorm_workspace_bytes", [GD], S),
@@ -310,9 +310,10 @@ def rewy_decay_fwd(desc, q, k, v, g, h0, o, ht, workspace, ws_bytes, stream) -> 
     return load().rewy_decay_fwd(ctypes.byref(desc), q, k, v, g, h0, o, ht, workspace, ws_bytes, stream)
 
 
-def rewy_decay_bwd(desc, q, k, v, g, h0, dO, dht, dq, dk, dv, dh0, workspace, ws_bytes, stream) -> int:
-    return load().rewy_decay_bwd(ctypes.byref(desc), q, k, v, g, h0, dO, dht, dq, dk, dv, dh0, workspace,
-                                 ws_bytes, stream)
+def rewy_decay_bwd(desc, q, k, v, g, h0, dO, dht, states, states_bytes, dq, dk, dv, dh0, workspace,
+                   ws_bytes, stream) -> int:
+    return load().rewy_decay_bwd(ctypes.byref(desc), q, k, v, g, h0, dO, dht, states, states_bytes, dq, dk, dv,
+                                 dh0, workspace, ws_bytes, stream)
 
 
 def rewy_decay_recurrent_fwd(desc, q, k, v, g, h0, o, ht, stream) -> int:

@@ -7,21 +7,24 @@
 namespace rewy {
 namespace {
 
-// Tokens of a segment, whole chunks, at least 256: as long as there are 512 pairs of a
-// segment and a head, two workgroups for each CU (a longer segment means fewer states to
-// join).  Packed sequences end with half a segment on average, which leaves the target
-// (N - 1) / 2 a head less, at least half of it.
+// Tokens of a segment, whole chunks, at least 128 (2 x 1000 tokens of 16 heads in 32 bits, a
+// training step's kernels: 86 us in segments of 128, 92 of 64, 101 of 256): as long as there
+// are 512 pairs of a segment and a head, two workgroups for each CU (a longer segment
+// means fewer states to join; 8192 tokens of 32 heads: 134 us in segments of 512, 157
+// of 256, 146 of 1024).  Packed sequences end with half a segment on average: as many pairs
+// more, so that the shorter ones fill up behind the longer (16 sequences, 9000 tokens
+// of 32 heads: 117 us in segments of 384, 126 of 512, 143 of 1088).
 int decay_segment(const SeqArgs& q, int H) {
   constexpr int64_t SEGMENTS = 512;
   int64_t want;
   if (q.cu) {
-    const int64_t whole = std::max(SEGMENTS - (int64_t)(q.N - 1) * H / 2, SEGMENTS / 2);
-    want = ((int64_t)q.total * H + whole - 1) / whole;
+    const int64_t pairs = SEGMENTS + std::min((int64_t)(q.N - 1) * H / 2, SEGMENTS);
+    want = ((int64_t)q.total * H + pairs - 1) / pairs;
   } else {
     const int64_t each = std::max<int64_t>(SEGMENTS / ((int64_t)q.N * H), 1);
     want = (q.T + each - 1) / each;
   }
-  return (int)std::min<int64_t>(INT32_MAX / CH * CH, std::max<int64_t>(256, up64(want)));
+  return (int)std::min<int64_t>(INT32_MAX / CH * CH, std::max<int64_t>(128, up64(want)));
 }
 
 int decay_args(const rewy_decay_desc* d, bool bwd, DecayArgs& a) {
@@ -53,7 +56,7 @@ int decay_args(const rewy_decay_desc* d, bool bwd, DecayArgs& a) {
   a.nslot = (int)std::min<int64_t>(nslot, INT32_MAX);
   // a launch takes fewer than 2^32 threads along x: the segments' states and walks, the
   // token-serial form and the pass, the heads' sums
-  const int64_t threads[] = {nslot * a.H * 512, (int64_t)a.seq.N * a.H * 256, bwd ? total * a.G * 32 + 256 : 0};
+  const int64_t threads[] = {nslot * a.H * (bwd ? 768 : 512), (int64_t)a.seq.N * a.H * 256, bwd ? total * a.G * 32 + 256 : 0};
   for (int64_t n : threads)
     if (n >= (int64_t)1 << 32)
       return fail(REWY_EUNSUPPORTED, "%lld sequences and %lld tokens of %d heads are too many", (long long)a.seq.N,
@@ -90,9 +93,6 @@ int decay_inputs(const void* q, const void* k, const void* v, const float* g, co
   return REWY_OK;
 }
 
-int decay_walk(const DecayArgs& a, int what, bool f32, hipStream_t s) {
-  return hip_check(traced("k_decay_walk", s, [&] { return launch_decay_walk(a, what, f32, s); }), "attention");
-}
 // The states of the segments that the walks need, and those that are handed out.
 int decay_states(const DecayArgs& a, int dirs, bool f32, hipStream_t s) {
   if (!dirs) return REWY_OK;
@@ -131,13 +131,14 @@ REWY_API int rewy_decay_fwd(const rewy_decay_desc* d, const void* q, const void*
     a.o = o; a.ht = ht;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     REWY_TRY(decay_states(a, a.two || ht ? 1 : 0, f32, s));
-    return some ? decay_walk(a, DECAY_O, f32, s) : (int)REWY_OK;
+    if (!some) return REWY_OK;
+    return hip_check(traced("k_decay_fwd", s, [&] { return launch_decay_fwd(a, f32, s); }), "attention");
   });
 }
 
 REWY_API int rewy_decay_bwd(const rewy_decay_desc* d, const void* q, const void* k, const void* v, const float* g,
-                            const float* h0, const void* dO, const float* dht, void* dq, void* dk, void* dv, float* dh0,
-                            void* workspace, size_t ws_bytes, void* stream) {
+                            const float* h0, const void* dO, const float* dht, const void* states, size_t states_bytes,
+                            void* dq, void* dk, void* dv, float* dh0, void* workspace, size_t ws_bytes, void* stream) {
   return guarded([&]() -> int {
     DecayArgs a;
     REWY_TRY(decay_args(d, true, a));
@@ -149,17 +150,18 @@ REWY_API int rewy_decay_bwd(const rewy_decay_desc* d, const void* q, const void*
     REWY_TRY(check_ptr("dk", dk, 16, some));
     REWY_TRY(check_ptr("dv", dv, 16, some));
     REWY_TRY(check_ptr("dh0", dh0, 16, h0 != nullptr));
+    DecayArgs f = a;  // the forward's layout
+    if (states) REWY_TRY(check_workspace(states, states_bytes, decay_layout(f, false, static_cast<char*>(const_cast<void*>(states)))));
     REWY_TRY(check_workspace(workspace, ws_bytes, decay_layout(a, true, static_cast<char*>(workspace))));
+    if (states) a.sf = f.sf;
     if (dh0 && (dh0 == h0 || dh0 == dht)) return fail(REWY_EINVAL, "dh0 may not be h0 or dht");
     for (const void* out : {dq, dk, dv})
       if (some && (out == q || out == k || out == v || out == dO)) return fail(REWY_EINVAL, "a gradient may not be an input");
     a.dO = dO; a.dht = dht; a.dq = dq; a.dk = dk; a.dv = dv; a.dh0 = dh0;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    REWY_TRY(decay_states(a, (a.two ? 3 : 0) | (dh0 ? 2 : 0), f32, s));
+    REWY_TRY(decay_states(a, (a.two ? (states ? 2 : 3) : 0) | (dh0 ? 2 : 0), f32, s));
     if (!some) return REWY_OK;
-    REWY_TRY(decay_walk(a, DECAY_DQ, f32, s));
-    REWY_TRY(decay_walk(a, DECAY_DV, f32, s));
-    REWY_TRY(decay_walk(a, DECAY_DK, f32, s));
+    REWY_TRY(hip_check(traced("k_decay_bwd", s, [&] { return launch_decay_bwd(a, f32, s); }), "attention backward"));
     if (a.per == 1) return REWY_OK;
     return hip_check(traced("k_decay_sum", s, [&] { return launch_decay_sum(a, f32, s); }), "head sums");
   });

@@ -39,6 +39,6 @@ REWY_API int rewy_e4m3_linear(const rewy_e4m3_desc* d, const void* a, const floa
     g.a = static_cast<const uint8_t*>(a); g.w = static_cast<const uint8_t*>(w);
     g.sa = a_scale; g.sw = w_scale; g.bias = bias; g.y = y;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return hip_check(traced(mm8_kernel(g, f32), s, [&] { return launch_mm8(g, f32, s); }), "e4m3 product");
+    return hip_check(traced(mm8_kernel(g), s, [&] { return launch_mm8(g, f32, s); }), "e4m3 product");
   });
 }

@@ -58,7 +58,8 @@ struct DecayArgs {
 // directions of the states: bit 0 forward, bit 1 reverse
 hipError_t launch_decay_state(const DecayArgs& a, bool f32, int dirs, hipStream_t s);
 hipError_t launch_decay_pass(const DecayArgs& a, int dirs, hipStream_t s);
-hipError_t launch_decay_walk(const DecayArgs& a, int what, bool f32, hipStream_t s);
+hipError_t launch_decay_fwd(const DecayArgs& a, bool f32, hipStream_t s);
+hipError_t launch_decay_bwd(const DecayArgs& a, bool f32, hipStream_t s);
 hipError_t launch_decay_sum(const DecayArgs& a, bool f32, hipStream_t s);
 hipError_t launch_decay_recurrent(const DecayArgs& a, bool f32, hipStream_t s);
 

@@ -17,29 +17,25 @@ __device__ __forceinline__ void decay_pow2(float g, int n, float& hi, float& lo)
   lo = (float)(d - (double)hi);
 }
 
-// frag_col of a tile whose columns store_acc_order has placed: columns 16 nt + (l & 15) of
-// the tile as it was
+// Row fragment (rows in slot order) of a tile with its columns as they are, for a
+// contraction whose partner lies in acc order (store_acc_order)
 template <typename T>
-__device__ __forceinline__ uint4 frag_col_acc(const T* p, int ld, int t0, int nt) {
+__device__ __forceinline__ uint4 frag_row_slot_acc(const T* p, int ld, int r0, int k0) {
+  const int l = lane_id();
   if constexpr (std::is_same_v<T, bf16>) {
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-    const int g = lane_id() >> 4, r = lane_id() & 15;
-    const T* q = p + (t0 + tr_row(g, r >> 2)) * ld + 32 * (nt >> 1) + 8 * (r & 3) + 4 * (nt & 1);
-    const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q)));
-    const uint2 y = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 16 * ld)));
+    const T* q = p + (r0 + slot_row<T>(l & 15)) * ld + k0 + 4 * (l >> 4);
+    const uint2 x = *reinterpret_cast<const uint2*>(q), y = *reinterpret_cast<const uint2*>(q + 16);
     return uint4{x.x, x.y, y.x, y.y};
   } else {
-    return frag_col<T>(p, ld, t0, 16 * nt);
+    return frag_row_slot<T>(p, ld, r0, k0);
   }
 }
 
 // S = dec S + sum_t B_t (al_t C_t)^T for the wave's CT tiles of 16 columns (B from the
-// tile sb, its columns as they are or, ACC, in acc order; C's columns in cf, scaled and
-// split into NS pieces; sal in slot order)
-template <typename T, int KA, int CT, int NS, bool ACC>
+// tile sb; C's columns in cf, scaled and split into NS pieces; sal in slot order)
+template <typename T, int KA, int CT, int NS>
 __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* sb, int ldb, const uint4 (&cf)[CT][CH / KG<T>],
-                                             const float* sal, float hi, float lo) {
+                                             const float* sal, const float (&hi)[CT], float lo) {
   constexpr int NQ = CH / KG<T>, VE = VEC<T>;
   const int g = lane_id() >> 4;
   uint4 uf[CT][NQ][NS];
@@ -64,7 +60,7 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
     for (int ct = 0; ct < CT; ++ct) u[ct] = zero4();
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const uint4 bf = ACC ? frag_col_acc<T>(sb, ldb, q * KG<T>, nt) : frag_col<T>(sb, ldb, q * KG<T>, 16 * nt);
+      const uint4 bf = frag_col<T>(sb, ldb, q * KG<T>, 16 * nt);
 #pragma unroll
       for (int s = NS - 1; s >= 0; --s)
 #pragma unroll
@@ -73,7 +69,7 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[ct][nt][i] = hi * S[ct][nt][i] + (lo * S[ct][nt][i] + u[ct][i]);
+      for (int i = 0; i < 4; ++i) S[ct][nt][i] = hi[ct] * S[ct][nt][i] + (lo * S[ct][nt][i] + u[ct][i]);
   }
 }
 
@@ -81,8 +77,11 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
 // values; reverse, the adjoint that its queries and output adjoints send to the state
 // that enters it.  Where a sequence is one segment the state starts from h0 (dht) and is
 // ht (dh0) itself.  Wave w holds 16 columns of the state.
+// (waves a SIMD: two workgroups of 512 threads a CU, or as many as the registers hold)
 template <typename T, int K, int V>
-__global__ __launch_bounds__(4 * V, 2) void k_decay_state(DecayArgs a, int dirs) {
+constexpr int state_waves() { return std::is_same_v<T, float> ? 2 : 4; }
+template <typename T, int K, int V>
+__global__ __launch_bounds__(4 * V, (state_waves<T, K, V>())) void k_decay_state(DecayArgs a, int dirs) {
   constexpr int NTH = 4 * V, LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>, NT = K / 16;
   __shared__ __align__(16) T sk[CH * LK];
   __shared__ __align__(16) T su[CH * LV];
@@ -133,7 +132,8 @@ __global__ __launch_bounds__(4 * V, 2) void k_decay_state(DecayArgs a, int dirs)
     uint4 ut[1][NQ];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) ut[0][q] = frag_col<T>(su, LV, q * KG<T>, 16 * w);
-    decay_update<T, K, 1, SPLIT<T>, false>(S, sk, LK, ut, sal, hi, lo);
+    const float dec[1] = {hi};
+    decay_update<T, K, 1, SPLIT<T>>(S, sk, LK, ut, sal, dec, lo);
     lds_barrier();
   }
   float* o = a.two ? (dir ? a.sr : a.sf) + ((int64_t)slot * a.H + h) * kv : end + seqhead;
@@ -257,8 +257,9 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
   // pairs of blocks right of the diagonal lie inside a contraction of 32: zeros, written once
   for (int i = threadIdx.x; i < CH * LM; i += NTH) sm[i] = (T)0.f;
   if (ODD && threadIdx.x == 0) *sodd = 0;
-  float hi, lo;
+  float hi, lo, hl, ll;  // of a chunk, and (REV) of the sequence's last one
   decay_pow2(g, CH, hi, lo);
+  decay_pow2(g, min(CH, t1 - t0 - (nch - 1) * CH), hl, ll);
   lds_barrier();
   // Coefficients of a lane: block (I, J) holds rows j = 16 J + slot_row(4 g4 + e), columns
   // i = 16 I + r; within a diagonal block lam^|i-j| or zero, 16 (n + 1) tokens away
@@ -275,7 +276,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
   auto put_tiles = [&](int c) {
     if (ODD && tile_not_finite<T, CV, NTH>(rc)) *sodd = c + 1;
     store_acc_order<T, KA, NTH>(ra, sa, LA);
-    store_acc_order<T, KA, NTH>(rb, sb, LA);
+    rb.store(sb, LA, threadIdx.x);
     rc.store(sc, LC, threadIdx.x);
   };
   put_tiles(0);
@@ -294,7 +295,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
         f32x4 acc = zero4();
 #pragma unroll
         for (int q = 0; q < KQ; ++q)
-          mma16B<T>(acc, frag_row_slot<T>(sb, LA, 16 * J, q * KG<T>), frag_row<T>(sa, LA, 16 * I, q * KG<T>));
+          mma16B<T>(acc, frag_row_slot_acc<T>(sb, LA, 16 * J, q * KG<T>), frag_row<T>(sa, LA, 16 * I, q * KG<T>));
         f32x4 m;
         const float p = X - Y == 3 ? p16[2] : X - Y == 2 ? p16[1] : p16[0];
 #pragma unroll
@@ -306,20 +307,19 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
       }
     }
     const bool odd = ODD && __builtin_amdgcn_readfirstlane(*sodd) == c + 1;
-    int first[CT];
     if (odd) {
-#pragma unroll
+#pragma unroll 1
       for (int ct = 0; ct < CT; ++ct) {
-        T* xc = sc + 16 * (CT * w + ct) + r;
-        first[ct] = CH;
+        const int col = 16 * (CT * w + ct) + r;
+        int first = CH;
 #pragma unroll 1
         for (int j = CH - 4 + g4; j >= 0; j -= 4)
-          if (!(fabsf((float)xc[j * LC]) <= 3.4028235e38f)) {
-            xc[j * LC] = (T)0.f;
-            first[ct] = j;
+          if (!(fabsf((float)sc[j * LC + col]) <= 3.4028235e38f)) {
+            sc[j * LC + col] = (T)0.f;
+            first = j;
           }
-        first[ct] = min(first[ct], __shfl_xor(first[ct], 16, 64));
-        first[ct] = min(first[ct], __shfl_xor(first[ct], 32, 64));
+        first = min(first, __shfl_xor(first, 16, 64));
+        sodd[1 + col] = min(first, __shfl_xor(first, 32, 64));
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
@@ -385,23 +385,20 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
     }
     if (c + 1 < nch) {
       constexpr int NS = std::is_same_v<T, bf16> ? 2 : 1;
-      float uh = hi, ul = lo;
-      if (REV && len < CH) decay_pow2(g, len, uh, ul);
-      decay_update<T, KA, CT, NS, true>(S, sb, LA, xt, sal, uh, ul);
+      const float uh = REV && c == 0 ? hl : hi, ul = REV && c == 0 ? ll : lo;
+      float dec[CT];
+      // (a column that held an infinity or NaN: its state is NaN from here on)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) dec[ct] = ODD && odd && sodd[1 + 16 * (CT * w + ct) + r] < CH ? __builtin_nanf("") : uh;
+      decay_update<T, KA, CT, NS>(S, sb, LA, xt, sal, dec, ul);
     }
     if (odd) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        T* yc = sc + 16 * (CT * w + ct) + r;
 #pragma unroll 1
-        for (int j = first[ct] + g4; j < CH; j += 4) yc[j * LC] = (T)__builtin_nanf("");
-        if (first[ct] < CH) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[ct][nt][i] = __builtin_nanf("");
-        }
+      for (int ct = 0; ct < CT; ++ct) {
+        const int col = 16 * (CT * w + ct) + r;
+#pragma unroll 1
+        for (int j = sodd[1 + col] + g4; j < CH; j += 4) sc[j * LC + col] = (T)__builtin_nanf("");
       }
     }
     lds_barrier();  // tiles and coefficients free, outputs complete
@@ -432,13 +429,10 @@ template <typename T, int KA, int CV>
 constexpr int walk_waves() { return std::is_same_v<T, float> && KA + CV > 128 ? 1 : 2; }
 
 template <typename T, int K, int V, int WHAT>
-__global__ __launch_bounds__((walk_threads<T, (WHAT & 1) ? K : V>()), (walk_waves<T, K, V>())) void k_decay_walk(DecayArgs a) {
+__device__ __forceinline__ void decay_one(const DecayArgs& a, T* lds, float* tab, int* sodd, int wk) {
   constexpr bool TS = WHAT & 1, REV = WHAT >= 2;  // (dq and dk)
   constexpr int KA = TS ? V : K, CV = TS ? K : V;
-  __shared__ __align__(16) T lds[walk_lds<T, KA, CV>()];
-  __shared__ __align__(16) float tab[2 * CH + 1];
-  __shared__ int sodd;
-  const int wk = xcd_range(blockIdx.x, a.nslot * a.H), slot = wk / a.H, h = wk - slot * a.H, grp = h / a.per;
+  const int slot = wk / a.H, h = wk - slot * a.H, grp = h / a.per;
   const Piece pc = find_piece(a.seq, slot, a.seg);
   if (!pc.on) return;
   WalkIo io = {};
@@ -450,7 +444,29 @@ __global__ __launch_bounds__((walk_threads<T, (WHAT & 1) ? K : V>()), (walk_wave
     io = WalkIo{a.k, a.q, a.dO, a.ks, a.qs, a.os, grp * K, h * K, h * V, a.dv, a.vpart, a.vpart ? (int64_t)a.H * V : a.dvs, h * V};
   else
     io = WalkIo{a.v, a.dO, a.q, a.vs, a.os, a.qs, grp * V, h * V, h * K, a.dk, a.kpart, a.kpart ? (int64_t)a.H * K : a.dks, h * K};
-  decay_walk<T, KA, CV, walk_ct<T, CV>(), REV, TS, WHAT == DECAY_O>(a, io, lds, tab, &sodd, pc, slot, h);
+  decay_walk<T, KA, CV, walk_ct<T, CV>(), REV, TS, WHAT == DECAY_O>(a, io, lds, tab, sodd, pc, slot, h);
+}
+
+template <typename T, int K, int V>
+__global__ __launch_bounds__((walk_threads<T, V>()), (walk_waves<T, K, V>())) void k_decay_fwd(DecayArgs a) {
+  __shared__ __align__(16) T lds[walk_lds<T, K, V>()];
+  __shared__ __align__(16) float tab[2 * CH + 1];
+  __shared__ int sodd[1 + V];  // last chunk with an infinity or NaN, from 1; each column's first
+  decay_one<T, K, V, DECAY_O>(a, lds, tab, sodd, xcd_range(blockIdx.x, a.nslot * a.H));
+}
+
+// The three walks of a segment and head are neighbours, so that the rows that they share
+// come from an L2 while they are there.
+template <typename T, int K, int V>
+__global__ __launch_bounds__((walk_threads<T, std::max(K, V)>()), (walk_waves<T, K, V>())) void k_decay_bwd(DecayArgs a) {
+  __shared__ __align__(16) T lds[std::max(walk_lds<T, K, V>(), walk_lds<T, V, K>())];
+  __shared__ __align__(16) float tab[2 * CH + 1];
+  const int wk = xcd_range(blockIdx.x, 3 * a.nslot * a.H), at = wk / 3, what = wk - 3 * at;
+  // (waves that a narrow output has no columns for leave; the barriers do without them)
+  if (threadIdx.x >= (what == 0 ? walk_threads<T, V>() : walk_threads<T, K>())) return;
+  if (what == 0) decay_one<T, K, V, DECAY_DV>(a, lds, tab, nullptr, at);
+  else if (what == 1) decay_one<T, K, V, DECAY_DK>(a, lds, tab, nullptr, at);
+  else decay_one<T, K, V, DECAY_DQ>(a, lds, tab, nullptr, at);
 }
 
 // dk and dv of a group: the sum over its heads, in order (rows behind the last sequence
@@ -548,16 +564,6 @@ hipError_t decay_kv(const DecayArgs& a, bool f32, F&& f) {
   };
   return dim(a.K, [&](auto k) { return dim(a.V, [&](auto v) { return f32 ? f(float{}, k, v) : f(bf16{}, k, v); }); });
 }
-template <int WHAT>
-hipError_t launch_walk(const DecayArgs& a, bool f32, hipStream_t s) {
-  return decay_kv(a, f32, [&](auto t, auto k, auto v) {
-    using T = decltype(t);
-    constexpr int K = decltype(k)::value, V = decltype(v)::value, CV = (WHAT & 1) ? K : V;
-    REWY_LAUNCH((k_decay_walk<T, K, V, WHAT>), dim3(a.nslot * a.H), dim3(walk_threads<T, CV>()), s, a);
-    return hipGetLastError();
-  });
-}
-
 }  // namespace
 
 hipError_t launch_decay_state(const DecayArgs& a, bool f32, int dirs, hipStream_t s) {
@@ -572,11 +578,21 @@ hipError_t launch_decay_pass(const DecayArgs& a, int dirs, hipStream_t s) {
   REWY_LAUNCH(k_decay_pass, dim3(a.seq.N * a.H, (a.K * a.V + 1023) / 1024, dirs == 3 ? 2 : 1), dim3(256), s, a, dirs);
   return hipGetLastError();
 }
-hipError_t launch_decay_walk(const DecayArgs& a, int what, bool f32, hipStream_t s) {
-  return what == DECAY_O    ? launch_walk<DECAY_O>(a, f32, s)
-         : what == DECAY_DQ ? launch_walk<DECAY_DQ>(a, f32, s)
-         : what == DECAY_DV ? launch_walk<DECAY_DV>(a, f32, s)
-                            : launch_walk<DECAY_DK>(a, f32, s);
+hipError_t launch_decay_fwd(const DecayArgs& a, bool f32, hipStream_t s) {
+  return decay_kv(a, f32, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = decltype(k)::value, V = decltype(v)::value;
+    REWY_LAUNCH((k_decay_fwd<T, K, V>), dim3(a.nslot * a.H), dim3(walk_threads<T, V>()), s, a);
+    return hipGetLastError();
+  });
+}
+hipError_t launch_decay_bwd(const DecayArgs& a, bool f32, hipStream_t s) {
+  return decay_kv(a, f32, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = decltype(k)::value, V = decltype(v)::value;
+    REWY_LAUNCH((k_decay_bwd<T, K, V>), dim3(3 * a.nslot * a.H), dim3(walk_threads<T, std::max(K, V)>()), s, a);
+    return hipGetLastError();
+  });
 }
 hipError_t launch_decay_sum(const DecayArgs& a, bool f32, hipStream_t s) {
   const int64_t n = (int64_t)a.seq.total * a.G * std::max(a.K, a.V) / 4;

@@ -34,17 +34,27 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
   const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-// a lane's 32 codes of a block
-struct Wide32 {
-  bf16x8 v[4];
-  __device__ __forceinline__ Wide32(uint4 x, uint4 y) : v{widen8(x.x, x.y), widen8(x.z, x.w), widen8(y.x, y.y), widen8(y.z, y.w)} {}
+// An operand of 16 rows and a block: as it is, or widened to bf16.
+template <bool WIDE>
+struct Oper {
+  i32x8 v;
+  __device__ __forceinline__ void set(uint4 x, uint4 y) { v = join16(x, y); }
 };
-__device__ __forceinline__ f32x4 mma_wide(const Wide32& w, const Wide32& a) {
+template <>
+struct Oper<true> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(uint4 x, uint4 y) {
+    v[0] = widen8(x.x, x.y); v[1] = widen8(x.z, x.w); v[2] = widen8(y.x, y.y); v[3] = widen8(y.z, y.w);
+  }
+};
+__device__ __forceinline__ f32x4 mma_block(const Oper<false>& w, const Oper<false>& a) { return mma8(w.v, a.v); }
+__device__ __forceinline__ f32x4 mma_block(const Oper<true>& w, const Oper<true>& a) {
   f32x4 p = zero4();
 #pragma unroll
   for (int q = 0; q < 4; ++q) p = mma(w.v[q], a.v[q], p);
   return p;
 }
+
 __device__ __forceinline__ float ld_bias(const Mm8Args& a, int n) { return a.bias ? ld_beta(a.bias, a.bias_f32, n) : 0.f; }
 
 // four neighbouring columns n .. of a row, as far as they exist
@@ -86,22 +96,40 @@ __global__ __launch_bounds__(512) void k_mm8_rows(Mm8Args a) {
   f32x4 acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = zero4();
-#pragma unroll 2
-  for (int kb = w; kb < a.nb; kb += 8) {
-    const int k = kb * 128 + 32 * g;
-    auto at = [&](uint32_t o, int h) { return k + h < a.K ? o + kb * 128 + h : OOB; };  // (past a row's end: zeros)
-    const Wide32 wf(gld16(gw, at(wo, 0)), gld16(gw, at(wo, 16)));
-    f32x4 sw;
+  // four blocks at a time, all their loads first (blocks past the last and bytes past a
+  // row's end: zeros)
+  constexpr int U = 4;
+#pragma unroll 1
+  for (int k0 = w; k0 < a.nb; k0 += 8 * U) {
+    uint4 wx[U][2], ax[U][MT][2];
+    float sw[U][4], sa[U][MT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw[i] = swp[i][kb];
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + 8 * u, k = kb * 128 + 32 * g, ks = min(kb, a.nb - 1);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const uint32_t o = ao + (uint32_t)(16 * t * a.as);
-      const Wide32 af(gld16(ga, at(o, 0)), gld16(ga, at(o, 16)));
-      const float sa = sap[t][a.ablk ? kb : 0];
-      const f32x4 p = mma_wide(wf, af);
+      for (int h = 0; h < 2; ++h) {
+        const bool in = k + 16 * h < a.K;
+        wx[u][h] = gld16(gw, in ? wo + kb * 128 + 16 * h : OOB);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] += p[i] * (sa * sw[i]);
+        for (int t = 0; t < MT; ++t) ax[u][t][h] = gld16(ga, in ? ao + (uint32_t)(16 * t * a.as) + kb * 128 + 16 * h : OOB);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sw[u][i] = swp[i][ks];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) sa[u][t] = sap[t][a.ablk ? ks : 0];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + 8 * u >= a.nb) break;  // (zeros, but not beside a scale that is no number)
+      Oper<true> wf, af;
+      wf.set(wx[u][0], wx[u][1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        af.set(ax[u][t][0], ax[u][t][1]);
+        const f32x4 p = mma_block(wf, af);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] += p[i] * (sa[u][t] * sw[u][i]);
+      }
     }
   }
 #pragma unroll
@@ -136,6 +164,10 @@ __device__ __forceinline__ void load_lds16(u32x4 b, uint32_t off, uint32_t dst) 
   dst = __builtin_amdgcn_readfirstlane(dst);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b) : "memory");
 }
+__device__ __forceinline__ void load_lds4(u32x4 b, uint32_t off, uint32_t dst) {  // the same with 4 bytes a lane
+  dst = __builtin_amdgcn_readfirstlane(dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b) : "memory");
+}
 // gbuf's resource as its four words
 __device__ __forceinline__ u32x4 buf_words(const void* base, uint32_t bytes) {
   const uint64_t p = (uint64_t)base;
@@ -144,292 +176,282 @@ __device__ __forceinline__ u32x4 buf_words(const void* base, uint32_t bytes) {
                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 
-// A wave's tiles, from row m0 of a and row n0 of w, with the bias
-template <typename O, int TM, int TN>
+// A wave's tiles, from row m0 of a and row n0 of w, with the bias (FULL: all of them
+// exist, TM TN stores)
+template <typename O, int TM, int TN, bool FULL>
 __device__ __forceinline__ void store_tile(const Mm8Args& a, const f32x4 (&acc)[TM][TN], int m0, int n0) {
   const int r = lane_id() & 15, g = lane_id() >> 4;
+  if constexpr (FULL && std::is_same_v<O, bf16> && TN % 2 == 0) {
+    // two tiles' columns change places between neighbouring lane groups, so that a lane
+    // stores eight of one tile: columns 8 (g >> 1) .. of tile j + (g & 1)
+#pragma unroll
+    for (int j = 0; j < TN; j += 2) {
+      float b[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[k][e] = ld_bias(a, n0 + 16 * (j + k) + 4 * g + e);
+      bf16* y = reinterpret_cast<bf16*>(a.y) + (m0 + r) * a.ys + n0 + 16 * (j + (g & 1)) + 8 * (g >> 1);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        uint32_t x[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            x[k][h] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)(acc[i][j + k][2 * h] + b[k][2 * h]),
+                                                          (bf16)(acc[i][j + k][2 * h + 1] + b[k][2 * h + 1])});
+        const auto p = __builtin_amdgcn_permlane16_swap(x[0][0], x[1][0], false, false);
+        const auto q = __builtin_amdgcn_permlane16_swap(x[0][1], x[1][1], false, false);
+        typedef u32x4 u32x4_u __attribute__((aligned(2)));
+        *reinterpret_cast<u32x4_u*>(y + 16 * i * a.ys) = u32x4{p[0], q[0], p[1], q[1]};
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const int n = n0 + 16 * j + 4 * g;
     f32x4 b = zero4();
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (n + e < a.N) b[e] = ld_bias(a, n + e);
+      if (FULL || n + e < a.N) b[e] = ld_bias(a, n + e);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int m = m0 + 16 * i + r;
-      if (m < a.M && n < a.N) store4<O>(a, m, n, acc[i][j] + b);
+      if constexpr (FULL) {
+        typename VecN<O, 4>::raw o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (O)(acc[i][j][e] + b[e]);
+        *reinterpret_cast<typename VecN<O, 4>::type*>(reinterpret_cast<O*>(a.y) + m * a.ys + n) = o;
+      } else if (m < a.M && n < a.N) {
+        store4<O>(a, m, n, acc[i][j] + b);
+      }
     }
   }
 }
 
-// First rows of a workgroup's tile: the workgroups go to the XCDs in turn, each of which
+// First rows of tile b: the workgroups go to the XCDs in turn, each of which
 // takes a contiguous range, eight tiles of rows by as many of columns as are at work at
 // once.
 template <int BM, int BN>
-__device__ __forceinline__ void tile_origin(const Mm8Args& a, int& m0, int& n0) {
-  const int nm = (a.M + BM - 1) / BM, nn = (a.N + BN - 1) / BN, id = xcd_range(blockIdx.x, nm * nn);
+__device__ __forceinline__ void tile_origin(const Mm8Args& a, int b, int& m0, int& n0) {
+  const int nm = (a.M + BM - 1) / BM, nn = (a.N + BN - 1) / BN, id = xcd_range(b, nm * nn);
   const int grp = id / (8 * nn), gm = min(8, nm - 8 * grp), in = id - grp * 8 * nn;
   m0 = (8 * grp + in % gm) * BM;
   n0 = in / gm * BN;
 }
-// Thread t's scales of each block: row t of [a's rows ; w's rows] of a tile
-template <int BM, int BN, int NTH, bool WROW>
-struct TileScales {
-  static constexpr int N = (BM + BN + NTH - 1) / NTH;
-  const float* p[N];
-  int step[N];
-  float v[N];
-  __device__ __forceinline__ TileScales(const Mm8Args& a, int m0, int n0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int t = threadIdx.x + i * NTH, n = min(n0 + max(t - BM, 0), a.N - 1);
-      p[i] = t < BM ? a.sa + (int64_t)min(m0 + t, a.M - 1) * (a.ablk ? a.nb : 1) : a.sw + (int64_t)(WROW ? n : n / 128) * a.nb;
-      step[i] = t < BM ? a.ablk : 1;
-    }
-  }
-  __device__ __forceinline__ void load(int kb) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = p[i][kb * step[i]];
-  }
-  __device__ __forceinline__ void store(float* s) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int t = threadIdx.x + i * NTH;
-      if (N * NTH == BM + BN || t < BM + BN) s[t] = v[i];
-    }
-  }
-};
-
-// Tiles of BM rows of a by BN rows of w, WM x WN waves; two blocks of 128 in LDS, the
-// next one on its way while one is used.  A row's eight pieces of 16 bytes lie in LDS at
-// their place xor the row's last three bits, so that sixteen lanes that read one piece
-// of sixteen rows meet the banks evenly.
-template <typename O, int BM, int BN, int WM, int WN, bool WROW>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_mm8_tile(Mm8Args a) {
-  constexpr int NTH = 64 * WM * WN, NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16, P = (BM + BN) / 8 / NW;
-  static_assert((BM + BN) % (8 * NW) == 0 && BM % (8 * P) == 0, "a wave's pieces are rows of one operand");
+// Tiles of BM rows of a by BN rows of w, WM x WN waves; NS blocks of 128 and their scales
+// in LDS, straight from memory, the later ones on their way while one is used.  A row's
+// eight pieces of 16 bytes lie in LDS at their place xor the row's last three bits, so
+// that sixteen lanes that read one piece of sixteen rows meet the banks evenly.  A
+// workgroup takes tiles blockIdx, + gridDim, ... as one run of blocks: the only barrier of a
+// block stands before the last row of its products, and behind it the next block's first
+// operands are read, so that the matrix unit does not wait at a block's start, nor at a
+// tile's.
+template <typename O, int BM, int BN, int WM, int WN, int NS, bool WROW, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_mm8_tile(Mm8Args a, int tiles) {
+  constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16, P = (BM + BN) / 8 / NW;
+  static_assert((BM + BN) % (8 * NW) == 0 && BM % (8 * P) == 0 && 8 * P <= 64, "a wave's pieces are rows of one operand");
   static_assert(WROW || BN / WN <= 128, "a wave's columns share a scale");
-  __shared__ __align__(16) uint8_t tile[2][(BM + BN) * 128];
-  __shared__ __align__(16) float sc[2][BM + BN];
+  __shared__ __align__(16) uint8_t tile[NS][(BM + BN) * 128];
+  __shared__ __align__(16) float sc[NS][BM + BN];
   const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), r = l & 15, g = l >> 4, wm = w / WN, wn = w - wm * WN;
-  int m0, n0;
-  tile_origin<BM, BN>(a, m0, n0);
-
   // the wave's pieces: eight rows of 128 bytes each, of a for the first waves, of w for the others
   const int row0 = w * P * 8;
   const bool is_a = row0 < BM;
   const int64_t st = is_a ? a.as : a.ws;
-  const int rows = is_a ? min(BM, a.M - m0) : min(BN, a.N - n0), rbase = is_a ? row0 : row0 - BM;
-  const u32x4 gb = buf_words(is_a ? a.a + m0 * a.as : a.w + n0 * a.ws, (uint32_t)((rows - 1) * st + a.K));
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)tile) + row0 * 128;
+  const int rbase = is_a ? row0 : row0 - BM;
+  const auto lds_at = [](const void* p) {
+    return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+  };
+  const uint32_t tile0 = lds_at(tile) + row0 * 128, sc0 = lds_at(sc) + row0 * 4;
   const int kc = 16 * ((l & 7) ^ (l >> 3));
   const uint32_t off = (uint32_t)((rbase + (l >> 3)) * st) + kc;
-  TileScales<BM, BN, NTH, WROW> sv(a, m0, n0);
-  auto fetch = [&](int kb) {
-    const uint32_t o = (kb * 128 + kc < a.K ? off : OOB) + kb * 128;  // (past a row's end: zeros)
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-      load_lds16(gb, o + (uint32_t)(8 * p * st), lds0 + (kb & 1) * (BM + BN) * 128 + 8 * p * 128);
-    sv.load(kb);
+  // a scale's rows share it, and it serves the whole row or a block
+  const int srows = is_a || WROW ? 1 : 128, sblocks = is_a && !a.ablk ? 1 : a.nb, sstep = sblocks == 1 ? 0 : 4;
+  const int ra = (wm * TM * 16 + r) * 128 + 16 * (g ^ (r & 7)), rw = (BM + wn * TN * 16 + r) * 128 + 16 * (g ^ (r & 7));
+  int buf = 0, to = 0;          // where the block in use lies, where the next loads go
+  int fb = blockIdx.x, fk = 0;  // tile and block of the next loads
+  u32x4 gb, gs;
+  uint32_t soff;
+  auto begin = [&] {
+    int m0, n0;
+    tile_origin<BM, BN>(a, fb, m0, n0);
+    const int rows = is_a ? min(BM, a.M - m0) : min(BN, a.N - n0);
+    gb = buf_words(is_a ? a.a + m0 * a.as : a.w + n0 * a.ws, (uint32_t)((rows - 1) * st + a.K));
+    // (lane l's scale is that of row rbase + l)
+    const int x0 = (is_a ? m0 : n0) / srows, xl = ((is_a ? m0 : n0) + rows - 1) / srows;
+    gs = buf_words((is_a ? a.sa : a.sw) + (int64_t)x0 * sblocks, (uint32_t)(xl - x0 + 1) * 4 * sblocks);
+    soff = (uint32_t)(((is_a ? m0 : n0) + rbase + l) / srows - x0) * 4 * sblocks;
+  };
+  // (behind the last tile fk stays at nb: loads of zeros that nobody reads)
+  auto advance = [&] {
+    to = to + 1 == NS ? 0 : to + 1;
+    if (++fk >= a.nb) {
+      fk = a.nb;
+      fb += gridDim.x;
+      if (fb < tiles) {
+        fk = 0;
+        begin();
+      }
+    }
+  };
+  // loads 0 .. P - 1 of a block: rows; load P: scales (bytes past a row's end, rows and
+  // blocks past the last: zeros)
+  auto piece = [&](int p) {
+    const uint32_t o = (fk * 128 + kc < a.K ? off : OOB) + fk * 128;
+    load_lds16(gb, o + (uint32_t)(8 * p * st), tile0 + to * (BM + BN) * 128 + 8 * p * 128);
+  };
+  auto piece_scales = [&] {
+    if (8 * P == 64 || l < 8 * P) load_lds4(gs, fk < a.nb ? soff + fk * sstep : OOB, sc0 + to * (BM + BN) * 4);
   };
   f32x4 acc[TM][TN];
+  Oper<WIDE> wf[TN], af[2];
+  f32x4 sw[WROW ? TN : 1], swn[WROW ? TN : 1];
+  float sa[3];
+  auto frag = [&](Oper<WIDE>& f, int from, int at) {
+    f.set(*reinterpret_cast<const uint4*>(tile[from] + at), *reinterpret_cast<const uint4*>(tile[from] + (at ^ 64)));
+  };
+  auto scale_w = [&](int from, int j) {
+    if constexpr (WROW) return *reinterpret_cast<const f32x4*>(sc[from] + BM + (wn * TN + j) * 16 + 4 * g);
+    else return f32x4{sc[from][BM + wn * TN * 16], 0.f, 0.f, 0.f};
+  };
+  auto scale_a = [&](int from, int i) { return sc[from][(wm * TM + i) * 16 + r]; };
+  // The products of the block in `buf`.  A row of tiles ahead its operand is read, and two
+  // tiles behind a product meets its scales, while the matrix unit works.  Before the
+  // last row: the next block's loads, sent for NS - 1 blocks ago, have arrived (those of the
+  // blocks behind it may be on their way), and all waves have read this one, whose place
+  // the next loads take.
+  auto block = [&] {
+    constexpr int LAST = (TM - 1) * TN, PT = (P + TN) / TN;
+    const int nxt = buf + 1 == NS ? 0 : buf + 1;
+    auto add = [&](auto I, auto J, const f32x4& p) {
+      constexpr int i = decltype(I)::value, j = decltype(J)::value;
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
-  const int ra = (wm * TM * 16 + r) * 128 + 16 * (g ^ (r & 7)), rw = (BM + wn * TN * 16 + r) * 128 + 16 * (g ^ (r & 7));
-  fetch(0);
-  sv.store(sc[0]);
-  wait_vm<0>();
-  lds_barrier();
-  auto block = [&](int kb) {
-    const uint8_t* t = tile[kb & 1];
-    const float* s = sc[kb & 1];
-    auto frag = [&](int at) {
-      return join16(*reinterpret_cast<const uint4*>(t + at), *reinterpret_cast<const uint4*>(t + (at ^ 64)));
+      for (int e = 0; e < 4; ++e) acc[i][j][e] += p[e] * (sa[i % 3] * (WROW ? sw[WROW ? j : 0][e] : sw[0][0]));
     };
-    i32x8 wf[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) wf[j] = frag(rw + j * 16 * 128);
-    f32x4 sw[WROW ? TN : 1];
-    if constexpr (WROW) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) sw[j] = *reinterpret_cast<const f32x4*>(s + BM + (wn * TN + j) * 16 + 4 * g);
-    } else {
-      sw[0][0] = s[BM + wn * TN * 16];
-    }
-    // a row of tiles ahead its operand is read, and two tiles behind a product meets its
-    // scales, while the matrix unit works
-    constexpr int LAG = 2;
+    // the next block's scales for column tile j, and a share of the loads
+    auto next = [&](auto J) {
+      constexpr int j = decltype(J)::value;
+      if constexpr (WROW || j == 0) swn[WROW ? j : 0] = scale_w(nxt, j);
+      if constexpr (j == TN - 1) sa[TM % 3] = scale_a(nxt, 0);
+      static_for<0, PT>([&](auto k) {
+        constexpr int q = j * PT + decltype(k)::value;
+        if constexpr (q < P) piece(q);
+        else if constexpr (q == P) piece_scales();
+      });
+    };
+    constexpr int LAG = std::min(2, TN);
     f32x4 p[LAG + 1];
-    static_assert(LAG <= TN, "a row's scale is kept for one row more");
-    float sa[3];
-    i32x8 af[2];
-    af[0] = frag(ra);
-    sa[0] = s[wm * TM * 16 + r] * (WROW ? 1.f : sw[0][0]);
     static_for<0, TM * TN + LAG>([&](auto T) {
       constexpr int t = decltype(T)::value, i = t / TN, j = t % TN, u = t - LAG;
       if constexpr (t < TM * TN) {
         if constexpr (j == 0 && i + 1 < TM) {
-          af[(i + 1) & 1] = frag(ra + (i + 1) * 16 * 128);
-          sa[(i + 1) % 3] = s[(wm * TM + i + 1) * 16 + r] * (WROW ? 1.f : sw[0][0]);
+          frag(af[(i + 1) & 1], buf, ra + (i + 1) * 16 * 128);
+          sa[(i + 1) % 3] = scale_a(buf, i + 1);
         }
-        p[t % (LAG + 1)] = mma8(wf[j], af[i & 1]);
+        if constexpr (t == LAST) {
+          wait_vm<(NS - 2) * (P + 1)>();
+          lds_barrier();
+          frag(af[TM & 1], nxt, ra);
+        }
+        p[t % (LAG + 1)] = mma_block(wf[j], af[i & 1]);
+        if constexpr (t >= LAST) {
+          frag(wf[j], nxt, rw + j * 16 * 128);
+          next(std::integral_constant<int, j>{});
+        }
       }
-      if constexpr (u >= 0) {
-        constexpr int ui = u / TN, uj = u % TN;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[ui][uj][e] += p[u % (LAG + 1)][e] * (WROW ? sa[ui % 3] * sw[WROW ? uj : 0][e] : sa[ui % 3]);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // (as written: the scheduler would gather the products first)
+      __builtin_amdgcn_sched_barrier(0);  // (as written: the next product first, then the sums of one that is done)
+      if constexpr (u >= 0) add(std::integral_constant<int, u / TN>{}, std::integral_constant<int, u % TN>{}, p[u % (LAG + 1)]);
+      __builtin_amdgcn_sched_barrier(0);
     });
+    // (all sums here: sunk behind a branch, they would keep every product alive)
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
+#pragma unroll
+    for (int j = 0; j < (WROW ? TN : 1); ++j) sw[j] = swn[j];
+    af[0] = af[TM & 1];
+    sa[0] = sa[TM % 3];
+    buf = nxt;
+    advance();
   };
-  for (int kb = 0; kb + 1 < a.nb; ++kb) {
-    fetch(kb + 1);
-    block(kb);
-    sv.store(sc[(kb + 1) & 1]);
-    wait_vm<0>();
-    lds_barrier();
+  begin();
+  for (int q = 0; q < NS; ++q) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) piece(p);
+    piece_scales();
+    advance();
   }
-  block(a.nb - 1);
-  // (all sums here: sunk into the stores' branches, they would keep every product alive)
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
-  store_tile<O>(a, acc, m0 + wm * TM * 16, n0 + wn * TN * 16);
-}
-
-// The same with the codes widened to bf16 on their way through registers into LDS, half
-// a block (64 columns) at a time, for a 32-bit y.  128 x 128, four waves, two
-// workgroups a CU.
-template <typename O, bool WROW>
-__global__ __launch_bounds__(256, 2) void k_mm8_wide(Mm8Args a) {
-  constexpr int BM = 128, BN = 128, NTH = 256, TM = 4, TN = 4, P = (BM + BN) * 4 / NTH;
-  __shared__ __align__(16) uint8_t tile[2][(BM + BN) * 128];
-  __shared__ __align__(16) float sc[2][BM + BN];
-  const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), r = l & 15, g = l >> 4, wm = w >> 1, wn = w & 1;
-  int m0, n0;
-  tile_origin<BM, BN>(a, m0, n0);
-  const GBuf ga = gbuf(a.a + m0 * a.as, (uint32_t)((min(BM, a.M - m0) - 1) * a.as + a.K));
-  const GBuf gw = gbuf(a.w + n0 * a.ws, (uint32_t)((min(BN, a.N - n0) - 1) * a.ws + a.K));
-  TileScales<BM, BN, NTH, WROW> sv(a, m0, n0);
-  const int pr = threadIdx.x >> 2, pk = 16 * (threadIdx.x & 3);  // a thread's rows pr + 64 j, columns pk .. + 15
-  uint4 st[P];
-  auto fetch = [&](int h) {  // half block h
-    const int k = 64 * h + pk;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const bool is_a = j < P / 2;
-      const int row = pr + 64 * (is_a ? j : j - P / 2);
-      st[j] = gld16(is_a ? ga : gw, k < a.K ? (uint32_t)(row * (is_a ? a.as : a.ws)) + k : OOB);
-    }
-  };
-  auto put = [&](int b) {
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      uint8_t* row = tile[b] + (pr + 64 * j) * 128;
-      const int c = pk / 8;  // 16-byte pieces c and c + 1 of the row
-      *reinterpret_cast<bf16x8*>(row + 16 * (c ^ (pr & 7))) = widen8(st[j].x, st[j].y);
-      *reinterpret_cast<bf16x8*>(row + 16 * ((c + 1) ^ (pr & 7))) = widen8(st[j].z, st[j].w);
-    }
-  };
-  f32x4 acc[TM][TN], p[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
-  const int ra = (wm * 64 + r) * 128, rw = (BM + wn * 64 + r) * 128;
-  auto half = [&](int b, bool first) {
-    const uint8_t* t = tile[b];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int c = 16 * ((4 * q + g) ^ (r & 7));
-      bf16x8 wf[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) wf[j] = *reinterpret_cast<const bf16x8*>(t + rw + j * 16 * 128 + c);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const bf16x8 af = *reinterpret_cast<const bf16x8*>(t + ra + i * 16 * 128 + c);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) p[i][j] = mma(wf[j], af, first && q == 0 ? zero4() : p[i][j]);
-      }
-    }
-  };
-  fetch(0);
-  sv.load(0);
-  put(0);
-  sv.store(sc[0]);
+  wait_vm<(NS - 1) * (P + 1)>();
   lds_barrier();
-  for (int kb = 0; kb < a.nb; ++kb) {
-    fetch(2 * kb + 1);
-    half(0, true);
-    put(1);
-    lds_barrier();
-    // (behind the last block: columns past the rows' end, zeros that nobody reads)
-    fetch(2 * kb + 2);
-    sv.load(min(kb + 1, a.nb - 1));
-    half(1, false);
-    const float* s = sc[kb & 1];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const float sa = s[wm * 64 + 16 * i + r];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        f32x4 sw;
-        if constexpr (WROW) sw = *reinterpret_cast<const f32x4*>(s + BM + wn * 64 + 16 * j + 4 * g);
-        else sw = f32x4{1.f, 1.f, 1.f, 1.f} * s[BM + wn * 64];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] += p[i][j][e] * (sa * sw[e]);
-      }
-    }
-    put(0);
-    sv.store(sc[(kb + 1) & 1]);
-    lds_barrier();
+  for (int j = 0; j < TN; ++j) {
+    frag(wf[j], 0, rw + j * 16 * 128);
+    if (WROW || j == 0) sw[WROW ? j : 0] = scale_w(0, j);
   }
-  store_tile<O>(a, acc, m0 + wm * 64, n0 + wn * 64);
+  frag(af[0], 0, ra);
+  sa[0] = scale_a(0, 0);
+  for (int b = blockIdx.x; b < tiles; b += gridDim.x) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
+    for (int kb = 0; kb < a.nb; ++kb) block();
+    int m0, n0;
+    tile_origin<BM, BN>(a, b, m0, n0);
+    m0 += wm * TM * 16;
+    n0 += wn * TN * 16;
+    if (m0 + TM * 16 <= a.M && n0 + TN * 16 <= a.N) store_tile<O, TM, TN, true>(a, acc, m0, n0);
+    else store_tile<O, TM, TN, false>(a, acc, m0, n0);
+  }
+  wait_vm<0>();  // (nothing may arrive in LDS behind the workgroup's end)
 }
 
-bool few_rows(const Mm8Args& a) { return a.M <= 64; }
+// up to 32 rows w is read straight into registers (N = K = 4096: 10.5 us a call up to 32
+// rows, 16.3 for 64; tiles of 64: 13.9 us for up to 128 rows)
+bool few_rows(const Mm8Args& a) { return a.M <= 32; }
 
 template <typename O>
 hipError_t mm8_t(const Mm8Args& a, hipStream_t s) {
   if (few_rows(a)) {
     const unsigned nt = (unsigned)((a.N + 15) / 16);
-    const int mt = (a.M + 15) / 16;
-    if (mt == 1) REWY_LAUNCH((k_mm8_rows<O, 1>), dim3(nt), dim3(512), s, a);
-    else if (mt == 2) REWY_LAUNCH((k_mm8_rows<O, 2>), dim3(nt), dim3(512), s, a);
-    else REWY_LAUNCH((k_mm8_rows<O, 4>), dim3(nt), dim3(512), s, a);
+    if (a.M <= 16) REWY_LAUNCH((k_mm8_rows<O, 1>), dim3(nt), dim3(512), s, a);
+    else REWY_LAUNCH((k_mm8_rows<O, 2>), dim3(nt), dim3(512), s, a);
     return hipGetLastError();
   }
-  if constexpr (std::is_same_v<O, float>) {
-    const dim3 grid((unsigned)(((a.M + 127) / 128) * (int64_t)((a.N + 127) / 128)));
-    if (a.wrow) REWY_LAUNCH((k_mm8_wide<O, true>), grid, dim3(256), s, a);
-    else REWY_LAUNCH((k_mm8_wide<O, false>), grid, dim3(256), s, a);
+  constexpr bool WIDE = std::is_same_v<O, float>;
+  // workgroups: as many as the chip holds at once
+  auto tile = [&](auto bm, auto bn, auto wm, auto wn, auto ns, int held) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value,
+                  NS = decltype(ns)::value;
+    const int tiles = (int)(((a.M + BM - 1) / BM) * (int64_t)((a.N + BN - 1) / BN));
+    const dim3 grid(std::min(tiles, held));
+    if (a.wrow) REWY_LAUNCH((k_mm8_tile<O, BM, BN, WM, WN, NS, true, WIDE>), grid, dim3(64 * WM * WN), s, a, tiles);
+    else REWY_LAUNCH((k_mm8_tile<O, BM, BN, WM, WN, NS, false, WIDE>), grid, dim3(64 * WM * WN), s, a, tiles);
     return hipGetLastError();
-  } else {
-    auto tile = [&](auto bm, auto bn, auto wm, auto wn) {
-      constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value;
-      const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * (int64_t)((a.N + BN - 1) / BN)));
-      if (a.wrow) REWY_LAUNCH((k_mm8_tile<O, BM, BN, WM, WN, true>), grid, dim3(64 * WM * WN), s, a);
-      else REWY_LAUNCH((k_mm8_tile<O, BM, BN, WM, WN, false>), grid, dim3(64 * WM * WN), s, a);
-      return hipGetLastError();
-    };
-    std::integral_constant<int, 128> c128;
-    std::integral_constant<int, 256> c256;
-    std::integral_constant<int, 2> c2;
-    std::integral_constant<int, 4> c4;
-    const int64_t big = ((a.M + 255) / 256) * (int64_t)((a.N + 255) / 256);
-    if (big >= 256) return tile(c256, c256, c2, c4);
-    return tile(c128, c128, c2, c2);
-  }
+  };
+  constexpr std::integral_constant<int, 2> c2;
+  constexpr std::integral_constant<int, 4> c4;
+  constexpr std::integral_constant<int, 64> c64;
+  constexpr std::integral_constant<int, 128> c128;
+  constexpr std::integral_constant<int, 256> c256;
+  auto count = [&](int64_t e) { return ((a.M + e - 1) / e) * ((a.N + e - 1) / e); };
+  // Tiles of 64 while they all run at once, two a CU (512 x 4096 x 4096: 19 us, tiles of 128
+  // 26; twice the rows: 35 and 29); tiles of 256 as soon as they fill the CUs (4096 x 4096 x
+  // 4096: 69 us, tiles of 128 80; half the rows: 58 and 42).  Widened operands leave no
+  // registers for the latter.
+  if (count(64) <= 512) return tile(c64, c64, c2, c2, c4, 512);
+  if constexpr (!WIDE)
+    if (count(256) >= 256) return tile(c256, c256, c2, c4, c2, 256);
+  return tile(c128, c128, c2, c2, c2, 512);
 }
 
 }  // namespace
 
-const char* mm8_kernel(const Mm8Args& a, bool f32) { return few_rows(a) ? "k_mm8_rows" : f32 ? "k_mm8_wide" : "k_mm8_tile"; }
+const char* mm8_kernel(const Mm8Args& a) { return few_rows(a) ? "k_mm8_rows" : "k_mm8_tile"; }
 hipError_t launch_mm8(const Mm8Args& a, bool f32, hipStream_t s) { return f32 ? mm8_t<float>(a, s) : mm8_t<bf16>(a, s); }
 
 }  // namespace rewy

@@ -19,7 +19,7 @@ struct Mm8Args {
   void* y;
 };
 // name of the kernel that the sizes take
-const char* mm8_kernel(const Mm8Args& a, bool f32);
+const char* mm8_kernel(const Mm8Args& a);
 hipError_t launch_mm8(const Mm8Args& a, bool f32, hipStream_t s);
 
 }  // namespace rewy

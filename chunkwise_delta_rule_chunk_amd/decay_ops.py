@@ -51,16 +51,18 @@ def decay_attention(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None,
     q [B, T, H, K], k [B, T, G, K], v [B, T, G, V] (slices of longer rows allowed; H / G
     neighbouring heads share a key and value head), log_decay [H] fp32 (at most 0),
     scale (K^-1/2 if None), h0 [N, H, K, V] fp32.  Returns (o, ht or None, ctx); ctx
-    feeds ``decay_attention_backward``.  A GPU cu_seqlens may end before T: o's rows
+    feeds ``decay_attention_backward``, with the states of the workspace where it is not the
+    caller's own.  A GPU cu_seqlens may end before T: o's rows
     behind the last sequence are then not written, or zeros with ``clear``."""
     desc, shape, cu, host = _problem(q, k, v, log_decay, h0, scale, cu_seqlens)
     with _On(q, stream, (q, k, v, log_decay, h0, cu)) as handle:
         o = _new_o(q, v, clear)
         ht = q.new_empty(shape, dtype=torch.float32) if output_final_state else None
-        ws = _workspace(B.rewy_decay_workspace_bytes(desc, 0), q, ws)
+        states, ws = ws is None, _workspace(B.rewy_decay_workspace_bytes(desc, 0), q, ws)
         _check(B.rewy_decay_fwd(desc, _p(q), _p(k), _p(v), _p(log_decay), _p(h0), _p(o), _p(ht), _p(ws),
                                 ws.numel(), handle), "rewy_decay_fwd")
-    return o, ht, dict(desc=desc, q=q, k=k, v=v, log_decay=log_decay, h0=h0, cu=cu, host=host)
+    return o, ht, dict(desc=desc, q=q, k=k, v=v, log_decay=log_decay, h0=h0, cu=cu, host=host,
+                       states=ws if states else None)
 
 
 def decay_attention_recurrent(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None, ht=None, stream=None):
@@ -83,7 +85,7 @@ def decay_attention_backward(ctx, do, dht=None, *, out=None, want_dh0=None, clea
     gives the places of those three (slices of one row, for the joint projection's
     backward); ``clear`` as in the forward, for the gradients that are made here.  dh0 is
     handed out where h0 was given, or as ``want_dh0`` says."""
-    q, k, v, log_decay, h0 = (ctx[n] for n in ("q", "k", "v", "log_decay", "h0"))
+    q, k, v, log_decay, h0, states = (ctx[n] for n in ("q", "k", "v", "log_decay", "h0", "states"))
     if tuple(do.shape) != (*q.shape[:3], v.shape[3]) or do.dtype != q.dtype:
         raise ValueError("do must have o's shape and type")
     f = ctx["desc"]
@@ -95,7 +97,7 @@ def decay_attention_backward(ctx, do, dht=None, *, out=None, want_dh0=None, clea
         for t, ref, name in zip(out, (q, k, v), ("dq", "dk", "dv")):
             if t.shape != ref.shape or t.dtype != ref.dtype:
                 raise ValueError(f"{name} must have the shape and type of its input")
-    with _On(q, stream, (q, k, v, log_decay, h0, ctx["cu"], do, dht, *(out or ()))) as handle:
+    with _On(q, stream, (q, k, v, log_decay, h0, ctx["cu"], do, dht, states, *(out or ()))) as handle:
         if out is None:
             out = tuple(_like_new(t, clear) for t in (q, k, v))
         dq, dk, dv = out
@@ -105,8 +107,9 @@ def decay_attention_backward(ctx, do, dht=None, *, out=None, want_dh0=None, clea
         # (the entry writes it wherever there is a state)
         dh0 = q.new_empty(shape, dtype=torch.float32) if want_dh0 or h0 is not None else None
         ws = _workspace(B.rewy_decay_workspace_bytes(desc, 1), q, ws)
-        _check(B.rewy_decay_bwd(desc, _p(q), _p(k), _p(v), _p(log_decay), _p(h0), _p(do), _p(dht), _p(dq), _p(dk),
-                                _p(dv), _p(dh0), _p(ws), ws.numel(), handle), "rewy_decay_bwd")
+        _check(B.rewy_decay_bwd(desc, _p(q), _p(k), _p(v), _p(log_decay), _p(h0), _p(do), _p(dht), _p(states),
+                                0 if states is None else states.numel(), _p(dq), _p(dk), _p(dv), _p(dh0), _p(ws),
+                                ws.numel(), handle), "rewy_decay_bwd")
     return dict(dq=dq, dk=dk, dv=dv, dh0=dh0 if want_dh0 else None)
 
 
@@ -118,7 +121,7 @@ class DecayAttentionFunction(torch.autograd.Function):
         fctx.set_materialize_grads(False)
         fctx.clear = isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda
         o, ht, ctx = decay_attention(q, k, v, log_decay, scale=scale, h0=h0, cu_seqlens=cu_seqlens, clear=fctx.clear)
-        fctx.save_for_backward(q, k, v, log_decay, h0, ctx["cu"])
+        fctx.save_for_backward(q, k, v, log_decay, h0, ctx["cu"], ctx["states"])
         fctx.host, fctx.scale = ctx["host"], scale
         return o, ht
 
@@ -126,9 +129,10 @@ class DecayAttentionFunction(torch.autograd.Function):
     @once_differentiable
     def backward(fctx, do, dht):
         names = ("q", "k", "v", "log_decay", "h0")
-        saved = fctx.saved_tensors
-        desc, _, cu, host = _saved_problem(_problem(*saved[:5], fctx.scale, saved[5]), fctx.host)
-        ctx = dict(zip(names, saved), desc=desc, cu=cu, host=host)
+        *saved, cu, states = fctx.saved_tensors
+        desc, _, cu, host = _saved_problem(_problem(*saved, fctx.scale, cu), fctx.host)
+        _like(states, saved[0], states.shape, "states", torch.uint8)  # (checked again: _saved_problem)
+        ctx = dict(zip(names, saved), desc=desc, cu=cu, host=host, states=states)
         q, v = ctx["q"], ctx["v"]
         do = q.new_zeros((*q.shape[:3], v.shape[3])) if do is None else do
         g = decay_attention_backward(ctx, _aligned(do), _aligned(dht), clear=fctx.clear)

@@ -414,18 +414,22 @@ typedef struct {
 size_t rewy_decay_workspace_bytes(const rewy_decay_desc *d, int phase);
 
 /* Forward in chunks of 64 tokens, for prompts and training.  h0 and ht may be NULL;
- * o does not depend on whether ht is given.  An infinity or NaN in a token's row
+ * o does not depend on whether ht is given.  The workspace is left with the states that
+ * rewy_decay_bwd takes as `states`.  An infinity or NaN in a token's row
  * reaches that token and the ones behind it, as in the recurrence. */
 int rewy_decay_fwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
                    const float *g, const float *h0, void *o, float *ht,
                    void *workspace, size_t ws_bytes, void *stream);
 
-/* Backward (nothing is kept between the calls).  dht may be NULL; dh0 must be given
- * when h0 is.  dk and dv are summed over the heads that share them.  Outputs are
+/* Backward.  states is the forward's workspace as it left it, for the same descriptor and
+ * inputs (gradients' strides may differ), or NULL: the states are then formed again, with
+ * the same result.  dht may be NULL; dh0 must be given when h0 is.  dk and dv are summed
+ * over the heads that share them.  Outputs are
  * overwritten.  Inputs are finite: an infinity or NaN may reach every gradient of its
  * sequence. */
 int rewy_decay_bwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
                    const float *g, const float *h0, const void *dO, const float *dht,
+                   const void *states, size_t states_bytes,
                    void *dq, void *dk, void *dv, float *dh0,
                    void *workspace, size_t ws_bytes, void *stream);
 

@@ -138,3 +138,19 @@ def test_forward_and_backward(B, T, H, G, K, V, dtype, lens, state, decay, joint
     fp = (300 + 4 * max(each)) * U32
     close(o3, ref["o"], fp * mag["o"], "o, token by token")
     close(ht3, ref["ht"], fp * mag["ht"], "ht, token by token")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_backward_with_and_without_the_forwards_states(dtype):
+    """A caller's own workspace is not kept: the states are formed again, bit by bit the same."""
+    from chunkwise_delta_rule_chunk_amd import binding as B
+    from chunkwise_delta_rule_chunk_amd import ops
+    args, h0, do, dht = inputs(2, 700, 3, 1, 64, 64, dtype, 5, 2)
+    o, ht, ctx = ops.decay_attention(*args, h0=h0)
+    ws = torch.empty(B.rewy_decay_workspace_bytes(ctx["desc"], 0), dtype=torch.uint8, device="cuda")
+    o2, ht2, ctx2 = ops.decay_attention(*args, h0=h0, ws=ws)
+    assert ctx["states"] is not None and ctx2["states"] is None
+    ws.fill_(255)
+    assert torch.equal(o, o2) and torch.equal(ht, ht2)
+    a, b = ops.decay_attention_backward(ctx, do, dht), ops.decay_attention_backward(ctx2, do, dht)
+    assert all(torch.equal(a[k], b[k]) for k in a)

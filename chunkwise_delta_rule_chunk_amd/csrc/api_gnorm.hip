@@ -115,14 +115,9 @@ REWY_API int rewy_gnorm_bwd(const rewy_gnorm_desc* d, const void* x, const void*
                          "group statistics"));
     if (some)
       REWY_TRY(hip_check(traced("k_gnorm_bwd", s, [&] { return launch_gnorm_bwd(a, f32, wf32, s); }), "group norm backward"));
-    const int np = some ? a.nblk : 0;
-    for (int k = 0; k < 2; ++k) {
-      void* out = k ? db : dw;
-      if (out)
-        REWY_TRY(hip_check(traced("k_colsum", s,
-                                  [&] { return launch_colsum(part + (int64_t)k * a.D, np, 2 * (int64_t)a.D, a.D, out, wf32, s); }),
-                           "parameter gradient"));
-    }
-    return REWY_OK;
+    if (!dw && !db) return REWY_OK;
+    const int64_t D = a.D;
+    return hip_check(traced("k_colsum", s, [&] { return launch_colsum(part, some ? a.nblk : 0, 2 * D, 2 * D, dw, wf32, s, db, D); }),
+                     "parameter gradients");
   });
 }

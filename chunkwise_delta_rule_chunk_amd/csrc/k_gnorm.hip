@@ -38,17 +38,28 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
 }
 
 // the activation's value, and its derivative
-__device__ __forceinline__ float act_value(float t, int act) {
-  return act == REWY_ACT_NONE ? t : act == REWY_ACT_SILU ? t * sigmoid_f(t) : sigmoid_f(t);
+template <int ACT>
+__device__ __forceinline__ float act_value(float t) {
+  return ACT == REWY_ACT_NONE ? t : ACT == REWY_ACT_SILU ? t * sigmoid_f(t) : sigmoid_f(t);
 }
-__device__ __forceinline__ float act_both(float t, int act, float& d) {
-  const float s = sigmoid_f(t);
-  if (act == REWY_ACT_SILU) {
-    d = s * (1.f + t * (1.f - s));
-    return t * s;
+template <int ACT>
+__device__ __forceinline__ float act_both(float t, float& d) {
+  if constexpr (ACT == REWY_ACT_NONE) {
+    d = 1.f;
+    return t;
+  } else {
+    const float s = sigmoid_f(t);
+    d = ACT == REWY_ACT_SILU ? s * (1.f + t * (1.f - s)) : s * (1.f - s);
+    return ACT == REWY_ACT_SILU ? t * s : s;
   }
-  d = act == REWY_ACT_NONE ? 1.f : s * (1.f - s);
-  return act == REWY_ACT_NONE ? t : s;
+}
+// f with the activation as a constant (the choice is the same in the whole launch and made
+// outside the loops over elements)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == REWY_ACT_SILU) f(std::integral_constant<int, REWY_ACT_SILU>{});
+  else if (act == REWY_ACT_SIGMOID) f(std::integral_constant<int, REWY_ACT_SIGMOID>{});
+  else f(std::integral_constant<int, REWY_ACT_NONE>{});
 }
 
 // The groups' statistics of a vector of a row, from memory: element e of columns j ..
@@ -101,13 +112,15 @@ __global__ __launch_bounds__(256) void k_gnorm_stats(GnormArgs a, int P) {
       const W* b = a.b ? reinterpret_cast<const W*>(a.b) + j0 : nullptr;
       const float mean = a.center ? a.mean[i] : 0.f, rstd = a.rstd[i];
       float s1 = 0.f, s2 = 0.f;
-      for (int j = p; j < a.L; j += P) {
-        const float xh = ((float)x[j] - mean) * rstd, wv = w ? (float)w[j] : 1.f;
-        float d, act = act_both(z ? (float)z[j] : xh * wv + (b ? (float)b[j] : 0.f), a.act, d);
-        const float u = (float)dy[j] * (z ? act : d) * wv;
-        s1 += u;
-        s2 += u * xh;
-      }
+      with_act(a.act, [&](auto act) {
+        for (int j = p; j < a.L; j += P) {
+          const float xh = ((float)x[j] - mean) * rstd, wv = w ? (float)w[j] : 1.f;
+          float d, v = act_both<decltype(act)::value>(z ? (float)z[j] : xh * wv + (b ? (float)b[j] : 0.f), d);
+          const float u = (float)dy[j] * (z ? v : d) * wv;
+          s1 += u;
+          s2 += u * xh;
+        }
+      });
       s1 = group_sum(s1, P) / (float)a.L;
       s2 = group_sum(s2, P) / (float)a.L;
       if (p == 0) {
@@ -117,6 +130,31 @@ __global__ __launch_bounds__(256) void k_gnorm_stats(GnormArgs a, int P) {
     }
   }
 }
+
+// A thread's NC vectors of a row as they lie in memory (columns past n: zeros).
+template <typename T, int NC>
+struct RawRow {
+  static constexpr int VE = Vec<T>::VE;
+  typename VecN<T, VE>::raw v[NC];
+  __device__ __forceinline__ void load(const T* p, int t, int tpr, int n) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = (c * tpr + t) * VE;
+      if (n - j >= VE) {
+        v[c] = *reinterpret_cast<const typename VecN<T, VE>::type*>(p + j);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[c][e] = j + e < n ? p[j + e] : (T)0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[NC][VE]) const {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f[c][e] = (float)v[c][e];
+  }
+};
 
 template <typename T, typename W, int TPR, int NC, bool GIVEN>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_fwd(GnormArgs a) {
@@ -180,14 +218,29 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_f
     float wv[VE], bv[VE];
     if (w) ldv<W, VE>(wv, w + j, D - j);
     if (b) ldv<W, VE>(bv, b + j, D - j);
+    if (w) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      float n = s[c][e];
-      if (w) n *= wv[e];
-      if (b) n += bv[e];
-      s[c][e] = z ? n * act_value(zv[c][e], a.act) : act_value(n, a.act);
+      for (int e = 0; e < VE; ++e) s[c][e] *= wv[e];
+    }
+    if (b) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s[c][e] += bv[e];
     }
   }
+  with_act(a.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    if (z) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) s[c][e] *= act_value<ACT>(zv[c][e]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) s[c][e] = act_value<ACT>(s[c][e]);
+    }
+  });
   if (a.y) {
     T* o = reinterpret_cast<T*>(a.y) + m * a.ys;
 #pragma unroll
@@ -220,7 +273,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_f
     } else if (c == 0 && t == 0 && on) {
       a.scale[m] = scale;
     }
-    store_codes<VE>(q + j, s[c], scale, a.quant == REWY_QUANT_E4M3, D - j);
+    store_codes_by<VE>(q + j, s[c], ScaleDiv(scale), a.quant == REWY_QUANT_E4M3, D - j);
   }
 }
 
@@ -247,21 +300,27 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
       dw[c][e] = db[c][e] = 0.f;
     }
   }
-  for (int64_t r0 = blockIdx.x * (int64_t)RPB; r0 < a.M; r0 += (int64_t)gridDim.x * RPB) {
+  // rows as they lie in memory, one ahead of its use
+  RawRow<T, NC> nx, nd, nz;
+  auto fetch = [&](int64_t r0) {
     const bool on = r0 + sub < a.M;
     const int64_t m = on ? r0 + sub : 0;
     const int n = on ? D : 0;
-    const T* xp = reinterpret_cast<const T*>(a.x) + m * a.xs;
-    const T* zp = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs : nullptr;
-    const T* dp = reinterpret_cast<const T*>(a.dy) + m * a.ys;
+    nx.load(reinterpret_cast<const T*>(a.x) + m * a.xs, t, TPR, n);
+    nd.load(reinterpret_cast<const T*>(a.dy) + m * a.ys, t, TPR, n);
+    if (a.z) nz.load(reinterpret_cast<const T*>(a.z) + m * a.zs, t, TPR, n);
+  };
+  if constexpr (NC == 1) fetch(blockIdx.x * (int64_t)RPB);
+  for (int64_t r0 = blockIdx.x * (int64_t)RPB; r0 < a.M; r0 += (int64_t)gridDim.x * RPB) {
+    const bool on = r0 + sub < a.M, zp = a.z != nullptr;
+    const int64_t m = on ? r0 + sub : 0;
+    const int n = on ? D : 0;
     float x[NC][VE], dy[NC][VE], zv[NC][VE];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int j = (c * TPR + t) * VE;
-      ldv<T, VE>(x[c], xp + j, n - j);
-      ldv<T, VE>(dy[c], dp + j, n - j);
-      if (zp) ldv<T, VE>(zv[c], zp + j, n - j);
-    }
+    if constexpr (NC > 1) fetch(r0);  // (no registers to hold a second row)
+    nx.get(x);
+    nd.get(dy);
+    if (zp) nz.get(zv);
+    if constexpr (NC == 1) fetch(r0 + (int64_t)gridDim.x * RPB);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
@@ -285,16 +344,32 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
           x[c][e] = j < n ? (x[c][e] - mean) * r : 0.f;
         }
       }
+      // dn (rows and columns past the end: zero), and dz
+      with_act(a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (zp) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            float d;
+            const float v = act_both<ACT>(zv[c][e], d);
+            zv[c][e] = dy[c][e] * (x[c][e] * wv[c][e] + bv[c][e]) * d;
+            dy[c][e] *= v;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            float d;
+            act_both<ACT>(x[c][e] * wv[c][e] + bv[c][e], d);
+            dy[c][e] *= d;
+          }
+        }
+      });
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const float nv = x[c][e] * wv[c][e] + bv[c][e];
-        float d, act = act_both(zp ? zv[c][e] : nv, a.act, d);
-        const float dn = dy[c][e] * (zp ? act : d);  // (rows and columns past the end: zero)
-        zv[c][e] = dy[c][e] * nv * d;
-        dw[c][e] += dn * x[c][e];
-        db[c][e] += dn;
-        dy[c][e] = dn * wv[c][e];
+        dw[c][e] += dy[c][e] * x[c][e];
+        db[c][e] += dy[c][e];
+        dy[c][e] *= wv[c][e];
         s1 += dy[c][e];
         s2 += dy[c][e] * x[c][e];
       }
@@ -346,8 +421,9 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
   }
 }
 
-// The row shape of a length: the fewest threads that hold it in at most 16 elements
-// each (x, z, dy and the parameters and their sums stay in registers).
+// The row shape of a length: one vector a thread as far as a block reaches, which leaves
+// registers for the next row (8192 x 4096 bf16 with a gate, backward: 76 us; with two
+// vectors and no row ahead 132).
 template <typename T, typename F>
 hipError_t gnorm_shape(int D, F&& f) {
   constexpr int VE = Vec<T>::VE;
@@ -356,14 +432,22 @@ hipError_t gnorm_shape(int D, F&& f) {
   if (v <= (TPR) * (NC)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NC>{})
   REWY_GNORM_SHAPE(16, 1);
   REWY_GNORM_SHAPE(64, 1);
-  REWY_GNORM_SHAPE(64, 2);
   REWY_GNORM_SHAPE(256, 1);
-  REWY_GNORM_SHAPE(256, 2);
+  REWY_GNORM_SHAPE(512, 1);
   REWY_GNORM_SHAPE(1024, 1);
   REWY_GNORM_SHAPE(1024, 2);
   if constexpr (VE == 4) REWY_GNORM_SHAPE(1024, 4);
 #undef REWY_GNORM_SHAPE
   return hipErrorInvalidValue;
+}
+// rows side by side in a block, and its threads
+template <typename T>
+void gnorm_block(int D, int& rows, int& threads) {
+  (void)gnorm_shape<T>(D, [&](auto tpr, auto) {
+    rows = std::max(1, NORM_BLOCK / decltype(tpr)::value);
+    threads = std::max(NORM_BLOCK, decltype(tpr)::value);
+    return hipSuccess;
+  });
 }
 
 template <typename T, typename W, bool GIVEN>
@@ -399,13 +483,12 @@ int gnorm_lanes(int L, bool f32) {
   return L % ve == 0 && n <= 64 && (n & (n - 1)) == 0 ? n : 0;
 }
 int gnorm_bwd_blocks(int64_t M, int D, bool f32) {
-  int rpb = 1;
-  auto take = [&](auto tpr, auto) {
-    rpb = std::max(1, NORM_BLOCK / decltype(tpr)::value);
-    return hipSuccess;
-  };
-  (void)(f32 ? gnorm_shape<float>(D, take) : gnorm_shape<bf16>(D, take));
-  return (int)std::min<int64_t>((M + rpb - 1) / rpb, 1024);
+  int rpb = 1, block = NORM_BLOCK;
+  if (f32) gnorm_block<float>(D, rpb, block);
+  else gnorm_block<bf16>(D, rpb, block);
+  // as many as are at work at once, 1024 threads a CU (8192 x 4096 bf16: 76 us with 512
+  // blocks of 512 threads, 106 with half and 87 with twice as many)
+  return (int)std::min<int64_t>((M + rpb - 1) / rpb, 256 * 1024 / block);
 }
 
 hipError_t launch_gnorm_stats(const GnormArgs& a, bool f32, bool wf32, bool bwd, hipStream_t s) {

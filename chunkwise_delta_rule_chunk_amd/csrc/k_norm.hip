@@ -213,7 +213,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_norm_bw
 // Column sums: 16 columns a block, 64 groups of partial rows, joined in LDS (1024
 // rows of 4096: 7.3 us, most of it latency; the rows lie in the last-level cache).
 template <typename O>
-__global__ __launch_bounds__(1024) void k_colsum(const float* part, int np, int64_t ld, int64_t n, O* out) {
+__global__ __launch_bounds__(1024) void k_colsum(const float* part, int np, int64_t ld, int64_t n, O* out, O* out2, int64_t split) {
   __shared__ float buf[64][17];
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
   const int64_t j = blockIdx.x * (int64_t)16 + c;
@@ -228,7 +228,8 @@ __global__ __launch_bounds__(1024) void k_colsum(const float* part, int np, int6
     float s = 0.f;
 #pragma unroll 16
     for (int i = 0; i < 64; ++i) s += buf[i][c];
-    out[j] = (O)s;
+    O* o = j < split ? out + j : out2 + (j - split);
+    if (j < split ? out != nullptr : out2 != nullptr) *o = (O)s;
   }
 }
 
@@ -296,12 +297,15 @@ hipError_t launch_norm_bwd(const NormArgs& a, bool f32, bool wf32, hipStream_t s
   return wf32 ? norm_bwd_t<bf16, float>(a, s) : norm_bwd_t<bf16, bf16>(a, s);
 }
 hipError_t launch_colsum(const float* part, int np, int64_t ld, int64_t n, void* out, bool out_f32,
-                         hipStream_t s) {
+                         hipStream_t s, void* out2, int64_t split) {
   const dim3 grid((unsigned)((n + 15) / 16)), block(1024);
+  if (split < 0) split = n;
   if (out_f32)
-    REWY_LAUNCH((k_colsum<float>), grid, block, s, part, np, ld, n, reinterpret_cast<float*>(out));
+    REWY_LAUNCH((k_colsum<float>), grid, block, s, part, np, ld, n, reinterpret_cast<float*>(out),
+                reinterpret_cast<float*>(out2), split);
   else
-    REWY_LAUNCH((k_colsum<bf16>), grid, block, s, part, np, ld, n, reinterpret_cast<bf16*>(out));
+    REWY_LAUNCH((k_colsum<bf16>), grid, block, s, part, np, ld, n, reinterpret_cast<bf16*>(out),
+                reinterpret_cast<bf16*>(out2), split);
   return hipGetLastError();
 }
 

@@ -99,9 +99,10 @@ struct NormArgs {
 int norm_bwd_blocks(int64_t M, int D, bool f32);
 hipError_t launch_norm_fwd(const NormArgs& a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, bool f32, bool wf32, hipStream_t s);
-// out[j] (bf16 or fp32) = sum over p < np of part[p * ld + j], j < n, in a fixed order
+// out[j] (bf16 or fp32) = sum over p < np of part[p * ld + j], j < n, in a fixed order; with
+// a split, columns from there on go to out2 (either may be nullptr: not written)
 hipError_t launch_colsum(const float* part, int np, int64_t ld, int64_t n, void* out, bool out_f32,
-                         hipStream_t s);
+                         hipStream_t s, void* out2 = nullptr, int64_t split = -1);
 
 // ---- sequences ------------------------------------------------------------------
 // First token of sequence n (n = N: the end of the last one): from the device

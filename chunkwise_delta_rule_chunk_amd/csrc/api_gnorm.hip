@@ -25,6 +25,7 @@ int gnorm_args(const rewy_gnorm_desc* d, GnormArgs& a) {
   a.ng = d->group ? (d->D + d->group - 1) / d->group : 1;
   const bool f32 = d->dtype == REWY_F32;
   a.lanes = gnorm_lanes(a.L, f32);
+  a.rL = 1.f / (float)a.L;
   a.nblk = gnorm_bwd_blocks(a.M, a.D, f32);
   REWY_TRY(check_stride("x_stride", d->x_stride, d->D, a.xs));
   REWY_TRY(check_stride("z_stride", d->z_stride, d->D, a.zs));

@@ -11,6 +11,7 @@ struct GnormArgs {
   int act, center, quant, group, ng;  // ng: scales per row
   float eps;
   int lanes;               // lanes that hold a group, 0: statistics come from memory
+  float rL;                // 1 / L (exact where lanes hold a group)
   int64_t xs, zs, ys, dxs, dzs;  // row strides (ys: y and dy)
   const void* x;
   const void* z;

@@ -157,6 +157,7 @@ REWY_API int rewy_decay_bwd(const rewy_decay_desc* d, const void* q, const void*
     if (dh0 && (dh0 == h0 || dh0 == dht)) return fail(REWY_EINVAL, "dh0 may not be h0 or dht");
     for (const void* out : {dq, dk, dv})
       if (some && (out == q || out == k || out == v || out == dO)) return fail(REWY_EINVAL, "a gradient may not be an input");
+    if (some && (dq == dk || dq == dv || dk == dv)) return fail(REWY_EINVAL, "the gradients need places of their own");
     a.dO = dO; a.dht = dht; a.dq = dq; a.dk = dk; a.dv = dv; a.dh0 = dh0;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     REWY_TRY(decay_states(a, (a.two ? (states ? 2 : 3) : 0) | (dh0 ? 2 : 0), f32, s));

@@ -36,6 +36,7 @@ REWY_API int rewy_e4m3_linear(const rewy_e4m3_desc* d, const void* a, const floa
     REWY_TRY(check_ptr("bias", bias, esize(d->bias_dtype), false));
     REWY_TRY(check_ptr("y", y, esize(d->dtype), some));
     if (!some) return REWY_OK;
+    if (y == a || y == w) return fail(REWY_EINVAL, "y may not be a or w");
     g.a = static_cast<const uint8_t*>(a); g.w = static_cast<const uint8_t*>(w);
     g.sa = a_scale; g.sw = w_scale; g.bias = bias; g.y = y;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -133,6 +133,8 @@ def e4m3_linear(a, a_scale, w, w_scale, bias=None, *, dtype=torch.bfloat16, stre
         raise TypeError(f"dtype must be bf16 or fp32 (got {dtype})")
     N, K = w.shape
     M = a.numel() // K if K else 0
+    if max(M, N, K) >= 1 << 31:
+        raise ValueError("a and w have fewer than 2^31 rows")
     nb = -(-K // 128)
     whole = a_scale.dim() == 2 and a_scale.shape[1] == 1 and nb > 1
     _like(a_scale, a, (M, 1 if whole else nb), "a_scale", torch.float32)

@@ -32,7 +32,10 @@ __device__ __forceinline__ uint4 frag_row_slot_acc(const T* p, int ld, int r0, i
 }
 
 // S = dec S + sum_t B_t (al_t C_t)^T for the wave's CT tiles of 16 columns (B from the
-// tile sb; C's columns in cf, scaled and split into NS pieces; sal in slot order)
+// tile sb; C's columns in cf, scaled and split into NS pieces; sal in slot order).  Two
+// pieces: the products are added onto hi S, one rounding of the state's size for each
+// matrix instruction, which the pieces' 2^-17 allow.  Else they are summed by themselves
+// and lo S joins them.
 template <typename T, int KA, int CT, int NS>
 __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* sb, int ldb, const uint4 (&cf)[CT][CH / KG<T>],
                                              const float* sal, const float (&hi)[CT], float lo) {
@@ -57,7 +60,9 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
   for (int nt = 0; nt < KA / 16; ++nt) {
     f32x4 u[CT];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) u[ct] = zero4();
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[ct][i] = NS == 2 ? hi[ct] * S[ct][nt][i] : 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const uint4 bf = frag_col<T>(sb, ldb, q * KG<T>, 16 * nt);
@@ -69,7 +74,8 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[ct][nt][i] = hi[ct] * S[ct][nt][i] + (lo * S[ct][nt][i] + u[ct][i]);
+      for (int i = 0; i < 4; ++i)
+        S[ct][nt][i] = NS == 2 ? u[ct][i] : hi[ct] * S[ct][nt][i] + (lo * S[ct][nt][i] + u[ct][i]);
   }
 }
 
@@ -216,7 +222,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
   const int t0 = pc.bos + pc.k * a.seg, t1 = min(t0 + a.seg, pc.eos), nch = max(t1 - t0 + CH - 1, 0) / CH;
   if (nch == 0) return;
   const int w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15;
-  const float g = a.g[h], sc1 = REV ? a.scale : 1.f, sc2 = REV ? 1.f : a.scale;
+  const float g = a.g[h];
   TileRegs<T, CH, KA, NTH> ra, rb;
   TileRegs<T, CH, CV, NTH> rc;
   auto chunk = [&](int c) { return REV ? nch - 1 - c : c; };
@@ -268,8 +274,8 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int d = REV ? slot_row<T>(4 * g4 + e) - r : r - slot_row<T>(4 * g4 + e);
-    pd[e] = d >= 0 ? sc1 * pw[max(d, 0)] : 0.f;
-    po[e] = sc1 * pw[16 + d];
+    pd[e] = d >= 0 ? a.scale * pw[max(d, 0)] : 0.f;
+    po[e] = a.scale * pw[16 + d];
   }
 #pragma unroll
   for (int e = 0; e < 3; ++e) p16[e] = pw[16 * e];
@@ -343,7 +349,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
     }
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
-      const float e = pw[REV ? max(len - 1 - 16 * I - r, 0) : 16 * I + r + 1];
+      const float e = REV ? pw[max(len - 1 - 16 * I - r, 0)] : a.scale * pw[16 * I + r + 1];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -376,12 +382,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
 #pragma unroll
       for (int I = 0; I < 4; ++I)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          f32x4 y = Y[ct][I];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] *= sc2;
-          st4<T>(xw + 16 * I * LC + 16 * ct, y);
-        }
+        for (int ct = 0; ct < CT; ++ct) st4<T>(xw + 16 * I * LC + 16 * ct, Y[ct][I]);
     }
     if (c + 1 < nch) {
       constexpr int NS = std::is_same_v<T, bf16> ? 2 : 1;

@@ -85,10 +85,15 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
 // ht (dh0) itself.  Wave w holds 16 columns of the state.
 // (waves a SIMD: two workgroups of 512 threads a CU, or as many as the registers hold)
 template <typename T, int K, int V>
-constexpr int state_waves() { return std::is_same_v<T, float> ? 2 : 4; }
+constexpr int state_waves() { return 2; }
+// 16-column tiles of a wave, threads of a workgroup
+template <typename T, int V>
+constexpr int state_ct() { return V == 128 ? 2 : 1; }
+template <typename T, int V>
+constexpr int state_threads() { return 4 * V / state_ct<T, V>(); }
 template <typename T, int K, int V>
-__global__ __launch_bounds__(4 * V, (state_waves<T, K, V>())) void k_decay_state(DecayArgs a, int dirs) {
-  constexpr int NTH = 4 * V, LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>, NT = K / 16;
+__global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) void k_decay_state(DecayArgs a, int dirs) {
+  constexpr int CT = state_ct<T, V>(), NTH = state_threads<T, V>(), LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>, NT = K / 16;
   __shared__ __align__(16) T sk[CH * LK];
   __shared__ __align__(16) T su[CH * LV];
   __shared__ float pw[CH + 1];                 // powers of the decay
@@ -107,13 +112,15 @@ __global__ __launch_bounds__(4 * V, (state_waves<T, K, V>())) void k_decay_state
   decay_pow2(g, CH, hi, lo);
 
   const int64_t kv = (int64_t)K * V, seqhead = ((int64_t)pc.n * a.H + h) * kv;
-  const int col = 16 * w + (l & 15), row = 4 * (l >> 4);
+  const int col = 16 * CT * w + (l & 15), row = 4 * (l >> 4);
   const float* init = a.two ? nullptr : dir ? a.dht : a.h0;
-  f32x4 S[1][NT];
+  f32x4 S[CT][NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[0][nt][i] = init ? init[seqhead + (16 * nt + row + i) * V + col] : 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[ct][nt][i] = init ? init[seqhead + (16 * nt + row + i) * V + col + 16 * ct] : 0.f;
   TileRegs<T, CH, K, NTH> rk;
   TileRegs<T, CH, V, NTH> ru;
   auto fetch = [&](int c) {
@@ -135,18 +142,24 @@ __global__ __launch_bounds__(4 * V, (state_waves<T, K, V>())) void k_decay_state
     }
     lds_barrier();
     if (c + 1 < nch) fetch(c + 1);
-    uint4 ut[1][NQ];
+    uint4 ut[CT][NQ];
+    float dec[CT];
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) ut[0][q] = frag_col<T>(su, LV, q * KG<T>, 16 * w);
-    const float dec[1] = {hi};
-    decay_update<T, K, 1, SPLIT<T>>(S, sk, LK, ut, sal, dec, lo);
+    for (int ct = 0; ct < CT; ++ct) {
+      dec[ct] = hi;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) ut[ct][q] = frag_col<T>(su, LV, q * KG<T>, 16 * (CT * w + ct));
+    }
+    decay_update<T, K, CT, SPLIT<T>>(S, sk, LK, ut, sal, dec, lo);
     lds_barrier();
   }
   float* o = a.two ? (dir ? a.sr : a.sf) + ((int64_t)slot * a.H + h) * kv : end + seqhead;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[(16 * nt + row + i) * V + col] = S[0][nt][i];
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[(16 * nt + row + i) * V + col + 16 * ct] = S[ct][nt][i];
 }
 
 // In place: the local states of a sequence's segments become the states that enter
@@ -571,7 +584,7 @@ hipError_t launch_decay_state(const DecayArgs& a, bool f32, int dirs, hipStream_
   return decay_kv(a, f32, [&](auto t, auto k, auto v) {
     using T = decltype(t);
     constexpr int K = decltype(k)::value, V = decltype(v)::value;
-    REWY_LAUNCH((k_decay_state<T, K, V>), dim3(a.nslot * a.H, dirs == 3 ? 2 : 1), dim3(4 * V), s, a, dirs);
+    REWY_LAUNCH((k_decay_state<T, K, V>), dim3(a.nslot * a.H, dirs == 3 ? 2 : 1), dim3((state_threads<T, V>())), s, a, dirs);
     return hipGetLastError();
   });
 }

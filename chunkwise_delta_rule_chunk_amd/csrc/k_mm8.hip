@@ -441,11 +441,15 @@ hipError_t mm8_t(const Mm8Args& a, hipStream_t s) {
   auto count = [&](int64_t e) { return ((a.M + e - 1) / e) * ((a.N + e - 1) / e); };
   // Tiles of 64 while they all run at once, two a CU (512 x 4096 x 4096: 19 us, tiles of 128
   // 26; twice the rows: 35 and 29); tiles of 256 as soon as they fill the CUs (4096 x 4096 x
-  // 4096: 69 us, tiles of 128 80; half the rows: 58 and 42).  Widened operands leave no
-  // registers for the latter.
+  // 4096: 69 us, tiles of 128 80; half the rows: 58 and 42).  Between them tiles of 128: where
+  // each has a CU to itself with twice the waves and blocks (1000 x 4096 x 2320: 19.6 us
+  // instead of 22.5; 1000 x 6144, two a CU: 32 instead of 29.7).  Widened operands leave no
+  // registers for tiles of 256, and gain nothing from more waves (32 and 31 us).
   if (count(64) <= 512) return tile(c64, c64, c2, c2, c4, 512);
-  if constexpr (!WIDE)
+  if constexpr (!WIDE) {
     if (count(256) >= 256) return tile(c256, c256, c2, c4, c2, 256);
+    if (count(128) <= 256) return tile(c128, c128, c2, c4, c4, 256);
+  }
   return tile(c128, c128, c2, c2, c2, 512);
 }
 

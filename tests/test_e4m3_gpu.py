@@ -60,7 +60,7 @@ SHAPES = [
     # M, N, K
     (1, 1, 16), (1, 4096, 4096), (3, 17, 144), (16, 128, 128), (17, 130, 2320), (33, 100, 1024), (64, 33, 2048),
     (65, 64, 128), (100, 300, 400), (128, 128, 256), (129, 257, 640), (300, 1000, 1040), (513, 385, 16), (1000, 4354, 2320),
-    (2049, 8192, 272), (4100, 4100, 384),
+    (1000, 3200, 528), (600, 5000, 416), (2049, 8192, 272), (4100, 4100, 384),
 ]
 
 

@@ -96,7 +96,7 @@ __global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) 
   constexpr int CT = state_ct<T, V>(), NTH = state_threads<T, V>(), LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>, NT = K / 16;
   __shared__ __align__(16) T sk[CH * LK];
   __shared__ __align__(16) T su[CH * LV];
-  __shared__ float pw[CH + 1];                 // powers of the decay
+  __shared__ float pw[CH + 1], pl[CH + 1];     // powers of the decay, and what their rounding left
   __shared__ __align__(16) float sal[CH];
   const int dir = dirs == 2 ? 1 : blockIdx.y;
   const int wk = xcd_range(blockIdx.x, a.nslot * a.H), slot = wk / a.H, h = wk - slot * a.H, grp = h / a.per;
@@ -107,9 +107,8 @@ __global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) 
   if (a.two && !end && (dir ? pc.k == 0 : t1 >= pc.eos)) return;  // nobody reads it
   const int nch = max(t1 - t0 + CH - 1, 0) / CH, w = wave_id(), l = lane_id();
   const float g = a.g[h];
-  if (threadIdx.x <= CH) pw[threadIdx.x] = (float)decay_pow(g, threadIdx.x);
-  float hi, lo;
-  decay_pow2(g, CH, hi, lo);
+  if (threadIdx.x <= CH) decay_pow2(g, threadIdx.x, pw[threadIdx.x], pl[threadIdx.x]);
+  float hi = 1.f, lo = 0.f;
 
   const int64_t kv = (int64_t)K * V, seqhead = ((int64_t)pc.n * a.H + h) * kv;
   const int col = 16 * CT * w + (l & 15), row = 4 * (l >> 4);
@@ -137,7 +136,8 @@ __global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) 
     ru.store(su, LV, threadIdx.x);
     if (len != last) {  // (at most twice: the sequence's end)
       if (w == 0) sal[slot_of<T>(l)] = dir ? a.scale * pw[l + 1] : l < len ? pw[len - 1 - l] : 0.f;
-      decay_pow2(g, len, hi, lo);
+      hi = pw[len];
+      lo = pl[len];
       last = len;
     }
     lds_barrier();
@@ -231,7 +231,8 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
   T* sb = sa + CH * LA;
   T* sc = sb + CH * LA;
   T* sm = sc + CH * LC;   // coefficients, columns in slot order
-  float *sal = tab, *pw = tab + CH;  // the update's factors in slot order; the powers 0 .. 64 of the decay
+  // the update's factors in slot order; the powers 0 .. 64 of the decay, and what their rounding left
+  float *sal = tab, *pw = tab + CH, *pl = pw + CH + 1;
   const int t0 = pc.bos + pc.k * a.seg, t1 = min(t0 + a.seg, pc.eos), nch = max(t1 - t0 + CH - 1, 0) / CH;
   if (nch == 0) return;
   const int w = wave_id(), l = lane_id(), g4 = l >> 4, r = l & 15;
@@ -269,17 +270,17 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io,
     }
   if (threadIdx.x <= CH) {
     const int i = threadIdx.x;
-    const float p = (float)decay_pow(g, i);
-    pw[i] = p;
+    decay_pow2(g, i, pw[i], pl[i]);
+    const float p = pw[i];
     if (REV ? i > 0 : i < CH) sal[slot_of<T>(REV ? i - 1 : CH - 1 - i)] = REV ? a.scale * p : p;
   }
   // pairs of blocks right of the diagonal lie inside a contraction of 32: zeros, written once
   for (int i = threadIdx.x; i < CH * LM; i += NTH) sm[i] = (T)0.f;
   if (ODD && threadIdx.x == 0) *sodd = 0;
-  float hi, lo, hl, ll;  // of a chunk, and (REV) of the sequence's last one
-  decay_pow2(g, CH, hi, lo);
-  decay_pow2(g, min(CH, t1 - t0 - (nch - 1) * CH), hl, ll);
   lds_barrier();
+  // of a chunk, and (REV) of the sequence's last one
+  const int nl = min(CH, t1 - t0 - (nch - 1) * CH);
+  const float hi = pw[CH], lo = pl[CH], hl = pw[nl], ll = pl[nl];
   // Coefficients of a lane: block (I, J) holds rows j = 16 J + slot_row(4 g4 + e), columns
   // i = 16 I + r; within a diagonal block lam^|i-j| or zero, 16 (n + 1) tokens away
   // lam^(16 n) lam^(16 +- (i-j)).
@@ -464,7 +465,7 @@ __device__ __forceinline__ void decay_one(const DecayArgs& a, T* lds, float* tab
 template <typename T, int K, int V>
 __global__ __launch_bounds__((walk_threads<T, V>()), (walk_waves<T, K, V>())) void k_decay_fwd(DecayArgs a) {
   __shared__ __align__(16) T lds[walk_lds<T, K, V>()];
-  __shared__ __align__(16) float tab[2 * CH + 1];
+  __shared__ __align__(16) float tab[3 * CH + 2];
   __shared__ int sodd[1 + V];  // last chunk with an infinity or NaN, from 1; each column's first
   decay_one<T, K, V, DECAY_O>(a, lds, tab, sodd, xcd_range(blockIdx.x, a.nslot * a.H));
 }
@@ -474,7 +475,7 @@ __global__ __launch_bounds__((walk_threads<T, V>()), (walk_waves<T, K, V>())) vo
 template <typename T, int K, int V>
 __global__ __launch_bounds__((walk_threads<T, std::max(K, V)>()), (walk_waves<T, K, V>())) void k_decay_bwd(DecayArgs a) {
   __shared__ __align__(16) T lds[std::max(walk_lds<T, K, V>(), walk_lds<T, V, K>())];
-  __shared__ __align__(16) float tab[2 * CH + 1];
+  __shared__ __align__(16) float tab[3 * CH + 2];
   const int wk = xcd_range(blockIdx.x, 3 * a.nslot * a.H), at = wk / 3, what = wk - 3 * at;
   // (waves that a narrow output has no columns for leave; the barriers do without them)
   if (threadIdx.x >= (what == 0 ? walk_threads<T, V>() : walk_threads<T, K>())) return;

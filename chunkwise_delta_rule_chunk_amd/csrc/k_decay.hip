@@ -82,7 +82,12 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
 // Local state of one segment and head: forward, from zero, the sum of its keys and
 // values; reverse, the adjoint that its queries and output adjoints send to the state
 // that enters it.  Where a sequence is one segment the state starts from h0 (dht) and is
-// ht (dh0) itself.  Wave w holds 16 columns of the state.
+// ht (dh0) itself.  Wave w holds 16 CT columns of the state.
+// Three pieces of bf16 (24 bits) a chunk make 48 products where one would make 16, so
+// the matrix unit and the pieces' arithmetic cost what the loads do: 8192 tokens of 32
+// heads, K = V = 128, bf16: 47 us for 134 MB read and 34 written (3.6 TB/s), 45 with all
+// heads on one key and value head, whose rows come from L2.  Two tiles of 16 columns a
+// wave read the key tile half as often (49 us with one, and with spills).
 // (waves a SIMD: two workgroups of 512 threads a CU, or as many as the registers hold)
 template <typename T, int K, int V>
 constexpr int state_waves() { return 2; }
@@ -164,7 +169,9 @@ __global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) 
 
 // In place: the local states of a sequence's segments become the states that enter
 // them (forward; from h0) or the adjoints of the states that leave them (reverse; from
-// dht); what is left at the end is ht or dh0.  Bound by HBM.
+// dht); what is left at the end is ht or dh0.  Bound by memory: 16 segments of 32 heads
+// of 128 x 128 in 13.4 us (5.0 TB/s read and written; loads eight segments ahead change
+// nothing).
 __global__ __launch_bounds__(256) void k_decay_pass(DecayArgs a, int dirs) {
   const int kv = a.K * a.V, n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, dir = dirs == 2 ? 1 : blockIdx.z;
   const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
@@ -221,6 +228,11 @@ struct WalkIo {
 // An infinity or NaN of C would reach rows on the other side of the diagonal through the
 // coefficients' zeros: forward, it leaves the tile and comes back as NaN in its own and
 // later rows (the backward's inputs are finite).
+// What bounds it: with 246 registers a thread two workgroups fit a CU, two waves a SIMD,
+// and a chunk's three barriers stand between a load, LDS, the products and the next tile;
+// matrix unit and vector unit are each at work a quarter of the time, LDS two fifths.
+// Rows that come from L2 alone are 4% faster, so it is not HBM.  Registers for three waves
+// a SIMD are not there (K = 64, V = 128 with spills: 86 us where this takes 57).
 template <typename T, int KA, int CV, int CT, bool REV, bool TS, bool ODD>
 __device__ __forceinline__ void decay_walk(const DecayArgs& a, const WalkIo& io, T* lds, float* tab, int* sodd,
                                            const Piece& pc, int slot, int h) {
@@ -462,6 +474,8 @@ __device__ __forceinline__ void decay_one(const DecayArgs& a, T* lds, float* tab
   decay_walk<T, KA, CV, walk_ct<T, CV>(), REV, TS, WHAT == DECAY_O>(a, io, lds, tab, sodd, pc, slot, h);
 }
 
+// 8192 tokens of 32 heads, K = V = 128, bf16: 65 us (4.1 TB/s); 9000 tokens in 16
+// sequences, 32 heads on 8, K = 64: 57 us; 2 x 1000 tokens of 16 heads, 64, fp32: 14.8 us.
 template <typename T, int K, int V>
 __global__ __launch_bounds__((walk_threads<T, V>()), (walk_waves<T, K, V>())) void k_decay_fwd(DecayArgs a) {
   __shared__ __align__(16) T lds[walk_lds<T, K, V>()];
@@ -471,7 +485,9 @@ __global__ __launch_bounds__((walk_threads<T, V>()), (walk_waves<T, K, V>())) vo
 }
 
 // The three walks of a segment and head are neighbours, so that the rows that they share
-// come from an L2 while they are there.
+// come from an L2 while they are there: 171 us for 8192 tokens of 32 heads, K = V = 128,
+// bf16 (151 in a row of calls), 805 MB past the CUs, 470 of them different (three launches
+// one behind the other 201, when this took 186).  2 x 1000 tokens of 16 heads, 64, fp32: 32.
 template <typename T, int K, int V>
 __global__ __launch_bounds__((walk_threads<T, std::max(K, V)>()), (walk_waves<T, K, V>())) void k_decay_bwd(DecayArgs a) {
   __shared__ __align__(16) T lds[std::max(walk_lds<T, K, V>(), walk_lds<T, V, K>())];
@@ -485,7 +501,9 @@ __global__ __launch_bounds__((walk_threads<T, std::max(K, V)>()), (walk_waves<T,
 }
 
 // dk and dv of a group: the sum over its heads, in order (rows behind the last sequence
-// were not written and stay)
+// were not written and stay).  Bound by memory: 8192 tokens of 32 heads on 8, 128 wide: 54
+// us for 302 MB (5.6 TB/s).  (A walk that took a group's heads one after the other would
+// keep the sum in registers, and leave a quarter of the workgroups.)
 template <typename T>
 __global__ __launch_bounds__(256) void k_decay_sum(DecayArgs a) {
   const int d = blockIdx.y ? a.V : a.K, q = d / 4;
@@ -505,7 +523,8 @@ __global__ __launch_bounds__(256) void k_decay_sum(DecayArgs a) {
 
 // Token by token: one workgroup per sequence and head, the state in registers, four
 // neighbouring columns of K V / 1024 rows a thread.  For one new token it costs the
-// state's bytes, read and written once.
+// state's bytes, read and written once: 64 sequences of 32 heads, K = V = 128: 53.6 us
+// (5.0 TB/s).
 template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void k_decay_recurrent(DecayArgs a) {
   constexpr int CQ = V / 4, RP = 256 / CQ, NR = (K + RP - 1) / RP;  // column quads, rows side by side, rows of a thread

@@ -74,15 +74,16 @@ __device__ __forceinline__ void store4(const Mm8Args& a, int m, int n, const f32
 }
 
 // Few rows: w is read once, straight into the operands' registers.  A workgroup takes
-// 16 rows of w and 16 MT rows of a, its eight waves every eighth block, joined
-// through LDS in their order.
+// 16 rows of w and all of a (at most 16 MT rows), its eight waves every eighth block, joined
+// through LDS in their order.  16 x 4096 x 4096: 7.5 us for 17 MB; a launch, one trip to
+// memory for rows and scales together, and the join, no rate.
 template <typename O, int MT>
 __global__ __launch_bounds__(512) void k_mm8_rows(Mm8Args a) {
   __shared__ float part[8][MT][4][64];
   const int w = wave_id(), l = lane_id(), r = l & 15, g = l >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
+  const int n0 = blockIdx.x * 16;
   const GBuf gw = gbuf(a.w + n0 * a.ws, (uint32_t)((min(16, a.N - n0) - 1) * a.ws + a.K));
-  const GBuf ga = gbuf(a.a + m0 * a.as, (uint32_t)((min(16 * MT, a.M - m0) - 1) * a.as + a.K));
+  const GBuf ga = gbuf(a.a, (uint32_t)((a.M - 1) * a.as + a.K));
   const uint32_t wo = (uint32_t)(r * a.ws) + 32 * g, ao = (uint32_t)(r * a.as) + 32 * g;
   const float* swp[4];
 #pragma unroll
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(512) void k_mm8_rows(Mm8Args a) {
   }
   const float* sap[MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) sap[t] = a.sa + (int64_t)min(m0 + 16 * t + r, a.M - 1) * (a.ablk ? a.nb : 1);
+  for (int t = 0; t < MT; ++t) sap[t] = a.sa + (int64_t)min(16 * t + r, a.M - 1) * (a.ablk ? a.nb : 1);
   f32x4 acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = zero4();
@@ -138,19 +139,16 @@ __global__ __launch_bounds__(512) void k_mm8_rows(Mm8Args a) {
     for (int i = 0; i < 4; ++i) part[w][t][i][l] = acc[t][i];
   __syncthreads();
   // wave t joins tile t
+  const int m = 16 * w + r, n = n0 + 4 * g;
+  if (w >= MT || m >= a.M) return;
+  f32x4 s = zero4();
 #pragma unroll
-  for (int t0 = 0; t0 < MT; t0 += 8) {
-    const int t = t0 + w, m = m0 + 16 * t + r, n = n0 + 4 * g;
-    if (t >= MT || m >= a.M) continue;
-    f32x4 s = zero4();
+  for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s[i] += part[q][t][i][l];
-      if (n + i < a.N) s[i] += ld_bias(a, n + i);
-    }
-    store4<O>(a, m, n, s);
+    for (int q = 0; q < 8; ++q) s[i] += part[q][w][i][l];
+    if (n + i < a.N) s[i] += ld_bias(a, n + i);
   }
+  store4<O>(a, m, n, s);
 }
 
 // Wait until at most N of the wave's vector memory operations are in flight.
@@ -248,7 +246,12 @@ __device__ __forceinline__ void tile_origin(const Mm8Args& a, int b, int& m0, in
 // workgroup takes tiles blockIdx, + gridDim, ... as one run of blocks: the only barrier of a
 // block stands before the last row of its products, and behind it the next block's first
 // operands are read, so that the matrix unit does not wait at a block's start, nor at a
-// tile's.
+// tile's.  8192 x 12288 x 4096 to bf16, tiles of 256: 398 us in a row of calls (2.07
+// PFLOP/s; a library's product without blocks' scales 2.7 at 8192 cubed); 1000 x 4354 x
+// 2320 with a scale for each row of w to fp32, tiles of 128: 45 us (450 TFLOP/s), where 24
+// of the 280 tiles share a CU with another one (256 tiles: 32 us).  Bound by the matrix
+// unit and the sums behind it (a scale's product and a sum for each of four columns a tile
+// and block), in small products by the latency of a block's loads, reads and products.
 template <typename O, int BM, int BN, int WM, int WN, int NS, bool WROW, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_mm8_tile(Mm8Args a, int tiles) {
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16, P = (BM + BN) / 8 / NW;

@@ -68,9 +68,6 @@ REWY_API int rewy_gnorm_fwd(const rewy_gnorm_desc* d, const void* x, const void*
     a.x = x; a.z = z; a.w = w; a.b = b; a.y = y; a.q = q; a.scale = scale; a.mean = mean; a.rstd = rstd;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->dtype == REWY_F32, wf32 = d->w_dtype == REWY_F32;
-    if (!a.lanes)
-      REWY_TRY(hip_check(traced("k_gnorm_stats", s, [&] { return launch_gnorm_stats(a, f32, wf32, false, s); }),
-                         "group statistics"));
     return hip_check(traced("k_gnorm_fwd", s, [&] { return launch_gnorm_fwd(a, f32, wf32, s); }), "group norm");
   });
 }
@@ -112,8 +109,8 @@ REWY_API int rewy_gnorm_bwd(const rewy_gnorm_desc* d, const void* x, const void*
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->dtype == REWY_F32, wf32 = d->w_dtype == REWY_F32;
     if (some && !a.lanes)
-      REWY_TRY(hip_check(traced("k_gnorm_stats", s, [&] { return launch_gnorm_stats(a, f32, wf32, true, s); }),
-                         "group statistics"));
+      REWY_TRY(hip_check(traced("k_gnorm_means", s, [&] { return launch_gnorm_means(a, f32, wf32, s); }),
+                         "group means"));
     if (some)
       REWY_TRY(hip_check(traced("k_gnorm_bwd", s, [&] { return launch_gnorm_bwd(a, f32, wf32, s); }), "group norm backward"));
     if (!dw && !db) return REWY_OK;

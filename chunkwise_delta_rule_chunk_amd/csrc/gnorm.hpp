@@ -10,7 +10,7 @@ struct GnormArgs {
   int D, G, L;             // channels, groups, channels of a group
   int act, center, quant, group, ng;  // ng: scales per row
   float eps;
-  int lanes;               // lanes that hold a group, 0: statistics come from memory
+  int lanes;               // lanes that hold a group, 0: any other group length
   float rL;                // 1 / L (exact where lanes hold a group)
   int64_t xs, zs, ys, dxs, dzs;  // row strides (ys: y and dy)
   const void* x;
@@ -34,7 +34,7 @@ struct GnormArgs {
 // lanes that hold a group of L channels, or 0
 int gnorm_lanes(int L, bool f32);
 int gnorm_bwd_blocks(int64_t M, int D, bool f32);
-hipError_t launch_gnorm_stats(const GnormArgs& a, bool f32, bool wf32, bool bwd, hipStream_t s);
+hipError_t launch_gnorm_means(const GnormArgs& a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_gnorm_fwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_gnorm_bwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s);
 

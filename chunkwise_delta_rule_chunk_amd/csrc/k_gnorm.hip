@@ -12,8 +12,9 @@
 // Memory is all it costs: each input is read once and each output written once.  A
 // row is held by TPR threads in registers (NC vectors of 16 bytes a thread).  Where a
 // group is a power of two of whole vectors, at most a wave, its lanes are neighbours
-// and its statistics a few lane moves; any other group length takes them from a pass
-// of its own (k_gnorm_stats), which reads the row a second time.
+// and its statistics a few lane moves.  Any other group length takes them from the row's
+// copy in LDS, and the backward its two means from a pass of its own (k_gnorm_means), which
+// reads the row a second time.
 #include "gnorm.hpp"
 
 namespace rewy {
@@ -96,55 +97,104 @@ struct GroupOf {
   }
 };
 
-// Statistics of every (row, group), P lanes each (a power of two): mean and rstd, or
-// for the backward the means of u and of u xh.
-template <typename T, typename W, bool BWD>
-__global__ __launch_bounds__(256) void k_gnorm_stats(GnormArgs a, int P) {
+// The backward's means of u and of u xh of every (row, group), P lanes each (a power of
+// two).
+template <typename T, typename W>
+__global__ __launch_bounds__(256) void k_gnorm_means(GnormArgs a, int P) {
   const int p = threadIdx.x & (P - 1), per = 256 / P;
   const int64_t n = a.M * a.G;
   for (int64_t i0 = blockIdx.x * (int64_t)per; i0 < n; i0 += (int64_t)gridDim.x * per) {
     const int64_t i = min(i0 + threadIdx.x / P, n - 1), m = i / a.G;  // (whole waves stay together for the lane moves)
     const int g = (int)(i - m * a.G), j0 = g * a.L;
     const T* x = reinterpret_cast<const T*>(a.x) + m * a.xs + j0;
-    if constexpr (!BWD) {
-      float s = 0.f, mean = 0.f;
-      if (a.center) {
-        for (int j = p; j < a.L; j += P) s += (float)x[j];
-        mean = group_sum(s, P) / (float)a.L;
-        s = 0.f;
-      }
+    const T* z = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs + j0 : nullptr;
+    const T* dy = reinterpret_cast<const T*>(a.dy) + m * a.ys + j0;
+    const W* w = a.w ? reinterpret_cast<const W*>(a.w) + j0 : nullptr;
+    const W* b = a.b ? reinterpret_cast<const W*>(a.b) + j0 : nullptr;
+    const float mean = a.center ? a.mean[i] : 0.f, rstd = a.rstd[i];
+    float s1 = 0.f, s2 = 0.f;
+    with_act(a.act, [&](auto act) {
       for (int j = p; j < a.L; j += P) {
-        const float d = (float)x[j] - mean;
-        s += d * d;
+        const float xh = ((float)x[j] - mean) * rstd, wv = w ? (float)w[j] : 1.f;
+        float d, v = act_both<decltype(act)::value>(z ? (float)z[j] : xh * wv + (b ? (float)b[j] : 0.f), d);
+        const float u = (float)dy[j] * (z ? v : d) * wv;
+        s1 += u;
+        s2 += u * xh;
       }
-      const float rstd = 1.f / sqrtf(group_sum(s, P) / (float)a.L + a.eps);
-      if (p == 0) {
-        if (a.center) a.mean[i] = mean;
-        a.rstd[i] = rstd;
+    });
+    s1 = group_sum(s1, P) / (float)a.L;
+    s2 = group_sum(s2, P) / (float)a.L;
+    if (p == 0) {
+      a.sums[2 * i] = a.center ? s1 : 0.f;
+      a.sums[2 * i + 1] = s2;
+    }
+  }
+}
+
+// Statistics of a row's groups from its copy q in LDS, by TPR threads, to memory: P lanes a
+// group (a power of two: about four channels a lane, or vectors where groups are whole
+// ones), or several waves where there are two for each group (8192 rows of one group of 4096
+// bf16: 49 us, with a wave 69).  m < 0: no row.
+template <typename T, int TPR>
+__device__ __forceinline__ void row_stats(const GnormArgs& a, const T* q, int t, int64_t m) {
+  constexpr int VE = Vec<T>::VE, LIM = TPR < 64 ? TPR : 64, NW = TPR / LIM;
+  __shared__ float part[2][NW];
+  const bool vec = a.L % VE == 0;
+  // f of a lane's share of x, lane p of n
+  auto all = [&](const T* x, int p, int n, auto&& f) {
+    if (vec) {
+      for (int j = p * VE; j < a.L; j += n * VE) {
+        const auto v = *reinterpret_cast<const typename VecN<T, VE>::raw*>(x + j);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f((float)v[e]);
       }
     } else {
-      const T* z = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs + j0 : nullptr;
-      const T* dy = reinterpret_cast<const T*>(a.dy) + m * a.ys + j0;
-      const W* w = a.w ? reinterpret_cast<const W*>(a.w) + j0 : nullptr;
-      const W* b = a.b ? reinterpret_cast<const W*>(a.b) + j0 : nullptr;
-      const float mean = a.center ? a.mean[i] : 0.f, rstd = a.rstd[i];
-      float s1 = 0.f, s2 = 0.f;
-      with_act(a.act, [&](auto act) {
-        for (int j = p; j < a.L; j += P) {
-          const float xh = ((float)x[j] - mean) * rstd, wv = w ? (float)w[j] : 1.f;
-          float d, v = act_both<decltype(act)::value>(z ? (float)z[j] : xh * wv + (b ? (float)b[j] : 0.f), d);
-          const float u = (float)dy[j] * (z ? v : d) * wv;
-          s1 += u;
-          s2 += u * xh;
-        }
-      });
-      s1 = group_sum(s1, P) / (float)a.L;
-      s2 = group_sum(s2, P) / (float)a.L;
-      if (p == 0) {
-        a.sums[2 * i] = a.center ? s1 : 0.f;
-        a.sums[2 * i + 1] = s2;
-      }
+      for (int j = p; j < a.L; j += n) f((float)x[j]);
     }
+  };
+  auto put = [&](int i, float mean, float rstd) {
+    if (m < 0 || i >= a.G) return;
+    if (a.center) a.mean[m * a.G + i] = mean;
+    a.rstd[m * a.G + i] = rstd;
+  };
+  if (NW > 1 && 2 * a.G <= NW) {
+    const int S = 1 << (31 - __builtin_clz(NW / a.G)), w = t / LIM, p = t - w * LIM, i = w / S;
+    const int at = (w & (S - 1)) * LIM + p;
+    const T* x = q + min(i, a.G - 1) * a.L;
+    auto join = [&](float (&buf)[NW], float s) {
+      s = group_sum(s, LIM);
+      if (p == 0) buf[w] = s;
+      __syncthreads();
+      s = 0.f;
+      for (int k = 0; k < S; ++k) s += buf[(w & -S) + k];
+      return s;
+    };
+    float s = 0.f, mean = 0.f;
+    if (a.center) {
+      all(x, at, S * LIM, [&](float v) { s += v; });
+      mean = join(part[0], s) / (float)a.L;
+      s = 0.f;
+    }
+    all(x, at, S * LIM, [&](float v) { s += (v - mean) * (v - mean); });
+    s = join(part[1], s);
+    if (at == 0) put(i, mean, rsqrtf(s / (float)a.L + a.eps));
+    return;
+  }
+  int P = 1;
+  while (P < LIM && 4 * P < a.L) P *= 2;
+  const int p = t & (P - 1), sh = __builtin_ctz(P), per = TPR >> sh;
+  for (int i0 = 0; i0 < a.G; i0 += per) {
+    const int i = i0 + (t >> sh);  // (whole waves stay together for the lane moves)
+    const T* x = q + min(i, a.G - 1) * a.L;
+    float s = 0.f, mean = 0.f;
+    if (a.center) {
+      all(x, p, P, [&](float v) { s += v; });
+      mean = group_sum(s, P) / (float)a.L;
+      s = 0.f;
+    }
+    all(x, p, P, [&](float v) { s += (v - mean) * (v - mean); });
+    const float rstd = rsqrtf(group_sum(s, P) / (float)a.L + a.eps);
+    if (p == 0) put(i, mean, rstd);
   }
 }
 
@@ -180,8 +230,9 @@ struct RawRow {
 // 1 / L, for the row's arithmetic costs nearly what its bytes do (with divisions 51.7 us
 // where this takes 45).  8192 rows of 32 groups of 128 bf16 with a gate: 47.8 us
 // (4.2 TB/s) to bf16, 45.0 us (3.7 TB/s) to e4m3 with a scale for each 128; 16 rows 4.1.
-// 2003 rows of 29 groups of 53 fp32 to int8: 12.2 us, behind 9.2 of k_gnorm_stats.
-template <typename T, typename W, int TPR, int NC, bool GIVEN>
+// 2003 rows of 29 groups of 53 fp32 to int8: 18.4 us (12.2 behind a launch of 9.2 that took
+// the statistics from memory; 8192 x 32 x 100 bf16 to bf16: 55 and 76 us a call).
+template <typename T, typename W, int TPR, int NC, bool ODD>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_fwd(GnormArgs a) {
   constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
   __shared__ uint32_t mbuf[BLOCK / 64];
@@ -195,7 +246,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_f
   const W* w = reinterpret_cast<const W*>(a.w);
   const W* b = reinterpret_cast<const W*>(a.b);
 
-  const int lsh = GIVEN ? 0 : __builtin_ctz(a.lanes);  // (a power of two)
+  const int lsh = ODD ? 0 : __builtin_ctz(a.lanes);  // (a power of two)
   float s[NC][VE], zv[NC][VE], wv[NC][VE], bv[NC][VE];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -215,10 +266,20 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_f
     if (w) ldv<W, VE>(wv[c], w + j, D - j);
     if (b) ldv<W, VE>(bv[c], b + j, D - j);
   }
+  if constexpr (ODD) {
+    constexpr int ROW = TPR * NC * VE;
+    __shared__ __align__(16) T copy[RPB * ROW];
+    T* q = copy + threadIdx.x / TPR * ROW;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) stv<T, VE>(q + (c * TPR + t) * VE, s[c], VE);  // (exact: as they were read)
+    __syncthreads();
+    row_stats<T, TPR>(a, q, t, on ? row : -1);
+    __syncthreads();  // (statistics of the block's own rows, read below)
+  }
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int j = (c * TPR + t) * VE;
-    if constexpr (GIVEN) {
+    if constexpr (ODD) {
       const GroupOf<VE> of(j, a.L, a.G);
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
@@ -483,14 +544,14 @@ void gnorm_block(int D, int& rows, int& threads) {
   });
 }
 
-template <typename T, typename W, bool GIVEN>
+template <typename T, typename W, bool ODD>
 hipError_t gnorm_fwd_t(const GnormArgs& a, hipStream_t s) {
   return gnorm_shape<T>(a.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
     constexpr int BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
     // (a launch takes fewer than 2^32 threads along x)
     const int64_t n = (a.M + RPB - 1) / RPB, gx = std::min<int64_t>(n, 1 << 20);
-    REWY_LAUNCH((k_gnorm_fwd<T, W, TPR, NC, GIVEN>), dim3((unsigned)gx, (unsigned)((n + gx - 1) / gx)), dim3(BLOCK), s, a);
+    REWY_LAUNCH((k_gnorm_fwd<T, W, TPR, NC, ODD>), dim3((unsigned)gx, (unsigned)((n + gx - 1) / gx)), dim3(BLOCK), s, a);
     return hipGetLastError();
   });
 }
@@ -524,16 +585,13 @@ int gnorm_bwd_blocks(int64_t M, int D, bool f32) {
   return (int)std::min<int64_t>((M + rpb - 1) / rpb, 256 * 1024 / block);
 }
 
-hipError_t launch_gnorm_stats(const GnormArgs& a, bool f32, bool wf32, bool bwd, hipStream_t s) {
+hipError_t launch_gnorm_means(const GnormArgs& a, bool f32, bool wf32, hipStream_t s) {
   int P = 1;  // about four channels a lane
   while (P < 64 && 4 * P < a.L) P *= 2;
   const int64_t n = (a.M * a.G * P + 255) / 256;
   const dim3 grid((unsigned)std::min<int64_t>(n, 1 << 20));
   return gnorm_types(f32, wf32, [&](auto t, auto w) {
-    using T = decltype(t);
-    using W = decltype(w);
-    if (bwd) REWY_LAUNCH((k_gnorm_stats<T, W, true>), grid, dim3(256), s, a, P);
-    else REWY_LAUNCH((k_gnorm_stats<T, T, false>), grid, dim3(256), s, a, P);
+    REWY_LAUNCH((k_gnorm_means<decltype(t), decltype(w)>), grid, dim3(256), s, a, P);
     return hipGetLastError();
   });
 }

@@ -524,8 +524,12 @@ hipError_t gnorm_shape(int D, F&& f) {
   const int v = (D + VE - 1) / VE;  // vectors of a row
 #define REWY_GNORM_SHAPE(TPR, NC) \
   if (v <= (TPR) * (NC)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NC>{})
+  REWY_GNORM_SHAPE(4, 1);
+  REWY_GNORM_SHAPE(8, 1);
   REWY_GNORM_SHAPE(16, 1);
+  REWY_GNORM_SHAPE(32, 1);
   REWY_GNORM_SHAPE(64, 1);
+  REWY_GNORM_SHAPE(128, 1);
   REWY_GNORM_SHAPE(256, 1);
   REWY_GNORM_SHAPE(512, 1);
   REWY_GNORM_SHAPE(1024, 1);

@@ -34,10 +34,8 @@ int gnorm_args(const rewy_gnorm_desc* d, GnormArgs& a) {
   return check_stride("dz_stride", d->dz_stride, d->D, a.dzs);
 }
 size_t gnorm_layout(GnormArgs& a, char* ws) {
-  const size_t part = up((size_t)a.nblk * 2 * a.D * 4);
   a.part = reinterpret_cast<float*>(ws);
-  a.sums = reinterpret_cast<float*>(ws + part);
-  return std::max<size_t>(part + (a.lanes ? 0 : up((size_t)a.M * a.G * 8)), ALIGN);
+  return std::max<size_t>(up((size_t)a.nblk * 2 * a.D * 4), ALIGN);
 }
 
 }  // namespace
@@ -108,9 +106,6 @@ REWY_API int rewy_gnorm_bwd(const rewy_gnorm_desc* d, const void* x, const void*
     if (!dw && !db) a.part = nullptr;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->dtype == REWY_F32, wf32 = d->w_dtype == REWY_F32;
-    if (some && !a.lanes)
-      REWY_TRY(hip_check(traced("k_gnorm_means", s, [&] { return launch_gnorm_means(a, f32, wf32, s); }),
-                         "group means"));
     if (some)
       REWY_TRY(hip_check(traced("k_gnorm_bwd", s, [&] { return launch_gnorm_bwd(a, f32, wf32, s); }), "group norm backward"));
     if (!dw && !db) return REWY_OK;

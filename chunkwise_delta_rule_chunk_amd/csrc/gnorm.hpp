@@ -28,13 +28,11 @@ struct GnormArgs {
   void* dw;
   void* db;
   float* part;             // [nblk, 2, D] partial sums of dw and db
-  float* sums;             // [M, G, 2] the backward's means over a group (lanes == 0)
   int nblk;
 };
 // lanes that hold a group of L channels, or 0
 int gnorm_lanes(int L, bool f32);
 int gnorm_bwd_blocks(int64_t M, int D, bool f32);
-hipError_t launch_gnorm_means(const GnormArgs& a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_gnorm_fwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s);
 hipError_t launch_gnorm_bwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s);
 

@@ -13,8 +13,7 @@
 // row is held by TPR threads in registers (NC vectors of 16 bytes a thread).  Where a
 // group is a power of two of whole vectors, at most a wave, its lanes are neighbours
 // and its statistics a few lane moves.  Any other group length takes them from the row's
-// copy in LDS, and the backward its two means from a pass of its own (k_gnorm_means), which
-// reads the row a second time.
+// copy in LDS, and the backward its two means from the row's u and u xh there.
 #include "gnorm.hpp"
 
 namespace rewy {
@@ -97,40 +96,6 @@ struct GroupOf {
   }
 };
 
-// The backward's means of u and of u xh of every (row, group), P lanes each (a power of
-// two).
-template <typename T, typename W>
-__global__ __launch_bounds__(256) void k_gnorm_means(GnormArgs a, int P) {
-  const int p = threadIdx.x & (P - 1), per = 256 / P;
-  const int64_t n = a.M * a.G;
-  for (int64_t i0 = blockIdx.x * (int64_t)per; i0 < n; i0 += (int64_t)gridDim.x * per) {
-    const int64_t i = min(i0 + threadIdx.x / P, n - 1), m = i / a.G;  // (whole waves stay together for the lane moves)
-    const int g = (int)(i - m * a.G), j0 = g * a.L;
-    const T* x = reinterpret_cast<const T*>(a.x) + m * a.xs + j0;
-    const T* z = a.z ? reinterpret_cast<const T*>(a.z) + m * a.zs + j0 : nullptr;
-    const T* dy = reinterpret_cast<const T*>(a.dy) + m * a.ys + j0;
-    const W* w = a.w ? reinterpret_cast<const W*>(a.w) + j0 : nullptr;
-    const W* b = a.b ? reinterpret_cast<const W*>(a.b) + j0 : nullptr;
-    const float mean = a.center ? a.mean[i] : 0.f, rstd = a.rstd[i];
-    float s1 = 0.f, s2 = 0.f;
-    with_act(a.act, [&](auto act) {
-      for (int j = p; j < a.L; j += P) {
-        const float xh = ((float)x[j] - mean) * rstd, wv = w ? (float)w[j] : 1.f;
-        float d, v = act_both<decltype(act)::value>(z ? (float)z[j] : xh * wv + (b ? (float)b[j] : 0.f), d);
-        const float u = (float)dy[j] * (z ? v : d) * wv;
-        s1 += u;
-        s2 += u * xh;
-      }
-    });
-    s1 = group_sum(s1, P) / (float)a.L;
-    s2 = group_sum(s2, P) / (float)a.L;
-    if (p == 0) {
-      a.sums[2 * i] = a.center ? s1 : 0.f;
-      a.sums[2 * i + 1] = s2;
-    }
-  }
-}
-
 // Statistics of a row's groups from its copy q in LDS, by TPR threads, to memory: P lanes a
 // group (a power of two: about four channels a lane, or vectors where groups are whole
 // ones), or several waves where there are two for each group (8192 rows of one group of 4096
@@ -138,7 +103,8 @@ __global__ __launch_bounds__(256) void k_gnorm_means(GnormArgs a, int P) {
 template <typename T, int TPR>
 __device__ __forceinline__ void row_stats(const GnormArgs& a, const T* q, int t, int64_t m) {
   constexpr int VE = Vec<T>::VE, LIM = TPR < 64 ? TPR : 64, NW = TPR / LIM;
-  __shared__ float part[2][NW];
+  __shared__ float parts[TPR < NORM_BLOCK ? NORM_BLOCK / TPR : 1][2][NW];  // (of each row of the block)
+  float(&part)[2][NW] = parts[threadIdx.x / TPR];
   const bool vec = a.L % VE == 0;
   // f of a lane's share of x, lane p of n
   auto all = [&](const T* x, int p, int n, auto&& f) {
@@ -195,6 +161,71 @@ __device__ __forceinline__ void row_stats(const GnormArgs& a, const T* q, int t,
     all(x, p, P, [&](float v) { s += (v - mean) * (v - mean); });
     const float rstd = rsqrtf(group_sum(s, P) / (float)a.L + a.eps);
     if (p == 0) put(i, mean, rstd);
+  }
+}
+
+// The means of u and v over a row's groups, from LDS and to each group's first place there
+// (shared out as in row_stats; a barrier before and after).
+template <int TPR>
+__device__ __forceinline__ void row_means(const GnormArgs& a, float* u, float* v, int t) {
+  constexpr int LIM = TPR < 64 ? TPR : 64, NW = TPR / LIM;
+  __shared__ float parts[TPR < NORM_BLOCK ? NORM_BLOCK / TPR : 1][2][NW];  // (of each row of the block)
+  float(&part)[2][NW] = parts[threadIdx.x / TPR];
+  const bool vec = a.L % 4 == 0;
+  auto sum = [&](int at, int p, int n, float& s1, float& s2) {
+    s1 = s2 = 0.f;
+    if (vec) {
+      for (int j = at + 4 * p; j < at + a.L; j += 4 * n) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(u + j), y = *reinterpret_cast<const f32x4*>(v + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s1 += x[e];
+          s2 += y[e];
+        }
+      }
+    } else {
+      for (int j = at + p; j < at + a.L; j += n) {
+        s1 += u[j];
+        s2 += v[j];
+      }
+    }
+  };
+  float s1, s2;
+  if (NW > 1 && 2 * a.G <= NW) {
+    const int S = 1 << (31 - __builtin_clz(NW / a.G)), w = t / LIM, p = t - w * LIM, i = w / S;
+    sum(min(i, a.G - 1) * a.L, (w & (S - 1)) * LIM + p, S * LIM, s1, s2);
+    s1 = group_sum(s1, LIM);
+    s2 = group_sum(s2, LIM);
+    if (p == 0) {
+      part[0][w] = s1;
+      part[1][w] = s2;
+    }
+    __syncthreads();
+    if (t < a.G) {
+      s1 = s2 = 0.f;
+      for (int k = 0; k < S; ++k) {
+        s1 += part[0][t * S + k];
+        s2 += part[1][t * S + k];
+      }
+      u[t * a.L] = s1 / (float)a.L;
+      v[t * a.L] = s2 / (float)a.L;
+    }
+    return;
+  }
+  int P = 1;
+  while (P < LIM && 4 * P < a.L) P *= 2;
+  const int p = t & (P - 1), sh = __builtin_ctz(P), per = TPR >> sh;
+  for (int i0 = 0; i0 < a.G; i0 += per) {
+    // (whole waves stay together for the lane moves; a lane that has no group takes part
+    // with the last one's and keeps nothing)
+    const int i = i0 + (t >> sh), at = min(i, a.G - 1) * a.L;
+    sum(at, p, P, s1, s2);
+    s1 = group_sum(s1, P);
+    s2 = group_sum(s2, P);
+    if (p == 0 && i < a.G) {
+      u[at] = s1 / (float)a.L;
+      v[at] = s2 / (float)a.L;
+    }
   }
 }
 
@@ -372,10 +403,13 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_f
 // registers; one partial row of each per block goes to the workspace (no atomics: the
 // same sums every time).  With one vector a thread the next row is sent for before this
 // one is counted.  8192 rows of 32 groups of 128 bf16 with a gate: 74.5 us (4.5 TB/s),
-// and 7.4 for the two column sums, whose floor is a launch's latency.
-template <typename T, typename W, int TPR, int NC, bool GIVEN>
+// and 7.4 for the two column sums, whose floor is a launch's latency.  Other group lengths
+// pay for their means in LDS: 65536 x 19 x 53 bf16 351 us a call (with the means by a
+// launch of its own 478), 65536 x 8 x 128 80.
+template <typename T, typename W, int TPR, int NC, bool ODD>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_bwd(GnormArgs a) {
   constexpr int VE = Vec<T>::VE, BLOCK = TPR > NORM_BLOCK ? TPR : NORM_BLOCK, RPB = BLOCK / TPR;
+  constexpr int ROW = TPR * NC * VE;
   __shared__ float wbuf[RPB > 1 ? BLOCK * NC * VE : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, D = a.D;
   const W* w = reinterpret_cast<const W*>(a.w);
@@ -393,7 +427,7 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
       dw[c][e] = db[c][e] = 0.f;
     }
   }
-  const int lsh = GIVEN ? 0 : __builtin_ctz(a.lanes);
+  const int lsh = ODD ? 0 : __builtin_ctz(a.lanes);
   // rows as they lie in memory, one ahead of its use
   RawRow<T, NC> nx, nd, nz;
   auto fetch = [&](int64_t r0) {
@@ -415,26 +449,24 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
     nd.get(dy);
     if (zp) nz.get(zv);
     if constexpr (NC == 1) fetch(r0 + (int64_t)gridDim.x * RPB);
+    float rs[NC][VE];  // (one value a vector unless ODD)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = (c * TPR + t) * VE;
-      float rs[VE], c1[VE], c2[VE];
-      if constexpr (GIVEN) {
+      if constexpr (ODD) {
         const GroupOf<VE> of(j, a.L, a.G);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const int64_t i = m * a.G + of.g[e];
-          rs[e] = a.rstd[i];
-          x[c][e] = j + e < n ? (x[c][e] - (a.center ? a.mean[i] : 0.f)) * rs[e] : 0.f;
-          c1[e] = a.sums[2 * i];
-          c2[e] = a.sums[2 * i + 1];
+          rs[c][e] = a.rstd[i];
+          x[c][e] = j + e < n ? (x[c][e] - (a.center ? a.mean[i] : 0.f)) * rs[c][e] : 0.f;
         }
       } else {
         const int64_t i = m * a.G + (j < n ? (c * TPR + t) >> lsh : 0);
         const float r = a.rstd[i], mean = a.center ? a.mean[i] : 0.f;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          rs[e] = r;
+          rs[c][e] = r;
           x[c][e] = j < n ? (x[c][e] - mean) * r : 0.f;
         }
       }
@@ -458,26 +490,53 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
           }
         }
       });
-      float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         dw[c][e] += dy[c][e] * x[c][e];
         db[c][e] += dy[c][e];
         dy[c][e] *= wv[c][e];
-        s1 += dy[c][e];
-        s2 += dy[c][e] * x[c][e];
       }
-      if constexpr (!GIVEN) {
+    }
+    float *mu = nullptr, *mv = nullptr;
+    if constexpr (ODD) {
+      __shared__ __align__(16) float us[RPB * ROW], vs[RPB * ROW];
+      mu = us + sub * ROW;
+      mv = vs + sub * ROW;
+      __syncthreads();  // (the row before has been read)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          mu[(c * TPR + t) * VE + e] = dy[c][e];
+          mv[(c * TPR + t) * VE + e] = dy[c][e] * x[c][e];
+        }
+      }
+      __syncthreads();
+      row_means<TPR>(a, mu, mv, t);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = (c * TPR + t) * VE;
+      if constexpr (ODD) {
+        const GroupOf<VE> of(j, a.L, a.G);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int at = of.g[e] * a.L;
+          dy[c][e] = rs[c][e] * (dy[c][e] - (a.center ? mu[at] : 0.f) - x[c][e] * mv[at]);
+        }
+      } else {
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          s1 += dy[c][e];
+          s2 += dy[c][e] * x[c][e];
+        }
         s1 = a.center ? group_sum(s1, a.lanes) * a.rL : 0.f;
         s2 = group_sum(s2, a.lanes) * a.rL;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          c1[e] = s1;
-          c2[e] = s2;
-        }
+        for (int e = 0; e < VE; ++e) dy[c][e] = rs[c][e] * (dy[c][e] - s1 - x[c][e] * s2);
       }
-#pragma unroll
-      for (int e = 0; e < VE; ++e) dy[c][e] = rs[e] * (dy[c][e] - c1[e] - x[c][e] * c2[e]);
       stv<T, VE>(reinterpret_cast<T*>(a.dx) + m * a.dxs + j, dy[c], n - j);
       if (zp) stv<T, VE>(reinterpret_cast<T*>(a.dz) + m * a.dzs + j, zv[c], n - j);
     }
@@ -517,7 +576,9 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
 
 // The row shape of a length: one vector a thread as far as a block reaches, which leaves
 // registers for the next row (8192 x 4096 bf16 with a gate, backward: 76 us; with two
-// vectors and no row ahead 132).
+// vectors and no row ahead 132), and as many threads as vectors to the next power of two:
+// threads without a vector cost what the others do (262144 x 256 bf16 by 32 threads a row 53
+// us, by 64 87; 1048576 x 32 by 4 threads 25, by 16 75).
 template <typename T, typename F>
 hipError_t gnorm_shape(int D, F&& f) {
   constexpr int VE = Vec<T>::VE;
@@ -559,11 +620,11 @@ hipError_t gnorm_fwd_t(const GnormArgs& a, hipStream_t s) {
     return hipGetLastError();
   });
 }
-template <typename T, typename W, bool GIVEN>
+template <typename T, typename W, bool ODD>
 hipError_t gnorm_bwd_t(const GnormArgs& a, hipStream_t s) {
   return gnorm_shape<T>(a.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    REWY_LAUNCH((k_gnorm_bwd<T, W, TPR, NC, GIVEN>), dim3(a.nblk), dim3(TPR > NORM_BLOCK ? TPR : NORM_BLOCK), s, a);
+    REWY_LAUNCH((k_gnorm_bwd<T, W, TPR, NC, ODD>), dim3(a.nblk), dim3(TPR > NORM_BLOCK ? TPR : NORM_BLOCK), s, a);
     return hipGetLastError();
   });
 }
@@ -589,16 +650,6 @@ int gnorm_bwd_blocks(int64_t M, int D, bool f32) {
   return (int)std::min<int64_t>((M + rpb - 1) / rpb, 256 * 1024 / block);
 }
 
-hipError_t launch_gnorm_means(const GnormArgs& a, bool f32, bool wf32, hipStream_t s) {
-  int P = 1;  // about four channels a lane
-  while (P < 64 && 4 * P < a.L) P *= 2;
-  const int64_t n = (a.M * a.G * P + 255) / 256;
-  const dim3 grid((unsigned)std::min<int64_t>(n, 1 << 20));
-  return gnorm_types(f32, wf32, [&](auto t, auto w) {
-    REWY_LAUNCH((k_gnorm_means<decltype(t), decltype(w)>), grid, dim3(256), s, a, P);
-    return hipGetLastError();
-  });
-}
 hipError_t launch_gnorm_fwd(const GnormArgs& a, bool f32, bool wf32, hipStream_t s) {
   return gnorm_types(f32, wf32, [&](auto t, auto w) {
     using T = decltype(t);

@@ -110,6 +110,8 @@ SHAPES = [
     (1, 1, 1), (3, 2, 8), (5, 32, 4), (7, 3, 16), (33, 4, 32), (9, 5, 64), (257, 2, 128), (6, 32, 128), (4, 16, 256),
     (3, 7, 512), (5, 29, 53), (2, 1, 1537), (3, 1, 16384), (2, 16384, 1), (4, 3, 600), (70000, 1, 8), (2, 5, 1000),
     (1500, 3, 24), (3, 2, 1030), (2, 3, 5000), (4, 2, 4096), (5, 1, 5),
+    # several waves a row and several rows a block, one group
+    (7, 1, 1000), (6, 1, 500), (9, 1, 260), (5, 3, 300), (130, 1, 200), (3, 5, 40),
 ]
 
 

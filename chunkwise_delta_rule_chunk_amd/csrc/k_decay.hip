@@ -170,8 +170,8 @@ __global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) 
 // In place: the local states of a sequence's segments become the states that enter
 // them (forward; from h0) or the adjoints of the states that leave them (reverse; from
 // dht); what is left at the end is ht or dh0.  Bound by memory: 16 segments of 32 heads
-// of 128 x 128 in 13.4 us (5.0 TB/s read and written; loads eight segments ahead change
-// nothing).
+// of 128 x 128 in 12.3 us (5.5 TB/s read and written), 2 x 8 of 16 heads of 64 x 64 in 4.8
+// (one segment's load at a time, behind the powers: 13.4 and 6.3).
 __global__ __launch_bounds__(256) void k_decay_pass(DecayArgs a, int dirs) {
   const int kv = a.K * a.V, n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, dir = dirs == 2 ? 1 : blockIdx.z;
   const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
@@ -184,23 +184,41 @@ __global__ __launch_bounds__(256) void k_decay_pass(DecayArgs a, int dirs) {
   float* end = dir ? a.dh0 : a.ht;
   const int64_t at = ((int64_t)n * a.H + h) * kv + e;
   const float g = a.g[h];
+  constexpr int U = 8;  // segments sent for at once
+  auto place = [&](int i) {
+    return reinterpret_cast<f32x4*>(st + ((int64_t)(base + (dir ? ns - 1 - i : i)) * a.H + h) * kv + e);
+  };
+  // (the last local state is there only if its end is handed out)
+  const int nl = end ? ns : ns - 1;
+  f32x4 loc[U];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < nl) loc[u] = *place(i0 + u);
+  };
+  fetch(0);
+  f32x4 S = zero4();
+  if (init) S = *reinterpret_cast<const f32x4*>(init + at);
   float hi, lo, hl, ll;  // a whole segment's decay, and the last one's
   decay_pow2(g, a.seg, hi, lo);
   decay_pow2(g, eos - bos - (ns - 1) * a.seg, hl, ll);
-  f32x4 S = zero4();
-  if (init) S = *reinterpret_cast<const f32x4*>(init + at);
-  for (int i = 0; i < ns; ++i) {
-    const int k = dir ? ns - 1 - i : i;
-    f32x4* p = reinterpret_cast<f32x4*>(st + ((int64_t)(base + k) * a.H + h) * kv + e);
-    if (i + 1 < ns || end) {
-      const f32x4 loc = *p;
-      const float dh = k + 1 < ns ? hi : hl, dl = k + 1 < ns ? lo : ll;
-      *p = S;
+  for (int i0 = 0; i0 < ns; i0 += U) {
+    f32x4 in[U];  // the states that enter
 #pragma unroll
-      for (int j = 0; j < 4; ++j) S[j] = dh * S[j] + (dl * S[j] + loc[j]);
-    } else {
-      *p = S;
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u;
+      in[u] = S;
+      if (i < nl) {
+        const bool last = dir ? i == 0 : i + 1 == ns;
+        const float dh = last ? hl : hi, dl = last ? ll : lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[j] = dh * S[j] + (dl * S[j] + loc[u][j]);
+      }
     }
+    fetch(i0 + U);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < ns) *place(i0 + u) = in[u];
   }
   if (end) *reinterpret_cast<f32x4*>(end + at) = S;
 }

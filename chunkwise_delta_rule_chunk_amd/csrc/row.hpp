@@ -22,6 +22,10 @@ __device__ __forceinline__ uint32_t lanes_max_n(uint32_t x, int lanes) {
   return x;
 }
 
+// first wave of the thread's row, where a block holds several rows of several waves
+template <int TPR>
+__device__ __forceinline__ int row_wave() { return TPR < NORM_BLOCK ? threadIdx.x / TPR * (TPR / 64) : 0; }
+
 // Sum (and maximum) over the TPR threads of a row; `buf` holds one word per
 // wave of the block and is used once per call site.
 template <int TPR>
@@ -34,7 +38,7 @@ __device__ __forceinline__ float row_sum(float x, float* buf) {
     __syncthreads();
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) t += buf[i];
+    for (int i = 0; i < TPR / 64; ++i) t += buf[row_wave<TPR>() + i];
     return t;
   }
 }
@@ -48,7 +52,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* buf) {
     __syncthreads();
     uint32_t t = 0;
 #pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) t = max(t, buf[i]);
+    for (int i = 0; i < TPR / 64; ++i) t = max(t, buf[row_wave<TPR>() + i]);
     return t;
   }
 }

@@ -164,7 +164,9 @@ def test_backward_is_the_forwards_derivative(L, act, gate):
 
 @pytest.mark.parametrize("quant", ["e4m3", "int8"])
 @pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
-@pytest.mark.parametrize("M,G,L,dtype", [(5, 4, 128, "bf16"), (3, 7, 11, "fp32"), (2, 3, 500, "bf16"), (4, 64, 4, "fp32")])
+@pytest.mark.parametrize("M,G,L,dtype", [(5, 4, 128, "bf16"), (3, 7, 11, "fp32"), (2, 3, 500, "bf16"), (4, 64, 4, "fp32"),
+                                         (7, 8, 128, "bf16"), (5, 4, 200, "bf16"), (6, 3, 150, "fp32"), (67, 1, 32, "bf16"),
+                                         (9, 1, 60, "bf16"), (11, 2, 100, "bf16"), (3, 1, 5000, "fp32")])
 def test_codes(M, G, L, dtype, group, quant):
     """Scales from the unrounded y; codes are y over the stored scale, rounded once."""
     from chunkwise_delta_rule_chunk_amd import ops

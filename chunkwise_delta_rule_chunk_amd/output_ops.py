@@ -144,9 +144,8 @@ def e4m3_linear(a, a_scale, w, w_scale, bias=None, *, dtype=torch.bfloat16, stre
     if bias is not None:
         bdt = _dtype(bias, "bias")
         _like(bias, a, (N,), "bias")
-    if a_scale.requires_grad or w_scale.requires_grad or (bias is not None and bias.requires_grad):
-        if torch.is_grad_enabled():
-            raise ValueError("e4m3_linear has no gradient: detach its inputs or run it under torch.no_grad()")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (a, a_scale, w, w_scale, bias)):
+        raise ValueError("e4m3_linear has no gradient: detach its inputs or run it under torch.no_grad()")
     desc = B.RewyE4m3Desc(M, N, K, 0 if whole else 128, 1 if rows else 128, _DT[dtype], bdt, _row_stride(a, "a", 1),
                           _row_stride(w, "w", 1), 0)
     with _On(a, stream, (a, a_scale, w, w_scale, bias)) as handle:

@@ -11,6 +11,8 @@ REWY_API int rewy_e4m3_linear(const rewy_e4m3_desc* d, const void* a, const floa
     if (!d) return fail(REWY_EINVAL, "desc is NULL");
     if (d->M < 0 || d->N <= 0 || d->K <= 0) return fail(REWY_EINVAL, "bad shape M=%d N=%d K=%d", d->M, d->N, d->K);
     if (d->K % 16) return fail(REWY_EUNSUPPORTED, "K=%d is not a multiple of 16", d->K);
+    // (a tile's last rows, up to 512 behind M, are counted in 32 bits)
+    if (d->M > INT32_MAX - 1023) return fail(REWY_EUNSUPPORTED, "M=%d is too large", d->M);
     if (d->K > 1 << 20 || d->N > 1 << 24) return fail(REWY_EUNSUPPORTED, "N=%d or K=%d is too large", d->N, d->K);
     if (d->a_block != 0 && d->a_block != 128) return fail(REWY_EINVAL, "bad a_block %d (0 or 128)", d->a_block);
     if (d->w_rows != 1 && d->w_rows != 128) return fail(REWY_EINVAL, "bad w_rows %d (1 or 128)", d->w_rows);
@@ -26,7 +28,7 @@ REWY_API int rewy_e4m3_linear(const rewy_e4m3_desc* d, const void* a, const floa
     if (g.as % 16 || g.ws % 16) return fail(REWY_EINVAL, "a_stride and w_stride are multiples of 16 bytes");
     if (g.as > 1 << 22 || g.ws > 1 << 22) return fail(REWY_EUNSUPPORTED, "a_stride or w_stride exceeds 2^22 bytes");
     // (a launch takes fewer than 2^32 threads: tiles of 128 by 128 of 256 threads)
-    if (((d->M + 127) / 128) * (int64_t)((d->N + 127) / 128) >= 1 << 24)
+    if (((int64_t)d->M + 127) / 128 * (((int64_t)d->N + 127) / 128) >= 1 << 24)
       return fail(REWY_EUNSUPPORTED, "M=%d by N=%d is too large", d->M, d->N);
     const bool some = d->M > 0, f32 = d->dtype == REWY_F32;
     REWY_TRY(check_ptr("a", a, 16, some));

@@ -487,7 +487,7 @@ int rewy_gnorm_bwd(const rewy_gnorm_desc *d, const void *x, const void *z, const
  * are fp32, y is rounded once.  A NaN code or scale reaches the outputs of its row of a
  * or w (and, for a scale that 128 rows of w share, of those rows). */
 typedef struct {
-    int32_t M;                      /* rows of a, >= 0 */
+    int32_t M;                      /* rows of a, 0 .. 2^31 - 1024 */
     int32_t N, K;                   /* rows of w; columns, a multiple of 16 */
     int32_t a_block;                /* columns per scale of a: 128, or 0 = the whole row */
     int32_t w_rows;                 /* rows per scale of w: 128, or 1 */

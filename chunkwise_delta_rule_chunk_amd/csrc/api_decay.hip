@@ -93,6 +93,24 @@ int decay_inputs(const void* q, const void* k, const void* v, const float* g, co
   return REWY_OK;
 }
 
+// Places of tokens' rows and of the sequences' states
+Place rows_of(const char* name, const void* p, const DecayArgs& a, int64_t row, int64_t stride, bool f32) {
+  const int64_t e = f32 ? 4 : 2;
+  return {name, p, a.seq.total, row * e, stride * e};
+}
+Place states_of(const char* name, const void* p, const DecayArgs& a) {
+  return whole(name, p, (int64_t)a.seq.N * a.H * a.K * a.V * 4);
+}
+// a forward's outputs are apart from each other and from its inputs (but ht may be h0
+// itself where `in_place`)
+int decay_apart(const DecayArgs& a, bool f32, bool in_place) {
+  const int64_t H = a.H, G = a.G, K = a.K, V = a.V;
+  return check_apart({rows_of("o", a.o, a, H * V, a.os, f32), states_of("ht", a.ht, a)},
+                     {rows_of("q", a.q, a, H * K, a.qs, f32), rows_of("k", a.k, a, G * K, a.ks, f32),
+                      rows_of("v", a.v, a, G * V, a.vs, f32), whole("g", a.g, H * 4),
+                      states_of("h0", in_place && a.ht == a.h0 ? nullptr : a.h0, a)});
+}
+
 // The states of the segments that the walks need, and those that are handed out.
 int decay_states(const DecayArgs& a, int dirs, bool f32, hipStream_t s) {
   if (!dirs) return REWY_OK;
@@ -129,6 +147,7 @@ REWY_API int rewy_decay_fwd(const rewy_decay_desc* d, const void* q, const void*
     if (ht && ht == h0) return fail(REWY_EINVAL, "ht may not be h0");
     if (some && (o == q || o == k || o == v)) return fail(REWY_EINVAL, "o may not be q, k or v");
     a.o = o; a.ht = ht;
+    REWY_TRY(decay_apart(a, f32, false));
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     REWY_TRY(decay_states(a, a.two || ht ? 1 : 0, f32, s));
     if (!some) return REWY_OK;
@@ -159,6 +178,12 @@ REWY_API int rewy_decay_bwd(const rewy_decay_desc* d, const void* q, const void*
       if (some && (out == q || out == k || out == v || out == dO)) return fail(REWY_EINVAL, "a gradient may not be an input");
     if (some && (dq == dk || dq == dv || dk == dv)) return fail(REWY_EINVAL, "the gradients need places of their own");
     a.dO = dO; a.dht = dht; a.dq = dq; a.dk = dk; a.dv = dv; a.dh0 = dh0;
+    const int64_t H = a.H, G = a.G, K = a.K, V = a.V;
+    REWY_TRY(check_apart({rows_of("dq", dq, a, H * K, a.dqs, f32), rows_of("dk", dk, a, G * K, a.dks, f32),
+                          rows_of("dv", dv, a, G * V, a.dvs, f32), states_of("dh0", dh0, a)},
+                         {rows_of("q", q, a, H * K, a.qs, f32), rows_of("k", k, a, G * K, a.ks, f32),
+                          rows_of("v", v, a, G * V, a.vs, f32), rows_of("dO", dO, a, H * V, a.os, f32),
+                          whole("g", g, H * 4), states_of("h0", h0, a), states_of("dht", dht, a)}));
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     REWY_TRY(decay_states(a, (a.two ? (states ? 2 : 3) : 0) | (dh0 ? 2 : 0), f32, s));
     if (!some) return REWY_OK;
@@ -179,6 +204,7 @@ REWY_API int rewy_decay_recurrent_fwd(const rewy_decay_desc* d, const void* q, c
     if (a.seq.total == 0 && !ht) return REWY_OK;
     if (a.seq.total > 0 && (o == q || o == k || o == v)) return fail(REWY_EINVAL, "o may not be q, k or v");
     a.o = o; a.ht = ht;
+    REWY_TRY(decay_apart(a, d->dtype == REWY_F32, true));
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     return hip_check(traced("k_decay_recurrent", s, [&] { return launch_decay_recurrent(a, d->dtype == REWY_F32, s); }),
                      "recurrent attention");

@@ -2,6 +2,8 @@
 // token mixer.
 #pragma once
 #include <exception>
+#include <initializer_list>
+#include <utility>
 
 #include "host.hpp"
 #include "layer.hpp"
@@ -49,6 +51,52 @@ inline int check_stride(const char* name, int64_t given, int64_t len, int64_t& o
 inline int check_workspace(const void* ws, size_t have, size_t need) {
   if (need && (!ws || !aligned(ws, ALIGN) || have < need))
     return fail(REWY_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, have);
+  return REWY_OK;
+}
+
+// ---- places ----------------------------------------------------------------------
+// Bytes of a tensor: `rows` rows of `row` bytes, `stride` bytes from one to the next.
+struct Place {
+  const char* name;
+  const void* p;
+  int64_t rows, row, stride;
+};
+inline Place whole(const char* name, const void* p, int64_t bytes) { return {name, p, 1, bytes, bytes}; }
+
+// Two tensors have a byte in common.  Rows may lie between each other's (slices of one
+// longer row), so what counts is the rows and not the ranges from first to last byte.
+inline bool meet(Place a, Place b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.row <= 0 || b.row <= 0) return false;
+  for (Place* t : {&a, &b})
+    if (t->rows == 1 || t->row == t->stride) *t = whole(t->name, t->p, (t->rows - 1) * t->stride + t->row);
+  if (a.rows > b.rows) std::swap(a, b);
+  const int64_t d = (int64_t)((uintptr_t)a.p - (uintptr_t)b.p), s = b.stride;  // a's first byte from b's
+  if (d >= (b.rows - 1) * s + b.row || -d >= (a.rows - 1) * a.stride + a.row) return false;
+  // first row of b that ends behind x
+  auto first = [&](int64_t x) {
+    const int64_t y = x - b.row, q = y / s - (y % s < 0);
+    return q + 1;
+  };
+  if (a.rows > 1 && a.stride == s) {
+    // row i of a meets row i + k of b for the same k everywhere
+    for (int64_t k = first(d); k * s < d + a.row; ++k)
+      if (std::max<int64_t>(0, -k) < std::min(a.rows, b.rows - k)) return true;
+    return false;
+  }
+  for (int64_t i = 0; i < a.rows; ++i) {
+    const int64_t x = d + i * a.stride, j = std::max<int64_t>(0, first(x));
+    if (j < b.rows && j * s < x + a.row) return true;
+  }
+  return false;
+}
+// No output shares a byte with an input or another output.
+inline int check_apart(std::initializer_list<Place> outs, std::initializer_list<Place> ins) {
+  for (const Place* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Place& i : ins)
+      if (meet(*o, i)) return fail(REWY_EINVAL, "%s overlaps %s", o->name, i.name);
+    for (const Place* p = outs.begin(); p != o; ++p)
+      if (meet(*o, *p)) return fail(REWY_EINVAL, "%s overlaps %s", o->name, p->name);
+  }
   return REWY_OK;
 }
 

@@ -38,6 +38,16 @@ size_t gnorm_layout(GnormArgs& a, char* ws) {
   return std::max<size_t>(up((size_t)a.nblk * 2 * a.D * 4), ALIGN);
 }
 
+// M rows of a tensor of the norm's type
+Place rows_of(const char* name, const void* p, const rewy_gnorm_desc* d, int64_t stride) {
+  const int64_t e = (int64_t)esize(d->dtype);
+  return {name, p, d->M, d->D * e, stride * e};
+}
+Place channels_of(const char* name, const void* p, const rewy_gnorm_desc* d) {
+  return whole(name, p, d->D * (int64_t)esize(d->w_dtype));
+}
+Place stats_of(const char* name, const void* p, const rewy_gnorm_desc* d) { return whole(name, p, d->M * d->G * 4); }
+
 }  // namespace
 }  // namespace rewy
 
@@ -63,6 +73,9 @@ REWY_API int rewy_gnorm_fwd(const rewy_gnorm_desc* d, const void* x, const void*
     if (!a.center && mean) return fail(REWY_EINVAL, "mean is given only with center");
     if (some && y && (y == x || y == z)) return fail(REWY_EINVAL, "y may not be x or z");
     if (!some) return REWY_OK;
+    REWY_TRY(check_apart({rows_of("y", y, d, a.ys), whole("q", q, d->M * d->D), whole("scale", scale, d->M * a.ng * 4),
+                          stats_of("mean", mean, d), stats_of("rstd", rstd, d)},
+                         {rows_of("x", x, d, a.xs), rows_of("z", z, d, a.zs), channels_of("w", w, d), channels_of("b", b, d)}));
     a.x = x; a.z = z; a.w = w; a.b = b; a.y = y; a.q = q; a.scale = scale; a.mean = mean; a.rstd = rstd;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool f32 = d->dtype == REWY_F32, wf32 = d->w_dtype == REWY_F32;
@@ -100,6 +113,9 @@ REWY_API int rewy_gnorm_bwd(const rewy_gnorm_desc* d, const void* x, const void*
     if (some && dx == dz) return fail(REWY_EINVAL, "dx may not be dz");
     const size_t need = gnorm_layout(a, static_cast<char*>(workspace));
     REWY_TRY(check_workspace(workspace, ws_bytes, need));
+    REWY_TRY(check_apart({rows_of("dx", dx, d, a.dxs), rows_of("dz", dz, d, a.dzs), channels_of("dw", dw, d), channels_of("db", db, d)},
+                         {rows_of("x", x, d, a.xs), rows_of("z", z, d, a.zs), rows_of("dy", dy, d, a.ys), channels_of("w", w, d),
+                          channels_of("b", b, d), stats_of("mean", mean, d), stats_of("rstd", rstd, d)}));
     a.x = x; a.z = z; a.w = w; a.b = b; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.dy = dy; a.dx = dx; a.dz = dz; a.dw = dw; a.db = db;
     const float* part = a.part;

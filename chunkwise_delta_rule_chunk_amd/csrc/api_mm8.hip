@@ -39,6 +39,11 @@ REWY_API int rewy_e4m3_linear(const rewy_e4m3_desc* d, const void* a, const floa
     REWY_TRY(check_ptr("y", y, esize(d->dtype), some));
     if (!some) return REWY_OK;
     if (y == a || y == w) return fail(REWY_EINVAL, "y may not be a or w");
+    const int64_t M = d->M, N = d->N, K = d->K, nb = g.nb, ye = (int64_t)esize(d->dtype);
+    REWY_TRY(check_apart({{"y", y, M, N * ye, g.ys * ye}},
+                         {{"a", a, M, K, g.as}, {"w", w, N, K, g.ws}, whole("a_scale", a_scale, 4 * M * (g.ablk ? nb : 1)),
+                          whole("w_scale", w_scale, 4 * (g.wrow ? N : (N + 127) / 128) * nb),
+                          whole("bias", bias, N * (int64_t)esize(d->bias_dtype))}));
     g.a = static_cast<const uint8_t*>(a); g.w = static_cast<const uint8_t*>(w);
     g.sa = a_scale; g.sw = w_scale; g.bias = bias; g.y = y;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -16,6 +16,9 @@ __device__ __forceinline__ void decay_pow2(float g, int n, float& hi, float& lo)
   hi = (float)d;
   lo = (float)(d - (double)hi);
 }
+// lo S of such a factor: an infinite S counts as the largest number, so that hi S stays what
+// it is (lo may be zero or negative)
+__device__ __forceinline__ float decay_low(float lo, float S) { return lo * __builtin_amdgcn_fmed3f(S, -3.4028235e38f, 3.4028235e38f); }
 
 // Row fragment (rows in slot order) of a tile with its columns as they are, for a
 // contraction whose partner lies in acc order (store_acc_order)
@@ -75,7 +78,7 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        S[ct][nt][i] = NS == 2 ? u[ct][i] : hi[ct] * S[ct][nt][i] + (lo * S[ct][nt][i] + u[ct][i]);
+        S[ct][nt][i] = NS == 2 ? u[ct][i] : hi[ct] * S[ct][nt][i] + (decay_low(lo, S[ct][nt][i]) + u[ct][i]);
   }
 }
 
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(256) void k_decay_pass(DecayArgs a, int dirs) {
         const bool last = dir ? i == 0 : i + 1 == ns;
         const float dh = last ? hl : hi, dl = last ? ll : lo;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[j] = dh * S[j] + (dl * S[j] + loc[u][j]);
+        for (int j = 0; j < 4; ++j) S[j] = dh * S[j] + (decay_low(dl, S[j]) + loc[u][j]);
       }
     }
     fetch(i0 + U);
@@ -575,7 +578,7 @@ __global__ __launch_bounds__(256) void k_decay_recurrent(DecayArgs a) {
       const float kx = sk[p][r0 + RP * i], qx = sq[p][r0 + RP * i];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        S[i][e] = hi * S[i][e] + (lo * S[i][e] + kx * v[e]);
+        S[i][e] = hi * S[i][e] + (decay_low(lo, S[i][e]) + kx * v[e]);
         y[e] += qx * S[i][e];
       }
     }

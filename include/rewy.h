@@ -416,7 +416,9 @@ size_t rewy_decay_workspace_bytes(const rewy_decay_desc *d, int phase);
 /* Forward in chunks of 64 tokens, for prompts and training.  h0 and ht may be NULL;
  * o does not depend on whether ht is given.  The workspace is left with the states that
  * rewy_decay_bwd takes as `states`.  An infinity or NaN in a token's row
- * reaches that token and the ones behind it, as in the recurrence. */
+ * reaches that token and the ones behind it, as in the recurrence; an infinite element of
+ * h0 stays what it is in ht and reaches the outputs of its column, as NaN where lam to the
+ * power of a segment's or chunk's tokens is zero in 32 bits. */
 int rewy_decay_fwd(const rewy_decay_desc *d, const void *q, const void *k, const void *v,
                    const float *g, const float *h0, void *o, float *ht,
                    void *workspace, size_t ws_bytes, void *stream);

@@ -395,7 +395,9 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_f
     } else if (c == 0 && t == 0 && on) {
       a.scale[m] = scale;
     }
-    store_codes_by<VE>(q + j, s[c], ScaleDiv(scale), a.quant == REWY_QUANT_E4M3, D - j);
+    const bool e4m3 = a.quant == REWY_QUANT_E4M3;
+    if (ScaleDiv::holds(scale)) store_codes_by<VE>(q + j, s[c], ScaleDiv(scale), e4m3, D - j);
+    else store_codes<VE>(q + j, s[c], scale, e4m3, D - j);
   }
 }
 

@@ -75,13 +75,18 @@ __device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d
   auto cv = [](float v) { return (uint32_t)(int)fminf(fmaxf(v != v ? 0.f : rintf(v), -127.f), 127.f) & 255u; };
   return cv(a) | cv(b) << 8 | cv(c) << 16 | cv(d) << 24;
 }
-// v / scale as the product with the scale's inverse and one correction: the quotient's own
-// rounding but for hardest cases (the inverse is rounded correctly and the remainder of
-// the first guess exact), in three operations instead of a division's nine.  A scale
-// that is infinite gives 0, and NaN for an infinite v, as the division does.
+// v / scale as the product with the scale's inverse and one correction, in three operations
+// instead of a division's nine, for scales from 2^-90.  The inverse is rounded correctly, so
+// the first guess q is within 1.5 steps and its remainder exact but for half a unit of its
+// last place: what is rounded last lies within 2^-22.7 steps of the quotient, which can round
+// apart only where v S' - T' S = +-1 .. 4 for the 24 bits S' of the scale and the 25 bits T'
+// of the middle between two floats.  Beside the borders between codes, whose T' are
+// one of 8 bits +- 1, none of these does: the codes are the division's.  Under 2^-90 the remainder
+// falls below the smallest float (and an infinite or NaN scale has no such inverse).
 struct ScaleDiv {
   float inv, s;
-  __device__ __forceinline__ explicit ScaleDiv(float scale) : inv(1.f / scale), s(__builtin_isinf(scale) ? 1.f : scale) {}
+  __device__ __forceinline__ explicit ScaleDiv(float scale) : inv(1.f / scale), s(scale) {}
+  static __device__ __forceinline__ bool holds(float scale) { return scale >= 0x1p-90f && scale <= 3.4028235e38f; }
   __device__ __forceinline__ float operator()(float v) const {
     const float q = v * inv;
     return fmaf(fmaf(-q, s, v), inv, q);

@@ -141,7 +141,8 @@ class DecayAttentionFunction(torch.autograd.Function):
 
 def decay_attention_autograd(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None):
     """Differentiable linear attention with a constant decay for each head on the HIP
-    path: (o, ht).  The decay is a constant: one that requires a gradient is refused."""
-    if log_decay.requires_grad:
+    path: (o, ht).  The decay is a constant: one that requires a gradient is refused while
+    gradients are recorded."""
+    if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay is a constant of the model and has no gradient (detach it)")
     return DecayAttentionFunction.apply(q, k, v, log_decay, h0, scale, cu_seqlens)

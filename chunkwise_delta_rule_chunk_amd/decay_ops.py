@@ -33,7 +33,7 @@ def _problem(q, k, v, log_decay, h0, scale, cu_seqlens):
     shape = (nseq, H, K, V)
     _like(h0, q, shape, "h0", torch.float32)
     desc = B.RewyDecayDesc(Bsz, T, H, G, K, V, n, _p(cu), None if host is None else ctypes.addressof(host), e,
-                           K ** -0.5 if scale is None else scale, _row_stride(q, "q", 2), _row_stride(k, "k", 2),
+                           max(K, 1) ** -0.5 if scale is None else scale, _row_stride(q, "q", 2), _row_stride(k, "k", 2),
                            _row_stride(v, "v", 2), 0, 0, 0, 0)
     return desc, shape, cu, host
 

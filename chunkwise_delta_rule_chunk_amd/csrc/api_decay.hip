@@ -13,9 +13,11 @@ namespace {
 // means fewer states to join; 8192 tokens of 32 heads: 134 us in segments of 512, 157
 // of 256, 146 of 1024).  Packed sequences end with half a segment on average: as many pairs
 // more, so that the shorter ones fill up behind the longer (16 sequences, 9000 tokens
-// of 32 heads: 117 us in segments of 384, 126 of 512, 143 of 1088).
+// of 32 heads: 117 us in segments of 384, 126 of 512, 143 of 1088).  At most 32768 tokens:
+// the walks of 16-bit tensors carry their state with six roundings a chunk from the
+// segment's start (decay_update), so 512 chunks add 2^-12.4, a tenth of the output's own step.
 int decay_segment(const SeqArgs& q, int H) {
-  constexpr int64_t SEGMENTS = 512;
+  constexpr int64_t SEGMENTS = 512, LONGEST = 512 * CH;
   int64_t want;
   if (q.cu) {
     const int64_t pairs = SEGMENTS + std::min((int64_t)(q.N - 1) * H / 2, SEGMENTS);
@@ -24,7 +26,7 @@ int decay_segment(const SeqArgs& q, int H) {
     const int64_t each = std::max<int64_t>(SEGMENTS / ((int64_t)q.N * H), 1);
     want = (q.T + each - 1) / each;
   }
-  return (int)std::min<int64_t>(INT32_MAX / CH * CH, std::max<int64_t>(128, up64(want)));
+  return (int)std::min<int64_t>(LONGEST, std::max<int64_t>(128, up64(want)));
 }
 
 int decay_args(const rewy_decay_desc* d, bool bwd, DecayArgs& a) {

@@ -10,7 +10,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding as B
-from .layer_ops import (_aligned, _check, _dtype, _like, _like_new, _On, _p, _row_stride, _saved_problem,
+from .layer_ops import (_aligned, _check, _dtype, _kept, _like, _like_new, _On, _p, _row_stride, _saved_problem,
                         _sequences, _workspace)
 
 
@@ -62,7 +62,7 @@ def decay_attention(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None,
         _check(B.rewy_decay_fwd(desc, _p(q), _p(k), _p(v), _p(log_decay), _p(h0), _p(o), _p(ht), _p(ws),
                                 ws.numel(), handle), "rewy_decay_fwd")
     return o, ht, dict(desc=desc, q=q, k=k, v=v, log_decay=log_decay, h0=h0, cu=cu, host=host,
-                       states=ws if states else None)
+                       states=ws if states else None, stream=handle)
 
 
 def decay_attention_recurrent(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None, ht=None, stream=None):
@@ -98,6 +98,7 @@ def decay_attention_backward(ctx, do, dht=None, *, out=None, want_dh0=None, clea
             if t.shape != ref.shape or t.dtype != ref.dtype:
                 raise ValueError(f"{name} must have the shape and type of its input")
     with _On(q, stream, (q, k, v, log_decay, h0, ctx["cu"], do, dht, states, *(out or ()))) as handle:
+        _kept(ctx, handle, q, ctx["cu"], states)
         if out is None:
             out = tuple(_like_new(t, clear) for t in (q, k, v))
         dq, dk, dv = out

@@ -118,6 +118,16 @@ class _On:
         return False
 
 
+def _kept(ctx, handle, ref, *tensors):
+    """What the forward made for its backward belongs to the forward's stream, and the caller may
+    not know of it: on another stream (the call's is the current one here) it is marked as used."""
+    if ctx.get("stream", handle) != handle:
+        stream = torch.cuda.current_stream(ref.device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _workspace(nbytes, ref, ws):
     if nbytes == 0:  # (the call itself would refuse the descriptor)
         raise B.RewyError(B.REWY_EINVAL, "workspace size")
@@ -192,7 +202,7 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0, ou
                                _p(rstd), handle), "rewy_norm_fwd")
     if s is None:
         s = x
-    return y, s, q, scale, dict(s=s, weight=weight, rstd=rstd, eps=eps)
+    return y, s, q, scale, dict(s=s, weight=weight, rstd=rstd, eps=eps, stream=handle)
 
 
 def rms_norm_backward(ctx, dy, ds=None, *, stream=None, ws=None):
@@ -209,6 +219,7 @@ def rms_norm_backward(ctx, dy, ds=None, *, stream=None, ws=None):
                           _row_stride(s, "s", 1), 0 if ds is None else _row_stride(ds, "ds", 1), 0,
                           _row_stride(dy, "dy", 1))
     with _On(s, stream, (s, weight, ctx["rstd"], dy, ds)) as handle:
+        _kept(ctx, handle, s, ctx["rstd"])
         dx = _like_new(s)
         dw = None if weight is None else torch.empty_like(weight)
         if dw is not None:
@@ -312,7 +323,7 @@ def short_conv(x, weight, bias=None, *, activation="silu", h0=None, cu_seqlens=N
         ht = x.new_empty(hshape) if output_final_state else None
         _check(B.rewy_conv_fwd(desc, _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(ht), handle),
                "rewy_conv_fwd")
-    return y, ht, dict(desc=desc, x=x, weight=weight, bias=bias, h0=h0, cu=cu, host=host)
+    return y, ht, dict(desc=desc, x=x, weight=weight, bias=bias, h0=h0, cu=cu, host=host, stream=handle)
 
 
 def short_conv_step(x, h0, weight, bias=None, *, activation="silu", ht=None, stream=None):
@@ -344,6 +355,7 @@ def short_conv_backward(ctx, dy, dht=None, *, clear=False, stream=None, ws=None)
     desc = B.RewyConvDesc(d.B, d.T, d.D, d.W, d.N, d.cu_seqlens, d.cu_seqlens_host, d.dtype, d.w_dtype,
                           d.act, d.x_stride, _row_stride(dy, "dy", 1), 0)
     with _On(x, stream, (x, weight, bias, h0, ctx["cu"], dy, dht)) as handle:
+        _kept(ctx, handle, x, ctx["cu"])
         dx = _like_new(x, clear)
         dw = torch.empty_like(weight)
         db = None if bias is None else torch.empty_like(bias)
@@ -427,7 +439,7 @@ def selective_scan(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seql
         _check(B.rewy_ssm_fwd(desc, _p(x), _p(dt), _p(a_log), _p(dt_bias), _p(b), _p(c), _p(d), _p(h0),
                               _p(y), _p(ht), _p(ws), ws.numel(), handle), "rewy_ssm_fwd")
     return y, ht, dict(desc=desc, x=x, dt=dt, a_log=a_log, b=b, c=c, d=d, dt_bias=dt_bias, h0=h0, cu=cu,
-                       host=host)
+                       host=host, stream=handle)
 
 
 def selective_scan_recurrent(x, dt, a_log, b, c, *, d=None, dt_bias=None, h0=None, cu_seqlens=None, ht=None,
@@ -465,6 +477,7 @@ def selective_scan_backward(ctx, dy, dht=None, *, out=None, want_dh0=None, clear
             if t.shape != ref.shape or t.dtype != ref.dtype:
                 raise ValueError(f"{name} must have the shape and type of its input")
     with _On(x, stream, (x, dt, a_log, b, c, d, dt_bias, h0, ctx["cu"], dy, dht, *(out or ()))) as handle:
+        _kept(ctx, handle, x, ctx["cu"])
         if out is None:
             out = tuple(_like_new(t, clear) for t in (x, b, c))
         dx, db, dc = out

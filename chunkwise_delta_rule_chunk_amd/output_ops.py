@@ -9,7 +9,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding as B
-from .layer_ops import _DT, _QDT, _QUANT, _adjoint, _check, _dtype, _like, _like_new, _On, _p, _row_stride, _workspace
+from .layer_ops import _DT, _QDT, _QUANT, _adjoint, _check, _dtype, _kept, _like, _like_new, _On, _p, _row_stride, _workspace
 
 _GATE = {None: B.REWY_ACT_NONE, "silu": B.REWY_ACT_SILU, "sigmoid": B.REWY_ACT_SIGMOID}
 
@@ -67,7 +67,7 @@ def group_norm(x, weight=None, bias=None, gate=None, *, groups, center=True, eps
         _check(B.rewy_gnorm_fwd(desc, _p(x), _p(gate), _p(weight), _p(bias), _p(y), _p(q), _p(scale), _p(mean),
                                 _p(rstd), handle), "rewy_gnorm_fwd")
     return y, q, scale, dict(x=x, weight=weight, bias=bias, gate=gate, mean=mean, rstd=rstd, groups=groups,
-                             center=center, eps=eps, activation=activation)
+                             center=center, eps=eps, activation=activation, stream=handle)
 
 
 def group_norm_backward(ctx, dy, *, stream=None, ws=None):
@@ -79,6 +79,7 @@ def group_norm_backward(ctx, dy, *, stream=None, ws=None):
     desc = _norm_problem(x, weight, bias, gate, ctx["groups"], ctx["center"], ctx["eps"], ctx["activation"], None, 0)
     desc.y_stride = _row_stride(dy, "dy", 1)
     with _On(x, stream, (x, weight, bias, gate, mean, rstd, dy)) as handle:
+        _kept(ctx, handle, x, mean, rstd)
         dx = _like_new(x)
         dz = None if gate is None else _like_new(gate)
         dw = None if weight is None else torch.empty_like(weight)

@@ -160,11 +160,11 @@ __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" :
 // wait_vm before the barrier behind which they are read.
 __device__ __forceinline__ void load_lds16(u32x4 b, uint32_t off, uint32_t dst) {
   dst = __builtin_amdgcn_readfirstlane(dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(u32x4 b, uint32_t off, uint32_t dst) {  // the same with 4 bytes a lane
   dst = __builtin_amdgcn_readfirstlane(dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b) : "memory", "m0");
 }
 // gbuf's resource as its four words
 __device__ __forceinline__ u32x4 buf_words(const void* base, uint32_t bytes) {

@@ -123,8 +123,10 @@ def e4m3_linear(a, a_scale, w, w_scale, bias=None, *, dtype=torch.bfloat16, stre
     float8_e4m3fn: a and a_scale as the norms hand them out (``quant="e4m3"``; ``group=128``:
     a_scale [rows, ceil(K / 128)], ``group=0``: [rows, 1]), w_scale [ceil(N / 128), ceil(K /
     128)] for blocks of 128 x 128 or [N, ceil(K / 128)] for rows.  ``dtype`` is y's, bf16 or
-    fp32.  Rows of a and w may have a stride; K is a multiple of 16.  For inference: 8-bit
-    codes have no gradient."""
+    fp32.  Rows of a and w may have a stride; K is a multiple of 16.  Sums are fp32 for an fp32
+    y and for up to 32 rows; a bf16 y of more rows may also miss 2^-10 of the sum of its terms'
+    magnitudes (rewy.h), so a row's bits may depend on how many share the call.  For inference:
+    8-bit codes have no gradient."""
     for t, name in ((a, "a"), (w, "w")):
         if t.dtype != torch.float8_e4m3fn:
             raise TypeError(f"{name} must be float8_e4m3fn (got {t.dtype})")

@@ -485,8 +485,14 @@ int rewy_gnorm_bwd(const rewy_gnorm_desc *d, const void *x, const void *z, const
  * blocks of 128 columns:
  *     y[m, n] = sum_b sa[m, b] sw[n, b] (sum_{k in b} a[m, k] w[n, k]) + bias[n],
  * b the blocks of 128 of the K columns (the last may be shorter).  a is what the norms
- * hand out as q, w a weight [N, K] as it is stored.  Products of codes are exact, sums
- * are fp32, y is rounded once.  A NaN code or scale reaches the outputs of its row of a
+ * hand out as q, w a weight [N, K] as it is stored.  y is rounded once.  A 32-bit y, and
+ * a 16-bit one of up to 32 rows, is formed from exact products of codes and their
+ * sums in fp32.  A 16-bit y of more rows comes from the 8-bit matrix instructions, which
+ * line up at most eight neighbouring products of a block 13 bits under the largest of them
+ * and drop what lies below: 2^-10 of sum |a w| sa sw at most, which an output whose terms
+ * cancel shows, and 1.5e-5 of y in norm for normally distributed codes.  So a row's bits may
+ * depend on how many rows share the call.  The product of two scales is formed first and
+ * has to lie within fp32's range.  A NaN code or scale reaches the outputs of its row of a
  * or w (and, for a scale that 128 rows of w share, of those rows). */
 typedef struct {
     int32_t M;                      /* rows of a, 0 .. 2^31 - 1024 */

@@ -9,13 +9,14 @@ namespace {
 
 // Tokens of a segment, whole chunks, at least 128 (2 x 1000 tokens of 16 heads in 32 bits, a
 // training step's kernels: 86 us in segments of 128, 92 of 64, 101 of 256): as long as there
-// are 512 pairs of a segment and a head, two workgroups for each CU (a longer segment
-// means fewer states to join; 8192 tokens of 32 heads: 134 us in segments of 512, 157
+// are at most 512 pairs of a segment and a head, two workgroups for each CU; the segments of a
+// sequence are a whole number, rounded down, so 257 to 511 pairs of a sequence and a head get one
+// each (a longer segment means fewer states to join; 8192 tokens of 32 heads: 134 us in segments of 512, 157
 // of 256, 146 of 1024).  Packed sequences end with half a segment on average: as many pairs
 // more, so that the shorter ones fill up behind the longer (16 sequences, 9000 tokens
 // of 32 heads: 117 us in segments of 384, 126 of 512, 143 of 1088).  At most 32768 tokens:
 // the walks of 16-bit tensors carry their state with six roundings a chunk from the
-// segment's start (decay_update), so 512 chunks add 2^-12.4, a tenth of the output's own step.
+// segment's start (decay_update), so 512 chunks add 2^-12.4, a tenth of the output's own half step.
 int decay_segment(const SeqArgs& q, int H) {
   constexpr int64_t SEGMENTS = 512, LONGEST = 512 * CH;
   int64_t want;

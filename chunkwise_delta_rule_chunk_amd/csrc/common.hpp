@@ -77,8 +77,9 @@ __device__ __forceinline__ int opaque_tid() {
 // Workgroup barrier for LDS traffic only: waits for this wave's LDS operations
 // and meets the other waves, but leaves global loads and stores in flight (a
 // full __syncthreads() fence also drains them, which would stall every barrier
-// on outstanding prefetches and output stores).  Global memory is never used
-// to communicate between the threads of one workgroup in these kernels.
+// on outstanding prefetches and output stores).  Where the threads of a workgroup
+// pass something on through global memory (the group norm's statistics do), the barrier
+// is a __syncthreads().
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }

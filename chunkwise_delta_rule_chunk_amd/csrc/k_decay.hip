@@ -88,19 +88,17 @@ __device__ __forceinline__ void decay_update(f32x4 (&S)[CT][KA / 16], const T* s
 // ht (dh0) itself.  Wave w holds 16 CT columns of the state.
 // Three pieces of bf16 (24 bits) a chunk make 48 products where one would make 16, so
 // the matrix unit and the pieces' arithmetic cost what the loads do: 8192 tokens of 32
-// heads, K = V = 128, bf16: 47 us for 134 MB read and 34 written (3.6 TB/s), 45 with all
+// heads, K = V = 128, bf16: 48 us for 134 MB read and 34 written (3.5 TB/s), 45 with all
 // heads on one key and value head, whose rows come from L2.  Two tiles of 16 columns a
 // wave read the key tile half as often (49 us with one, and with spills).
-// (waves a SIMD: two workgroups of 512 threads a CU, or as many as the registers hold)
-template <typename T, int K, int V>
-constexpr int state_waves() { return 2; }
+// Two waves a SIMD: two workgroups of 256 threads a CU, four of 128 (V = 32).
 // 16-column tiles of a wave, threads of a workgroup
 template <typename T, int V>
 constexpr int state_ct() { return V == 128 ? 2 : 1; }
 template <typename T, int V>
 constexpr int state_threads() { return 4 * V / state_ct<T, V>(); }
 template <typename T, int K, int V>
-__global__ __launch_bounds__((state_threads<T, V>()), (state_waves<T, K, V>())) void k_decay_state(DecayArgs a, int dirs) {
+__global__ __launch_bounds__((state_threads<T, V>()), 2) void k_decay_state(DecayArgs a, int dirs) {
   constexpr int CT = state_ct<T, V>(), NTH = state_threads<T, V>(), LK = pitch<T>(K), LV = pitch<T>(V), NQ = CH / KG<T>, NT = K / 16;
   __shared__ __align__(16) T sk[CH * LK];
   __shared__ __align__(16) T su[CH * LV];
@@ -251,7 +249,8 @@ struct WalkIo {
 // later rows (the backward's inputs are finite).
 // What bounds it: with 246 registers a thread two workgroups fit a CU, two waves a SIMD,
 // and a chunk's three barriers stand between a load, LDS, the products and the next tile;
-// matrix unit and vector unit are each at work a quarter of the time, LDS two fifths.
+// the matrix unit is at work 27% of the time, the vector unit 33%, LDS 46% (8192 tokens of 32
+// heads, K = V = 128).
 // Rows that come from L2 alone are 4% faster, so it is not HBM.  Registers for three waves
 // a SIMD are not there (K = 64, V = 128 with spills: 86 us where this takes 57).
 template <typename T, int KA, int CV, int CT, bool REV, bool TS, bool ODD>
@@ -496,7 +495,9 @@ __device__ __forceinline__ void decay_one(const DecayArgs& a, T* lds, float* tab
 }
 
 // 8192 tokens of 32 heads, K = V = 128, bf16: 65 us (4.1 TB/s); 9000 tokens in 16
-// sequences, 32 heads on 8, K = 64: 57 us; 2 x 1000 tokens of 16 heads, 64, fp32: 14.8 us.
+// sequences, 32 heads on 8, K = 64: 58 us; 2 x 1000 tokens of 16 heads, 64, fp32: 15.2 us;
+// fp32, 8192 tokens of 32 heads, a call with its states: K = V = 64 114 us, 128 363 (one
+// workgroup a CU beside 120 KB of LDS).
 template <typename T, int K, int V>
 __global__ __launch_bounds__((walk_threads<T, V>()), (walk_waves<T, K, V>())) void k_decay_fwd(DecayArgs a) {
   __shared__ __align__(16) T lds[walk_lds<T, K, V>()];

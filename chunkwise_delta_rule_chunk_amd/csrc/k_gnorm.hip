@@ -54,7 +54,8 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x, int lanes) {
   return x;
 }
 
-// the activation's value, and its derivative
+// the activation's value, and its derivative.  The sigmoid is the hardware's exponential and
+// reciprocal: within (2 |t| + 8) 2^-24 of itself, for 32-bit tensors too.
 template <int ACT>
 __device__ __forceinline__ float act_value(float t) {
   return ACT == REWY_ACT_NONE ? t : ACT == REWY_ACT_SILU ? t * sigmoid_f(t) : sigmoid_f(t);
@@ -260,8 +261,8 @@ struct RawRow {
 // use; group and scale indices are shifts and a group's mean a product with an exact
 // 1 / L, for the row's arithmetic costs nearly what its bytes do (with divisions 51.7 us
 // where this takes 45).  8192 rows of 32 groups of 128 bf16 with a gate: 47.8 us
-// (4.2 TB/s) to bf16, 45.0 us (3.7 TB/s) to e4m3 with a scale for each 128; 16 rows 4.1.
-// 2003 rows of 29 groups of 53 fp32 to int8: 18.4 us (12.2 behind a launch of 9.2 that took
+// (4.2 TB/s) to bf16, 45.7 us (3.7 TB/s) to e4m3 with a scale for each 128; 16 rows 4.1.
+// 2003 rows of 29 groups of 53 fp32 to int8: 18.9 us (12.2 behind a launch of 9.2 that took
 // the statistics from memory; 8192 x 32 x 100 bf16 to bf16: 55 and 76 us a call).
 template <typename T, typename W, int TPR, int NC, bool ODD>
 __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_fwd(GnormArgs a) {
@@ -581,6 +582,12 @@ __global__ __launch_bounds__(TPR > NORM_BLOCK ? TPR : NORM_BLOCK) void k_gnorm_b
 // vectors and no row ahead 132), and as many threads as vectors to the next power of two:
 // threads without a vector cost what the others do (262144 x 256 bf16 by 32 threads a row 53
 // us, by 64 87; 1048576 x 32 by 4 threads 25, by 16 75).
+// The backward of the longest rows asks for more than the 128 registers that 1024 threads leave
+// and spills: with two vectors of bf16 or four of fp32 (past 8192 channels) about 200 bytes a
+// thread with groups in lanes and 650 with others, 60 to 150 with others from 4097 channels.  With
+// a gate, weight and bias, 2048 rows of 16384 bf16 take 158 us with groups in lanes (128 of 128;
+// 68.6 at copy rate) and 440 with others (8 of 2048), 1024 rows of 16384 fp32 133 and 308; the
+// forward does not spill (47, 66, 43 and 52 us; 41.2).
 template <typename T, typename F>
 hipError_t gnorm_shape(int D, F&& f) {
   constexpr int VE = Vec<T>::VE;

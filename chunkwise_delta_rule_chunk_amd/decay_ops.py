@@ -67,7 +67,7 @@ def decay_attention(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None,
 
 def decay_attention_recurrent(q, k, v, log_decay, *, scale=None, h0=None, cu_seqlens=None, ht=None, stream=None):
     """The same attention token by token (decoding).  Returns (o, ht); ``ht`` may be h0
-    itself (updated in place)."""
+    itself (updated in place).  o's rows behind the last sequence are not written."""
     desc, shape, cu, host = _problem(q, k, v, log_decay, h0, scale, cu_seqlens)
     _like(ht, q, shape, "ht", torch.float32)
     with _On(q, stream, (q, k, v, log_decay, h0, cu, ht)) as handle:
@@ -83,7 +83,7 @@ def decay_attention_backward(ctx, do, dht=None, *, out=None, want_dh0=None, clea
     """Gradients of the attention: dict(dq, dk, dv, dh0), dk and dv summed over the heads
     that share them.  do [B, T, H, V] may be a slice of longer rows.  ``out=(dq, dk, dv)``
     gives the places of those three (slices of one row, for the joint projection's
-    backward); ``clear`` as in the forward, for the gradients that are made here.  dh0 is
+    backward; they share no byte with each other or an input); ``clear`` as in the forward, for the gradients that are made here.  dh0 is
     handed out where h0 was given, or as ``want_dh0`` says."""
     q, k, v, log_decay, h0, states = (ctx[n] for n in ("q", "k", "v", "log_decay", "h0", "states"))
     if tuple(do.shape) != (*q.shape[:3], v.shape[3]) or do.dtype != q.dtype:

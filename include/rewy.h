@@ -397,7 +397,8 @@ int rewy_ssm_recurrent_fwd(const rewy_ssm_desc *d, const void *x, const void *dt
  * dtype tensors and states are 16-byte aligned and strides a multiple of 16 bytes, at
  * most 2^22 elements.  K and V are 32, 64 or 128.  With bf16 operands the coefficients
  * inside a chunk and the states that only 16-bit outputs read are rounded to bf16 as
- * operands; the states that are handed out keep 24 bits. */
+ * operands; the states that are handed out keep 24 bits.  Outputs share no byte with an
+ * input or each other; slices of one row may lie between each other. */
 typedef struct {
     int32_t B, T, H, G, K, V;
     int32_t N;                      /* sequences: B (or 0) without cu_seqlens */
@@ -445,7 +446,8 @@ int rewy_decay_recurrent_fwd(const rewy_decay_desc *d, const void *q, const void
  * output: row by row, for each of G groups of L = D / G neighbouring channels,
  *     mean = avg x (0 without center),  rstd = (avg (x - mean)^2 + eps)^-1/2,
  *     n = (x - mean) rstd w + b,   y = n act(z),  or  y = act(n) without a gate z,
- * and scale and q from the unrounded y as for the RMS norm.  With the heads of a
+ * and scale and q from the unrounded y as for the RMS norm.  act is formed by the hardware's
+ * exponential and reciprocal, within (2 |t| + 8) 2^-24 of itself at an argument t.  With the heads of a
  * token mixer as the groups this is the norm behind it; q and scale (group 128) are
  * what rewy_e4m3_linear reads. */
 typedef struct {
